@@ -335,6 +335,81 @@ int fg_fp8_mqa_logits(int S, int T, int H, int D, const uint8_t* q, const uint8_
                       const float* kv_sf, const float* weights, const int32_t* ks,
                       const int32_t* ke, int clean_logits, float* out, fg_stream_t stream);
 
+/*
+ * Operators of an MoE decode step: the router, the whole MoE MLP for a few tokens, and a
+ * projection with per-token adapters.  They keep the conventions above (caller-owned device
+ * arrays, asynchronous on `stream`, the GEMMs' operand and scale layouts, bounded waits).
+ */
+typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_score;
+
+/*
+ * MoE router.  Per token t, over its E logits l:
+ *   s = softmax(l) or sigmoid(l)  (score: fg_score);   key = l, or s + bias where bias is given
+ *   group limit (n_group > 1): the E experts form n_group groups of E / n_group; a group's score
+ *     is its largest key, or with a bias the sum of its two largest; only the experts of the
+ *     topk_group best groups can be chosen
+ *   the topk experts with the largest keys, in falling order; ties go to the lowest index
+ *   weight = s (without the bias), divided by the sum of the chosen ones if renormalize, * scale
+ * A logit of -inf or NaN (or a NaN bias) takes its expert out; a slot without an expert gets id
+ * -1 and weight 0 (fg_*_moe_mlp skips it).
+ *   logits [T][E] FP32;  bias [E] FP32 or NULL;  topk_ids [T][topk] int32;  topk_weights FP32
+ * Supported: E <= 1024, topk <= 32, n_group <= 32; topk <= topk_group * E / n_group.
+ */
+int fg_moe_route(int T, int E, int topk, int n_group, int topk_group, int score, int renormalize, float scale,
+                 const float* logits, const float* bias, int32_t* topk_ids, float* topk_weights,
+                 fg_stream_t stream);
+
+/*
+ * The whole MoE MLP for a few tokens, in two launches: no gather, no grouped operands, no
+ * combine step around it.  Per token t:
+ *   W(t, e) = sum of topk_weights[t][j] over the slots j with topk_ids[t][j] == expert_base + e
+ *   g, u    = A[t,:] @ w13[e]^T  (I gate rows, then I up rows);   y = W(t, e) * SiLU(g) * u
+ *   (q, s)  = E4M3 codes and 1x128 UE8M0 scales of y, as fg_quantize_1x128_rows makes them
+ *   D[t,:]  = sum over the experts e that t uses of (q * s) @ w2[e]^T
+ * accumulated in FP32 over all experts and rounded once.  Ids outside [expert_base,
+ * expert_base + E) belong to other shards (or are -1) and are skipped; a token without an
+ * expert here gets zeros whatever its row holds.  Non-finite activations of an expert make the
+ * rows of the tokens that use it NaN, and no others.
+ *   a    [T][H] E4M3, sfa as for fg_fp8_gemm_nt      w13 [E][2I][H], sf13 [E][ceil(H/512)][align4(2I/128)]
+ *   w2   [E][H][I], sf2 [E][ceil(I/512)][align4(H/128)]
+ *   topk_ids [T][topk] int32, topk_weights [T][topk] FP32;  d [T][H] BF16 or FP32
+ * FP4 weights: w13 [E][2I][H/2], sf13 [E][H/128][align4(2I)], w2 [E][H][I/2], sf2
+ * [E][I/128][align4(H)], the weight arrays 32-byte aligned.
+ * workspace: fg_moe_mlp_workspace bytes, 256-byte aligned, zeroed once before its first call
+ * (every completed call leaves its counters zero again; zero it anew after a time-out).  One
+ * that is large enough serves calls of any sizes, of both MoE MLPs and of the projection below,
+ * one after another; calls that may run at the same time need one each.
+ * H % 128 == 0, I % 128 == 0, T >= 0.  Supported: T <= 128, E <= 1024, topk <= 32; more tokens
+ * take the grouped GEMMs.
+ */
+long long fg_moe_mlp_workspace(int T, int H, int I, int E);   /* bytes, or -1 */
+int fg_fp8_moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t* a, const int32_t* sfa,
+                   const uint8_t* w13, const int32_t* sf13, const uint8_t* w2, const int32_t* sf2,
+                   const int32_t* topk_ids, const float* topk_weights, void* d, int d_dtype, void* workspace,
+                   fg_stream_t stream);
+int fg_fp8_fp4_moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t* a, const int32_t* sfa,
+                       const uint8_t* w13, const int32_t* sf13, const uint8_t* w2, const int32_t* sf2,
+                       const int32_t* topk_ids, const float* topk_weights, void* d, int d_dtype, void* workspace,
+                       fg_stream_t stream);
+
+/*
+ * Projection shared by all tokens plus each token's own low-rank adapter:
+ *   D[m,:] = A[m,:] @ B^T + scaling[l] * (x[m,:] @ lora_a[l]^T) @ lora_b[l]^T,   l = ids[m]
+ * A, sfa, B, sfb as for fg_fp8_gemm_nt; the adapters read the BF16 activations x and take part
+ * in the same FP32 accumulation, D is rounded once.  x @ lora_a^T enters the second product as
+ * a sum of BF16 parts: two (16 mantissa bits) for a BF16 D, three (24) for an FP32 D.  ids[m] < 0: no adapter; ids[m] >= L: no adapter, and a
+ * device contract violation is recorded (0x106).
+ *   x [M][K] BF16;  lora_a [L][R][K], lora_b [L][N][R] BF16 (smaller ranks zero-padded to R);
+ *   scaling [L] FP32;  ids [M] int32;  d [M][N] BF16 or FP32
+ *   workspace: fg_lora_workspace bytes, under the same rules as fg_moe_mlp_workspace
+ * M >= 0, N % 16 == 0, K % 128 == 0, R % 8 == 0, 8 <= R <= 128, M <= 65536.  Supported: L <= 1024.
+ */
+long long fg_lora_workspace(int M, int N, int K, int R);
+int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, const int32_t* sfa, const uint8_t* b,
+                        const int32_t* sfb, const void* x, const void* lora_a, const void* lora_b,
+                        const float* scaling, const int32_t* ids, void* d, int d_dtype, void* workspace,
+                        fg_stream_t stream);
+
 /* Row alignment of each group segment in the contiguous layout: 128, the M block
  * (docsearch section 9 item 2 and section 10). */
 int fg_get_mk_alignment_for_contiguous_layout(void);
@@ -369,6 +444,7 @@ int fg_get_pdl(void);
  *   0x103  a masked_m entry lies outside [0, M_max]
  *   0x104  K-grouped ks entries negative, not multiples of 128, or not summing to K_total
  *   0x105  internal: a split-K launch without one tile per cluster
+ *   0x106  an adapter id >= L
  *   0x2xx  a bounded wait inside a kernel ran out (xx says which role waited)
  * The word is one per device and shared by every stream: a kernel of another stream that
  * records an event concurrently is reported by this call or by the next one (the read

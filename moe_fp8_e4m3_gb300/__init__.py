@@ -21,6 +21,8 @@ FG_ERR_DEVICE_CONTRACT = -4
 FG_ERR_DEVICE_TIMEOUT = -5
 FG_BF16 = 0
 FG_F32 = 1
+FG_SCORE_SOFTMAX = 0
+FG_SCORE_SIGMOID = 1
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -46,6 +48,12 @@ _SIGNATURES = {
     "fg_quantize_128x128_blocks": (_I, [_I, _I, _I, _P, _P, _P, _P]),
     "fg_quantize_1x128_cols": (_I, [_I, _I, _P, _P, _P, _P]),
     "fg_quantize_mxfp4": (_I, [_I, _I, _I, _P, _P, _P, _P]),
+    "fg_moe_route": (_I, [_I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "fg_moe_mlp_workspace": (ctypes.c_longlong, [_I, _I, _I, _I]),
+    "fg_fp8_moe_mlp": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "fg_fp8_fp4_moe_mlp": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "fg_lora_workspace": (ctypes.c_longlong, [_I, _I, _I, _I]),
+    "fg_fp8_gemm_nt_lora": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_get_tma_aligned_size": (_I, [_I, _I]),
     "fg_set_num_sms": (None, [_I]),
@@ -351,6 +359,101 @@ def quantize_1x128_cols(x, q, sf, stream=None) -> None:
     k, mn = x.shape
     _check(lib.fg_quantize_1x128_cols(k, mn, _ptr(x), _ptr(q), _ptr(sf), _stream(stream)),
            "quantize_1x128_cols")
+
+
+def moe_route(logits, topk_ids, topk_weights, bias=None, score="softmax", n_group=1, topk_group=1,
+              renormalize=True, scale=1.0, stream=None) -> None:
+    """MoE router.  logits float32 [T,E]; topk_ids int32 [T,topk] and topk_weights float32
+    [T,topk] (out); bias float32 [E] added to the scores for the choice only; score "softmax" or
+    "sigmoid"; the choice is limited to the topk_group best of n_group groups of experts."""
+    _f32(logits, "logits"); _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
+    if bias is not None:
+        _f32(bias, "bias")
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    t, e = logits.shape
+    topk = topk_ids.shape[1]
+    if topk_ids.shape[0] != t or topk_weights.shape != topk_ids.shape or (bias is not None and bias.numel() != e):
+        raise ValueError("topk_ids and topk_weights must be [T, topk], bias [E]")
+    _check(lib.fg_moe_route(t, e, topk, n_group, topk_group,
+                            FG_SCORE_SIGMOID if score == "sigmoid" else FG_SCORE_SOFTMAX, 1 if renormalize else 0,
+                            scale, _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights), _stream(stream)),
+           "moe_route")
+
+
+def _workspace(nbytes, device, where):
+    import torch
+    if nbytes < 0:
+        _check(FG_ERR_INVALID_ARG, where)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def moe_mlp_workspace(t, h, i, e, device="cuda"):
+    """Zeroed workspace of fp8_moe_mlp / fp8_fp4_moe_mlp for t tokens; reusable, one per concurrent call."""
+    return _workspace(lib.fg_moe_mlp_workspace(t, h, i, e), device, "moe_mlp_workspace")
+
+
+def _moe_mlp(fn, name, weight, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base, stream):
+    _fp8(a, "a"); weight(w13, "w13"); weight(w2, "w2"); _i32(sfa, "sfa"); _i32(sf13, "sf13"); _i32(sf2, "sf2")
+    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
+    code = _out(d, "d")
+    t, h = a.shape
+    e, i = w13.shape[0], w13.shape[1] // 2
+    topk = topk_ids.shape[1]
+    if w2.shape[:2] != (e, h) or topk_ids.shape[0] != t or topk_weights.shape != topk_ids.shape or d.shape != a.shape:
+        raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I], topk_ids and topk_weights [T,topk]")
+    if not workspace.is_cuda or workspace.numel() < lib.fg_moe_mlp_workspace(t, h, i, e):
+        raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
+    _check(fn(t, h, i, e, topk, expert_base, _ptr(a), _ptr(sfa), _ptr(w13), _ptr(sf13), _ptr(w2), _ptr(sf2),
+              _ptr(topk_ids), _ptr(topk_weights), _ptr(d), code, _ptr(workspace), _stream(stream)), name)
+
+
+def fp8_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base=0, stream=None) -> None:
+    """The whole MoE MLP for at most 128 tokens.  a [T,H] E4M3 with sfa; w13 [E,2I,H] (I gate rows,
+    then I up rows) with sf13 [E, ceil(H/512), align4(2I/128)]; w2 [E,H,I] with sf2; topk_ids int32
+    and topk_weights float32 [T,topk]; d [T,H] BF16/FP32 (out).  Ids outside [expert_base,
+    expert_base + E) are skipped.  workspace from moe_mlp_workspace."""
+    _moe_mlp(lib.fg_fp8_moe_mlp, "fp8_moe_mlp", _fp8, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace,
+             expert_base, stream)
+
+
+def fp8_fp4_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base=0,
+                    stream=None) -> None:
+    """fp8_moe_mlp with FP4 weights: w13 [E,2I,H/2] packed E2M1 with sf13 [E, H/128, align4(2I)],
+    w2 [E,H,I/2] with sf2 [E, I/128, align4(H)] (one UE8M0 scale per 32 K elements of a row)."""
+    _moe_mlp(lib.fg_fp8_fp4_moe_mlp, "fp8_fp4_moe_mlp", _fp4, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d,
+             workspace, expert_base, stream)
+
+
+def _bf16(t, name):
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
+        raise TypeError(f"{name} must be a contiguous CUDA bfloat16 tensor")
+
+
+def lora_workspace(m, n, k, r, device="cuda"):
+    """Zeroed workspace of fp8_gemm_nt_lora; reusable, one per concurrent call."""
+    return _workspace(lib.fg_lora_workspace(m, n, k, r), device, "lora_workspace")
+
+
+def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspace, stream=None) -> None:
+    """D[m] = A[m] @ B.T + scaling[l] * (x[m] @ lora_a[l].T) @ lora_b[l].T with l = ids[m] (-1: no
+    adapter).  a, sfa, b, sfb as fp8_gemm_nt; x [M,K], lora_a [L,R,K], lora_b [L,N,R] BF16; scaling
+    float32 [L]; ids int32 [M]; d [M,N] BF16/FP32 (out).  workspace from lora_workspace."""
+    _fp8(a, "a"); _fp8(b, "b"); _i32(sfa, "sfa"); _i32(sfb, "sfb"); _i32(ids, "ids")
+    _bf16(x, "x"); _bf16(lora_a, "lora_a"); _bf16(lora_b, "lora_b"); _f32(scaling, "scaling")
+    code = _out(d, "d")
+    m, k = a.shape
+    n = b.shape[0]
+    l, r = lora_a.shape[:2]
+    if (b.shape[1] != k or x.shape != a.shape or lora_a.shape[2] != k or lora_b.shape != (l, n, r) or
+            scaling.numel() != l or ids.numel() != m or d.shape != (m, n)):
+        raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
+    if not workspace.is_cuda or workspace.numel() < lib.fg_lora_workspace(m, n, k, r):
+        raise ValueError("workspace is smaller than lora_workspace(m, n, k, r)")
+    _check(lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(x), _ptr(lora_a),
+                                   _ptr(lora_b), _ptr(scaling), _ptr(ids), _ptr(d), code, _ptr(workspace),
+                                   _stream(stream)), "fp8_gemm_nt_lora")
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "fg.h"
+#include "fg_host.h"
 #include "fg_launch.h"
 #include "fg_mqa.cuh"
 
@@ -623,6 +624,32 @@ int dense_mn(int maj, int M, int N, int K, const uint8_t* a, const int32_t* sfa,
 }
 
 }  // namespace
+
+namespace fg {
+
+int host_state(HostState* out) {
+    DeviceState* st = nullptr;
+    const int rc = device_state(&st);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    *out = HostState{sms_in_use(*st), st->status, g_timeout_ns, g_pdl, g_debug_stall};
+    return FG_OK;
+}
+
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                  const uint64_t* pitches, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; one[i] = 1; }
+    for (int i = 0; i + 1 < rank; ++i) s[i] = pitches[i];
+    return g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool print_configs_enabled() { return print_configs(); }
+
+}  // namespace fg
 
 extern "C" {
 

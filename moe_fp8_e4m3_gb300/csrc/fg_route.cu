@@ -1,0 +1,202 @@
+// fg_route.cu - MoE router: logits -> top-k expert ids and routing weights.
+//
+// One warp per token, the token's E logits in its registers (E / 32 per lane).  The k-th best
+// expert is found k times: each lane keeps its best key, one warp-wide integer maximum over
+// order-preserving bits finds the winner, one minimum over the winners' indices breaks ties to
+// the lowest expert, and only the winning lane looks for its next best.  Bound: latency for few
+// tokens, instruction issue (about 60 warp instructions per chosen expert) for many; the bytes,
+// 4 E per token, are read once.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fg.h"
+#include "fg_host.h"
+#include "fg_ptx.cuh"
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+struct RouteParams {
+    const float* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int T, E, topk, groups, keep, sigmoid, renormalize;
+    float scale;
+};
+
+// Unsigned order of floats; 0 stands for "never": -inf and NaN.  (x + 0 makes -0 equal to +0.)
+__device__ __forceinline__ uint32_t ordered(float x) {
+    if (!(x > kNegInf)) return 0u;
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+// Two largest of a group, as one order with -inf allowed.
+__device__ __forceinline__ uint32_t ordered_any(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+template <int V>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p) {
+    extern __shared__ float keys_s[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kWarps + warp;
+    fg::grid_dependency_wait();
+    if (threadIdx.x == 0) fg::grid_launch_dependents();
+    if (t >= p.T) return;
+    constexpr uint32_t kAll = 0xffffffffu;
+    float s[V];
+    const float* row = p.logits + (long long)t * p.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        s[i] = e < p.E ? __ldcg(row + e) : kNegInf;
+        if (!(s[i] == s[i])) s[i] = kNegInf;               // NaN: never chosen, no share of the softmax
+    }
+    uint32_t key[V];
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        top = fmaxf(top, s[i]);
+        key[i] = ordered(s[i]);
+    }
+    if (p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = 1.0f / (1.0f + expf(-s[i]));       // 0 for -inf
+    } else {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = s[i] > kNegInf ? expf(s[i] - top) : 0.0f;
+            sum += s[i];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = sum > 0.0f ? s[i] / sum : (sum == sum ? 0.0f : sum);
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i]) key[i] = ordered(s[i] + __ldg(p.bias + i * 32 + lane));
+    }
+    if (p.groups > 1) {
+        // group score: its largest key, or with a bias the sum of its two largest; lane g looks at group g
+        uint32_t* ks = reinterpret_cast<uint32_t*>(keys_s) + warp * p.E;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < p.E) ks[i * 32 + lane] = key[i];
+        __syncwarp();
+        const int per = p.E / p.groups;
+        uint32_t a = 0, b = 0;                                // two largest
+        if (lane < p.groups)
+            for (int j = 0; j < per; ++j) {
+                const uint32_t k = ks[lane * per + j];
+                if (k > a) { b = a; a = k; }
+                else if (k > b) b = k;
+            }
+        auto value = [](uint32_t k) {
+            return k == 0 ? kNegInf : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+        };
+        const uint32_t score = ordered_any(p.bias && per > 1 ? value(a) + value(b) : value(a));
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t other = __shfl_sync(kAll, score, g);
+            rank += other > score || (other == score && g < lane);
+        }
+        const uint32_t kept = __ballot_sync(kAll, lane < p.groups && rank < p.keep);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < p.E && !(kept >> ((i * 32 + lane) / per) & 1u)) key[i] = 0;
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    int my_id = -1;
+    float my_w = 0.0f;
+    for (int j = 0; j < p.topk; ++j) {
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        if (m == 0) break;                                    // nothing left: the slots stay -1
+        uint32_t e = 0xffffffffu;
+        if (best == m) {
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                if (key[i] == m) e = i * 32 + lane;
+        }
+        const uint32_t win = __reduce_min_sync(kAll, e);
+        float w = 0.0f;
+        if (e == win) {
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (i * 32 + lane == win) { w = s[i]; key[i] = 0; }
+                best = max(best, key[i]);
+            }
+        }
+        w = __shfl_sync(kAll, w, win & 31);
+        if (lane == j) { my_id = static_cast<int>(win); my_w = w; }
+    }
+    if (p.renormalize) {
+        float sum = my_w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        my_w = sum > 0.0f ? my_w / sum : (sum == sum ? 0.0f : sum);
+    }
+    if (lane < p.topk) {
+        p.ids[(long long)t * p.topk + lane] = my_id;
+        p.weights[(long long)t * p.topk + lane] = my_id >= 0 ? my_w * p.scale : 0.0f;
+    }
+}
+
+template <int V>
+cudaError_t launch(const RouteParams& p, int pdl, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.T + kWarps - 1) / kWarps));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = p.groups > 1 ? kWarps * p.E * sizeof(float) : 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, route_kernel<V>, p);
+}
+
+bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" int fg_moe_route(int T, int E, int topk, int n_group, int topk_group, int score, int renormalize, float scale,
+                            const float* logits, const float* bias, int32_t* topk_ids, float* topk_weights,
+                            fg_stream_t stream) {
+    if (T < 0 || E < 1 || topk < 1 || topk > E || n_group < 1 || E % n_group != 0 || topk_group < 1 ||
+        topk_group > n_group || topk > topk_group * (E / n_group) || (score != FG_SCORE_SOFTMAX && score != FG_SCORE_SIGMOID))
+        return FG_ERR_INVALID_ARG;
+    if (E > 1024 || topk > 32 || n_group > 32) return FG_ERR_UNSUPPORTED;
+    if (T == 0) return FG_OK;
+    if (!logits || !topk_ids || !topk_weights || !al4(logits) || !al4(topk_ids) || !al4(topk_weights) || !al4(bias))
+        return FG_ERR_INVALID_ARG;
+    fg::HostState st;
+    if (const int rc = fg::host_state(&st)) return rc;
+    const RouteParams p{logits, bias, topk_ids, topk_weights, T, E, topk, n_group, topk_group,
+                        score == FG_SCORE_SIGMOID, renormalize != 0, scale};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int v = (E + 31) / 32;
+    const cudaError_t e = v <= 1 ? launch<1>(p, st.pdl, s) : v <= 2 ? launch<2>(p, st.pdl, s)
+                        : v <= 4 ? launch<4>(p, st.pdl, s) : v <= 8 ? launch<8>(p, st.pdl, s)
+                        : v <= 16 ? launch<16>(p, st.pdl, s) : launch<32>(p, st.pdl, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return FG_ERR_CUDA;
+    }
+    return FG_OK;
+}

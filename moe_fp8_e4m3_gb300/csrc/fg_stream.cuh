@@ -1,0 +1,857 @@
+// fg_stream.cuh - weight-streaming kernels for few tokens: one kernel template behind the
+// whole-layer MoE MLP (fg_moe.cu) and the projection with per-token adapters (fg_lora.cu).
+//
+// With few tokens every product is bound by reading its weights once, so the operands swap
+// places: the weights are the tensor core's M operand (two blocks of 128 rows per tile, 32 KB
+// of a K-group of 128 per ring stage) and the tokens its N operand (BN = 16, 32, 64 or 128
+// columns; the host takes the smallest that holds them).  Every token is multiplied with
+// every weight block read; a token that does not use it is masked where the result is
+// formed.  The tensor core has room for that (a 256 x 128 x 128 K-group takes ~0.3 us of it,
+// reading its weights from HBM takes an SM 0.7 us), and no token is gathered or sorted.
+//
+// Work split: the units of one launch - (tile, K-group) pairs, tile by tile - form one line
+// that is cut into equal shares, one per CTA, wherever the cuts fall ("stream-K"): every SM
+// streams the same number of bytes whatever the number of experts, tiles and K-groups.  A
+// tile cut by a share's border is accumulated by several CTAs: each writes its FP32 partial
+// to the workspace and counts itself in; the one that arrives last adds the partials up in
+// CTA order (so the result does not depend on which came last) and finishes the tile.  No
+// CTA ever waits for another.  The counters wrap to zero by themselves (atomicInc).
+//
+// Modes
+//   kGateUp  tile = 128 gate rows + the 128 up rows of one expert; epilogue: SiLU(gate) * up *
+//            routing weight, per token and 128 outputs one UE8M0 scale, E4M3 codes -> workspace
+//   kDown    tile = 256 output rows; its K axis runs over all active experts one after
+//            another, so the sum over experts happens in the FP32 accumulator
+//   kShrink  tile = 256 rows of the distinct adapters' A matrices (BF16); epilogue: each
+//            token keeps its own adapter's rows, scaled, as a sum of BF16 parts: two (16 mantissa
+//            bits) for a BF16 result, three (24) for an FP32 one
+//   kProj    tile = 256 output rows; K-groups of the shared FP8 weights, then units of the
+//            adapters' B matrices (BF16 against the kShrink result), in one accumulator
+//
+// Warp roles: 0, 2 TMA producers of the weight tiles (even / odd stages); 1 TMEM owner and
+// MMA issuer; 3 TMA producer of the token operand; 4-7 epilogue; 8 scale loader (kShrink:
+// warps 8-15 load the adapter rows by cp.async, since a tile gathers many short row blocks).
+// Every wait is bounded: on expiry the CTA records a time-out in the status word, all its
+// roles wind down and the kernel returns.
+#pragma once
+
+#include "fg_gemm_kernel.cuh"
+
+namespace fg {
+
+enum StreamMode : int { kGateUp = 0, kDown = 1, kProj = 2, kShrink = 3 };
+
+enum : int { kChkAdapter = 6 };          // an adapter id >= L
+
+constexpr int kMaxListed = 1024;         // experts of a shard, adapters of a call
+constexpr int kMaxTokenTiles = 512;      // kProj: token tiles of one call
+constexpr int kMaxStreamCtas = 256;      // shares of a launch (partial slots in the workspace)
+constexpr int kMaxCounters = 512;        // of one launch: kMaxStreamCtas, or one per token tile (kShrink)
+constexpr int kCounterBytes = 2 * kMaxCounters * 4;   // head of a workspace: both launches' counters
+
+struct StreamMaps {
+    CUtensorMap w;       // weights
+    CUtensorMap x;       // token operand
+    CUtensorMap lb;      // kProj: adapters' B
+    CUtensorMap v;       // kProj: kShrink results
+};
+
+struct StreamParams {
+    int tokens;                  // rows of the token operand
+    int nk;                      // K-groups of one tile (kDown: of one expert; kShrink: 64-wide chunks)
+    int row_tiles;               // kGateUp: I / 128 per expert; kDown, kProj: ceil(rows / 256)
+    int out_rows;                // kGateUp: I; kDown: H; kProj: N (row length of d)
+    int experts, expert_base, topk;
+    const int32_t* ids;          // MoE: [tokens][topk]; LoRA: [tokens]
+    const float* weights;        // routing weights [tokens][topk]
+    const int32_t* sfw;          // weight scales
+    int sfw_ld, sfw_rows;        // words per word row; words of it that exist
+    long long sfw_gstride;       // words between experts
+    const int32_t* sft;          // token scales
+    int sft_ld;
+    uint8_t* hq;                 // kGateUp out: [slot][BN][I] E4M3
+    uint8_t* sfh;                // and its scale words [slot][ceil(I/512)][BN]
+    float* part;                 // [CTA][2][2][BN][128] partial tiles
+    unsigned* ctr;               // [kMaxCounters]: one per share
+    void* d;
+    int d_f32;
+    // adapters
+    int lora_r, lora_rp, lora_k, lora_count, max_slots, token_tiles;
+    int parts, unit_cols;        // BF16 parts of a kShrink result; rank columns of a kProj unit
+    const uint16_t* lora_a;      // [L][R][K] BF16
+    const float* scaling;        // [L]
+    uint16_t* v;                 // [token tile][slot][parts][BN][rp] BF16
+    int* slot_ids;               // [token tile][max_slots] distinct adapters, ascending
+    int* slot_count;             // [token tile]
+    int min_units;               // least units of a share
+    int* status;
+    unsigned long long timeout_ns;
+    int debug_stall, pdl;
+};
+
+// D(tmem) (+)= A(smem) x B(smem)^T, BF16 inputs, FP32 accumulation in TMEM.
+__device__ __forceinline__ void tc_mma_bf16(uint32_t d_taddr, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_taddr), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of kind::f16: FP32 accumulator (1 at bits 4-5), BF16 A and B (1 at
+// bits 7-9 and 10-12), K-major operands, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t make_idesc_bf16(int m, int n) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
+}
+// mxf8f6f4 with E2M1 A (the swapped operand order): format code at bits 7-9.
+__host__ __device__ constexpr uint32_t make_idesc_stream(int n, bool fp4) {
+    return make_idesc_mxf8(128, n, false, false) | (fp4 ? kFmtE2M1 << 7 : 0u);
+}
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared::cta.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// Orders generic-proxy global writes (the codes that the next kernel loads by TMA).
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+template <int kMode, int BN>
+struct StreamCfg {
+    static constexpr int kABytes = 32768;                                   // two 128-row blocks x 128 bytes
+    static constexpr int kBBytes = BN * 128 * (kMode == kProj ? 2 : 1);     // kProj: the parts of an adapter unit
+    static constexpr int kSfBytes = kMode == kShrink ? 0 : 3 * 512;         // weight block 0, 1, tokens
+    static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+    static constexpr int kMiscBytes = 512 + 512 + BN * 8 + 128 + 2 * kMaxListed +
+                                      (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
+    static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
+    static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
+    static constexpr int kNumAcc = BN <= 64 ? 2 : 1;
+    static constexpr int kSfCol0 = kNumAcc * 2 * BN;
+    static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
+    static constexpr int kThreads = kMode == kShrink ? 512 : 288;
+    static constexpr int kOffB = kStages * kABytes;
+    static constexpr int kOffSf = kOffB + kStages * kBBytes;
+    static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
+    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 3;
+    static constexpr int kOffMisc = kOffBar + 512 - 64;                     // TMEM address, abort flag, count, last flag
+    static constexpr int kOffRed = kOffBar + 512;                           // [4][16] amax words, then 64 exponents
+    static constexpr int kOffTok = kOffRed + 512;                           // [BN] weights / adapter ids, [BN] flags
+    static constexpr int kOffBits = kOffTok + BN * 8;
+    static constexpr int kOffList = kOffBits + 128;
+    static constexpr int kOffPre = kOffList + 2 * kMaxListed;
+    static constexpr int kSmemBytes = kOffBar + kMiscBytes + 1024;          // + alignment slack
+    static_assert(kNumBars * 8 <= 512 - 64, "barrier area");
+    static_assert(kSfCol0 + 64 <= 512, "TMEM columns");
+    static_assert(kStages >= 3 && kSmemBytes <= kSmemLimit, "shared memory");
+};
+
+// One share's piece of one tile: units [k0, k1) of nk.
+struct StreamSeg {
+    int tile, tt, k0, k1, nk;
+    int first_unit;      // of the tile
+    bool whole;
+};
+
+struct StreamPlan {
+    int units, shares, nk, row_tiles;
+    const int* pre;      // kProj: units before each token tile
+};
+
+__device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
+    return static_cast<int>((long long)c * pl.units / pl.shares);
+}
+// The share that unit u belongs to: the last c with share_begin(c) <= u.
+__device__ __forceinline__ int share_of(const StreamPlan& pl, int u) {
+    return static_cast<int>((((long long)u + 1) * pl.shares - 1) / pl.units);
+}
+
+template <int kMode>
+struct StreamWalk {
+    int u, end, tt;
+    __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share) : u(0), end(0), tt(0) {
+        if (share < pl.shares) {
+            u = share_begin(pl, share);
+            end = share_begin(pl, share + 1);
+        }
+    }
+    __device__ __forceinline__ bool next(const StreamPlan& pl, StreamSeg& s) {
+        if (u >= end) return false;
+        int base = 0;
+        s.nk = pl.nk;
+        if (kMode == kProj) {
+            while (u >= pl.pre[tt + 1]) ++tt;
+            base = pl.pre[tt];
+            s.nk = (pl.pre[tt + 1] - base) / pl.row_tiles;
+        }
+        s.tt = tt;
+        s.tile = (u - base) / s.nk;
+        s.first_unit = base + s.tile * s.nk;
+        s.k0 = u - s.first_unit;
+        s.k1 = min(s.nk, s.k0 + (end - u));
+        s.whole = s.k0 == 0 && s.k1 == s.nk;
+        u += s.k1 - s.k0;
+        return true;
+    }
+};
+
+// Ascending list of the distinct ids in [base, base + count) among ids[0, n); all threads.
+__device__ __forceinline__ void list_distinct(const int32_t* ids, int n, int base, int count, uint32_t* bits,
+                                              uint16_t* list, int* listed) {
+    const int t = threadIdx.x, lane = t & 31;
+    if (t < 32) bits[t] = 0;
+    __syncthreads();
+    for (int i = t; i < n; i += blockDim.x) {
+        const unsigned v = static_cast<unsigned>(__ldcg(ids + i)) - static_cast<unsigned>(base);
+        if (v < static_cast<unsigned>(count)) atomicOr(bits + (v >> 5), 1u << (v & 31));
+    }
+    __syncthreads();
+    if (t < 32) {
+        uint32_t m = bits[lane];
+        const int c = __popc(m);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int pos = incl - c;
+        for (; m; m &= m - 1) list[pos++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
+        if (lane == 31) *listed = incl;
+    }
+    __syncthreads();
+}
+
+template <int kMode, int BN, bool kFp4>
+__global__ void __launch_bounds__(StreamCfg<kMode, BN>::kThreads, 1)
+fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) {
+    using C = StreamCfg<kMode, BN>;
+    constexpr bool kMoe = kMode == kGateUp || kMode == kDown;
+    static_assert(!kFp4 || kMode != kShrink, "the adapters are BF16");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar0 = sbase + C::kOffBar;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * C::kStages + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * C::kStages + C::kNumAcc + b); };
+    const uint32_t drain = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc);     // MMAs done: on the way out
+    const uint32_t turn = drain + 8;                                           // MMAs done: before another kind
+    const uint32_t esync_bar = drain + 16;                                     // the four epilogue warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    int* listed = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 12);
+    uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kOffRed);
+    float* tok_w = reinterpret_cast<float*>(smem + C::kOffTok);               // routing weight of the tile's expert
+    int* tok_id = reinterpret_cast<int*>(smem + C::kOffTok);                  // kShrink: adapter of each token
+    int* tok_on = tok_id + BN;                                                // the token uses the tile's expert
+    uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::kOffBits);
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
+    int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            // kShrink: 256 loader threads and the token producer; else the two TMA producers and
+            // the scale loader's 32 lanes
+            mbar_init(full_bar(s), kMode == kShrink ? 257 : 34);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < C::kNumAcc; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), 4);
+        }
+        mbar_init(drain, 1);
+        mbar_init(turn, 1);
+        mbar_init(esync_bar, 4);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if (kMode != kShrink) tma_prefetch_map(&maps.w);
+        tma_prefetch_map(&maps.x);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // kDown runs behind its own kGateUp launch, which let it start only after its own wait: the
+    // ids and weights it reads before this launch's wait were complete before that.  Only the
+    // roles that touch what kGateUp writes wait.
+    if (kMode != kDown) {
+        grid_dependency_wait();
+        if (threadIdx.x == 0) grid_launch_dependents();
+    }
+    StreamPlan pl;
+    int nlist = 0;
+    const int tt0 = kMode == kShrink ? static_cast<int>(blockIdx.y) : 0;
+    if constexpr (kMoe) {
+        list_distinct(p.ids, p.tokens * p.topk, p.expert_base, p.experts, bits, list, listed);
+        nlist = *listed;
+        pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
+        pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
+    } else if constexpr (kMode == kShrink) {
+        const int n = min(BN, p.tokens - tt0 * BN);
+        list_distinct(p.ids + (long long)tt0 * BN, n, 0, p.lora_count, bits, list, listed);
+        nlist = *listed;
+        for (int t = threadIdx.x; t < BN; t += C::kThreads) {
+            const int id = t < n ? __ldg(p.ids + (long long)tt0 * BN + t) : -1;
+            if (id >= p.lora_count) record_status(p.status, kErrContract | kChkAdapter);
+            tok_id[t] = id;
+        }
+        if (blockIdx.x == 0) {       // for kProj
+            for (int i = threadIdx.x; i < nlist; i += C::kThreads) p.slot_ids[tt0 * p.max_slots + i] = list[i];
+            if (threadIdx.x == 0) p.slot_count[tt0] = nlist;
+        }
+        pl.nk = p.nk;
+        pl.units = (nlist * p.lora_rp + 255) / 256 * pl.nk;
+        __syncthreads();
+    } else {
+        // units of a token tile: row tiles x (K-groups + adapter units of unit_cols rank columns)
+        if (warp == 0) {
+            int run = 0;
+            for (int i0 = 0; i0 < p.token_tiles; i0 += 32) {
+                const int i = i0 + lane;
+                const int c = i < p.token_tiles ? __ldcg(p.slot_count + i) : 0;
+                const int v = i < p.token_tiles ? p.row_tiles * (p.nk + (c * p.lora_rp + p.unit_cols - 1) / p.unit_cols) : 0;
+                int incl = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                if (i < p.token_tiles) pre[i] = run + incl - v;
+                run += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (lane == 0) pre[p.token_tiles] = run;
+        }
+        __syncthreads();
+        pl.nk = p.nk;
+        pl.units = pre[p.token_tiles];
+    }
+    pl.row_tiles = p.row_tiles;
+    pl.pre = pre;
+    pl.shares = max(1, min(static_cast<int>(gridDim.x), (pl.units + p.min_units - 1) / p.min_units));
+    const int share = static_cast<int>(blockIdx.x);
+    const uint32_t tmem_base = *tmem_slot;
+    const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
+    // kDown: expert (list index) and K-group within it of unit k of a tile
+    auto down_expert = [&](int k) { return kMode == kDown ? k / p.nk : 0; };
+    // kProj: adapter units behind the K-groups
+    const int ucols = min(p.lora_rp, p.unit_cols), rb = ucols * 2;           // rank columns of an adapter in a unit, bytes
+    const int per_unit = kMode == kProj ? max(1, p.unit_cols / p.lora_rp) : 1;   // adapters in a unit
+    const int pieces = kMode == kProj ? max(1, p.lora_rp / p.unit_cols) : 1;     // units of one adapter
+
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ weight tiles
+        if (kMode != kShrink && lane == 0) {
+            const uint32_t par = warp == 0 ? 0u : 1u;
+            int s = 0;
+            uint32_t ph = 0, n = 0, armed = 0, armed_par = 0;
+            bool stall = p.debug_stall != 0 && par == 0, aborted = false;
+            StreamWalk<kMode> walk(pl, share);
+            StreamSeg sg;
+            while (!aborted && walk.next(pl, sg)) {
+                for (int k = sg.k0; k < sg.k1; ++k, ++n) {
+                    if ((n & 1u) == par) {
+                        if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducer)) { aborted = true; break; }
+                        if (stall) {
+                            stall = false;       // this stage stays unfilled: the MMA issuer times out
+                        } else {
+                            const uint32_t fb = full_bar(s), dst = sbase + s * C::kABytes;
+                            armed |= 1u << s;
+                            armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                            if (kMode == kProj && k >= p.nk) {
+                                const int u = k - p.nk;
+                                const int nslots = __ldcg(p.slot_count + sg.tt);
+                                const int s0 = pieces > 1 ? u / pieces : u * per_unit;
+                                const int cnt = min(per_unit, nslots - s0);
+                                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * 256 * rb));
+                                for (int j = 0; j < cnt; ++j)
+                                    tma_load_3d(dst + j * 256 * rb, &maps.lb, fb, pieces > 1 ? (u % pieces) * ucols : 0,
+                                                sg.tile * 256, __ldcg(p.slot_ids + sg.tt * p.max_slots + s0 + j));
+                            } else {
+                                // packed FP4: the transaction counts the bytes read, half of those filled
+                                mbar_arrive_expect_tx(fb, kFp4 ? C::kABytes / 2 : C::kABytes);
+                                if constexpr (kMode == kGateUp) {
+                                    const int e = list[sg.tile / p.row_tiles];
+                                    tma_load_3d(dst, &maps.w, fb, k * 128, sg.tile % p.row_tiles * 128, 2 * e);
+                                } else if constexpr (kMode == kDown) {
+                                    const int li = down_expert(k);
+                                    tma_load_3d(dst, &maps.w, fb, (k - li * p.nk) * 128, sg.tile * 256, list[li]);
+                                } else {
+                                    tma_load_3d(dst, &maps.w, fb, k * 128, sg.tile * 256, 0);
+                                }
+                            }
+                        }
+                    }
+                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (aborted || *abort_flag)
+                for (int i = 0; i < C::kStages; ++i)
+                    if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ----------------------------------------------------------- token operand
+        if (lane == 0) {
+            if (kMode == kDown) {
+                grid_dependency_wait();
+                grid_launch_dependents();
+                fence_proxy_async_global();
+            }
+            int s = 0;
+            uint32_t ph = 0, armed = 0, armed_par = 0;
+            bool aborted = false;
+            StreamWalk<kMode> walk(pl, share);
+            StreamSeg sg;
+            while (!aborted && walk.next(pl, sg)) {
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB)) { aborted = true; break; }
+                    const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
+                    armed |= 1u << s;
+                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    if (kMode == kProj && k >= p.nk) {
+                        const int u = k - p.nk;
+                        const int nslots = __ldcg(p.slot_count + sg.tt);
+                        const int s0 = pieces > 1 ? u / pieces : u * per_unit;
+                        const int cnt = min(per_unit, nslots - s0);
+                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * p.parts * BN * rb));
+                        for (int j = 0; j < cnt * p.parts; ++j)      // an adapter's parts follow one another
+                            tma_load_2d(dst + j * BN * rb, &maps.v, fb, pieces > 1 ? (u % pieces) * ucols : 0,
+                                        ((sg.tt * p.max_slots + s0) * p.parts + j) * BN);
+                    } else {
+                        mbar_arrive_expect_tx(fb, BN * 128);
+                        if constexpr (kMode == kDown) {
+                            const int li = down_expert(k);
+                            tma_load_2d(dst, &maps.x, fb, (k - li * p.nk) * 128, li * BN);
+                        } else if constexpr (kMode == kShrink) {
+                            tma_load_2d(dst, &maps.x, fb, k * 64, tt0 * BN);
+                        } else {
+                            tma_load_2d(dst, &maps.x, fb, k * 128, sg.tt * BN);
+                        }
+                    }
+                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (aborted || *abort_flag)
+                for (int i = 0; i < C::kStages; ++i)
+                    if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t kIdesc = make_idesc_stream(BN, kFp4);
+            constexpr uint32_t kIdescBf16 = make_idesc_bf16(128, BN);
+            // scale slots in rotation: FP4 weights bring new words every K-group, E4M3 every fourth
+            constexpr uint32_t kSfSlots = kFp4 ? 4u : 2u;
+            const uint64_t a0 = make_sdesc(sbase, 0, 1024, kLayoutSw128);
+            const uint64_t b0 = make_sdesc(sbase + C::kOffB, 0, 1024, kLayoutSw128);
+            int s = 0, acc = 0;
+            uint32_t ph = 0, acc_ph = 0, kcount = 0, turn_ph = 0;
+            bool aborted = false;
+            StreamWalk<kMode> walk(pl, share);
+            StreamSeg sg;
+            while (!aborted && walk.next(pl, sg)) {
+                if (!wait_bar(acce_bar(acc), acc_ph ^ 1u, wctl, kWaitMma)) { aborted = true; break; }
+                tc_fence_after();
+                const uint32_t d0 = tmem_base + acc * 2 * BN, d1 = d0 + BN;
+                uint32_t add = 0;                     // 0: the first product of the segment overwrites
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    if (!wait_bar(full_bar(s), ph, wctl, kWaitMma)) { aborted = true; break; }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
+                    const uint64_t bd = b0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
+                    if constexpr (kMode == kShrink) {
+                        fence_proxy_async_smem();     // adapter rows written by cp.async
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            tc_mma_bf16(d0, ad + 2 * j, bd + 2 * j, kIdescBf16, add);
+                            tc_mma_bf16(d1, ad + 1024 + 2 * j, bd + 2 * j, kIdescBf16, add);
+                            add = 1;
+                        }
+                    } else if (kMode == kProj && k >= p.nk) {
+                        if (k == p.nk && add) {
+                            // let the scaled FP8 products finish before another kind adds to their sums
+                            tc_commit(turn);
+                            if (!wait_bar(turn, turn_ph, wctl, kWaitMma)) { aborted = true; break; }
+                            turn_ph ^= 1u;
+                            tc_fence_after();
+                        }
+                        const int u = k - p.nk;
+                        const int nslots = __ldcg(p.slot_count + sg.tt);
+                        const int cnt = pieces > 1 ? 1 : min(per_unit, nslots - u * per_unit);
+                        const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
+                        const uint32_t sa = sbase + s * C::kABytes, sb = sbase + C::kOffB + s * C::kBBytes;
+                        for (int j = 0; j < cnt; ++j) {
+                            const uint64_t aj = make_sdesc(sa + j * 256 * rb, 0, 8 * rb, layout);
+                            const uint64_t bj = make_sdesc(sb + j * p.parts * BN * rb, 0, 8 * rb, layout);
+                            const uint32_t half = static_cast<uint32_t>(128 * rb) >> 4, part = static_cast<uint32_t>(BN * rb) >> 4;
+                            for (int c = 0; c < rb / 32; ++c)
+                                for (int o = 0; o < p.parts; ++o) {
+                                    tc_mma_bf16(d0, aj + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
+                                    tc_mma_bf16(d1, aj + half + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
+                                    add = 1;
+                                }
+                        }
+                    } else {
+                        const int kl = kMode == kDown ? k - down_expert(k) * p.nk : k;
+                        const uint32_t sf_id = static_cast<uint32_t>(kl) & 3u;
+                        if (kFp4 || k == sg.k0 || sf_id == 0) {
+                            ++kcount;
+                            const uint32_t t = tmem_base + C::kSfCol0 + (kcount % kSfSlots) * 16;
+                            const uint32_t ss = sbase + C::kOffSf + s * C::kSfBytes;
+                            fence_proxy_async_smem();   // scale words written by cp.async
+                            tc_cp_32x128b_warpx4(t, make_sdesc(ss, 0, 128, kLayoutNone));
+                            tc_cp_32x128b_warpx4(t + 4, make_sdesc(ss + 512, 0, 128, kLayoutNone));
+                            tc_cp_32x128b_warpx4(t + 8, make_sdesc(ss + 1024, 0, 128, kLayoutNone));
+                        }
+                        const uint32_t t = tmem_base + C::kSfCol0 + (kcount % kSfSlots) * 16;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t idesc = idesc_sf_ids(kIdesc, kFp4 ? static_cast<uint32_t>(j) : sf_id, sf_id);
+                            tc_mma_mxf8(d0, ad + 2 * j, bd + 2 * j, idesc, t, t + 8, add);
+                            tc_mma_mxf8(d1, ad + 1024 + 2 * j, bd + 2 * j, idesc, t + 4, t + 8, add);
+                            add = 1;
+                        }
+                    }
+                    tc_commit(empty_bar(s));
+                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                }
+                if (aborted) break;
+                tc_commit(accf_bar(acc));
+                if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
+            }
+            tc_commit(drain);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(drain, 0)) {
+                if (globaltimer_ns() - t0 > p.timeout_ns) { record_status(p.status, kErrTimeout | kWaitDrain); break; }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        if constexpr (kMode == kShrink) {
+            // ------------------------------------------------- adapter rows (256 threads)
+            // Thread t copies 16 bytes (column chunk t % 8) of rows t / 8 + 32 i of the tile;
+            // row r holds rank row r % rp of the tile's adapter r / rp, zero past R or the list.
+            const int t = static_cast<int>(threadIdx.x) - 256, c = t & 7, r0 = t >> 3;
+            int s = 0;
+            uint32_t ph = 0;
+            bool aborted = false;
+            StreamWalk<kMode> walk(pl, share);
+            StreamSeg sg;
+            while (!aborted && walk.next(pl, sg)) {
+                const uint16_t* src[8];
+                uint32_t ok = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = sg.tile * 256 + r0 + 32 * i;
+                    const int slot = r / p.lora_rp, rr = r - slot * p.lora_rp;
+                    const bool in = slot < nlist && rr < p.lora_r;
+                    ok |= (in ? 1u : 0u) << i;
+                    src[i] = p.lora_a + (in ? ((long long)list[slot] * p.lora_r + rr) * p.lora_k + c * 8 : 0);
+                }
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
+                    if (!__all_sync(0xffffffffu, go)) { aborted = true; break; }
+                    const uint32_t dst = sbase + s * C::kABytes;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + 32 * i;
+                        cp_async_16z(dst + r * 128 + ((c ^ (r & 7)) << 4), src[i] + (long long)k * 64, ok >> i & 1u ? 16u : 0u);
+                    }
+                    cp_async_mbar_arrive(full_bar(s));
+                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+            cp_async_wait_all();
+            __syncwarp();
+        } else {
+            // --------------------------------------------------------- scale loader
+            // Word (lane, j) of a 512-byte atom holds row j * 32 + lane, the form tcgen05.cp reads.
+            if (kMode == kDown) grid_dependency_wait();
+            int s = 0;
+            uint32_t ph = 0;
+            bool aborted = false;
+            StreamWalk<kMode> walk(pl, share);
+            StreamSeg sg;
+            const int h_words = (p.out_rows + 511) / 512;      // kGateUp's own out_rows is I
+            (void)h_words;
+            while (!aborted && walk.next(pl, sg)) {
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
+                    if (!__all_sync(0xffffffffu, go)) { aborted = true; break; }
+                    const bool fp8 = kMode != kProj || k < p.nk;
+                    const int li = down_expert(k);
+                    const int kl = kMode == kDown ? k - li * p.nk : k;
+                    if (fp8 && (kFp4 || k == sg.k0 || (kl & 3) == 0)) {
+                        const uint32_t da = sbase + C::kOffSf + s * C::kSfBytes + lane * 16;
+                        const int e = kMode == kGateUp ? list[sg.tile / p.row_tiles] : (kMode == kDown ? list[li] : 0);
+                        const int32_t* pw = p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? kl : kl >> 2) * p.sfw_ld;
+                        // first rows of the tile's two weight blocks
+                        const int row0 = kMode == kGateUp ? sg.tile % p.row_tiles * 128 : sg.tile * 256;
+                        const int row1 = kMode == kGateUp ? p.out_rows + row0 : row0 + 128;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int row = b ? row1 : row0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int i = kFp4 ? row + j * 32 + lane : row >> 7;
+                                const bool in = i < p.sfw_rows;
+                                cp_async_4(da + 512 * b + 4 * j, in ? pw + i : pw, in ? 4u : 0u);
+                            }
+                        }
+                        const int32_t* pt;
+                        if (kMode == kDown) pt = p.sft + ((long long)li * ((p.nk + 3) / 4) + (kl >> 2)) * BN;
+                        else pt = p.sft + (long long)(kl >> 2) * p.sft_ld + sg.tt * BN;
+                        const int nt = kMode == kDown ? BN : min(BN, p.tokens - sg.tt * BN);
+#pragma unroll
+                        for (int j = 0; j < (BN + 31) / 32; ++j) {
+                            const int i = j * 32 + lane;
+                            const bool in = i < nt;
+                            cp_async_4(da + 1024 + 4 * j, in ? pt + i : pt, in ? 4u : 0u);
+                        }
+                    }
+                    cp_async_mbar_arrive(full_bar(s));
+                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+            cp_async_wait_all();
+            __syncwarp();
+        }
+    } else {
+        // ----------------------------------------------------------------- epilogue
+        const int q = warp & 3, row = q * 32 + lane;
+        const int te = static_cast<int>(threadIdx.x) - 128;            // 0..127 over the four warps
+        if (kMode == kDown) grid_dependency_wait();
+        if (kMode == kDown && nlist == 0) {
+            // no token uses an expert of this shard: the sum is empty
+            const long long n = (long long)p.tokens * p.out_rows;
+            for (long long i = (long long)blockIdx.x * 128 + te; i < n; i += (long long)gridDim.x * 128) {
+                if (p.d_f32) static_cast<float*>(p.d)[i] = 0.0f;
+                else static_cast<__nv_bfloat16*>(p.d)[i] = __float2bfloat16(0.0f);
+            }
+        }
+        uint32_t e_ph = 0;
+        // all four epilogue warps, bounded like every wait (a warp that gave up never arrives)
+        auto esync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(esync_bar);
+            const bool ok = wait_bar(esync_bar, e_ph, wctl, kWaitEpilogueSync);
+            e_ph ^= 1u;
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        const int cta = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);
+        const long long part_tile = 2LL * BN * 128;                       // floats of one partial
+        int acc = 0;
+        uint32_t acc_ph = 0;
+        bool aborted = false;
+        StreamWalk<kMode> walk(pl, share);
+        StreamSeg sg;
+        while (!aborted && walk.next(pl, sg)) {
+            const bool ok = wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * BN;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce_bar(acc));
+            };
+            int c_first = share, c_last = share;
+            if (!sg.whole) {
+                // this share's part of the tile: 0 where the tile began in an earlier share, else 1
+                float* mine = p.part + (2LL * cta + (sg.k0 > 0 ? 0 : 1)) * part_tile + row;
+                for (int c0 = 0; c0 < 2 * BN; c0 += 16) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(ta + c0, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) __stcg(mine + (c0 + i) * 128, __uint_as_float(r[i]));
+                }
+                release();
+                __threadfence();
+                if (!esync()) { aborted = true; break; }
+                c_first = share_of(pl, sg.first_unit);
+                c_last = share_of(pl, sg.first_unit + sg.nk - 1);
+                if (te == 0) {
+                    // only the last tile that begins in a share goes on into the next one, so a cut
+                    // tile is told by its first share; the count wraps to 0 with the last arrival
+                    const unsigned n = static_cast<unsigned>(c_last - c_first);
+                    *last_flag = atomicInc(p.ctr + (cta - share + c_first), n) == n;
+                }
+                if (!esync()) { aborted = true; break; }
+                const bool last = *last_flag != 0;
+                __threadfence();
+                if (!last) {
+                    if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
+                    continue;
+                }
+            }
+            // ---- finish the tile
+            int expert = 0;
+            if constexpr (kMode == kGateUp) {
+                const int li = sg.tile / p.row_tiles;
+                expert = p.expert_base + list[li];
+                for (int t = te; t < BN; t += 128) {
+                    float w = 0.0f;
+                    int on = 0;
+                    if (t < p.tokens)
+                        for (int j = 0; j < p.topk; ++j)
+                            if (__ldg(p.ids + (long long)t * p.topk + j) == expert) {
+                                w += __ldg(p.weights + (long long)t * p.topk + j);
+                                on = 1;
+                            }
+                    tok_w[t] = w;
+                    tok_on[t] = on;
+                }
+                if (!esync()) { aborted = true; break; }
+            }
+            for (int c0 = 0; c0 < BN; c0 += 16) {
+                float v0[16], v1[16];
+                if (sg.whole) {
+                    uint32_t r0[16], r1[16];
+                    tmem_ld_32x32b_x16(ta + c0, r0);
+                    tmem_ld_32x32b_x16(ta + BN + c0, r1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
+                    if (c0 + 16 == BN) release();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
+                    for (int c = c_first; c <= c_last; ++c) {
+                        const int slot = share_begin(pl, c) > sg.first_unit ? 0 : 1;
+                        const float* src = p.part + (2LL * (cta - share + c) + slot) * part_tile + c0 * 128 + row;
+                        float x0[16], x1[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) { x0[i] = __ldcg(src + i * 128); x1[i] = __ldcg(src + (BN + i) * 128); }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) { v0[i] += x0[i]; v1[i] += x1[i]; }
+                    }
+                }
+                if constexpr (kMode == kGateUp) {
+                    // y = w * SiLU(gate) * up, then one scale for each token's 128 values (the rows of
+                    // this block): maximum of |y| over the warp's lanes, then over the four warps
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float y = swiglu_value(__float_as_uint(v0[i]), __float_as_uint(v1[i])) * tok_w[c0 + i];
+                        v0[i] = tok_on[c0 + i] ? y : 0.0f;
+                        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v0[i]) & 0x7fffffffu);
+                        if (lane == i) red[q * 16 + i] = m;
+                    }
+                    if (!esync()) { aborted = true; break; }
+                    const int li = sg.tile / p.row_tiles, it = sg.tile % p.row_tiles;
+                    uint8_t* hq = p.hq + ((long long)li * BN + c0) * p.out_rows + it * 128 + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t m = max(max(red[i], red[16 + i]), max(red[32 + i], red[48 + i]));
+                        const bool finite = m < 0x7f800000u;
+                        const int e = finite ? scale_exponent(__uint_as_float(m)) : 0;
+                        const uint32_t code = finite ? e4m3(v0[i] * pow2_neg(e)) : 0x7Fu;   // not finite: NaN codes
+                        hq[(long long)i * p.out_rows] = static_cast<uint8_t>(code);
+                        if (te == i)
+                            p.sfh[(((long long)li * ((p.row_tiles + 3) / 4) + (it >> 2)) * BN + c0 + i) * 4 + (it & 3)] =
+                                static_cast<uint8_t>(e + 127);
+                    }
+                    if (!esync()) { aborted = true; break; }      // red is rewritten by the next columns
+                } else if constexpr (kMode == kShrink) {
+                    // a token keeps the rows of its own adapter, scaled; each part holds what the
+                    // parts before it leave
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int r = sg.tile * 256 + b * 128 + row;
+                        const int slot = r / p.lora_rp, rr = r - slot * p.lora_rp;
+                        if (slot < nlist) {
+                            const int id = list[slot];
+                            const float sc = __ldg(p.scaling + id);
+                            uint16_t* dst = p.v + (((long long)tt0 * p.max_slots + slot) * p.parts * BN + c0) * p.lora_rp + rr;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float x = tok_id[c0 + i] == id ? sc * (b ? v1[i] : v0[i]) : 0.0f;
+                                for (int o = 0; o < p.parts; ++o) {
+                                    const __nv_bfloat16 h = __float2bfloat16(x);
+                                    dst[(long long)(o * BN + i) * p.lora_rp] = __bfloat16_as_ushort(h);
+                                    x -= __bfloat162float(h);
+                                    if (!(x == x)) x = 0.0f;       // an infinite or NaN part leaves nothing
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    const int nt = min(BN, p.tokens - sg.tt * BN);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int r = sg.tile * 256 + b * 128 + row;
+                        if (r < p.out_rows) {
+                            const long long at = ((long long)sg.tt * BN + c0) * p.out_rows + r;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (c0 + i >= nt) break;
+                                const float x = b ? v1[i] : v0[i];
+                                if (p.d_f32) static_cast<float*>(p.d)[at + (long long)i * p.out_rows] = x;
+                                else static_cast<__nv_bfloat16*>(p.d)[at + (long long)i * p.out_rows] = __float2bfloat16(x);
+                            }
+                        }
+                    }
+                }
+            }
+            if (aborted) break;
+            if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
+        }
+        if (kMode == kGateUp || kMode == kShrink) fence_proxy_async_global();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+}
+
+template <int kMode, int BN, bool kFp4>
+cudaError_t launch_stream_bn(const StreamParams& p, const StreamMaps& maps, dim3 grid, cudaStream_t stream) {
+    using C = StreamCfg<kMode, BN>;
+    static bool configured[256] = {};        // set once per device; setting it again is harmless
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        err = cudaFuncSetAttribute(fg_stream_kernel<kMode, BN, kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   C::kSmemBytes);
+        if (err != cudaSuccess) return err;
+        configured[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (p.pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, fg_stream_kernel<kMode, BN, kFp4>, p, maps);
+}
+
+template <int kMode, bool kFp4>
+cudaError_t launch_stream(int bn, const StreamParams& p, const StreamMaps& maps, dim3 grid, cudaStream_t stream) {
+    switch (bn) {
+        case 16: return launch_stream_bn<kMode, 16, kFp4>(p, maps, grid, stream);
+        case 32: return launch_stream_bn<kMode, 32, kFp4>(p, maps, grid, stream);
+        case 64: return launch_stream_bn<kMode, 64, kFp4>(p, maps, grid, stream);
+        default: return launch_stream_bn<kMode, 128, kFp4>(p, maps, grid, stream);
+    }
+}
+
+// Token columns of a tile: the smallest width that holds them.
+inline int stream_bn(int tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
+
+}  // namespace fg
