@@ -29,8 +29,9 @@
 //            adapters' B matrices (BF16 against the kShrink result), in one accumulator
 //
 // Warp roles: 0, 2 TMA producers of the weight tiles (even / odd stages); 1 TMEM owner and
-// MMA issuer; 3 TMA producer of the token operand; 4-7 epilogue; 8 scale loader (kShrink:
-// warps 8-15 load the adapter rows by cp.async, since a tile gathers many short row blocks).
+// MMA issuer of the tile's first block, 9 (kShrink: 2) of the second; 3 TMA producer of the
+// token operand; 4-7 epilogue; 8 scale loader (kShrink: warps 8-15 load the adapter rows by
+// cp.async, since a tile gathers many short row blocks).
 // Every wait is bounded: on expiry the CTA records a time-out in the status word, all its
 // roles wind down and the kernel returns.
 #pragma once
@@ -127,11 +128,11 @@ struct StreamCfg {
     static constexpr int kNumAcc = BN <= 64 ? 2 : 1;
     static constexpr int kSfCol0 = kNumAcc * 2 * BN;
     static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
-    static constexpr int kThreads = kMode == kShrink ? 512 : 288;
+    static constexpr int kThreads = kMode == kShrink ? 512 : 320;
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
     static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 3;
+    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 5;
     static constexpr int kOffMisc = kOffBar + 512 - 64;                     // TMEM address, abort flag, count, last flag
     static constexpr int kOffRed = kOffBar + 512;                           // [4][16] amax words, then 64 exponents
     static constexpr int kOffTok = kOffRed + 512;                           // [BN] weights / adapter ids, [BN] flags
@@ -235,9 +236,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * C::kStages + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * C::kStages + C::kNumAcc + b); };
-    const uint32_t drain = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc);     // MMAs done: on the way out
-    const uint32_t turn = drain + 8;                                           // MMAs done: before another kind
-    const uint32_t esync_bar = drain + 16;                                     // the four epilogue warps
+    // per issuer: its MMAs done, on the way out and before products of another kind
+    auto drain_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + b); };
+    auto turn_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 2 + b); };
+    const uint32_t esync_bar = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4);   // the four epilogue warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     int* listed = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
@@ -255,14 +257,16 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             // kShrink: 256 loader threads and the token producer; else the two TMA producers and
             // the scale loader's 32 lanes
             mbar_init(full_bar(s), kMode == kShrink ? 257 : 34);
-            mbar_init(empty_bar(s), 1);
+            mbar_init(empty_bar(s), 2);          // both issuers' commits
         }
         for (int b = 0; b < C::kNumAcc; ++b) {
-            mbar_init(accf_bar(b), 1);
+            mbar_init(accf_bar(b), 2);
             mbar_init(acce_bar(b), 4);
         }
-        mbar_init(drain, 1);
-        mbar_init(turn, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(drain_of(b), 1);
+            mbar_init(turn_of(b), 1);
+        }
         mbar_init(esync_bar, 4);
         *abort_flag = 0;
         fence_mbar_init();
@@ -343,7 +347,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int per_unit = kMode == kProj ? max(1, p.unit_cols / p.lora_rp) : 1;   // adapters in a unit
     const int pieces = kMode == kProj ? max(1, p.lora_rp / p.unit_cols) : 1;     // units of one adapter
 
-    if (warp == 0 || warp == 2) {
+    if (warp == 0 || (warp == 2 && kMode != kShrink)) {
         // ------------------------------------------------------------ weight tiles
         if (kMode != kShrink && lane == 0) {
             const uint32_t par = warp == 0 ? 0u : 1u;
@@ -441,15 +445,23 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // -------------------------------------------------------------- MMA issuer
+    } else if (warp == 1 || warp == (kMode == kShrink ? 2 : 9)) {
+        // ------------------------------------------------------------- MMA issuers
+        // One for each 128-row block of the tile: a thread needs ~80 clocks to issue a
+        // tcgen05.mma, so one issuer's eight per unit (~0.45 us with the waits) would pace the
+        // FP4 weights, whose unit takes HBM 0.38 us.
         if (lane == 0) {
+            const int blk = warp == 1 ? 0 : 1;
             constexpr uint32_t kIdesc = make_idesc_stream(BN, kFp4);
             constexpr uint32_t kIdescBf16 = make_idesc_bf16(128, BN);
-            // scale slots in rotation: FP4 weights bring new words every K-group, E4M3 every fourth
+            // scale slots in rotation (this issuer's: its block's words, the tokens' words): FP4
+            // weights bring new words every K-group, E4M3 every fourth
             constexpr uint32_t kSfSlots = kFp4 ? 4u : 2u;
-            const uint64_t a0 = make_sdesc(sbase, 0, 1024, kLayoutSw128);
+            const uint32_t sf0 = tmem_base + C::kSfCol0 + 8 * blk;
+            const uint64_t a0 = make_sdesc(sbase + blk * 16384, 0, 1024, kLayoutSw128);
             const uint64_t b0 = make_sdesc(sbase + C::kOffB, 0, 1024, kLayoutSw128);
+            const uint64_t w0 = make_sdesc(sbase + C::kOffSf + 512 * blk, 0, 128, kLayoutNone);
+            const uint64_t t0w = make_sdesc(sbase + C::kOffSf + 1024, 0, 128, kLayoutNone);
             int s = 0, acc = 0;
             uint32_t ph = 0, acc_ph = 0, kcount = 0, turn_ph = 0;
             bool aborted = false;
@@ -458,8 +470,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             while (!aborted && walk.next(pl, sg)) {
                 if (!wait_bar(acce_bar(acc), acc_ph ^ 1u, wctl, kWaitMma)) { aborted = true; break; }
                 tc_fence_after();
-                const uint32_t d0 = tmem_base + acc * 2 * BN, d1 = d0 + BN;
+                const uint32_t dt = tmem_base + (acc * 2 + blk) * BN;
                 uint32_t add = 0;                     // 0: the first product of the segment overwrites
+                int kl = kMode == kDown ? sg.k0 % p.nk : sg.k0;      // K-group (kDown: within the expert)
                 for (int k = sg.k0; k < sg.k1; ++k) {
                     if (!wait_bar(full_bar(s), ph, wctl, kWaitMma)) { aborted = true; break; }
                     tc_fence_after();
@@ -469,15 +482,14 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         fence_proxy_async_smem();     // adapter rows written by cp.async
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            tc_mma_bf16(d0, ad + 2 * j, bd + 2 * j, kIdescBf16, add);
-                            tc_mma_bf16(d1, ad + 1024 + 2 * j, bd + 2 * j, kIdescBf16, add);
+                            tc_mma_bf16(dt, ad + 2 * j, bd + 2 * j, kIdescBf16, add);
                             add = 1;
                         }
                     } else if (kMode == kProj && k >= p.nk) {
                         if (k == p.nk && add) {
                             // let the scaled FP8 products finish before another kind adds to their sums
-                            tc_commit(turn);
-                            if (!wait_bar(turn, turn_ph, wctl, kWaitMma)) { aborted = true; break; }
+                            tc_commit(turn_of(blk));
+                            if (!wait_bar(turn_of(blk), turn_ph, wctl, kWaitMma)) { aborted = true; break; }
                             turn_ph ^= 1u;
                             tc_fence_after();
                         }
@@ -485,49 +497,46 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         const int nslots = __ldcg(p.slot_count + sg.tt);
                         const int cnt = pieces > 1 ? 1 : min(per_unit, nslots - u * per_unit);
                         const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
-                        const uint32_t sa = sbase + s * C::kABytes, sb = sbase + C::kOffB + s * C::kBBytes;
+                        const uint32_t sa = sbase + s * C::kABytes + blk * 128 * rb, sb = sbase + C::kOffB + s * C::kBBytes;
                         for (int j = 0; j < cnt; ++j) {
                             const uint64_t aj = make_sdesc(sa + j * 256 * rb, 0, 8 * rb, layout);
                             const uint64_t bj = make_sdesc(sb + j * p.parts * BN * rb, 0, 8 * rb, layout);
-                            const uint32_t half = static_cast<uint32_t>(128 * rb) >> 4, part = static_cast<uint32_t>(BN * rb) >> 4;
+                            const uint32_t part = static_cast<uint32_t>(BN * rb) >> 4;
                             for (int c = 0; c < rb / 32; ++c)
                                 for (int o = 0; o < p.parts; ++o) {
-                                    tc_mma_bf16(d0, aj + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
-                                    tc_mma_bf16(d1, aj + half + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
+                                    tc_mma_bf16(dt, aj + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
                                     add = 1;
                                 }
                         }
                     } else {
-                        const int kl = kMode == kDown ? k - down_expert(k) * p.nk : k;
                         const uint32_t sf_id = static_cast<uint32_t>(kl) & 3u;
                         if (kFp4 || k == sg.k0 || sf_id == 0) {
                             ++kcount;
-                            const uint32_t t = tmem_base + C::kSfCol0 + (kcount % kSfSlots) * 16;
-                            const uint32_t ss = sbase + C::kOffSf + s * C::kSfBytes;
+                            const uint32_t t = sf0 + (kcount % kSfSlots) * 16;
+                            const uint32_t so = static_cast<uint32_t>(s * C::kSfBytes) >> 4;
                             fence_proxy_async_smem();   // scale words written by cp.async
-                            tc_cp_32x128b_warpx4(t, make_sdesc(ss, 0, 128, kLayoutNone));
-                            tc_cp_32x128b_warpx4(t + 4, make_sdesc(ss + 512, 0, 128, kLayoutNone));
-                            tc_cp_32x128b_warpx4(t + 8, make_sdesc(ss + 1024, 0, 128, kLayoutNone));
+                            tc_cp_32x128b_warpx4(t, w0 + so);
+                            tc_cp_32x128b_warpx4(t + 4, t0w + so);
                         }
-                        const uint32_t t = tmem_base + C::kSfCol0 + (kcount % kSfSlots) * 16;
+                        const uint32_t t = sf0 + (kcount % kSfSlots) * 16;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t idesc = idesc_sf_ids(kIdesc, kFp4 ? static_cast<uint32_t>(j) : sf_id, sf_id);
-                            tc_mma_mxf8(d0, ad + 2 * j, bd + 2 * j, idesc, t, t + 8, add);
-                            tc_mma_mxf8(d1, ad + 1024 + 2 * j, bd + 2 * j, idesc, t + 4, t + 8, add);
+                            tc_mma_mxf8(dt, ad + 2 * j, bd + 2 * j, idesc, t, t + 4, add);
                             add = 1;
                         }
                     }
                     tc_commit(empty_bar(s));
                     if (++s == C::kStages) { s = 0; ph ^= 1u; }
+                    if (++kl == p.nk && kMode == kDown) kl = 0;
                 }
                 if (aborted) break;
                 tc_commit(accf_bar(acc));
                 if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
             }
-            tc_commit(drain);
+            tc_commit(drain_of(blk));
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(drain, 0)) {
+            while (!mbar_try_wait(drain_of(blk), 0)) {
                 if (globaltimer_ns() - t0 > p.timeout_ns) { record_status(p.status, kErrTimeout | kWaitDrain); break; }
             }
         }
