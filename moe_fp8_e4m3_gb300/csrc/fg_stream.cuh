@@ -30,8 +30,8 @@
 //
 // Warp roles: 0, 2 TMA producers of the weight tiles (even / odd stages); 1 TMEM owner and
 // MMA issuer of the tile's first block, 9 (kShrink: 2) of the second; 3 TMA producer of the
-// token operand; 4-7 epilogue; 8 scale loader (kShrink: warps 8-15 load the adapter rows by
-// cp.async, since a tile gathers many short row blocks).
+// token operand; 4-7 epilogue; 8, 10 scale loaders (kShrink: warps 8-15 load the adapter rows
+// by cp.async, since a tile gathers many short row blocks).
 // Every wait is bounded: on expiry the CTA records a time-out in the status word, all its
 // roles wind down and the kernel returns.
 #pragma once
@@ -128,7 +128,7 @@ struct StreamCfg {
     static constexpr int kNumAcc = BN <= 64 ? 2 : 1;
     static constexpr int kSfCol0 = kNumAcc * 2 * BN;
     static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
-    static constexpr int kThreads = kMode == kShrink ? 512 : 320;
+    static constexpr int kThreads = kMode == kShrink ? 512 : 352;
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
     static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
@@ -191,6 +191,35 @@ struct StreamWalk {
         s.whole = s.k0 == 0 && s.k1 == s.nk;
         u += s.k1 - s.k0;
         return true;
+    }
+};
+
+// Walks a share unit by unit.  li, kl: kDown's expert (list index) and K-group within it (else
+// kl == k); no division per unit.
+template <int kMode>
+struct StreamCursor {
+    StreamWalk<kMode> walk;
+    StreamSeg sg;
+    int k, li, kl, per;
+    bool valid;
+    __device__ __forceinline__ StreamCursor(const StreamPlan& pl, int share, int per_expert)
+        : walk(pl, share), k(0), li(0), kl(0), per(per_expert) { enter(pl); }
+    __device__ __forceinline__ void enter(const StreamPlan& pl) {
+        valid = walk.next(pl, sg);
+        if (!valid) return;
+        k = kl = sg.k0;
+        if (kMode == kDown) { li = k / per; kl = k - li * per; }
+    }
+    __device__ __forceinline__ void step(const StreamPlan& pl) {
+        ++k;
+        ++kl;
+        if (kMode == kDown && kl == per) { kl = 0; ++li; }
+        if (k == sg.k1) enter(pl);
+    }
+    // the unit brings new scale words: FP4 weights every K-group, else at the segment's first and
+    // every fourth K-group
+    __device__ __forceinline__ bool new_words(bool fp4, int fp8_units) const {
+        return (kMode != kProj || k < fp8_units) && (fp4 || k == sg.k0 || (kl & 3) == 0);
     }
 };
 
@@ -340,8 +369,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int share = static_cast<int>(blockIdx.x);
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
-    // kDown: expert (list index) and K-group within it of unit k of a tile
-    auto down_expert = [&](int k) { return kMode == kDown ? k / p.nk : 0; };
     // kProj: adapter units behind the K-groups
     const int ucols = min(p.lora_rp, p.unit_cols), rb = ucols * 2;           // rank columns of an adapter in a unit, bytes
     const int per_unit = kMode == kProj ? max(1, p.unit_cols / p.lora_rp) : 1;   // adapters in a unit
@@ -354,44 +381,40 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             int s = 0;
             uint32_t ph = 0, n = 0, armed = 0, armed_par = 0;
             bool stall = p.debug_stall != 0 && par == 0, aborted = false;
-            StreamWalk<kMode> walk(pl, share);
-            StreamSeg sg;
-            while (!aborted && walk.next(pl, sg)) {
-                for (int k = sg.k0; k < sg.k1; ++k, ++n) {
-                    if ((n & 1u) == par) {
-                        if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducer)) { aborted = true; break; }
-                        if (stall) {
-                            stall = false;       // this stage stays unfilled: the MMA issuer times out
+            StreamCursor<kMode> c(pl, share, p.nk);
+            for (; c.valid; c.step(pl), ++n) {
+                if ((n & 1u) == par) {
+                    if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducer)) { aborted = true; break; }
+                    if (stall) {
+                        stall = false;       // this stage stays unfilled: the MMA issuer times out
+                    } else {
+                        const uint32_t fb = full_bar(s), dst = sbase + s * C::kABytes;
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                        if (kMode == kProj && c.k >= p.nk) {
+                            const int u = c.k - p.nk;
+                            const int nslots = __ldcg(p.slot_count + c.sg.tt);
+                            const int s0 = pieces > 1 ? u / pieces : u * per_unit;
+                            const int cnt = min(per_unit, nslots - s0);
+                            mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * 256 * rb));
+                            for (int j = 0; j < cnt; ++j)
+                                tma_load_3d(dst + j * 256 * rb, &maps.lb, fb, pieces > 1 ? (u % pieces) * ucols : 0,
+                                            c.sg.tile * 256, __ldcg(p.slot_ids + c.sg.tt * p.max_slots + s0 + j));
                         } else {
-                            const uint32_t fb = full_bar(s), dst = sbase + s * C::kABytes;
-                            armed |= 1u << s;
-                            armed_par = (armed_par & ~(1u << s)) | (ph << s);
-                            if (kMode == kProj && k >= p.nk) {
-                                const int u = k - p.nk;
-                                const int nslots = __ldcg(p.slot_count + sg.tt);
-                                const int s0 = pieces > 1 ? u / pieces : u * per_unit;
-                                const int cnt = min(per_unit, nslots - s0);
-                                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * 256 * rb));
-                                for (int j = 0; j < cnt; ++j)
-                                    tma_load_3d(dst + j * 256 * rb, &maps.lb, fb, pieces > 1 ? (u % pieces) * ucols : 0,
-                                                sg.tile * 256, __ldcg(p.slot_ids + sg.tt * p.max_slots + s0 + j));
+                            // packed FP4: the transaction counts the bytes read, half of those filled
+                            mbar_arrive_expect_tx(fb, kFp4 ? C::kABytes / 2 : C::kABytes);
+                            if constexpr (kMode == kGateUp) {
+                                const int e = list[c.sg.tile / p.row_tiles];
+                                tma_load_3d(dst, &maps.w, fb, c.k * 128, c.sg.tile % p.row_tiles * 128, 2 * e);
+                            } else if constexpr (kMode == kDown) {
+                                tma_load_3d(dst, &maps.w, fb, c.kl * 128, c.sg.tile * 256, list[c.li]);
                             } else {
-                                // packed FP4: the transaction counts the bytes read, half of those filled
-                                mbar_arrive_expect_tx(fb, kFp4 ? C::kABytes / 2 : C::kABytes);
-                                if constexpr (kMode == kGateUp) {
-                                    const int e = list[sg.tile / p.row_tiles];
-                                    tma_load_3d(dst, &maps.w, fb, k * 128, sg.tile % p.row_tiles * 128, 2 * e);
-                                } else if constexpr (kMode == kDown) {
-                                    const int li = down_expert(k);
-                                    tma_load_3d(dst, &maps.w, fb, (k - li * p.nk) * 128, sg.tile * 256, list[li]);
-                                } else {
-                                    tma_load_3d(dst, &maps.w, fb, k * 128, sg.tile * 256, 0);
-                                }
+                                tma_load_3d(dst, &maps.w, fb, c.k * 128, c.sg.tile * 256, 0);
                             }
                         }
                     }
-                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
                 }
+                if (++s == C::kStages) { s = 0; ph ^= 1u; }
             }
             if (aborted || *abort_flag)
                 for (int i = 0; i < C::kStages; ++i)
@@ -409,36 +432,28 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_par = 0;
             bool aborted = false;
-            StreamWalk<kMode> walk(pl, share);
-            StreamSeg sg;
-            while (!aborted && walk.next(pl, sg)) {
-                for (int k = sg.k0; k < sg.k1; ++k) {
-                    if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB)) { aborted = true; break; }
-                    const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
-                    armed |= 1u << s;
-                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
-                    if (kMode == kProj && k >= p.nk) {
-                        const int u = k - p.nk;
-                        const int nslots = __ldcg(p.slot_count + sg.tt);
-                        const int s0 = pieces > 1 ? u / pieces : u * per_unit;
-                        const int cnt = min(per_unit, nslots - s0);
-                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * p.parts * BN * rb));
-                        for (int j = 0; j < cnt * p.parts; ++j)      // an adapter's parts follow one another
-                            tma_load_2d(dst + j * BN * rb, &maps.v, fb, pieces > 1 ? (u % pieces) * ucols : 0,
-                                        ((sg.tt * p.max_slots + s0) * p.parts + j) * BN);
-                    } else {
-                        mbar_arrive_expect_tx(fb, BN * 128);
-                        if constexpr (kMode == kDown) {
-                            const int li = down_expert(k);
-                            tma_load_2d(dst, &maps.x, fb, (k - li * p.nk) * 128, li * BN);
-                        } else if constexpr (kMode == kShrink) {
-                            tma_load_2d(dst, &maps.x, fb, k * 64, tt0 * BN);
-                        } else {
-                            tma_load_2d(dst, &maps.x, fb, k * 128, sg.tt * BN);
-                        }
-                    }
-                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
+            StreamCursor<kMode> c(pl, share, p.nk);
+            for (; c.valid; c.step(pl)) {
+                if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB)) { aborted = true; break; }
+                const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
+                armed |= 1u << s;
+                armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                if (kMode == kProj && c.k >= p.nk) {
+                    const int u = c.k - p.nk;
+                    const int nslots = __ldcg(p.slot_count + c.sg.tt);
+                    const int s0 = pieces > 1 ? u / pieces : u * per_unit;
+                    const int cnt = min(per_unit, nslots - s0);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * p.parts * BN * rb));
+                    for (int j = 0; j < cnt * p.parts; ++j)      // an adapter's parts follow one another
+                        tma_load_2d(dst + j * BN * rb, &maps.v, fb, pieces > 1 ? (u % pieces) * ucols : 0,
+                                    ((c.sg.tt * p.max_slots + s0) * p.parts + j) * BN);
+                } else {
+                    mbar_arrive_expect_tx(fb, BN * 128);
+                    if constexpr (kMode == kDown) tma_load_2d(dst, &maps.x, fb, c.kl * 128, c.li * BN);
+                    else if constexpr (kMode == kShrink) tma_load_2d(dst, &maps.x, fb, c.k * 64, tt0 * BN);
+                    else tma_load_2d(dst, &maps.x, fb, c.k * 128, c.sg.tt * BN);
                 }
+                if (++s == C::kStages) { s = 0; ph ^= 1u; }
             }
             if (aborted || *abort_flag)
                 for (int i = 0; i < C::kStages; ++i)
@@ -579,33 +594,43 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             cp_async_wait_all();
             __syncwarp();
         } else {
-            // --------------------------------------------------------- scale loader
-            // Word (lane, j) of a 512-byte atom holds row j * 32 + lane, the form tcgen05.cp reads.
+            // -------------------------------------------------------- scale loaders
+            // Warp 8 fills the even stages of the unit sequence, warp 10 the odd ones.  Word (lane, j)
+            // of a 512-byte atom holds row j * 32 + lane, the form tcgen05.cp reads.  The weights'
+            // words are asked into L2 kAhead units early: a unit's words are a few short pieces of
+            // the array, which come from HBM later than the unit's weight tile would.
+            constexpr int kAhead = C::kStages + 6;
             if (kMode == kDown) grid_dependency_wait();
+            const uint32_t par = warp == 8 ? 0u : 1u;
             int s = 0;
-            uint32_t ph = 0;
-            bool aborted = false;
-            StreamWalk<kMode> walk(pl, share);
-            StreamSeg sg;
-            const int h_words = (p.out_rows + 511) / 512;      // kGateUp's own out_rows is I
-            (void)h_words;
-            while (!aborted && walk.next(pl, sg)) {
-                for (int k = sg.k0; k < sg.k1; ++k) {
+            uint32_t ph = 0, n = 0;
+            StreamCursor<kMode> c(pl, share, p.nk), ahead(pl, share, p.nk);
+            auto words_of = [&](const StreamCursor<kMode>& at) {
+                const int e = kMode == kGateUp ? list[at.sg.tile / p.row_tiles] : (kMode == kDown ? list[at.li] : 0);
+                return p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? at.kl : at.kl >> 2) * p.sfw_ld;
+            };
+            // first row of the tile's weight block b
+            auto row_of = [&](const StreamCursor<kMode>& at, int b) {
+                return kMode == kGateUp ? at.sg.tile % p.row_tiles * 128 + b * p.out_rows : at.sg.tile * 256 + b * 128;
+            };
+            auto prefetch = [&]() {
+                if (ahead.new_words(kFp4, p.nk) && lane < 2) {
+                    const int i = kFp4 ? row_of(ahead, lane) : row_of(ahead, lane) >> 7;
+                    if (i < p.sfw_rows) prefetch_l2_bulk(words_of(ahead) + (i & ~3), kFp4 ? 512u : 16u);
+                }
+            };
+            for (int i = 0; i < kAhead && ahead.valid; ++i, ahead.step(pl))
+                if ((static_cast<uint32_t>(i) & 1u) == par) prefetch();
+            for (; c.valid; c.step(pl), ++n) {
+                if ((n & 1u) == par) {
                     const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
-                    if (!__all_sync(0xffffffffu, go)) { aborted = true; break; }
-                    const bool fp8 = kMode != kProj || k < p.nk;
-                    const int li = down_expert(k);
-                    const int kl = kMode == kDown ? k - li * p.nk : k;
-                    if (fp8 && (kFp4 || k == sg.k0 || (kl & 3) == 0)) {
+                    if (!__all_sync(0xffffffffu, go)) break;
+                    if (c.new_words(kFp4, p.nk)) {
                         const uint32_t da = sbase + C::kOffSf + s * C::kSfBytes + lane * 16;
-                        const int e = kMode == kGateUp ? list[sg.tile / p.row_tiles] : (kMode == kDown ? list[li] : 0);
-                        const int32_t* pw = p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? kl : kl >> 2) * p.sfw_ld;
-                        // first rows of the tile's two weight blocks
-                        const int row0 = kMode == kGateUp ? sg.tile % p.row_tiles * 128 : sg.tile * 256;
-                        const int row1 = kMode == kGateUp ? p.out_rows + row0 : row0 + 128;
+                        const int32_t* pw = words_of(c);
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const int row = b ? row1 : row0;
+                            const int row = row_of(c, b);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int i = kFp4 ? row + j * 32 + lane : row >> 7;
@@ -614,9 +639,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             }
                         }
                         const int32_t* pt;
-                        if (kMode == kDown) pt = p.sft + ((long long)li * ((p.nk + 3) / 4) + (kl >> 2)) * BN;
-                        else pt = p.sft + (long long)(kl >> 2) * p.sft_ld + sg.tt * BN;
-                        const int nt = kMode == kDown ? BN : min(BN, p.tokens - sg.tt * BN);
+                        if (kMode == kDown) pt = p.sft + ((long long)c.li * ((p.nk + 3) / 4) + (c.kl >> 2)) * BN;
+                        else pt = p.sft + (long long)(c.kl >> 2) * p.sft_ld + c.sg.tt * BN;
+                        const int nt = kMode == kDown ? BN : min(BN, p.tokens - c.sg.tt * BN);
 #pragma unroll
                         for (int j = 0; j < (BN + 31) / 32; ++j) {
                             const int i = j * 32 + lane;
@@ -625,8 +650,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         }
                     }
                     cp_async_mbar_arrive(full_bar(s));
-                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
                 }
+                if (ahead.valid) {
+                    if (((n + kAhead) & 1u) == par) prefetch();
+                    ahead.step(pl);
+                }
+                if (++s == C::kStages) { s = 0; ph ^= 1u; }
             }
             cp_async_wait_all();
             __syncwarp();
@@ -661,6 +690,34 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         StreamWalk<kMode> walk(pl, share);
         StreamSeg sg;
         while (!aborted && walk.next(pl, sg)) {
+            if constexpr (kMode == kGateUp) {
+                // the tile's routing weights, while its weights stream
+                const int expert = p.expert_base + list[sg.tile / p.row_tiles];
+                for (int t = te; t < BN; t += 128) {
+                    float w = 0.0f;
+                    int on = 0;
+                    if (t < p.tokens) {
+                        const int32_t* ids = p.ids + (long long)t * p.topk;
+                        const float* weights = p.weights + (long long)t * p.topk;
+                        for (int j0 = 0; j0 < p.topk; j0 += 8) {
+                            int id[8];
+                            float x[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const bool in = j0 + j < p.topk;
+                                id[j] = in ? __ldg(ids + j0 + j) : -1;
+                                x[j] = in ? __ldg(weights + j0 + j) : 0.0f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (id[j] == expert && j0 + j < p.topk) { w += x[j]; on = 1; }
+                        }
+                    }
+                    tok_w[t] = w;
+                    tok_on[t] = on;
+                }
+                if (!esync()) break;
+            }
             const bool ok = wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -701,24 +758,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 }
             }
             // ---- finish the tile
-            int expert = 0;
-            if constexpr (kMode == kGateUp) {
-                const int li = sg.tile / p.row_tiles;
-                expert = p.expert_base + list[li];
-                for (int t = te; t < BN; t += 128) {
-                    float w = 0.0f;
-                    int on = 0;
-                    if (t < p.tokens)
-                        for (int j = 0; j < p.topk; ++j)
-                            if (__ldg(p.ids + (long long)t * p.topk + j) == expert) {
-                                w += __ldg(p.weights + (long long)t * p.topk + j);
-                                on = 1;
-                            }
-                    tok_w[t] = w;
-                    tok_on[t] = on;
-                }
-                if (!esync()) { aborted = true; break; }
-            }
             for (int c0 = 0; c0 < BN; c0 += 16) {
                 float v0[16], v1[16];
                 if (sg.whole) {
