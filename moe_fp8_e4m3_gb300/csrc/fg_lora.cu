@@ -1,6 +1,8 @@
 // fg_lora.cu - an FP8 projection shared by all tokens plus each token's own low-rank adapter,
-// in two launches (fg_stream.cuh): x times the adapters' A, then the projection's K-groups and
-// the adapters' B in one accumulator.
+// in two launches: v = scaling * x @ A^T per token and adapter (here), then the projection's
+// K-groups and the adapters' B against v in one accumulator (fg_stream.cuh).
+#include <cuda_bf16.h>
+
 #include <cstdio>
 #include <cstring>
 
@@ -31,8 +33,7 @@ Layout layout(int M, int R) {
     l.count = l.ids + up256((long long)l.tiles * l.bn * 4);
     l.v = l.count + up256((long long)l.tiles * 4);
     l.part = l.v + up256((long long)l.tiles * l.bn * 3 * l.bn * l.rp * 2);
-    const long long ctas = l.tiles > fg::kMaxStreamCtas ? l.tiles : fg::kMaxStreamCtas;
-    l.bytes = l.part + ctas * 2 * 2 * l.bn * 128 * 4;
+    l.bytes = l.part + (long long)fg::kMaxStreamCtas * 2 * 2 * l.bn * 128 * 4;
     return l;
 }
 
@@ -42,6 +43,189 @@ bool shapes_ok(int M, int N, int K, int R) {
     return l.tiles <= fg::kMaxTokenTiles &&
            (long long)l.tiles * ceil_div(N, 256) * (K / 128 + 4 * l.bn) < (1LL << 31) &&
            (long long)l.tiles * l.bn * 3 * l.bn < (1LL << 31);
+}
+
+// ---------------------------------------------------------------- v = scaling * x @ A^T
+// One CTA per (token tile, distinct adapter of it, 8 * NB of the tokens that use it): the
+// adapter's rows are the M operand of mma.sync (MB blocks of 16), its tokens the N operand (NB
+// blocks of 8), gathered by their row numbers.  The 16 warps split K and read both operands
+// straight into registers, 16 bytes (8 consecutive k) per row and lane: k is summed over, so a
+// lane's 8 values may stand for any k as long as A and x agree; they feed two 16-wide steps.
+// There is nothing to stage: each A element is used by one CTA (latency-bound: its bytes in
+// flight are what counts, U blocks of 32 k per warp), and tcgen05's 128 rows would be mostly
+// empty.  The partial sums meet in shared memory, in warp order.
+struct ShrinkParams {
+    int tokens, bn, K, R, rp, L, max_slots, parts;
+    const int32_t* ids;
+    const uint16_t* x;          // [tokens][K] BF16
+    const uint16_t* lora_a;     // [L][R][K] BF16
+    const float* scaling;
+    uint16_t* v;                // [token tile][slot][parts][bn][rp] BF16
+    int* slot_ids;
+    int* slot_count;
+    int* status;
+};
+
+constexpr int kShrinkWarps = 16;
+
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x as a sum of BF16 parts: each holds what the parts before it leave.
+__device__ __forceinline__ void store_parts(uint16_t* dst, long long stride, int parts, float x) {
+    for (int o = 0; o < parts; ++o) {
+        const __nv_bfloat16 h = __float2bfloat16(x);
+        dst[o * stride] = __bfloat16_as_ushort(h);
+        x -= __bfloat162float(h);
+        if (!(x == x)) x = 0.0f;       // an infinite or NaN part leaves nothing
+    }
+}
+
+template <int MB, int NB, int U>
+__global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const ShrinkParams p) {
+    constexpr int kTok = 8 * NB;
+    __shared__ uint32_t bits[32];
+    __shared__ uint16_t list[fg::kMaxListed];
+    __shared__ int listed, members;
+    __shared__ int16_t member[128];               // tokens of the tile that use the adapter, in order
+    __shared__ float red[kShrinkWarps / 2][MB * 16][kTok];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = blockIdx.x, first = blockIdx.y * kTok, tt = blockIdx.z;
+    fg::grid_dependency_wait();
+    if (threadIdx.x == 0) fg::grid_launch_dependents();
+    const int n = min(p.bn, p.tokens - tt * p.bn);
+    const int32_t* ids = p.ids + (long long)tt * p.bn;
+    fg::list_distinct(ids, n, 0, p.L, bits, list, &listed);
+    if (slot == 0 && first == 0) {
+        for (int i = threadIdx.x; i < listed; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = list[i];
+        if (threadIdx.x == 0) p.slot_count[tt] = listed;
+        for (int i = threadIdx.x; i < n; i += blockDim.x)
+            if (__ldcg(ids + i) >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
+    }
+    if (slot >= listed) return;
+    const int id = list[slot];
+    uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
+    const long long part = (long long)p.bn * p.rp;
+    if (warp == 0) {
+        int run = 0;
+        for (int t0 = 0; t0 < p.bn; t0 += 32) {
+            const int t = t0 + lane;
+            const bool mine = t < n && __ldcg(ids + t) == id;
+            const uint32_t m = __ballot_sync(0xffffffffu, mine);
+            if (mine) member[run + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(t);
+            run += __popc(m);
+        }
+        if (lane == 0) members = run;
+    } else if (first == 0 && warp == 1) {
+        // the other tokens' rows are zero: they are multiplied with this adapter's B too
+        for (int t = lane; t < p.bn; t += 32)
+            if (!(t < n && __ldcg(ids + t) == id))
+                for (int o = 0; o < p.parts; ++o)
+                    for (int c = 0; c < p.rp; c += 8)
+                        *reinterpret_cast<uint4*>(v + o * part + (long long)t * p.rp + c) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int mine = min(kTok, members - first);
+    if (mine <= 0) return;
+    const float scale = __ldg(p.scaling + id);
+    const int g = lane >> 2, q = lane & 3;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4* xrow[NB];
+    bool xon[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int i = 8 * j + g;
+        xon[j] = i < mine;
+        xrow[j] = reinterpret_cast<const uint4*>(p.x + ((long long)tt * p.bn + (xon[j] ? member[first + i] : 0)) * p.K) + q;
+    }
+    const int blocks = p.K / 32;                   // 64 bytes of a row each: four lanes' 16
+    for (int m0 = 0; m0 < p.rp; m0 += 16 * MB) {
+        float acc[MB][NB][4] = {};
+        const uint4* arow[MB][2];
+        bool aon[MB][2];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m0 + 16 * i + 8 * h + g;
+                aon[i][h] = r < p.R;
+                arow[i][h] = reinterpret_cast<const uint4*>(p.lora_a + ((long long)id * p.R + (aon[i][h] ? r : 0)) * p.K) + q;
+            }
+        for (int b0 = warp; b0 < blocks; b0 += kShrinkWarps * U) {
+            uint4 a[U][MB][2], x[U][NB];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = b0 + u * kShrinkWarps;
+                const bool in = b < blocks;
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) a[u][i][h] = in && aon[i][h] ? __ldg(arow[i][h] + b * 4) : zero;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) x[u][j] = in && xon[j] ? __ldg(xrow[j] + b * 4) : zero;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        mma_bf16_16x8x16(acc[i][j], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, x[u][j].x, x[u][j].y);
+                        mma_bf16_16x8x16(acc[i][j], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, x[u][j].z, x[u][j].w);
+                    }
+        }
+        // the upper eight warps' sums first, then the lower eight add theirs
+#pragma unroll
+        for (int pass = 1; pass >= 0; --pass) {
+            if (warp / 8 == pass) {
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float& at = red[warp & 7][16 * i + g + 8 * (c >> 1)][8 * j + 2 * q + (c & 1)];
+                            at = pass ? acc[i][j][c] : at + acc[i][j][c];
+                        }
+            }
+            __syncthreads();
+        }
+        for (int o = threadIdx.x; o < MB * 16 * mine; o += blockDim.x) {
+            const int r = o % (MB * 16), t = o / (MB * 16);
+            float sum = red[0][r][t];
+#pragma unroll
+            for (int w = 1; w < kShrinkWarps / 2; ++w) sum += red[w][r][t];
+            if (m0 + r < p.rp) store_parts(v + (long long)member[first + t] * p.rp + m0 + r, part, p.parts, scale * sum);
+        }
+        __syncthreads();
+    }
+    fg::fence_proxy_async_global();
+}
+
+cudaError_t launch_shrink(const ShrinkParams& p, int tiles, int pdl, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.blockDim = dim3(32 * kShrinkWarps);
+    cfg.stream = stream;
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const unsigned slots = static_cast<unsigned>(p.L < p.bn ? p.L : p.bn);
+    auto go = [&](auto kernel, int tok) {
+        cfg.gridDim = dim3(slots, static_cast<unsigned>(ceil_div(p.bn, tok)), static_cast<unsigned>(tiles));
+        return cudaLaunchKernelEx(&cfg, kernel, p);
+    };
+    // 8 tokens at a time where there are few per adapter (small tiles), 32 in a prompt's tiles
+    if (p.bn <= 64)
+        return p.rp <= 16 ? go(lora_shrink_kernel<1, 1, 8>, 8) : go(lora_shrink_kernel<2, 1, 4>, 8);
+    return p.rp <= 16 ? go(lora_shrink_kernel<1, 4, 2>, 32) : go(lora_shrink_kernel<2, 4, 2>, 32);
 }
 
 }  // namespace
@@ -71,40 +255,32 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
     const int grid = st.sms < fg::kMaxStreamCtas ? st.sms : fg::kMaxStreamCtas;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
+    // parts of x @ lora_a^T: 16 mantissa bits under a BF16 result, 24 under an FP32 one; an adapter
+    // unit's parts x columns fit the stage's token area
+    const int parts = d_dtype == FG_F32 ? 3 : 2, unit_cols = d_dtype == FG_F32 ? 32 : 64;
+    if (fg::print_configs_enabled())
+        std::fprintf(stderr, "[fg] fp8_gemm_nt_lora M=%d N=%d K=%d L=%d R=%d BN=%d rank=%d grid=%d\n", M, N, K, L, R, l.bn,
+                     l.rp, grid);
+    const ShrinkParams sp{M, l.bn, K, R, l.rp, L, l.bn, parts, ids, static_cast<const uint16_t*>(x),
+                          static_cast<const uint16_t*>(lora_a), scaling, reinterpret_cast<uint16_t*>(ws + l.v),
+                          reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<int*>(ws + l.count), st.status};
+    if (launch_shrink(sp, l.tiles, st.pdl, s) != cudaSuccess) {
+        cudaGetLastError();
+        return FG_ERR_CUDA;
+    }
     fg::StreamParams p{};
     p.tokens = M;
     p.ids = ids;
     p.part = reinterpret_cast<float*>(ws + l.part);
-    p.lora_r = R; p.lora_rp = l.rp; p.lora_k = K; p.lora_count = L;
+    p.lora_rp = l.rp; p.lora_count = L;
     p.max_slots = l.bn; p.token_tiles = l.tiles;
-    // parts of x @ lora_a^T: 16 mantissa bits under a BF16 result, 24 under an FP32 one
-    p.parts = d_dtype == FG_F32 ? 3 : 2;
-    p.unit_cols = d_dtype == FG_F32 ? 32 : 64;        // parts x columns fit the stage's token area
-    p.lora_a = static_cast<const uint16_t*>(lora_a);
-    p.scaling = scaling;
-    p.v = reinterpret_cast<uint16_t*>(ws + l.v);
-    p.slot_ids = reinterpret_cast<int*>(ws + l.ids);
-    p.slot_count = reinterpret_cast<int*>(ws + l.count);
+    p.parts = parts; p.unit_cols = unit_cols;
+    p.slot_ids = sp.slot_ids;
+    p.slot_count = sp.slot_count;
     p.min_units = 4;
     p.status = st.status; p.timeout_ns = st.timeout_ns; p.pdl = st.pdl;
     fg::StreamMaps m;
     std::memset(&m, 0, sizeof(m));
-    if (fg::print_configs_enabled())
-        std::fprintf(stderr, "[fg] fp8_gemm_nt_lora M=%d N=%d K=%d L=%d R=%d BN=%d rank=%d grid=%d\n", M, N, K, L, R, l.bn,
-                     l.rp, grid);
-    {   // x times the distinct adapters' A, token tile by token tile
-        const uint64_t xd[2] = {(uint64_t)K, (uint64_t)M}, xp[1] = {(uint64_t)K * 2};
-        const uint32_t xb[2] = {64, (uint32_t)l.bn};
-        if (!fg::encode_tiled(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xp, xb, CU_TENSOR_MAP_SWIZZLE_128B))
-            return FG_ERR_INVALID_ARG;
-        p.nk = K / 64;
-        p.ctr = reinterpret_cast<unsigned*>(ws);
-        const int per_tile = grid / l.tiles > 0 ? grid / l.tiles : 1;
-        if (fg::launch_stream<fg::kShrink, false>(l.bn, p, m, dim3(per_tile, l.tiles), s) != cudaSuccess) {
-            cudaGetLastError();
-            return FG_ERR_CUDA;
-        }
-    }
     {   // the projection and the adapters' B
         const uint64_t wd[3] = {(uint64_t)K, (uint64_t)N, 1}, wp[2] = {(uint64_t)K, (uint64_t)K * N};
         const uint32_t wb[3] = {128, 256, 1};
@@ -120,7 +296,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         if (!fg::encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, b, wd, wp, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !fg::encode_tiled(&m.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, xd, xp, xb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !fg::encode_tiled(&m.lb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_b, ld, lp, lb, sw) ||
-            !fg::encode_tiled(&m.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.v, vd, vp, vb, sw))
+            !fg::encode_tiled(&m.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, sp.v, vd, vp, vb, sw))
             return FG_ERR_INVALID_ARG;
         p.nk = K / 128; p.row_tiles = ceil_div(N, 256); p.out_rows = N;
         p.sfw = sfb;

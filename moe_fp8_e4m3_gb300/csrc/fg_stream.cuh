@@ -22,16 +22,13 @@
 //            routing weight, per token and 128 outputs one UE8M0 scale, E4M3 codes -> workspace
 //   kDown    tile = 256 output rows; its K axis runs over all active experts one after
 //            another, so the sum over experts happens in the FP32 accumulator
-//   kShrink  tile = 256 rows of the distinct adapters' A matrices (BF16); epilogue: each
-//            token keeps its own adapter's rows, scaled, as a sum of BF16 parts: two (16 mantissa
-//            bits) for a BF16 result, three (24) for an FP32 one
 //   kProj    tile = 256 output rows; K-groups of the shared FP8 weights, then units of the
-//            adapters' B matrices (BF16 against the kShrink result), in one accumulator
+//            adapters' B matrices (BF16, against x @ A^T from fg_lora.cu), in one accumulator
 //
 // Warp roles: 0, 2 TMA producers of the weight tiles (even / odd stages); 1 TMEM owner and
-// MMA issuer of the tile's first block, 9 (kShrink: 2) of the second; 3 TMA producer of the
-// token operand; 4-7 epilogue; 8, 10 scale loaders (kShrink: warps 8-15 load the adapter rows
-// by cp.async, since a tile gathers many short row blocks).
+// MMA issuer of the tile's first block, 9 of the second; 3 TMA producer of the token operand;
+// 8, 10 scale loaders; 4-7 and 12-15 epilogue, the first four on the first half of the tile's
+// token columns, the others on the second.
 // Every wait is bounded: on expiry the CTA records a time-out in the status word, all its
 // roles wind down and the kernel returns.
 #pragma once
@@ -40,26 +37,26 @@
 
 namespace fg {
 
-enum StreamMode : int { kGateUp = 0, kDown = 1, kProj = 2, kShrink = 3 };
+enum StreamMode : int { kGateUp = 0, kDown = 1, kProj = 2 };
 
 enum : int { kChkAdapter = 6 };          // an adapter id >= L
 
 constexpr int kMaxListed = 1024;         // experts of a shard, adapters of a call
 constexpr int kMaxTokenTiles = 512;      // kProj: token tiles of one call
 constexpr int kMaxStreamCtas = 256;      // shares of a launch (partial slots in the workspace)
-constexpr int kMaxCounters = 512;        // of one launch: kMaxStreamCtas, or one per token tile (kShrink)
+constexpr int kMaxCounters = 512;        // of one launch: two per share, one for each half of the columns
 constexpr int kCounterBytes = 2 * kMaxCounters * 4;   // head of a workspace: both launches' counters
 
 struct StreamMaps {
     CUtensorMap w;       // weights
     CUtensorMap x;       // token operand
     CUtensorMap lb;      // kProj: adapters' B
-    CUtensorMap v;       // kProj: kShrink results
+    CUtensorMap v;       // kProj: x @ A^T, [token tile][slot][part][BN][rp]
 };
 
 struct StreamParams {
     int tokens;                  // rows of the token operand
-    int nk;                      // K-groups of one tile (kDown: of one expert; kShrink: 64-wide chunks)
+    int nk;                      // K-groups of one tile (kDown: of one expert)
     int row_tiles;               // kGateUp: I / 128 per expert; kDown, kProj: ceil(rows / 256)
     int out_rows;                // kGateUp: I; kDown: H; kProj: N (row length of d)
     int experts, expert_base, topk;
@@ -73,17 +70,14 @@ struct StreamParams {
     uint8_t* hq;                 // kGateUp out: [slot][BN][I] E4M3
     uint8_t* sfh;                // and its scale words [slot][ceil(I/512)][BN]
     float* part;                 // [CTA][2][2][BN][128] partial tiles
-    unsigned* ctr;               // [kMaxCounters]: one per share
+    unsigned* ctr;               // [kMaxCounters]
     void* d;
     int d_f32;
     // adapters
-    int lora_r, lora_rp, lora_k, lora_count, max_slots, token_tiles;
-    int parts, unit_cols;        // BF16 parts of a kShrink result; rank columns of a kProj unit
-    const uint16_t* lora_a;      // [L][R][K] BF16
-    const float* scaling;        // [L]
-    uint16_t* v;                 // [token tile][slot][parts][BN][rp] BF16
-    int* slot_ids;               // [token tile][max_slots] distinct adapters, ascending
-    int* slot_count;             // [token tile]
+    int lora_rp, lora_count, max_slots, token_tiles;
+    int parts, unit_cols;        // BF16 parts of x @ A^T; rank columns of a unit
+    const int* slot_ids;         // [token tile][max_slots] distinct adapters, ascending
+    const int* slot_count;       // [token tile]
     int min_units;               // least units of a share
     int* status;
     unsigned long long timeout_ns;
@@ -109,8 +103,11 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int m, int n) {
 __host__ __device__ constexpr uint32_t make_idesc_stream(int n, bool fp4) {
     return make_idesc_mxf8(128, n, false, false) | (fp4 ? kFmtE2M1 << 7 : 0u);
 }
-__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared::cta.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// 8 consecutive 32-bit TMEM columns of this warp's 32 lanes (one column per register).
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 // Orders generic-proxy global writes (the codes that the next kernel loads by TMA).
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
@@ -119,23 +116,25 @@ template <int kMode, int BN>
 struct StreamCfg {
     static constexpr int kABytes = 32768;                                   // two 128-row blocks x 128 bytes
     static constexpr int kBBytes = BN * 128 * (kMode == kProj ? 2 : 1);     // kProj: the parts of an adapter unit
-    static constexpr int kSfBytes = kMode == kShrink ? 0 : 3 * 512;         // weight block 0, 1, tokens
+    static constexpr int kSfBytes = 3 * 512;                                // weight block 0, 1, tokens
     static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-    static constexpr int kMiscBytes = 512 + 512 + BN * 8 + 128 + 2 * kMaxListed +
+    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + 128 + 2 * kMaxListed +
                                       (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
     static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
     static constexpr int kNumAcc = BN <= 64 ? 2 : 1;
     static constexpr int kSfCol0 = kNumAcc * 2 * BN;
     static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
-    static constexpr int kThreads = kMode == kShrink ? 512 : 352;
+    static constexpr int kThreads = 512;
+    static constexpr int kChunk = BN >= 32 ? 16 : 8;                        // token columns an epilogue group takes at a time
+    static constexpr int kJoin = 32 / kChunk;                               // partials it loads at a time
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
     static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 5;
+    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 6;
     static constexpr int kOffMisc = kOffBar + 512 - 64;                     // TMEM address, abort flag, count, last flag
-    static constexpr int kOffRed = kOffBar + 512;                           // [4][16] amax words, then 64 exponents
-    static constexpr int kOffTok = kOffRed + 512;                           // [BN] weights / adapter ids, [BN] flags
+    static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
+    static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
     static constexpr int kOffBits = kOffTok + BN * 8;
     static constexpr int kOffList = kOffBits + 128;
     static constexpr int kOffPre = kOffList + 2 * kMaxListed;
@@ -255,7 +254,6 @@ __global__ void __launch_bounds__(StreamCfg<kMode, BN>::kThreads, 1)
 fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) {
     using C = StreamCfg<kMode, BN>;
     constexpr bool kMoe = kMode == kGateUp || kMode == kDown;
-    static_assert(!kFp4 || kMode != kShrink, "the adapters are BF16");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -268,38 +266,34 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     // per issuer: its MMAs done, on the way out and before products of another kind
     auto drain_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + b); };
     auto turn_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 2 + b); };
-    const uint32_t esync_bar = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4);   // the four epilogue warps
+    auto esync_bar = [&](int g) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g); };   // an epilogue group
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     int* listed = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 12);
-    uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kOffRed);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [2]
     float* tok_w = reinterpret_cast<float*>(smem + C::kOffTok);               // routing weight of the tile's expert
-    int* tok_id = reinterpret_cast<int*>(smem + C::kOffTok);                  // kShrink: adapter of each token
-    int* tok_on = tok_id + BN;                                                // the token uses the tile's expert
+    int* tok_on = reinterpret_cast<int*>(tok_w + BN);                         // the token uses the tile's expert
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::kOffBits);
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
     int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            // kShrink: 256 loader threads and the token producer; else the two TMA producers and
-            // the scale loader's 32 lanes
-            mbar_init(full_bar(s), kMode == kShrink ? 257 : 34);
+            mbar_init(full_bar(s), 34);          // the two TMA producers, the scale loader's 32 lanes
             mbar_init(empty_bar(s), 2);          // both issuers' commits
         }
         for (int b = 0; b < C::kNumAcc; ++b) {
             mbar_init(accf_bar(b), 2);
-            mbar_init(acce_bar(b), 4);
+            mbar_init(acce_bar(b), 8);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(drain_of(b), 1);
             mbar_init(turn_of(b), 1);
+            mbar_init(esync_bar(b), 4);
         }
-        mbar_init(esync_bar, 4);
         *abort_flag = 0;
         fence_mbar_init();
-        if (kMode != kShrink) tma_prefetch_map(&maps.w);
+        tma_prefetch_map(&maps.w);
         tma_prefetch_map(&maps.x);
     }
     if (warp == 1) {
@@ -309,37 +303,31 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // kDown runs behind its own kGateUp launch, which let it start only after its own wait: the
-    // ids and weights it reads before this launch's wait were complete before that.  Only the
-    // roles that touch what kGateUp writes wait.
-    if (kMode != kDown) {
+    // kDown runs behind its own kGateUp launch, and kProj behind x @ A^T, which let it start only
+    // after their own wait: the ids, weights and adapters they read before this launch's wait were
+    // complete before that.  Only the roles that touch what the launch before writes wait.
+    const bool one_tile = kMode == kProj && p.token_tiles == 1;
+    if (kMode == kGateUp || (kMode == kProj && !one_tile)) {
         grid_dependency_wait();
         if (threadIdx.x == 0) grid_launch_dependents();
     }
     StreamPlan pl;
     int nlist = 0;
-    const int tt0 = kMode == kShrink ? static_cast<int>(blockIdx.y) : 0;
     if constexpr (kMoe) {
         list_distinct(p.ids, p.tokens * p.topk, p.expert_base, p.experts, bits, list, listed);
         nlist = *listed;
         pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
         pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
-    } else if constexpr (kMode == kShrink) {
-        const int n = min(BN, p.tokens - tt0 * BN);
-        list_distinct(p.ids + (long long)tt0 * BN, n, 0, p.lora_count, bits, list, listed);
+    } else if (one_tile) {
+        list_distinct(p.ids, p.tokens, 0, p.lora_count, bits, list, listed);
         nlist = *listed;
-        for (int t = threadIdx.x; t < BN; t += C::kThreads) {
-            const int id = t < n ? __ldg(p.ids + (long long)tt0 * BN + t) : -1;
-            if (id >= p.lora_count) record_status(p.status, kErrContract | kChkAdapter);
-            tok_id[t] = id;
+        if (threadIdx.x == 0) {
+            pre[0] = 0;
+            pre[1] = p.row_tiles * (p.nk + (nlist * p.lora_rp + p.unit_cols - 1) / p.unit_cols);
         }
-        if (blockIdx.x == 0) {       // for kProj
-            for (int i = threadIdx.x; i < nlist; i += C::kThreads) p.slot_ids[tt0 * p.max_slots + i] = list[i];
-            if (threadIdx.x == 0) p.slot_count[tt0] = nlist;
-        }
-        pl.nk = p.nk;
-        pl.units = (nlist * p.lora_rp + 255) / 256 * pl.nk;
         __syncthreads();
+        pl.nk = p.nk;
+        pl.units = pre[1];
     } else {
         // units of a token tile: row tiles x (K-groups + adapter units of unit_cols rank columns)
         if (warp == 0) {
@@ -363,6 +351,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         pl.nk = p.nk;
         pl.units = pre[p.token_tiles];
     }
+    auto slots_of = [&](int tt) { return one_tile ? nlist : __ldcg(p.slot_count + tt); };
+    auto adapter_of = [&](int tt, int slot) { return one_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
     pl.row_tiles = p.row_tiles;
     pl.pre = pre;
     pl.shares = max(1, min(static_cast<int>(gridDim.x), (pl.units + p.min_units - 1) / p.min_units));
@@ -374,9 +364,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int per_unit = kMode == kProj ? max(1, p.unit_cols / p.lora_rp) : 1;   // adapters in a unit
     const int pieces = kMode == kProj ? max(1, p.lora_rp / p.unit_cols) : 1;     // units of one adapter
 
-    if (warp == 0 || (warp == 2 && kMode != kShrink)) {
+    if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ weight tiles
-        if (kMode != kShrink && lane == 0) {
+        if (lane == 0) {
             const uint32_t par = warp == 0 ? 0u : 1u;
             int s = 0;
             uint32_t ph = 0, n = 0, armed = 0, armed_par = 0;
@@ -393,13 +383,13 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         armed_par = (armed_par & ~(1u << s)) | (ph << s);
                         if (kMode == kProj && c.k >= p.nk) {
                             const int u = c.k - p.nk;
-                            const int nslots = __ldcg(p.slot_count + c.sg.tt);
+                            const int nslots = slots_of(c.sg.tt);
                             const int s0 = pieces > 1 ? u / pieces : u * per_unit;
                             const int cnt = min(per_unit, nslots - s0);
                             mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * 256 * rb));
                             for (int j = 0; j < cnt; ++j)
                                 tma_load_3d(dst + j * 256 * rb, &maps.lb, fb, pieces > 1 ? (u % pieces) * ucols : 0,
-                                            c.sg.tile * 256, __ldcg(p.slot_ids + c.sg.tt * p.max_slots + s0 + j));
+                                            c.sg.tile * 256, adapter_of(c.sg.tt, s0 + j));
                         } else {
                             // packed FP4: the transaction counts the bytes read, half of those filled
                             mbar_arrive_expect_tx(fb, kFp4 ? C::kABytes / 2 : C::kABytes);
@@ -432,15 +422,21 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_par = 0;
             bool aborted = false;
+            bool waited = !one_tile;
             StreamCursor<kMode> c(pl, share, p.nk);
             for (; c.valid; c.step(pl)) {
+                if (kMode == kProj && !waited && c.k >= p.nk) {      // x @ A^T from here on
+                    grid_dependency_wait();
+                    fence_proxy_async_global();
+                    waited = true;
+                }
                 if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB)) { aborted = true; break; }
                 const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
                 armed |= 1u << s;
                 armed_par = (armed_par & ~(1u << s)) | (ph << s);
                 if (kMode == kProj && c.k >= p.nk) {
                     const int u = c.k - p.nk;
-                    const int nslots = __ldcg(p.slot_count + c.sg.tt);
+                    const int nslots = slots_of(c.sg.tt);
                     const int s0 = pieces > 1 ? u / pieces : u * per_unit;
                     const int cnt = min(per_unit, nslots - s0);
                     mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * p.parts * BN * rb));
@@ -450,7 +446,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 } else {
                     mbar_arrive_expect_tx(fb, BN * 128);
                     if constexpr (kMode == kDown) tma_load_2d(dst, &maps.x, fb, c.kl * 128, c.li * BN);
-                    else if constexpr (kMode == kShrink) tma_load_2d(dst, &maps.x, fb, c.k * 64, tt0 * BN);
                     else tma_load_2d(dst, &maps.x, fb, c.k * 128, c.sg.tt * BN);
                 }
                 if (++s == C::kStages) { s = 0; ph ^= 1u; }
@@ -460,7 +455,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
         }
         __syncwarp();
-    } else if (warp == 1 || warp == (kMode == kShrink ? 2 : 9)) {
+    } else if (warp == 1 || warp == 9) {
         // ------------------------------------------------------------- MMA issuers
         // One for each 128-row block of the tile: a thread needs ~80 clocks to issue a
         // tcgen05.mma, so one issuer's eight per unit (~0.45 us with the waits) would pace the
@@ -493,14 +488,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     tc_fence_after();
                     const uint64_t ad = a0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
                     const uint64_t bd = b0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
-                    if constexpr (kMode == kShrink) {
-                        fence_proxy_async_smem();     // adapter rows written by cp.async
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            tc_mma_bf16(dt, ad + 2 * j, bd + 2 * j, kIdescBf16, add);
-                            add = 1;
-                        }
-                    } else if (kMode == kProj && k >= p.nk) {
+                    if (kMode == kProj && k >= p.nk) {
                         if (k == p.nk && add) {
                             // let the scaled FP8 products finish before another kind adds to their sums
                             tc_commit(turn_of(blk));
@@ -509,7 +497,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             tc_fence_after();
                         }
                         const int u = k - p.nk;
-                        const int nslots = __ldcg(p.slot_count + sg.tt);
+                        const int nslots = slots_of(sg.tt);
                         const int cnt = pieces > 1 ? 1 : min(per_unit, nslots - u * per_unit);
                         const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
                         const uint32_t sa = sbase + s * C::kABytes + blk * 128 * rb, sb = sbase + C::kOffB + s * C::kBBytes;
@@ -556,134 +544,104 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             }
         }
         __syncwarp();
-    } else if (warp >= 8) {
-        if constexpr (kMode == kShrink) {
-            // ------------------------------------------------- adapter rows (256 threads)
-            // Thread t copies 16 bytes (column chunk t % 8) of rows t / 8 + 32 i of the tile;
-            // row r holds rank row r % rp of the tile's adapter r / rp, zero past R or the list.
-            const int t = static_cast<int>(threadIdx.x) - 256, c = t & 7, r0 = t >> 3;
-            int s = 0;
-            uint32_t ph = 0;
-            bool aborted = false;
-            StreamWalk<kMode> walk(pl, share);
-            StreamSeg sg;
-            while (!aborted && walk.next(pl, sg)) {
-                const uint16_t* src[8];
-                uint32_t ok = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = sg.tile * 256 + r0 + 32 * i;
-                    const int slot = r / p.lora_rp, rr = r - slot * p.lora_rp;
-                    const bool in = slot < nlist && rr < p.lora_r;
-                    ok |= (in ? 1u : 0u) << i;
-                    src[i] = p.lora_a + (in ? ((long long)list[slot] * p.lora_r + rr) * p.lora_k + c * 8 : 0);
-                }
-                for (int k = sg.k0; k < sg.k1; ++k) {
-                    const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
-                    if (!__all_sync(0xffffffffu, go)) { aborted = true; break; }
-                    const uint32_t dst = sbase + s * C::kABytes;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + 32 * i;
-                        cp_async_16z(dst + r * 128 + ((c ^ (r & 7)) << 4), src[i] + (long long)k * 64, ok >> i & 1u ? 16u : 0u);
-                    }
-                    cp_async_mbar_arrive(full_bar(s));
-                    if (++s == C::kStages) { s = 0; ph ^= 1u; }
-                }
-            }
-            cp_async_wait_all();
-            __syncwarp();
-        } else {
-            // -------------------------------------------------------- scale loaders
-            // Warp 8 fills the even stages of the unit sequence, warp 10 the odd ones.  Word (lane, j)
-            // of a 512-byte atom holds row j * 32 + lane, the form tcgen05.cp reads.  The weights'
-            // words are asked into L2 kAhead units early: a unit's words are a few short pieces of
-            // the array, which come from HBM later than the unit's weight tile would.
-            constexpr int kAhead = C::kStages + 6;
-            if (kMode == kDown) grid_dependency_wait();
-            const uint32_t par = warp == 8 ? 0u : 1u;
-            int s = 0;
-            uint32_t ph = 0, n = 0;
-            StreamCursor<kMode> c(pl, share, p.nk), ahead(pl, share, p.nk);
-            auto words_of = [&](const StreamCursor<kMode>& at) {
-                const int e = kMode == kGateUp ? list[at.sg.tile / p.row_tiles] : (kMode == kDown ? list[at.li] : 0);
-                return p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? at.kl : at.kl >> 2) * p.sfw_ld;
-            };
-            // first row of the tile's weight block b
-            auto row_of = [&](const StreamCursor<kMode>& at, int b) {
-                return kMode == kGateUp ? at.sg.tile % p.row_tiles * 128 + b * p.out_rows : at.sg.tile * 256 + b * 128;
-            };
-            auto prefetch = [&]() {
-                if (ahead.new_words(kFp4, p.nk) && lane < 2) {
-                    const int i = kFp4 ? row_of(ahead, lane) : row_of(ahead, lane) >> 7;
-                    if (i < p.sfw_rows) prefetch_l2_bulk(words_of(ahead) + (i & ~3), kFp4 ? 512u : 16u);
-                }
-            };
-            for (int i = 0; i < kAhead && ahead.valid; ++i, ahead.step(pl))
-                if ((static_cast<uint32_t>(i) & 1u) == par) prefetch();
-            for (; c.valid; c.step(pl), ++n) {
-                if ((n & 1u) == par) {
-                    const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
-                    if (!__all_sync(0xffffffffu, go)) break;
-                    if (c.new_words(kFp4, p.nk)) {
-                        const uint32_t da = sbase + C::kOffSf + s * C::kSfBytes + lane * 16;
-                        const int32_t* pw = words_of(c);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int row = row_of(c, b);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int i = kFp4 ? row + j * 32 + lane : row >> 7;
-                                const bool in = i < p.sfw_rows;
-                                cp_async_4(da + 512 * b + 4 * j, in ? pw + i : pw, in ? 4u : 0u);
-                            }
-                        }
-                        const int32_t* pt;
-                        if (kMode == kDown) pt = p.sft + ((long long)c.li * ((p.nk + 3) / 4) + (c.kl >> 2)) * BN;
-                        else pt = p.sft + (long long)(c.kl >> 2) * p.sft_ld + c.sg.tt * BN;
-                        const int nt = kMode == kDown ? BN : min(BN, p.tokens - c.sg.tt * BN);
-#pragma unroll
-                        for (int j = 0; j < (BN + 31) / 32; ++j) {
-                            const int i = j * 32 + lane;
-                            const bool in = i < nt;
-                            cp_async_4(da + 1024 + 4 * j, in ? pt + i : pt, in ? 4u : 0u);
-                        }
-                    }
-                    cp_async_mbar_arrive(full_bar(s));
-                }
-                if (ahead.valid) {
-                    if (((n + kAhead) & 1u) == par) prefetch();
-                    ahead.step(pl);
-                }
-                if (++s == C::kStages) { s = 0; ph ^= 1u; }
-            }
-            cp_async_wait_all();
-            __syncwarp();
-        }
-    } else {
-        // ----------------------------------------------------------------- epilogue
-        const int q = warp & 3, row = q * 32 + lane;
-        const int te = static_cast<int>(threadIdx.x) - 128;            // 0..127 over the four warps
+    } else if (warp == 8 || warp == 10) {
+        // -------------------------------------------------------- scale loaders
+        // Warp 8 fills the even stages of the unit sequence, warp 10 the odd ones.  Word (lane, j)
+        // of a 512-byte atom holds row j * 32 + lane, the form tcgen05.cp reads.  The weights'
+        // words are asked into L2 kAhead units early: a unit's words are a few short pieces of
+        // the array, which come from HBM later than the unit's weight tile would.
+        constexpr int kAhead = C::kStages + 6;
         if (kMode == kDown) grid_dependency_wait();
+        const uint32_t par = warp == 8 ? 0u : 1u;
+        int s = 0;
+        uint32_t ph = 0, n = 0;
+        StreamCursor<kMode> c(pl, share, p.nk), ahead(pl, share, p.nk);
+        auto words_of = [&](const StreamCursor<kMode>& at) {
+            const int e = kMode == kGateUp ? list[at.sg.tile / p.row_tiles] : (kMode == kDown ? list[at.li] : 0);
+            return p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? at.kl : at.kl >> 2) * p.sfw_ld;
+        };
+        // first row of the tile's weight block b
+        auto row_of = [&](const StreamCursor<kMode>& at, int b) {
+            return kMode == kGateUp ? at.sg.tile % p.row_tiles * 128 + b * p.out_rows : at.sg.tile * 256 + b * 128;
+        };
+        auto prefetch = [&]() {
+            if (ahead.new_words(kFp4, p.nk) && lane < 2) {
+                const int i = kFp4 ? row_of(ahead, lane) : row_of(ahead, lane) >> 7;
+                if (i < p.sfw_rows) prefetch_l2_bulk(words_of(ahead) + (i & ~3), kFp4 ? 512u : 16u);
+            }
+        };
+        for (int i = 0; i < kAhead && ahead.valid; ++i, ahead.step(pl))
+            if ((static_cast<uint32_t>(i) & 1u) == par) prefetch();
+        for (; c.valid; c.step(pl), ++n) {
+            if ((n & 1u) == par) {
+                const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
+                if (!__all_sync(0xffffffffu, go)) break;
+                if (c.new_words(kFp4, p.nk)) {
+                    const uint32_t da = sbase + C::kOffSf + s * C::kSfBytes + lane * 16;
+                    const int32_t* pw = words_of(c);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int row = row_of(c, b);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int i = kFp4 ? row + j * 32 + lane : row >> 7;
+                            const bool in = i < p.sfw_rows;
+                            cp_async_4(da + 512 * b + 4 * j, in ? pw + i : pw, in ? 4u : 0u);
+                        }
+                    }
+                    const int32_t* pt;
+                    if (kMode == kDown) pt = p.sft + ((long long)c.li * ((p.nk + 3) / 4) + (c.kl >> 2)) * BN;
+                    else pt = p.sft + (long long)(c.kl >> 2) * p.sft_ld + c.sg.tt * BN;
+                    const int nt = kMode == kDown ? BN : min(BN, p.tokens - c.sg.tt * BN);
+#pragma unroll
+                    for (int j = 0; j < (BN + 31) / 32; ++j) {
+                        const int i = j * 32 + lane;
+                        const bool in = i < nt;
+                        cp_async_4(da + 1024 + 4 * j, in ? pt + i : pt, in ? 4u : 0u);
+                    }
+                }
+                cp_async_mbar_arrive(full_bar(s));
+            }
+            if (ahead.valid) {
+                if (((n + kAhead) & 1u) == par) prefetch();
+                ahead.step(pl);
+            }
+            if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        }
+        cp_async_wait_all();
+        __syncwarp();
+    } else if (warp >= 4 && warp != 11) {
+        // ----------------------------------------------------------------- epilogue
+        // Group g's four warps hold the tile's 2 x 128 rows (thread = row of both blocks) and take
+        // columns [g * BN/2, (g + 1) * BN/2), kChunk at a time.  The groups share nothing but the
+        // accumulator's release: each joins, counts and finishes its own half of a cut tile.
+        constexpr int kHalf = BN / 2, kChunk = C::kChunk, kJoin = C::kJoin;
+        const int q = warp & 3, row = q * 32 + lane, grp = warp >= 8 ? 1 : 0;
+        const int te = row;                                            // 0..127 over the group
+        if (kMode == kDown || one_tile) grid_dependency_wait();
+        if (one_tile && threadIdx.x == 128) grid_launch_dependents();
         if (kMode == kDown && nlist == 0) {
             // no token uses an expert of this shard: the sum is empty
             const long long n = (long long)p.tokens * p.out_rows;
-            for (long long i = (long long)blockIdx.x * 128 + te; i < n; i += (long long)gridDim.x * 128) {
+            for (long long i = ((long long)blockIdx.x * 2 + grp) * 128 + te; i < n; i += (long long)gridDim.x * 256) {
                 if (p.d_f32) static_cast<float*>(p.d)[i] = 0.0f;
                 else static_cast<__nv_bfloat16*>(p.d)[i] = __float2bfloat16(0.0f);
             }
         }
         uint32_t e_ph = 0;
-        // all four epilogue warps, bounded like every wait (a warp that gave up never arrives)
+        // the group's four warps, bounded like every wait (a warp that gave up never arrives)
         auto esync = [&]() {
             __syncwarp();
-            if (lane == 0) mbar_arrive(esync_bar);
-            const bool ok = wait_bar(esync_bar, e_ph, wctl, kWaitEpilogueSync);
+            if (lane == 0) mbar_arrive(esync_bar(grp));
+            const bool ok = wait_bar(esync_bar(grp), e_ph, wctl, kWaitEpilogueSync);
             e_ph ^= 1u;
             return __all_sync(0xffffffffu, ok) != 0;
         };
-        const int cta = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);
-        const long long part_tile = 2LL * BN * 128;                       // floats of one partial
+        uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kOffRed) + grp * 128;
+        int red_at = 0;                                                // alternates: one wait per chunk
+        constexpr long long part_tile = 2LL * BN * 128;                // floats of one partial
+        // a partial: [half][chunk of columns][block][column][row]
+        const int my_part = grp * 2 * kHalf * 128 + row;
         int acc = 0;
         uint32_t acc_ph = 0;
         bool aborted = false;
@@ -693,7 +651,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             if constexpr (kMode == kGateUp) {
                 // the tile's routing weights, while its weights stream
                 const int expert = p.expert_base + list[sg.tile / p.row_tiles];
-                for (int t = te; t < BN; t += 128) {
+                if (te < kHalf) {
+                    const int t = grp * kHalf + te;
                     float w = 0.0f;
                     int on = 0;
                     if (t < p.tokens) {
@@ -721,22 +680,38 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             const bool ok = wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * BN;
+            const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * BN + grp * kHalf;
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acce_bar(acc));
             };
+            // columns c0.. of both blocks from the accumulator
+            auto load_acc = [&](int c0, float (&v0)[kChunk], float (&v1)[kChunk]) {
+                uint32_t r0[kChunk], r1[kChunk];
+                if constexpr (kChunk == 16) {
+                    tmem_ld_32x32b_x16(ta + c0, r0);
+                    tmem_ld_32x32b_x16(ta + BN + c0, r1);
+                } else {
+                    tmem_ld_32x32b_x8(ta + c0, r0);
+                    tmem_ld_32x32b_x8(ta + BN + c0, r1);
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
+            };
             int c_first = share, c_last = share;
             if (!sg.whole) {
                 // this share's part of the tile: 0 where the tile began in an earlier share, else 1
-                float* mine = p.part + (2LL * cta + (sg.k0 > 0 ? 0 : 1)) * part_tile + row;
-                for (int c0 = 0; c0 < 2 * BN; c0 += 16) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(ta + c0, r);
-                    tmem_wait_ld();
+                float* mine = p.part + (2LL * share + (sg.k0 > 0 ? 0 : 1)) * part_tile + my_part;
+                for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
+                    float v0[kChunk], v1[kChunk];
+                    load_acc(c0, v0, v1);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) __stcg(mine + (c0 + i) * 128, __uint_as_float(r[i]));
+                    for (int i = 0; i < kChunk; ++i) {
+                        __stcg(mine + (2 * c0 + i) * 128, v0[i]);
+                        __stcg(mine + (2 * c0 + kChunk + i) * 128, v1[i]);
+                    }
                 }
                 release();
                 __threadfence();
@@ -747,10 +722,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     // only the last tile that begins in a share goes on into the next one, so a cut
                     // tile is told by its first share; the count wraps to 0 with the last arrival
                     const unsigned n = static_cast<unsigned>(c_last - c_first);
-                    *last_flag = atomicInc(p.ctr + (cta - share + c_first), n) == n;
+                    last_flag[grp] = atomicInc(p.ctr + 2 * c_first + grp, n) == n;
                 }
                 if (!esync()) { aborted = true; break; }
-                const bool last = *last_flag != 0;
+                const bool last = last_flag[grp] != 0;
                 __threadfence();
                 if (!last) {
                     if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
@@ -758,87 +733,74 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 }
             }
             // ---- finish the tile
-            for (int c0 = 0; c0 < BN; c0 += 16) {
-                float v0[16], v1[16];
+            for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
+                const int t0 = grp * kHalf + c0;                       // first token column
+                float v0[kChunk], v1[kChunk];
                 if (sg.whole) {
-                    uint32_t r0[16], r1[16];
-                    tmem_ld_32x32b_x16(ta + c0, r0);
-                    tmem_ld_32x32b_x16(ta + BN + c0, r1);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
-                    if (c0 + 16 == BN) release();
+                    load_acc(c0, v0, v1);
+                    if (c0 + kChunk == kHalf) release();
                 } else {
+                    // the partials in CTA order, kJoin of them in flight
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const int slot = share_begin(pl, c) > sg.first_unit ? 0 : 1;
-                        const float* src = p.part + (2LL * (cta - share + c) + slot) * part_tile + c0 * 128 + row;
-                        float x0[16], x1[16];
+                    for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.0f;
+                    for (int c = c_first; c <= c_last; c += kJoin) {
+                        float x0[kJoin][kChunk], x1[kJoin][kChunk];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) { x0[i] = __ldcg(src + i * 128); x1[i] = __ldcg(src + (BN + i) * 128); }
+                        for (int u = 0; u < kJoin; ++u) {
+                            const int cc = min(c + u, c_last);
+                            const int slot = share_begin(pl, cc) > sg.first_unit ? 0 : 1;
+                            const float* src = p.part + (2LL * cc + slot) * part_tile + my_part + 2 * c0 * 128;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) { v0[i] += x0[i]; v1[i] += x1[i]; }
+                            for (int i = 0; i < kChunk; ++i) {
+                                x0[u][i] = __ldcg(src + i * 128);
+                                x1[u][i] = __ldcg(src + (kChunk + i) * 128);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < kJoin; ++u)
+                            if (c + u <= c_last) {
+#pragma unroll
+                                for (int i = 0; i < kChunk; ++i) { v0[i] += x0[u][i]; v1[i] += x1[u][i]; }
+                            }
                     }
                 }
                 if constexpr (kMode == kGateUp) {
                     // y = w * SiLU(gate) * up, then one scale for each token's 128 values (the rows of
-                    // this block): maximum of |y| over the warp's lanes, then over the four warps
+                    // this block): maximum of |y| over the warp's lanes, then over the four warps.
+                    // Lane i of every warp works out column i's scale for the others.
+                    uint32_t* rd = red + red_at;
+                    red_at ^= 64;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float y = swiglu_value(__float_as_uint(v0[i]), __float_as_uint(v1[i])) * tok_w[c0 + i];
-                        v0[i] = tok_on[c0 + i] ? y : 0.0f;
+                    for (int i = 0; i < kChunk; ++i) {
+                        const float y = swiglu_value(__float_as_uint(v0[i]), __float_as_uint(v1[i])) * tok_w[t0 + i];
+                        v0[i] = tok_on[t0 + i] ? y : 0.0f;
                         const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v0[i]) & 0x7fffffffu);
-                        if (lane == i) red[q * 16 + i] = m;
+                        if (lane == i) rd[q * 16 + i] = m;
                     }
                     if (!esync()) { aborted = true; break; }
                     const int li = sg.tile / p.row_tiles, it = sg.tile % p.row_tiles;
-                    uint8_t* hq = p.hq + ((long long)li * BN + c0) * p.out_rows + it * 128 + row;
+                    const int lc = lane & (kChunk - 1);
+                    const uint32_t m = max(max(rd[lc], rd[16 + lc]), max(rd[32 + lc], rd[48 + lc]));
+                    const bool finite = m < 0x7f800000u;
+                    const int e = finite ? scale_exponent(__uint_as_float(m)) : 0;
+                    const float sc = finite ? pow2_neg(e) : __int_as_float(0x7fc00000);   // not finite: NaN codes
+                    if (q == 0 && lane < kChunk)
+                        p.sfh[(((long long)li * ((p.row_tiles + 3) / 4) + (it >> 2)) * BN + t0 + lane) * 4 + (it & 3)] =
+                            static_cast<uint8_t>(e + 127);
+                    uint8_t* hq = p.hq + ((long long)li * BN + t0) * p.out_rows + it * 128 + row;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t m = max(max(red[i], red[16 + i]), max(red[32 + i], red[48 + i]));
-                        const bool finite = m < 0x7f800000u;
-                        const int e = finite ? scale_exponent(__uint_as_float(m)) : 0;
-                        const uint32_t code = finite ? e4m3(v0[i] * pow2_neg(e)) : 0x7Fu;   // not finite: NaN codes
-                        hq[(long long)i * p.out_rows] = static_cast<uint8_t>(code);
-                        if (te == i)
-                            p.sfh[(((long long)li * ((p.row_tiles + 3) / 4) + (it >> 2)) * BN + c0 + i) * 4 + (it & 3)] =
-                                static_cast<uint8_t>(e + 127);
-                    }
-                    if (!esync()) { aborted = true; break; }      // red is rewritten by the next columns
-                } else if constexpr (kMode == kShrink) {
-                    // a token keeps the rows of its own adapter, scaled; each part holds what the
-                    // parts before it leave
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int r = sg.tile * 256 + b * 128 + row;
-                        const int slot = r / p.lora_rp, rr = r - slot * p.lora_rp;
-                        if (slot < nlist) {
-                            const int id = list[slot];
-                            const float sc = __ldg(p.scaling + id);
-                            uint16_t* dst = p.v + (((long long)tt0 * p.max_slots + slot) * p.parts * BN + c0) * p.lora_rp + rr;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float x = tok_id[c0 + i] == id ? sc * (b ? v1[i] : v0[i]) : 0.0f;
-                                for (int o = 0; o < p.parts; ++o) {
-                                    const __nv_bfloat16 h = __float2bfloat16(x);
-                                    dst[(long long)(o * BN + i) * p.lora_rp] = __bfloat16_as_ushort(h);
-                                    x -= __bfloat162float(h);
-                                    if (!(x == x)) x = 0.0f;       // an infinite or NaN part leaves nothing
-                                }
-                            }
-                        }
-                    }
+                    for (int i = 0; i < kChunk; ++i)
+                        hq[(long long)i * p.out_rows] = static_cast<uint8_t>(e4m3(v0[i] * __shfl_sync(0xffffffffu, sc, i)));
                 } else {
                     const int nt = min(BN, p.tokens - sg.tt * BN);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int r = sg.tile * 256 + b * 128 + row;
                         if (r < p.out_rows) {
-                            const long long at = ((long long)sg.tt * BN + c0) * p.out_rows + r;
+                            const long long at = ((long long)sg.tt * BN + t0) * p.out_rows + r;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (c0 + i >= nt) break;
+                            for (int i = 0; i < kChunk; ++i) {
+                                if (t0 + i >= nt) break;
                                 const float x = b ? v1[i] : v0[i];
                                 if (p.d_f32) static_cast<float*>(p.d)[at + (long long)i * p.out_rows] = x;
                                 else static_cast<__nv_bfloat16*>(p.d)[at + (long long)i * p.out_rows] = __float2bfloat16(x);
@@ -850,7 +812,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             if (aborted) break;
             if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
         }
-        if (kMode == kGateUp || kMode == kShrink) fence_proxy_async_global();
+        if (kMode == kGateUp) fence_proxy_async_global();
     }
     tc_fence_before();
     __syncthreads();
