@@ -277,7 +277,6 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
     p.parts = parts; p.unit_cols = unit_cols;
     p.slot_ids = sp.slot_ids;
     p.slot_count = sp.slot_count;
-    p.min_units = 4;
     p.status = st.status; p.timeout_ns = st.timeout_ns; p.pdl = st.pdl;
     fg::StreamMaps m;
     std::memset(&m, 0, sizeof(m));

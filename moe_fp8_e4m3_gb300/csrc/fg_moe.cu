@@ -67,7 +67,6 @@ int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t
     p.ids = ids; p.weights = weights;
     p.hq = ws + l.hq; p.sfh = ws + l.sfh;
     p.part = reinterpret_cast<float*>(ws + l.part);
-    p.min_units = 4;
     p.status = st.status; p.timeout_ns = st.timeout_ns; p.pdl = st.pdl; p.debug_stall = st.debug_stall;
     fg::StreamMaps m;
     std::memset(&m, 0, sizeof(m));

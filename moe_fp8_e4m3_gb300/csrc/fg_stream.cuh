@@ -15,7 +15,8 @@
 // tile cut by a share's border is accumulated by several CTAs: each writes its FP32 partial
 // to the workspace and counts itself in; the one that arrives last adds the partials up in
 // CTA order (so the result does not depend on which came last) and finishes the tile.  No
-// CTA ever waits for another.  The counters wrap to zero by themselves (atomicInc).
+// CTA ever waits for another.  The counters wrap to zero by themselves (atomicInc).  Where the
+// tiles fit the SMs, whole tiles or equal pieces of each are dealt instead (plan_shares).
 //
 // Modes
 //   kGateUp  tile = 128 gate rows + the 128 up rows of one expert; epilogue: SiLU(gate) * up *
@@ -78,7 +79,6 @@ struct StreamParams {
     int parts, unit_cols;        // BF16 parts of x @ A^T; rank columns of a unit
     const int* slot_ids;         // [token tile][max_slots] distinct adapters, ascending
     const int* slot_count;       // [token tile]
-    int min_units;               // least units of a share
     int* status;
     unsigned long long timeout_ns;
     int debug_stall, pdl;
@@ -127,6 +127,7 @@ struct StreamCfg {
     static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
     static constexpr int kThreads = 512;
     static constexpr int kChunk = BN >= 32 ? 16 : 8;                        // token columns an epilogue group takes at a time
+    static constexpr int kChunks = BN / 2 / kChunk;                         // of a group
     static constexpr int kJoin = 32 / kChunk;                               // partials it loads at a time
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
@@ -153,15 +154,60 @@ struct StreamSeg {
 
 struct StreamPlan {
     int units, shares, nk, row_tiles;
+    int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares
+    int q, r;            // equal shares: r shares of q + 1 units, then shares of q
     const int* pre;      // kProj: units before each token tile
 };
 
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
-    return static_cast<int>((long long)c * pl.units / pl.shares);
+    if (pl.pieces) {
+        const int t = c / pl.pieces;
+        return t * pl.nk + (c - t * pl.pieces) * pl.nk / pl.pieces;
+    }
+    return c * pl.q + min(c, pl.r);
 }
-// The share that unit u belongs to: the last c with share_begin(c) <= u.
-__device__ __forceinline__ int share_of(const StreamPlan& pl, int u) {
-    return static_cast<int>((((long long)u + 1) * pl.shares - 1) / pl.units);
+// The first and the last share of the tile of units [u0, u0 + nk).
+__device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, int& first, int& last) {
+    if (pl.pieces) {
+        first = u0 / pl.nk * pl.pieces;
+        last = first + pl.pieces - 1;
+        return;
+    }
+    auto of = [&](int u) {
+        const int big = (pl.q + 1) * pl.r;
+        return u < big ? u / (pl.q + 1) : pl.r + (u - big) / pl.q;
+    };
+    first = of(u0);
+    last = of(u0 + nk - 1);
+}
+
+// How `tiles` tiles of nk units each become shares for at most `grid` CTAs: s pieces per tile
+// (s = 1: no cut), where all pieces find a CTA, or equal shares cut anywhere.  A tile's time is
+// the larger of a CTA's units at the pace of its MMA issuers and all units at HBM's, plus the join
+// of a cut tile: counting in (~2.2 us) and reading the n partials, kJoin at a time per chunk
+// (~0.9 us each); equal shares cut a tile at both ends of a share.  Measured on GB300: a unit
+// takes an SM 0.35 us when HBM keeps up, all SMs together 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM.
+__device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int join,
+                                            bool even_ok) {
+    const float hbm = pl.units * (fp4 ? 0.0025f : 0.00475f);
+    auto joined = [&](int n) { return n > 1 ? 2.2f + 0.9f * ((n + join - 1) / join) * chunks : 0.0f; };
+    const int per = (pl.units + grid - 1) / grid;
+    const int n = per > 0 ? (pl.nk + per - 1) / per + 1 : 1;
+    float best = fmaxf(per * 0.35f, hbm) + 2.0f * joined(n);
+    pl.shares = min(grid, pl.units);
+    pl.pieces = 0;
+    if (even_ok)
+        for (int s = 1; s * tiles <= grid && s <= pl.nk && s <= 16; ++s) {
+            const float t = fmaxf((pl.nk + s - 1) / s * 0.35f, hbm) + joined(s);
+            if (t < best) {
+                best = t;
+                pl.pieces = s;
+                pl.shares = s * tiles;
+            }
+        }
+    if (pl.shares < 1) pl.shares = 1;
+    pl.q = pl.units / pl.shares;
+    pl.r = pl.units - pl.q * pl.shares;
 }
 
 template <int kMode>
@@ -355,7 +401,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     auto adapter_of = [&](int tt, int slot) { return one_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
     pl.row_tiles = p.row_tiles;
     pl.pre = pre;
-    pl.shares = max(1, min(static_cast<int>(gridDim.x), (pl.units + p.min_units - 1) / p.min_units));
+    const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
+    if (one_tile) pl.nk = pl.units / p.row_tiles;
+    plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, C::kJoin, kMoe || one_tile);
     const int share = static_cast<int>(blockIdx.x);
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
@@ -551,7 +599,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         // words are asked into L2 kAhead units early: a unit's words are a few short pieces of
         // the array, which come from HBM later than the unit's weight tile would.
         constexpr int kAhead = C::kStages + 6;
-        if (kMode == kDown) grid_dependency_wait();
         const uint32_t par = warp == 8 ? 0u : 1u;
         int s = 0;
         uint32_t ph = 0, n = 0;
@@ -572,6 +619,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         };
         for (int i = 0; i < kAhead && ahead.valid; ++i, ahead.step(pl))
             if ((static_cast<uint32_t>(i) & 1u) == par) prefetch();
+        if (kMode == kDown) grid_dependency_wait();
         for (; c.valid; c.step(pl), ++n) {
             if ((n & 1u) == par) {
                 const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
@@ -716,8 +764,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 release();
                 __threadfence();
                 if (!esync()) { aborted = true; break; }
-                c_first = share_of(pl, sg.first_unit);
-                c_last = share_of(pl, sg.first_unit + sg.nk - 1);
+                shares_of(pl, sg.first_unit, sg.nk, c_first, c_last);
                 if (te == 0) {
                     // only the last tile that begins in a share goes on into the next one, so a cut
                     // tile is told by its first share; the count wraps to 0 with the last arrival
