@@ -109,6 +109,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
+// True in one lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 // Orders generic-proxy global writes (the codes that the next kernel loads by TMA).
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
@@ -303,7 +309,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the warp's number from a shuffle and the plan's below: what follows is uniform over a warp
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t bar0 = sbase + C::kOffBar;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
@@ -399,13 +406,16 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     }
     auto slots_of = [&](int tt) { return one_tile ? nlist : __ldcg(p.slot_count + tt); };
     auto adapter_of = [&](int tt, int slot) { return one_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
+    pl.units = __shfl_sync(0xffffffffu, pl.units, 0);
+    nlist = __shfl_sync(0xffffffffu, nlist, 0);
+    pl.nk = __shfl_sync(0xffffffffu, pl.nk, 0);
     pl.row_tiles = p.row_tiles;
     pl.pre = pre;
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
     plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, C::kJoin, kMoe || one_tile);
     const int share = static_cast<int>(blockIdx.x);
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
     // kProj: adapter units behind the K-groups
     const int ucols = min(p.lora_rp, p.unit_cols), rb = ucols * 2;           // rank columns of an adapter in a unit, bytes
@@ -508,7 +518,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         // One for each 128-row block of the tile: a thread needs ~80 clocks to issue a
         // tcgen05.mma, so one issuer's eight per unit (~0.45 us with the waits) would pace the
         // FP4 weights, whose unit takes HBM 0.38 us.
-        if (lane == 0) {
+        {
             const int blk = warp == 1 ? 0 : 1;
             constexpr uint32_t kIdesc = make_idesc_stream(BN, kFp4);
             constexpr uint32_t kIdescBf16 = make_idesc_bf16(128, BN);
@@ -520,72 +530,86 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             const uint64_t b0 = make_sdesc(sbase + C::kOffB, 0, 1024, kLayoutSw128);
             const uint64_t w0 = make_sdesc(sbase + C::kOffSf + 512 * blk, 0, 128, kLayoutNone);
             const uint64_t t0w = make_sdesc(sbase + C::kOffSf + 1024, 0, 128, kLayoutNone);
+            // adapter units: an adapter's rows are rb bytes long, swizzled over as many
+            const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
+            const uint64_t la0 = make_sdesc(sbase + blk * 128 * rb, 0, 8 * rb, layout);
+            const uint64_t lb0 = make_sdesc(sbase + C::kOffB, 0, 8 * rb, layout);
             int s = 0, acc = 0;
             uint32_t ph = 0, acc_ph = 0, kcount = 0, turn_ph = 0;
             bool aborted = false;
+            auto wait_all = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait_bar(bar, parity, wctl, kWaitMma)) != 0;
+            };
             StreamWalk<kMode> walk(pl, share);
             StreamSeg sg;
             while (!aborted && walk.next(pl, sg)) {
-                if (!wait_bar(acce_bar(acc), acc_ph ^ 1u, wctl, kWaitMma)) { aborted = true; break; }
+                if (!wait_all(acce_bar(acc), acc_ph ^ 1u)) { aborted = true; break; }
                 tc_fence_after();
                 const uint32_t dt = tmem_base + (acc * 2 + blk) * BN;
                 uint32_t add = 0;                     // 0: the first product of the segment overwrites
                 int kl = kMode == kDown ? sg.k0 % p.nk : sg.k0;      // K-group (kDown: within the expert)
                 for (int k = sg.k0; k < sg.k1; ++k) {
-                    if (!wait_bar(full_bar(s), ph, wctl, kWaitMma)) { aborted = true; break; }
+                    if (!wait_all(full_bar(s), ph)) { aborted = true; break; }
                     tc_fence_after();
                     const uint64_t ad = a0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
                     const uint64_t bd = b0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
                     if (kMode == kProj && k >= p.nk) {
                         if (k == p.nk && add) {
                             // let the scaled FP8 products finish before another kind adds to their sums
-                            tc_commit(turn_of(blk));
-                            if (!wait_bar(turn_of(blk), turn_ph, wctl, kWaitMma)) { aborted = true; break; }
+                            if (elect_one()) tc_commit(turn_of(blk));
+                            __syncwarp();
+                            if (!wait_all(turn_of(blk), turn_ph)) { aborted = true; break; }
                             turn_ph ^= 1u;
                             tc_fence_after();
                         }
                         const int u = k - p.nk;
                         const int nslots = slots_of(sg.tt);
                         const int cnt = pieces > 1 ? 1 : min(per_unit, nslots - u * per_unit);
-                        const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
-                        const uint32_t sa = sbase + s * C::kABytes + blk * 128 * rb, sb = sbase + C::kOffB + s * C::kBBytes;
-                        for (int j = 0; j < cnt; ++j) {
-                            const uint64_t aj = make_sdesc(sa + j * 256 * rb, 0, 8 * rb, layout);
-                            const uint64_t bj = make_sdesc(sb + j * p.parts * BN * rb, 0, 8 * rb, layout);
-                            const uint32_t part = static_cast<uint32_t>(BN * rb) >> 4;
-                            for (int c = 0; c < rb / 32; ++c)
-                                for (int o = 0; o < p.parts; ++o) {
-                                    tc_mma_bf16(dt, aj + 2 * c, bj + o * part + 2 * c, kIdescBf16, add);
-                                    add = 1;
-                                }
+                        if (elect_one()) {
+                            uint64_t aj = la0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
+                            uint64_t bj = lb0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
+                            uint32_t keep = add;
+                            for (int i = 0; i < cnt; ++i, aj += 16 * rb)
+                                for (int o = 0; o < p.parts; ++o, bj += BN / 16 * rb)
+                                    for (int c = 0; c < rb / 32; ++c) {
+                                        tc_mma_bf16(dt, aj + 2 * c, bj + 2 * c, kIdescBf16, keep);
+                                        keep = 1;
+                                    }
+                            tc_commit(empty_bar(s));
                         }
+                        add = 1;
                     } else {
                         const uint32_t sf_id = static_cast<uint32_t>(kl) & 3u;
-                        if (kFp4 || k == sg.k0 || sf_id == 0) {
-                            ++kcount;
-                            const uint32_t t = sf0 + (kcount % kSfSlots) * 16;
-                            const uint32_t so = static_cast<uint32_t>(s * C::kSfBytes) >> 4;
-                            fence_proxy_async_smem();   // scale words written by cp.async
-                            tc_cp_32x128b_warpx4(t, w0 + so);
-                            tc_cp_32x128b_warpx4(t + 4, t0w + so);
-                        }
+                        const bool words = kFp4 || k == sg.k0 || sf_id == 0;
+                        if (words) ++kcount;
                         const uint32_t t = sf0 + (kcount % kSfSlots) * 16;
+                        if (elect_one()) {
+                            if (words) {
+                                const uint32_t so = static_cast<uint32_t>(s * C::kSfBytes) >> 4;
+                                fence_proxy_async_smem();   // scale words written by cp.async
+                                tc_cp_32x128b_warpx4(t, w0 + so);
+                                tc_cp_32x128b_warpx4(t + 4, t0w + so);
+                            }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t idesc = idesc_sf_ids(kIdesc, kFp4 ? static_cast<uint32_t>(j) : sf_id, sf_id);
-                            tc_mma_mxf8(dt, ad + 2 * j, bd + 2 * j, idesc, t, t + 4, add);
-                            add = 1;
+                            for (int j = 0; j < 4; ++j)
+                                tc_mma_mxf8(dt, ad + 2 * j, bd + 2 * j,
+                                            idesc_sf_ids(kIdesc, kFp4 ? static_cast<uint32_t>(j) : sf_id, sf_id), t, t + 4,
+                                            j ? 1u : add);
+                            tc_commit(empty_bar(s));
                         }
+                        add = 1;
                     }
-                    tc_commit(empty_bar(s));
+                    __syncwarp();
                     if (++s == C::kStages) { s = 0; ph ^= 1u; }
                     if (++kl == p.nk && kMode == kDown) kl = 0;
                 }
                 if (aborted) break;
-                tc_commit(accf_bar(acc));
+                if (elect_one()) tc_commit(accf_bar(acc));
+                __syncwarp();
                 if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
             }
-            tc_commit(drain_of(blk));
+            if (elect_one()) tc_commit(drain_of(blk));
+            __syncwarp();
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(drain_of(blk), 0)) {
                 if (globaltimer_ns() - t0 > p.timeout_ns) { record_status(p.status, kErrTimeout | kWaitDrain); break; }
