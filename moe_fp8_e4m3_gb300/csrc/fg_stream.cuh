@@ -115,6 +115,33 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
+// Bulk copy of [src, src + bytes) to shared memory (16-byte aligned, bytes a multiple of 16).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// Maximum over the warp's lanes of each of C columns (C = 8 or 16 values per lane): halves of the
+// columns are exchanged until a lane holds one column, then its copies are joined.  Returns the
+// maximum of column_of<C>(lane).
+template <int C>
+__device__ __forceinline__ uint32_t column_max(uint32_t (&m)[C], int lane) {
+    int o = 16;
+#pragma unroll
+    for (int n = C / 2; n >= 1; n /= 2, o /= 2) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + n], o);
+            m[i] = max(up ? m[i + n] : m[i], got);
+        }
+    }
+    for (; o >= 1; o /= 2) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    return m[0];
+}
+template <int C>
+__device__ __forceinline__ int column_of(int lane) {
+    return lane / (32 / C);          // the lane bits from the top choose the halves in turn
+}
 // Orders generic-proxy global writes (the codes that the next kernel loads by TMA).
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
@@ -132,13 +159,16 @@ struct StreamCfg {
     static constexpr int kSfCol0 = kNumAcc * 2 * BN;
     static constexpr int kTmemCols = kSfCol0 + 64 <= 128 ? 128 : (kSfCol0 + 64 <= 256 ? 256 : 512);
     static constexpr int kThreads = 512;
+    // join of a share's last tile: partials through the idle ring, kJoinSlots pieces per group
     static constexpr int kChunk = BN >= 32 ? 16 : 8;                        // token columns an epilogue group takes at a time
     static constexpr int kChunks = BN / 2 / kChunk;                         // of a group
     static constexpr int kJoin = 32 / kChunk;                               // partials it loads at a time
+    static constexpr int kPieceBytes = kChunk * 2 * 128 * 4;                // a chunk of one partial
+    static constexpr int kJoinSlots = kStages * kABytes / 2 / kPieceBytes > 10 ? 10 : kStages * kABytes / 2 / kPieceBytes;
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
     static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 6;
+    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 4 + 2 * kJoinSlots;
     static constexpr int kOffMisc = kOffBar + 512 - 64;                     // TMEM address, abort flag, count, last flag
     static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
     static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
@@ -216,33 +246,53 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
     pl.r = pl.units - pl.q * pl.shares;
 }
 
+// The pieces of one share: first the tile that goes on into the next share, then the others in
+// order (so a tile that the share before began comes next, whole tiles last).  A cut tile's parts
+// are then the first thing its shares do, and joining them hides behind the whole tiles.
 template <int kMode>
 struct StreamWalk {
-    int u, end, tt;
-    __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share) : u(0), end(0), tt(0) {
-        if (share < pl.shares) {
-            u = share_begin(pl, share);
-            end = share_begin(pl, share + 1);
-        }
+    int u, end, tail, tail_end, tt;      // [u, end) is left; before it [tail, tail_end) if tail >= 0
+    __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share) : u(0), end(0), tail(-1), tail_end(0), tt(0) {
+        if (share >= pl.shares) return;
+        u = share_begin(pl, share);
+        end = tail_end = share_begin(pl, share + 1);
+        StreamSeg s;
+        locate(pl, end - 1, s);
+        tt = 0;
+        if (s.first_unit + s.nk != end && s.first_unit > u) end = tail = s.first_unit;
     }
-    __device__ __forceinline__ bool next(const StreamPlan& pl, StreamSeg& s) {
-        if (u >= end) return false;
+    // the tile of unit v (token tiles are searched from tt on)
+    __device__ __forceinline__ void locate(const StreamPlan& pl, int v, StreamSeg& s) {
         int base = 0;
         s.nk = pl.nk;
         if (kMode == kProj) {
-            while (u >= pl.pre[tt + 1]) ++tt;
+            while (v >= pl.pre[tt + 1]) ++tt;
             base = pl.pre[tt];
             s.nk = (pl.pre[tt + 1] - base) / pl.row_tiles;
         }
         s.tt = tt;
-        s.tile = (u - base) / s.nk;
+        s.tile = (v - base) / s.nk;
         s.first_unit = base + s.tile * s.nk;
+    }
+    __device__ __forceinline__ bool next(const StreamPlan& pl, StreamSeg& s) {
+        if (tail >= 0) {
+            locate(pl, tail, s);
+            tt = 0;
+            s.k0 = 0;
+            s.k1 = tail_end - tail;
+            s.whole = false;
+            tail = -1;
+            return true;
+        }
+        if (u >= end) return false;
+        locate(pl, u, s);
         s.k0 = u - s.first_unit;
         s.k1 = min(s.nk, s.k0 + (end - u));
         s.whole = s.k0 == 0 && s.k1 == s.nk;
         u += s.k1 - s.k0;
         return true;
     }
+    __device__ __forceinline__ bool done() const { return tail < 0 && u >= end; }
 };
 
 // Walks a share unit by unit.  li, kl: kDown's expert (list index) and K-group within it (else
@@ -319,13 +369,14 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     // per issuer: its MMAs done, on the way out and before products of another kind
     auto drain_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + b); };
     auto turn_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 2 + b); };
-    auto esync_bar = [&](int g) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g); };   // an epilogue group
+    // a group's pieces of partials on their way into the ring
+    auto join_bar = [&](int g, int i) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g * C::kJoinSlots + i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     int* listed = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [2]
-    float* tok_w = reinterpret_cast<float*>(smem + C::kOffTok);               // routing weight of the tile's expert
-    int* tok_on = reinterpret_cast<int*>(tok_w + BN);                         // the token uses the tile's expert
+    // per token: routing weight of the tile's expert, 1 where the token uses it
+    float2* tok = reinterpret_cast<float2*>(smem + C::kOffTok);
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::kOffBits);
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
     int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
@@ -342,7 +393,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         for (int b = 0; b < 2; ++b) {
             mbar_init(drain_of(b), 1);
             mbar_init(turn_of(b), 1);
-            mbar_init(esync_bar(b), 4);
+            for (int i = 0; i < C::kJoinSlots; ++i) mbar_init(join_bar(b, i), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -569,12 +620,22 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             uint64_t aj = la0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
                             uint64_t bj = lb0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
                             uint32_t keep = add;
-                            for (int i = 0; i < cnt; ++i, aj += 16 * rb)
-                                for (int o = 0; o < p.parts; ++o, bj += BN / 16 * rb)
-                                    for (int c = 0; c < rb / 32; ++c) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i >= cnt) break;
+#pragma unroll
+                                for (int o = 0; o < 3; ++o) {
+                                    if (o >= p.parts) break;
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        if (c >= rb / 32) break;
                                         tc_mma_bf16(dt, aj + 2 * c, bj + 2 * c, kIdescBf16, keep);
                                         keep = 1;
                                     }
+                                    bj += BN / 16 * rb;
+                                }
+                                aj += 16 * rb;
+                            }
                             tc_commit(empty_bar(s));
                         }
                         add = 1;
@@ -700,14 +761,15 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 else static_cast<__nv_bfloat16*>(p.d)[i] = __float2bfloat16(0.0f);
             }
         }
-        uint32_t e_ph = 0;
-        // the group's four warps, bounded like every wait (a warp that gave up never arrives)
-        auto esync = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(esync_bar(grp));
-            const bool ok = wait_bar(esync_bar(grp), e_ph, wctl, kWaitEpilogueSync);
-            e_ph ^= 1u;
-            return __all_sync(0xffffffffu, ok) != 0;
+        // The group's four warps.  Whether to give up is voted once per tile, so all four take the
+        // same path and every barrier below is reached by all of them.
+        auto esync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
+        auto evote = [&](bool ok) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(r) : "r"(ok ? 1u : 0u), "r"(1 + grp) : "memory");
+            return r != 0;
         };
         uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kOffRed) + grp * 128;
         int red_at = 0;                                                // alternates: one wait per chunk
@@ -716,17 +778,15 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         const int my_part = grp * 2 * kHalf * 128 + row;
         int acc = 0;
         uint32_t acc_ph = 0;
-        bool aborted = false;
         StreamWalk<kMode> walk(pl, share);
         StreamSeg sg;
-        while (!aborted && walk.next(pl, sg)) {
+        while (walk.next(pl, sg)) {
             if constexpr (kMode == kGateUp) {
                 // the tile's routing weights, while its weights stream
                 const int expert = p.expert_base + list[sg.tile / p.row_tiles];
                 if (te < kHalf) {
                     const int t = grp * kHalf + te;
-                    float w = 0.0f;
-                    int on = 0;
+                    float w = 0.0f, on = 0.0f;
                     if (t < p.tokens) {
                         const int32_t* ids = p.ids + (long long)t * p.topk;
                         const float* weights = p.weights + (long long)t * p.topk;
@@ -741,17 +801,16 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             }
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                if (id[j] == expert && j0 + j < p.topk) { w += x[j]; on = 1; }
+                                if (id[j] == expert && j0 + j < p.topk) { w += x[j]; on = 1.0f; }
                         }
                     }
-                    tok_w[t] = w;
-                    tok_on[t] = on;
+                    tok[t] = make_float2(w, on);
                 }
-                if (!esync()) break;
             }
-            const bool ok = wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!evote(wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue))) break;
             tc_fence_after();
+            // token columns of this group that exist
+            const int cols = min(kHalf, min(BN, p.tokens - sg.tt * BN) - grp * kHalf);
             const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * BN + grp * kHalf;
             auto release = [&]() {
                 tc_fence_before();
@@ -776,51 +835,95 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             if (!sg.whole) {
                 // this share's part of the tile: 0 where the tile began in an earlier share, else 1
                 float* mine = p.part + (2LL * share + (sg.k0 > 0 ? 0 : 1)) * part_tile + my_part;
-                for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
+                for (int c0 = 0; c0 < cols; c0 += kChunk) {
                     float v0[kChunk], v1[kChunk];
                     load_acc(c0, v0, v1);
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) {
+                        if (c0 + i >= cols) break;
                         __stcg(mine + (2 * c0 + i) * 128, v0[i]);
                         __stcg(mine + (2 * c0 + kChunk + i) * 128, v1[i]);
                     }
                 }
                 release();
-                __threadfence();
-                if (!esync()) { aborted = true; break; }
+                if (cols <= 0) {
+                    if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
+                    continue;
+                }
                 shares_of(pl, sg.first_unit, sg.nk, c_first, c_last);
+                esync();
                 if (te == 0) {
                     // only the last tile that begins in a share goes on into the next one, so a cut
                     // tile is told by its first share; the count wraps to 0 with the last arrival
                     const unsigned n = static_cast<unsigned>(c_last - c_first);
+                    __threadfence();                     // this group's stores, ordered by the barrier
                     last_flag[grp] = atomicInc(p.ctr + 2 * c_first + grp, n) == n;
+                    __threadfence();
                 }
-                if (!esync()) { aborted = true; break; }
-                const bool last = last_flag[grp] != 0;
-                __threadfence();
-                if (!last) {
+                esync();
+                if (!last_flag[grp]) {
                     if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
                     continue;
                 }
             }
             // ---- finish the tile
-            for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
+            // Partials of the share's last tile come through the ring, idle by now (this tile's
+            // products were its last): pieces (chunk, share) in order, kJoinSlots in flight.  Those of
+            // an earlier tile, joined while others stream, come into registers.
+            const bool by_ring = !sg.whole && walk.done();
+            const int n_parts = c_last - c_first + 1;
+            const int pieces_all = by_ring ? (cols + kChunk - 1) / kChunk * n_parts : 0;
+            const uint32_t jbuf = sbase + grp * C::kJoinSlots * C::kPieceBytes;
+            const float* jsmem = reinterpret_cast<const float*>(smem + grp * C::kJoinSlots * C::kPieceBytes);
+            auto part_of = [&](int c) {
+                return p.part + (2LL * c + (share_begin(pl, c) > sg.first_unit ? 0 : 1)) * part_tile + grp * 2 * kHalf * 128;
+            };
+            int fetched = 0;
+            auto fetch = [&](int i) {                    // piece i of the join; one thread
+                ++fetched;
+                const int ch = i / n_parts, slot = i % C::kJoinSlots;
+                mbar_arrive_expect_tx(join_bar(grp, slot), C::kPieceBytes);
+                bulk_load(jbuf + slot * C::kPieceBytes, part_of(c_first + i - ch * n_parts) + ch * 2 * kChunk * 128,
+                          C::kPieceBytes, join_bar(grp, slot));
+            };
+            if (by_ring && te == 0) {
+                fence_proxy_async_global();
+                for (int i = 0; i < min(pieces_all, C::kJoinSlots); ++i) fetch(i);
+            }
+            int piece = 0;
+            bool lost = false;
+            for (int c0 = 0; c0 < cols; c0 += kChunk) {
                 const int t0 = grp * kHalf + c0;                       // first token column
                 float v0[kChunk], v1[kChunk];
                 if (sg.whole) {
                     load_acc(c0, v0, v1);
-                    if (c0 + kChunk == kHalf) release();
+                    if (c0 + kChunk >= cols) release();
+                } else if (by_ring) {
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.0f;
+                    for (int c = 0; c < n_parts; ++c, ++piece) {
+                        const int slot = piece % C::kJoinSlots;
+                        if (!wait_bar(join_bar(grp, slot), (piece / C::kJoinSlots) & 1, wctl, kWaitExchange)) lost = true;
+                        const float* src = jsmem + slot * (C::kPieceBytes / 4) + row;
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            v0[i] += src[i * 128];
+                            v1[i] += src[(kChunk + i) * 128];
+                        }
+                        if (piece + C::kJoinSlots < pieces_all) {
+                            esync();                                   // the slot is free
+                            if (te == 0 && !lost) fetch(piece + C::kJoinSlots);
+                        }
+                    }
                 } else {
-                    // the partials in CTA order, kJoin of them in flight
+                    // the partials in share order, kJoin of them in flight
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.0f;
                     for (int c = c_first; c <= c_last; c += kJoin) {
                         float x0[kJoin][kChunk], x1[kJoin][kChunk];
 #pragma unroll
                         for (int u = 0; u < kJoin; ++u) {
-                            const int cc = min(c + u, c_last);
-                            const int slot = share_begin(pl, cc) > sg.first_unit ? 0 : 1;
-                            const float* src = p.part + (2LL * cc + slot) * part_tile + my_part + 2 * c0 * 128;
+                            const float* src = part_of(min(c + u, c_last)) + 2 * c0 * 128 + row;
 #pragma unroll
                             for (int i = 0; i < kChunk; ++i) {
                                 x0[u][i] = __ldcg(src + i * 128);
@@ -841,29 +944,33 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     // Lane i of every warp works out column i's scale for the others.
                     uint32_t* rd = red + red_at;
                     red_at ^= 64;
+                    uint32_t m[kChunk];
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) {
-                        const float y = swiglu_value(__float_as_uint(v0[i]), __float_as_uint(v1[i])) * tok_w[t0 + i];
-                        v0[i] = tok_on[t0 + i] ? y : 0.0f;
-                        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v0[i]) & 0x7fffffffu);
-                        if (lane == i) rd[q * 16 + i] = m;
+                        const float2 w = tok[t0 + i];
+                        const float y = swiglu_value(__float_as_uint(v0[i]), __float_as_uint(v1[i])) * w.x;
+                        v0[i] = w.y != 0.0f ? y : 0.0f;
+                        m[i] = __float_as_uint(v0[i]) & 0x7fffffffu;
                     }
-                    if (!esync()) { aborted = true; break; }
+                    const uint32_t top = column_max<kChunk>(m, lane);
+                    if ((lane & (32 / kChunk - 1)) == 0) rd[q * 16 + column_of<kChunk>(lane)] = top;
+                    esync();
                     const int li = sg.tile / p.row_tiles, it = sg.tile % p.row_tiles;
                     const int lc = lane & (kChunk - 1);
-                    const uint32_t m = max(max(rd[lc], rd[16 + lc]), max(rd[32 + lc], rd[48 + lc]));
-                    const bool finite = m < 0x7f800000u;
-                    const int e = finite ? scale_exponent(__uint_as_float(m)) : 0;
+                    const uint32_t all = max(max(rd[lc], rd[16 + lc]), max(rd[32 + lc], rd[48 + lc]));
+                    const bool finite = all < 0x7f800000u;
+                    const int e = finite ? scale_exponent(__uint_as_float(all)) : 0;
                     const float sc = finite ? pow2_neg(e) : __int_as_float(0x7fc00000);   // not finite: NaN codes
-                    if (q == 0 && lane < kChunk)
+                    if (q == 0 && lane < kChunk && c0 + lane < cols)
                         p.sfh[(((long long)li * ((p.row_tiles + 3) / 4) + (it >> 2)) * BN + t0 + lane) * 4 + (it & 3)] =
                             static_cast<uint8_t>(e + 127);
                     uint8_t* hq = p.hq + ((long long)li * BN + t0) * p.out_rows + it * 128 + row;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i)
-                        hq[(long long)i * p.out_rows] = static_cast<uint8_t>(e4m3(v0[i] * __shfl_sync(0xffffffffu, sc, i)));
+                    for (int i = 0; i < kChunk; ++i) {
+                        const float x = v0[i] * __shfl_sync(0xffffffffu, sc, i);
+                        if (c0 + i < cols) hq[(long long)i * p.out_rows] = static_cast<uint8_t>(e4m3(x));
+                    }
                 } else {
-                    const int nt = min(BN, p.tokens - sg.tt * BN);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int r = sg.tile * 256 + b * 128 + row;
@@ -871,7 +978,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             const long long at = ((long long)sg.tt * BN + t0) * p.out_rows + r;
 #pragma unroll
                             for (int i = 0; i < kChunk; ++i) {
-                                if (t0 + i >= nt) break;
+                                if (c0 + i >= cols) break;
                                 const float x = b ? v1[i] : v0[i];
                                 if (p.d_f32) static_cast<float*>(p.d)[at + (long long)i * p.out_rows] = x;
                                 else static_cast<__nv_bfloat16*>(p.d)[at + (long long)i * p.out_rows] = __float2bfloat16(x);
@@ -880,7 +987,11 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     }
                 }
             }
-            if (aborted) break;
+            if (sg.whole && cols <= 0) release();
+            if (lost && te == 0)       // pieces that may still be landing
+                for (int i = max(0, fetched - C::kJoinSlots); i < fetched; ++i)
+                    drain_bar(join_bar(grp, i % C::kJoinSlots), (i / C::kJoinSlots) & 1, 20000000ull);
+            if (!evote(!lost)) break;
             if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
         }
         if (kMode == kGateUp) fence_proxy_async_global();
