@@ -97,9 +97,10 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+        # the handle of torch.cuda.current_stream(), without making a Stream object (2.8 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -361,23 +362,50 @@ def quantize_1x128_cols(x, q, sf, stream=None) -> None:
            "quantize_1x128_cols")
 
 
+_SCORES = {"softmax": FG_SCORE_SOFTMAX, "sigmoid": FG_SCORE_SIGMOID}
+_DTYPES = {}
+
+
+def _dtypes():
+    """Dtypes by the letter that _check_all takes, looked up once."""
+    import torch
+    _DTYPES.update(q={torch.uint8, torch.float8_e4m3fn}, i={torch.int32}, f={torch.float32}, b={torch.bfloat16},
+                   p={torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)}, o={torch.bfloat16, torch.float32})
+    return _DTYPES
+
+
+_NAMES = {"q": "uint8/float8_e4m3fn", "i": "int32", "f": "float32", "b": "bfloat16", "p": "uint8/float4_e2m1fn_x2 (packed E2M1)",
+          "o": "bfloat16/float32"}
+
+
+def _check_all(*args):
+    """(tensor, name, letter) triples in a row: contiguous CUDA tensors of the letter's dtype.  A
+    decode step's calls are short, so their checks are one pass (0.2 us a tensor)."""
+    kinds = _DTYPES or _dtypes()
+    for k in range(0, len(args), 3):
+        t = args[k]
+        if t.dtype not in kinds[args[k + 2]] or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{args[k + 1]} must be a contiguous CUDA {_NAMES[args[k + 2]]} tensor")
+
+
 def moe_route(logits, topk_ids, topk_weights, bias=None, score="softmax", n_group=1, topk_group=1,
               renormalize=True, scale=1.0, stream=None) -> None:
     """MoE router.  logits float32 [T,E]; topk_ids int32 [T,topk] and topk_weights float32
     [T,topk] (out); bias float32 [E] added to the scores for the choice only; score "softmax" or
     "sigmoid"; the choice is limited to the topk_group best of n_group groups of experts."""
-    _f32(logits, "logits"); _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
-    if bias is not None:
-        _f32(bias, "bias")
-    if score not in ("softmax", "sigmoid"):
-        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    _check_all(logits, "logits", "f", topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f")
     t, e = logits.shape
-    topk = topk_ids.shape[1]
-    if topk_ids.shape[0] != t or topk_weights.shape != topk_ids.shape or (bias is not None and bias.numel() != e):
-        raise ValueError("topk_ids and topk_weights must be [T, topk], bias [E]")
-    _check(lib.fg_moe_route(t, e, topk, n_group, topk_group,
-                            FG_SCORE_SIGMOID if score == "sigmoid" else FG_SCORE_SOFTMAX, 1 if renormalize else 0,
-                            scale, _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights), _stream(stream)),
+    shape = topk_ids.shape
+    if bias is not None:
+        _check_all(bias, "bias", "f")
+        if bias.numel() != e:
+            raise ValueError("bias must be [E]")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if len(shape) != 2 or shape[0] != t or topk_weights.shape != shape:
+        raise ValueError("topk_ids and topk_weights must be [T, topk]")
+    _check(lib.fg_moe_route(t, e, shape[1], n_group, topk_group, _SCORES[score], 1 if renormalize else 0, scale,
+                            logits.data_ptr(), _ptr(bias), topk_ids.data_ptr(), topk_weights.data_ptr(), _stream(stream)),
            "moe_route")
 
 
@@ -393,19 +421,23 @@ def moe_mlp_workspace(t, h, i, e, device="cuda"):
     return _workspace(lib.fg_moe_mlp_workspace(t, h, i, e), device, "moe_mlp_workspace")
 
 
-def _moe_mlp(fn, name, weight, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base, stream):
-    _fp8(a, "a"); weight(w13, "w13"); weight(w2, "w2"); _i32(sfa, "sfa"); _i32(sf13, "sf13"); _i32(sf2, "sf2")
-    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
-    code = _out(d, "d")
+def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base, stream):
+    _check_all(a, "a", "q", sfa, "sfa", "i", w13, "w13", letter, sf13, "sf13", "i", w2, "w2", letter, sf2, "sf2", "i",
+               topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f", d, "d", "o")
     t, h = a.shape
-    e, i = w13.shape[0], w13.shape[1] // 2
-    topk = topk_ids.shape[1]
-    if w2.shape[:2] != (e, h) or topk_ids.shape[0] != t or topk_weights.shape != topk_ids.shape or d.shape != a.shape:
+    e, i2, _ = w13.shape
+    i = i2 // 2
+    ids = topk_ids.shape
+    e2, h2, _ = w2.shape
+    if e2 != e or h2 != h or len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape:
         raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I], topk_ids and topk_weights [T,topk]")
-    if not workspace.is_cuda or workspace.numel() < lib.fg_moe_mlp_workspace(t, h, i, e):
+    if not workspace.is_cuda or workspace.nbytes < lib.fg_moe_mlp_workspace(t, h, i, e):
         raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
-    _check(fn(t, h, i, e, topk, expert_base, _ptr(a), _ptr(sfa), _ptr(w13), _ptr(sf13), _ptr(w2), _ptr(sf2),
-              _ptr(topk_ids), _ptr(topk_weights), _ptr(d), code, _ptr(workspace), _stream(stream)), name)
+    st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
+            sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), d.data_ptr(),
+            FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
+    if st != FG_OK:
+        _check(st, name)
 
 
 def fp8_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base=0, stream=None) -> None:
@@ -413,7 +445,7 @@ def fp8_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace
     then I up rows) with sf13 [E, ceil(H/512), align4(2I/128)]; w2 [E,H,I] with sf2; topk_ids int32
     and topk_weights float32 [T,topk]; d [T,H] BF16/FP32 (out).  Ids outside [expert_base,
     expert_base + E) are skipped.  workspace from moe_mlp_workspace."""
-    _moe_mlp(lib.fg_fp8_moe_mlp, "fp8_moe_mlp", _fp8, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace,
+    _moe_mlp(lib.fg_fp8_moe_mlp, "fp8_moe_mlp", "q", a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace,
              expert_base, stream)
 
 
@@ -421,14 +453,8 @@ def fp8_fp4_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, works
                     stream=None) -> None:
     """fp8_moe_mlp with FP4 weights: w13 [E,2I,H/2] packed E2M1 with sf13 [E, H/128, align4(2I)],
     w2 [E,H,I/2] with sf2 [E, I/128, align4(H)] (one UE8M0 scale per 32 K elements of a row)."""
-    _moe_mlp(lib.fg_fp8_fp4_moe_mlp, "fp8_fp4_moe_mlp", _fp4, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d,
+    _moe_mlp(lib.fg_fp8_fp4_moe_mlp, "fp8_fp4_moe_mlp", "p", a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d,
              workspace, expert_base, stream)
-
-
-def _bf16(t, name):
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
-        raise TypeError(f"{name} must be a contiguous CUDA bfloat16 tensor")
 
 
 def lora_workspace(m, n, k, r, device="cuda"):
@@ -440,20 +466,22 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
     """D[m] = A[m] @ B.T + scaling[l] * (x[m] @ lora_a[l].T) @ lora_b[l].T with l = ids[m] (-1: no
     adapter).  a, sfa, b, sfb as fp8_gemm_nt; x [M,K], lora_a [L,R,K], lora_b [L,N,R] BF16; scaling
     float32 [L]; ids int32 [M]; d [M,N] BF16/FP32 (out).  workspace from lora_workspace."""
-    _fp8(a, "a"); _fp8(b, "b"); _i32(sfa, "sfa"); _i32(sfb, "sfb"); _i32(ids, "ids")
-    _bf16(x, "x"); _bf16(lora_a, "lora_a"); _bf16(lora_b, "lora_b"); _f32(scaling, "scaling")
-    code = _out(d, "d")
+    _check_all(a, "a", "q", sfa, "sfa", "i", b, "b", "q", sfb, "sfb", "i", x, "x", "b", lora_a, "lora_a", "b",
+               lora_b, "lora_b", "b", scaling, "scaling", "f", ids, "ids", "i", d, "d", "o")
     m, k = a.shape
-    n = b.shape[0]
-    l, r = lora_a.shape[:2]
-    if (b.shape[1] != k or x.shape != a.shape or lora_a.shape[2] != k or lora_b.shape != (l, n, r) or
-            scaling.numel() != l or ids.numel() != m or d.shape != (m, n)):
+    n, kb = b.shape
+    l, r, ka = lora_a.shape
+    lb, nb, rb = lora_b.shape
+    if (kb != k or x.shape != a.shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
+            ids.numel() != m or d.shape != (m, n)):
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
-    if not workspace.is_cuda or workspace.numel() < lib.fg_lora_workspace(m, n, k, r):
+    if not workspace.is_cuda or workspace.nbytes < lib.fg_lora_workspace(m, n, k, r):
         raise ValueError("workspace is smaller than lora_workspace(m, n, k, r)")
-    _check(lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(x), _ptr(lora_a),
-                                   _ptr(lora_b), _ptr(scaling), _ptr(ids), _ptr(d), code, _ptr(workspace),
-                                   _stream(stream)), "fp8_gemm_nt_lora")
+    st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
+                                 lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), ids.data_ptr(), d.data_ptr(),
+                                 FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
+    if st != FG_OK:
+        _check(st, "fp8_gemm_nt_lora")
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

@@ -192,13 +192,15 @@ struct StreamPlan {
     int units, shares, nk, row_tiles;
     int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares
     int q, r;            // equal shares: r shares of q + 1 units, then shares of q
+    int light;           // kProj: units of a tile before its adapter units, which take twice as long
     const int* pre;      // kProj: units before each token tile
 };
 
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
     if (pl.pieces) {
         const int t = c / pl.pieces;
-        return t * pl.nk + (c - t * pl.pieces) * pl.nk / pl.pieces;
+        const int cost = (c - t * pl.pieces) * (2 * pl.nk - pl.light) / pl.pieces;
+        return t * pl.nk + (cost <= pl.light ? cost : pl.light + (cost - pl.light) / 2);
     }
     return c * pl.q + min(c, pl.r);
 }
@@ -219,22 +221,25 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 
 // How `tiles` tiles of nk units each become shares for at most `grid` CTAs: s pieces per tile
 // (s = 1: no cut), where all pieces find a CTA, or equal shares cut anywhere.  A tile's time is
-// the larger of a CTA's units at the pace of its MMA issuers and all units at HBM's, plus the join
-// of a cut tile: counting in (~2.2 us) and reading the n partials, kJoin at a time per chunk
-// (~0.9 us each); equal shares cut a tile at both ends of a share.  Measured on GB300: a unit
-// takes an SM 0.35 us when HBM keeps up, all SMs together 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM.
-__device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int join,
+// the larger of a CTA's units at the pace of its MMA issuers and all units at HBM's (less `early`
+// units per share, which stream before the launch can begin), plus the join of a cut tile;
+// equal shares cut a tile at both ends of a share.  Measured on GB300: a unit takes an SM 0.3 us
+// when HBM keeps up, all SMs together 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM; counting in takes
+// 2 us and a partial's chunk 0.25 us.
+__device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int early,
                                             bool even_ok) {
-    const float hbm = pl.units * (fp4 ? 0.0025f : 0.00475f);
-    auto joined = [&](int n) { return n > 1 ? 2.2f + 0.9f * ((n + join - 1) / join) * chunks : 0.0f; };
-    const int per = (pl.units + grid - 1) / grid;
-    const int n = per > 0 ? (pl.nk + per - 1) / per + 1 : 1;
-    float best = fmaxf(per * 0.35f, hbm) + 2.0f * joined(n);
+    const float unit_hbm = fp4 ? 0.0025f : 0.00475f;
+    auto time = [&](int shares, int per, int n) {
+        const float t = fmaxf(per * 0.3f, (pl.units - min(pl.units, early * shares)) * unit_hbm);
+        return t + (n > 1 ? 2.0f + 0.25f * n * chunks : 0.0f);
+    };
     pl.shares = min(grid, pl.units);
     pl.pieces = 0;
+    const int per = (pl.units + grid - 1) / grid;
+    float best = time(pl.shares, per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + 2.0f;
     if (even_ok)
         for (int s = 1; s * tiles <= grid && s <= pl.nk && s <= 16; ++s) {
-            const float t = fmaxf((pl.nk + s - 1) / s * 0.35f, hbm) + joined(s);
+            const float t = time(s * tiles, (pl.nk + s - 1) / s, s);
             if (t < best) {
                 best = t;
                 pl.pieces = s;
@@ -383,7 +388,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full_bar(s), 34);          // the two TMA producers, the scale loader's 32 lanes
+            mbar_init(full_bar(s), 66);          // two TMA producers; the lanes of the scale loader and of warp 3
             mbar_init(empty_bar(s), 2);          // both issuers' commits
         }
         for (int b = 0; b < C::kNumAcc; ++b) {
@@ -464,7 +469,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     pl.pre = pre;
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
-    plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, C::kJoin, kMoe || one_tile);
+    pl.light = one_tile ? p.nk : pl.nk;
+    plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
+                kMoe || one_tile);
     const int share = static_cast<int>(blockIdx.x);
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
@@ -521,26 +528,30 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         }
         __syncwarp();
     } else if (warp == 3) {
-        // ----------------------------------------------------------- token operand
-        if (lane == 0) {
-            if (kMode == kDown) {
-                grid_dependency_wait();
+        // ----------------------------------------------- token operand and its scale words
+        // Only this warp (and the epilogue) waits for the launch before: in kDown and kProj the
+        // weights and their scales stream meanwhile.
+        if (kMode == kDown) {
+            grid_dependency_wait();
+            if (lane == 0) {
                 grid_launch_dependents();
                 fence_proxy_async_global();
             }
-            int s = 0;
-            uint32_t ph = 0, armed = 0, armed_par = 0;
-            bool aborted = false;
-            bool waited = !one_tile;
-            StreamCursor<kMode> c(pl, share, p.nk);
-            for (; c.valid; c.step(pl)) {
-                if (kMode == kProj && !waited && c.k >= p.nk) {      // x @ A^T from here on
-                    grid_dependency_wait();
-                    fence_proxy_async_global();
-                    waited = true;
-                }
-                if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB)) { aborted = true; break; }
-                const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
+        }
+        int s = 0;
+        uint32_t ph = 0, armed = 0, armed_par = 0;
+        bool aborted = false, waited = !one_tile;
+        StreamCursor<kMode> c(pl, share, p.nk);
+        for (; c.valid; c.step(pl)) {
+            if (kMode == kProj && !waited && c.k >= p.nk) {      // x @ A^T from here on
+                grid_dependency_wait();
+                fence_proxy_async_global();
+                waited = true;
+            }
+            const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducerB);
+            if (!__all_sync(0xffffffffu, go)) { aborted = true; break; }
+            const uint32_t fb = full_bar(s), dst = sbase + C::kOffB + s * C::kBBytes;
+            if (lane == 0) {
                 armed |= 1u << s;
                 armed_par = (armed_par & ~(1u << s)) | (ph << s);
                 if (kMode == kProj && c.k >= p.nk) {
@@ -557,12 +568,28 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     if constexpr (kMode == kDown) tma_load_2d(dst, &maps.x, fb, c.kl * 128, c.li * BN);
                     else tma_load_2d(dst, &maps.x, fb, c.k * 128, c.sg.tt * BN);
                 }
-                if (++s == C::kStages) { s = 0; ph ^= 1u; }
             }
-            if (aborted || *abort_flag)
-                for (int i = 0; i < C::kStages; ++i)
-                    if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
+            __syncwarp();
+            if (c.new_words(kFp4, p.nk)) {
+                const uint32_t dt = sbase + C::kOffSf + s * C::kSfBytes + 1024 + lane * 16;
+                const int32_t* pt;
+                if (kMode == kDown) pt = p.sft + ((long long)c.li * ((p.nk + 3) / 4) + (c.kl >> 2)) * BN;
+                else pt = p.sft + (long long)(c.kl >> 2) * p.sft_ld + c.sg.tt * BN;
+                const int nt = kMode == kDown ? BN : min(BN, p.tokens - c.sg.tt * BN);
+#pragma unroll
+                for (int j = 0; j < (BN + 31) / 32; ++j) {
+                    const int i = j * 32 + lane;
+                    const bool in = i < nt;
+                    cp_async_4(dt + 4 * j, in ? pt + i : pt, in ? 4u : 0u);
+                }
+            }
+            cp_async_mbar_arrive(fb);
+            if (++s == C::kStages) { s = 0; ph ^= 1u; }
         }
+        cp_async_wait_all();
+        if (lane == 0 && (aborted || *abort_flag))
+            for (int i = 0; i < C::kStages; ++i)
+                if (armed >> i & 1u) drain_bar(full_bar(i), armed_par >> i & 1u, 20000000ull);
         __syncwarp();
     } else if (warp == 1 || warp == 9) {
         // ------------------------------------------------------------- MMA issuers
@@ -704,7 +731,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         };
         for (int i = 0; i < kAhead && ahead.valid; ++i, ahead.step(pl))
             if ((static_cast<uint32_t>(i) & 1u) == par) prefetch();
-        if (kMode == kDown) grid_dependency_wait();
         for (; c.valid; c.step(pl), ++n) {
             if ((n & 1u) == par) {
                 const bool go = wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitScales);
@@ -721,16 +747,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             const bool in = i < p.sfw_rows;
                             cp_async_4(da + 512 * b + 4 * j, in ? pw + i : pw, in ? 4u : 0u);
                         }
-                    }
-                    const int32_t* pt;
-                    if (kMode == kDown) pt = p.sft + ((long long)c.li * ((p.nk + 3) / 4) + (c.kl >> 2)) * BN;
-                    else pt = p.sft + (long long)(c.kl >> 2) * p.sft_ld + c.sg.tt * BN;
-                    const int nt = kMode == kDown ? BN : min(BN, p.tokens - c.sg.tt * BN);
-#pragma unroll
-                    for (int j = 0; j < (BN + 31) / 32; ++j) {
-                        const int i = j * 32 + lane;
-                        const bool in = i < nt;
-                        cp_async_4(da + 1024 + 4 * j, in ? pt + i : pt, in ? 4u : 0u);
                     }
                 }
                 cp_async_mbar_arrive(full_bar(s));
@@ -868,7 +884,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             }
             // ---- finish the tile
             // Partials of the share's last tile come through the ring, idle by now (this tile's
-            // products were its last): pieces (chunk, share) in order, kJoinSlots in flight.  Those of
+            // products were its last): pieces (chunk, share) in order, kJoinSlots in flight, issued by
+            // the four warps in turn (one thread's bulk copies complete one after another).  Those of
             // an earlier tile, joined while others stream, come into registers.
             const bool by_ring = !sg.whole && walk.done();
             const int n_parts = c_last - c_first + 1;
@@ -879,16 +896,16 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 return p.part + (2LL * c + (share_begin(pl, c) > sg.first_unit ? 0 : 1)) * part_tile + grp * 2 * kHalf * 128;
             };
             int fetched = 0;
-            auto fetch = [&](int i) {                    // piece i of the join; one thread
-                ++fetched;
+            auto fetch = [&](int i) {                    // piece i of the join; lane 0 of warp i mod 4
+                fetched = i + 1;
                 const int ch = i / n_parts, slot = i % C::kJoinSlots;
                 mbar_arrive_expect_tx(join_bar(grp, slot), C::kPieceBytes);
                 bulk_load(jbuf + slot * C::kPieceBytes, part_of(c_first + i - ch * n_parts) + ch * 2 * kChunk * 128,
                           C::kPieceBytes, join_bar(grp, slot));
             };
-            if (by_ring && te == 0) {
+            if (by_ring && lane == 0) {
                 fence_proxy_async_global();
-                for (int i = 0; i < min(pieces_all, C::kJoinSlots); ++i) fetch(i);
+                for (int i = q; i < min(pieces_all, C::kJoinSlots); i += 4) fetch(i);
             }
             int piece = 0;
             bool lost = false;
@@ -912,7 +929,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         }
                         if (piece + C::kJoinSlots < pieces_all) {
                             esync();                                   // the slot is free
-                            if (te == 0 && !lost) fetch(piece + C::kJoinSlots);
+                            if (lane == 0 && ((piece + C::kJoinSlots) & 3) == q && !lost) fetch(piece + C::kJoinSlots);
                         }
                     }
                 } else {
@@ -988,8 +1005,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 }
             }
             if (sg.whole && cols <= 0) release();
-            if (lost && te == 0)       // pieces that may still be landing
-                for (int i = max(0, fetched - C::kJoinSlots); i < fetched; ++i)
+            if (lost && lane == 0)     // pieces that may still be landing
+                for (int i = fetched - 1; i >= 0 && i >= fetched - C::kJoinSlots; i -= 4)
                     drain_bar(join_bar(grp, i % C::kJoinSlots), (i / C::kJoinSlots) & 1, 20000000ull);
             if (!evote(!lost)) break;
             if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
