@@ -46,9 +46,9 @@ bool shapes_ok(int M, int N, int K, int R) {
 }
 
 // ---------------------------------------------------------------- v = scaling * x @ A^T
-// One CTA per (token tile, distinct adapter of it, 8 * NB of the tokens that use it): the
-// adapter's rows are the M operand of mma.sync (MB blocks of 16), its tokens the N operand (NB
-// blocks of 8), gathered by their row numbers.  The 16 warps split K and read both operands
+// A work item is (distinct adapter of a token tile, 8 * NB of the tokens that use it); a token
+// tile's CTAs share its items.  The adapter's rows are the M operand of mma.sync (MB blocks of
+// 16), its tokens the N operand (NB blocks of 8), gathered by their row numbers.  The 16 warps split K and read both operands
 // straight into registers, 16 bytes (8 consecutive k) per row and lane: k is summed over, so a
 // lane's 8 values may stand for any k as long as A and x agree; they feed two 16-wide steps.
 // There is nothing to stage: each A element is used by one CTA (latency-bound: its bytes in
@@ -90,70 +90,111 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     constexpr int kTok = 8 * NB;
     __shared__ uint32_t bits[32];
     __shared__ uint16_t list[fg::kMaxListed];
-    __shared__ int listed, members;
-    __shared__ int16_t member[128];               // tokens of the tile that use the adapter, in order
+    __shared__ int listed;
+    __shared__ int16_t slot_of[128];              // of each token of the tile, -1 without an adapter
+    __shared__ int first_item[129];               // items before each slot
+    __shared__ int16_t member[128];               // tokens that use the item's adapter, in order
     __shared__ float red[kShrinkWarps / 2][MB * 16][kTok];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slot = blockIdx.x, first = blockIdx.y * kTok, tt = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tt = blockIdx.y;
     fg::grid_dependency_wait();
     if (threadIdx.x == 0) fg::grid_launch_dependents();
     const int n = min(p.bn, p.tokens - tt * p.bn);
     const int32_t* ids = p.ids + (long long)tt * p.bn;
+    const int my_id = threadIdx.x < static_cast<unsigned>(n) ? __ldcg(ids + threadIdx.x) : -1;
     fg::list_distinct(ids, n, 0, p.L, bits, list, &listed);
-    if (slot == 0 && first == 0) {
-        for (int i = threadIdx.x; i < listed; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = list[i];
-        if (threadIdx.x == 0) p.slot_count[tt] = listed;
-        for (int i = threadIdx.x; i < n; i += blockDim.x)
-            if (__ldcg(ids + i) >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
+    const int slots = listed;
+    if (threadIdx.x < 128) {
+        int slot = -1;
+        if (my_id >= 0 && my_id < p.L)            // its rank in the list
+            for (int lo = 0, hi = slots; lo < hi;) {
+                const int mid = (lo + hi) / 2;
+                if (list[mid] <= my_id) { slot = mid; lo = mid + 1; }
+                else hi = mid;
+            }
+        slot_of[threadIdx.x] = static_cast<int16_t>(slot);
     }
-    if (slot >= listed) return;
-    const int id = list[slot];
-    uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
-    const long long part = (long long)p.bn * p.rp;
-    if (warp == 0) {
-        int run = 0;
-        for (int t0 = 0; t0 < p.bn; t0 += 32) {
-            const int t = t0 + lane;
-            const bool mine = t < n && __ldcg(ids + t) == id;
-            const uint32_t m = __ballot_sync(0xffffffffu, mine);
-            if (mine) member[run + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(t);
-            run += __popc(m);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < slots; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = list[i];
+        if (threadIdx.x == 0) p.slot_count[tt] = slots;
+        if (my_id >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {                      // items of slot threadIdx.x, then their prefix sums
+        int c = 0;
+        if (static_cast<int>(threadIdx.x) < slots)
+            for (int t = 0; t < n; ++t) c += slot_of[t] == static_cast<int>(threadIdx.x);
+        c = (c + kTok - 1) / kTok;
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
         }
-        if (lane == 0) members = run;
-    } else if (first == 0 && warp == 1) {
+        first_item[threadIdx.x + 1] = incl;
+        if (threadIdx.x == 0) first_item[0] = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32 && threadIdx.x < 128) {
+        int before = first_item[32];
+        if (warp >= 2) before += first_item[64];
+        if (warp >= 3) before += first_item[96];
+        const int v = first_item[threadIdx.x + 1] + before;
+        asm volatile("bar.sync 1, 96;" ::: "memory");
+        first_item[threadIdx.x + 1] = v;
+    }
+    __syncthreads();
+    const int items = first_item[128];
+    const long long part = (long long)p.bn * p.rp;
+    const int g = lane >> 2, q = lane & 3;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    int slot = 0;
+    for (int lo = 0, hi = slots; lo < hi;) {      // the last slot whose first item is not behind `item`
+        const int mid = (lo + hi) / 2;
+        if (first_item[mid] <= item) { slot = mid; lo = mid + 1; }
+        else hi = mid;
+    }
+    const int first = (item - first_item[slot]) * kTok, id = list[slot];
+    uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
+    __syncthreads();                              // the item before is done with member
+    int members = 0;
+    if (warp == 0) {
+        for (int t0 = 0; t0 < p.bn; t0 += 32) {
+            const bool mine = t0 + lane < n && slot_of[t0 + lane] == slot;
+            const uint32_t m = __ballot_sync(0xffffffffu, mine);
+            if (mine) member[members + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(t0 + lane);
+            members += __popc(m);
+        }
+    } else {
+        for (int t = 0; t < n; ++t) members += slot_of[t] == slot;
         // the other tokens' rows are zero: they are multiplied with this adapter's B too
-        for (int t = lane; t < p.bn; t += 32)
-            if (!(t < n && __ldcg(ids + t) == id))
-                for (int o = 0; o < p.parts; ++o)
-                    for (int c = 0; c < p.rp; c += 8)
-                        *reinterpret_cast<uint4*>(v + o * part + (long long)t * p.rp + c) = make_uint4(0, 0, 0, 0);
+        if (first == 0) {
+            const int per = p.rp / 8;             // 16-byte pieces of a row
+            for (int i = threadIdx.x - 32; i < p.parts * p.bn * per; i += blockDim.x - 32) {
+                const int row = i / per, t = row % p.bn;
+                if (t >= n || slot_of[t] != slot) *reinterpret_cast<uint4*>(v + (long long)i * 8) = zero;
+            }
+        }
     }
     __syncthreads();
     const int mine = min(kTok, members - first);
-    if (mine <= 0) return;
     const float scale = __ldg(p.scaling + id);
-    const int g = lane >> 2, q = lane & 3;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4* xrow[NB];
-    bool xon[NB];
+    // rows by their offset in 16-byte pieces from the tile's and the adapter's first, -1: none
+    const uint4* xb = reinterpret_cast<const uint4*>(p.x + (long long)tt * p.bn * p.K) + q;
+    const uint4* ab = reinterpret_cast<const uint4*>(p.lora_a + (long long)id * p.R * p.K) + q;
+    int xrow[NB];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int i = 8 * j + g;
-        xon[j] = i < mine;
-        xrow[j] = reinterpret_cast<const uint4*>(p.x + ((long long)tt * p.bn + (xon[j] ? member[first + i] : 0)) * p.K) + q;
-    }
+    for (int j = 0; j < NB; ++j) xrow[j] = 8 * j + g < mine ? member[first + 8 * j + g] * (p.K / 8) : -1;
     const int blocks = p.K / 32;                   // 64 bytes of a row each: four lanes' 16
     for (int m0 = 0; m0 < p.rp; m0 += 16 * MB) {
         float acc[MB][NB][4] = {};
-        const uint4* arow[MB][2];
-        bool aon[MB][2];
+        int arow[MB][2];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = m0 + 16 * i + 8 * h + g;
-                aon[i][h] = r < p.R;
-                arow[i][h] = reinterpret_cast<const uint4*>(p.lora_a + ((long long)id * p.R + (aon[i][h] ? r : 0)) * p.K) + q;
+                arow[i][h] = r < p.R ? r * (p.K / 8) : -1;
             }
         for (int b0 = warp; b0 < blocks; b0 += kShrinkWarps * U) {
             uint4 a[U][MB][2], x[U][NB];
@@ -164,9 +205,9 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) a[u][i][h] = in && aon[i][h] ? __ldg(arow[i][h] + b * 4) : zero;
+                    for (int h = 0; h < 2; ++h) a[u][i][h] = in && arow[i][h] >= 0 ? __ldg(ab + arow[i][h] + b * 4) : zero;
 #pragma unroll
-                for (int j = 0; j < NB; ++j) x[u][j] = in && xon[j] ? __ldg(xrow[j] + b * 4) : zero;
+                for (int j = 0; j < NB; ++j) x[u][j] = in && xrow[j] >= 0 ? __ldg(xb + xrow[j] + b * 4) : zero;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -203,10 +244,11 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
         }
         __syncthreads();
     }
+    }
     fg::fence_proxy_async_global();
 }
 
-cudaError_t launch_shrink(const ShrinkParams& p, int tiles, int pdl, cudaStream_t stream) {
+cudaError_t launch_shrink(const ShrinkParams& p, int tiles, int sms, int pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.blockDim = dim3(32 * kShrinkWarps);
@@ -217,9 +259,11 @@ cudaError_t launch_shrink(const ShrinkParams& p, int tiles, int pdl, cudaStream_
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const unsigned slots = static_cast<unsigned>(p.L < p.bn ? p.L : p.bn);
     auto go = [&](auto kernel, int tok) {
-        cfg.gridDim = dim3(slots, static_cast<unsigned>(ceil_div(p.bn, tok)), static_cast<unsigned>(tiles));
+        // a tile has at most min(bn, L) + bn / tok items; one CTA an item, as far as one wave of SMs goes
+        const int most = (p.L < p.bn ? p.L : p.bn) + p.bn / tok;
+        const int share = sms / tiles > 1 ? sms / tiles : 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(tiles));
         return cudaLaunchKernelEx(&cfg, kernel, p);
     };
     // 8 tokens at a time where there are few per adapter (small tiles), 32 in a prompt's tiles
@@ -264,7 +308,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
     const ShrinkParams sp{M, l.bn, K, R, l.rp, L, l.bn, parts, ids, static_cast<const uint16_t*>(x),
                           static_cast<const uint16_t*>(lora_a), scaling, reinterpret_cast<uint16_t*>(ws + l.v),
                           reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<int*>(ws + l.count), st.status};
-    if (launch_shrink(sp, l.tiles, st.pdl, s) != cudaSuccess) {
+    if (launch_shrink(sp, l.tiles, st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
         return FG_ERR_CUDA;
     }
