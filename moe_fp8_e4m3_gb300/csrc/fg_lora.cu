@@ -41,7 +41,7 @@ bool shapes_ok(int M, int N, int K, int R) {
     if (M < 0 || N < 16 || N % 16 != 0 || K < 128 || K % 128 != 0 || R < 8 || R % 8 != 0 || R > 128) return false;
     const Layout l = layout(M > 0 ? M : 1, R);
     return l.tiles <= fg::kMaxTokenTiles &&
-           (long long)l.tiles * ceil_div(N, 256) * (K / 128 + 4 * l.bn) < (1LL << 31) &&
+           (long long)l.tiles * ceil_div(N, 256) * (K / 128 + 8 * l.bn) < (1LL << 31) &&
            (long long)l.tiles * l.bn * 3 * l.bn < (1LL << 31);
 }
 
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     __shared__ uint16_t list[fg::kMaxListed];
     __shared__ int listed;
     __shared__ int16_t slot_of[128];              // of each token of the tile, -1 without an adapter
-    __shared__ int first_item[129];               // items before each slot
+    __shared__ int count[128], first_item[129];   // tokens of each slot, items before it
     __shared__ int16_t member[128];               // tokens that use the item's adapter, in order
     __shared__ float red[kShrinkWarps / 2][MB * 16][kTok];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tt = blockIdx.y;
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     const int n = min(p.bn, p.tokens - tt * p.bn);
     const int32_t* ids = p.ids + (long long)tt * p.bn;
     const int my_id = threadIdx.x < static_cast<unsigned>(n) ? __ldcg(ids + threadIdx.x) : -1;
+    if (threadIdx.x < 128) count[threadIdx.x] = 0;
     fg::list_distinct(ids, n, 0, p.L, bits, list, &listed);
     const int slots = listed;
     if (threadIdx.x < 128) {
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
                 else hi = mid;
             }
         slot_of[threadIdx.x] = static_cast<int16_t>(slot);
+        if (slot >= 0) atomicAdd(count + slot, 1);
     }
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i < slots; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = list[i];
@@ -119,28 +121,26 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
         if (my_id >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
     }
     __syncthreads();
-    if (threadIdx.x < 128) {                      // items of slot threadIdx.x, then their prefix sums
-        int c = 0;
-        if (static_cast<int>(threadIdx.x) < slots)
-            for (int t = 0; t < n; ++t) c += slot_of[t] == static_cast<int>(threadIdx.x);
-        c = (c + kTok - 1) / kTok;
-        int incl = c;
+    if (warp == 0) {                              // items of each slot, four slots a lane, and their prefix sums
+        int c[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = (count[4 * lane + i] + kTok - 1) / kTok;
+            sum += c[i];
+        }
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        first_item[threadIdx.x + 1] = incl;
-        if (threadIdx.x == 0) first_item[0] = 0;
-    }
-    __syncthreads();
-    if (threadIdx.x >= 32 && threadIdx.x < 128) {
-        int before = first_item[32];
-        if (warp >= 2) before += first_item[64];
-        if (warp >= 3) before += first_item[96];
-        const int v = first_item[threadIdx.x + 1] + before;
-        asm volatile("bar.sync 1, 96;" ::: "memory");
-        first_item[threadIdx.x + 1] = v;
+        int at = incl - sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            first_item[4 * lane + i] = at;
+            at += c[i];
+        }
+        if (lane == 31) first_item[128] = at;
     }
     __syncthreads();
     const int items = first_item[128];
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     const int first = (item - first_item[slot]) * kTok, id = list[slot];
     uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
     __syncthreads();                              // the item before is done with member
-    int members = 0;
     if (warp == 0) {
+        int members = 0;
         for (int t0 = 0; t0 < p.bn; t0 += 32) {
             const bool mine = t0 + lane < n && slot_of[t0 + lane] == slot;
             const uint32_t m = __ballot_sync(0xffffffffu, mine);
@@ -166,7 +166,6 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
             members += __popc(m);
         }
     } else {
-        for (int t = 0; t < n; ++t) members += slot_of[t] == slot;
         // the other tokens' rows are zero: they are multiplied with this adapter's B too
         if (first == 0) {
             const int per = p.rp / 8;             // 16-byte pieces of a row
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
         }
     }
     __syncthreads();
-    const int mine = min(kTok, members - first);
+    const int mine = min(kTok, count[slot] - first);
     const float scale = __ldg(p.scaling + id);
     // rows by their offset in 16-byte pieces from the tile's and the adapter's first, -1: none
     const uint4* xb = reinterpret_cast<const uint4*>(p.x + (long long)tt * p.bn * p.K) + q;
@@ -301,7 +300,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
 
     // parts of x @ lora_a^T: 16 mantissa bits under a BF16 result, 24 under an FP32 one; an adapter
     // unit's parts x columns fit the stage's token area
-    const int parts = d_dtype == FG_F32 ? 3 : 2, unit_cols = d_dtype == FG_F32 ? 32 : 64;
+    const int parts = d_dtype == FG_F32 ? 3 : 2, unit_cols = d_dtype == FG_F32 ? 16 : 32;
     if (fg::print_configs_enabled())
         std::fprintf(stderr, "[fg] fp8_gemm_nt_lora M=%d N=%d K=%d L=%d R=%d BN=%d rank=%d grid=%d\n", M, N, K, L, R, l.bn,
                      l.rp, grid);

@@ -148,10 +148,10 @@ __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence
 template <int kMode, int BN>
 struct StreamCfg {
     static constexpr int kABytes = 32768;                                   // two 128-row blocks x 128 bytes
-    static constexpr int kBBytes = BN * 128 * (kMode == kProj ? 2 : 1);     // kProj: the parts of an adapter unit
+    static constexpr int kBBytes = BN * 128;                                // kProj: also the parts of an adapter unit
     static constexpr int kSfBytes = 3 * 512;                                // weight block 0, 1, tokens
     static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + 128 + 2 * kMaxListed +
+    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + 128 + 64 + 2 * kMaxListed +
                                       (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
     static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
@@ -162,7 +162,7 @@ struct StreamCfg {
     // join of a share's last tile: partials through the idle ring, kJoinSlots pieces per group
     static constexpr int kChunk = BN >= 32 ? 16 : 8;                        // token columns an epilogue group takes at a time
     static constexpr int kChunks = BN / 2 / kChunk;                         // of a group
-    static constexpr int kJoin = 32 / kChunk;                               // partials it loads at a time
+    static constexpr int kJoin = 16 / kChunk;                               // partials it loads at a time
     static constexpr int kPieceBytes = kChunk * 2 * 128 * 4;                // a chunk of one partial
     static constexpr int kJoinSlots = kStages * kABytes / 2 / kPieceBytes > 10 ? 10 : kStages * kABytes / 2 / kPieceBytes;
     static constexpr int kOffB = kStages * kABytes;
@@ -173,7 +173,8 @@ struct StreamCfg {
     static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
     static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
     static constexpr int kOffBits = kOffTok + BN * 8;
-    static constexpr int kOffList = kOffBits + 128;
+    static constexpr int kOffWalk = kOffBits + 128;
+    static constexpr int kOffList = kOffWalk + 64;
     static constexpr int kOffPre = kOffList + 2 * kMaxListed;
     static constexpr int kSmemBytes = kOffBar + kMiscBytes + 1024;          // + alignment slack
     static_assert(kNumBars * 8 <= 512 - 64, "barrier area");
@@ -192,15 +193,13 @@ struct StreamPlan {
     int units, shares, nk, row_tiles;
     int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares
     int q, r;            // equal shares: r shares of q + 1 units, then shares of q
-    int light;           // kProj: units of a tile before its adapter units, which take twice as long
     const int* pre;      // kProj: units before each token tile
 };
 
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
     if (pl.pieces) {
         const int t = c / pl.pieces;
-        const int cost = (c - t * pl.pieces) * (2 * pl.nk - pl.light) / pl.pieces;
-        return t * pl.nk + (cost <= pl.light ? cost : pl.light + (cost - pl.light) / 2);
+        return t * pl.nk + (c - t * pl.pieces) * pl.nk / pl.pieces;
     }
     return c * pl.q + min(c, pl.r);
 }
@@ -233,20 +232,19 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
         const float t = fmaxf(per * 0.3f, (pl.units - min(pl.units, early * shares)) * unit_hbm);
         return t + (n > 1 ? 2.0f + 0.25f * n * chunks : 0.0f);
     };
-    pl.shares = min(grid, pl.units);
-    pl.pieces = 0;
-    const int per = (pl.units + grid - 1) / grid;
-    float best = time(pl.shares, per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + 2.0f;
-    if (even_ok)
-        for (int s = 1; s * tiles <= grid && s <= pl.nk && s <= 16; ++s) {
-            const float t = time(s * tiles, (pl.nk + s - 1) / s, s);
-            if (t < best) {
-                best = t;
-                pl.pieces = s;
-                pl.shares = s * tiles;
-            }
-        }
-    if (pl.shares < 1) pl.shares = 1;
+    // lane s > 0 looks at s pieces per tile, lane 0 at equal shares; the least time (its bits, the
+    // lane in the low five) wins
+    const int s = static_cast<int>(threadIdx.x & 31);
+    float t = 1e30f;
+    if (s == 0) {
+        const int per = (pl.units + grid - 1) / grid;
+        t = time(min(grid, pl.units), per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + 2.0f;
+    } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.nk) {
+        t = time(s * tiles, (pl.nk + s - 1) / s, s);
+    }
+    const uint32_t best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | s);
+    pl.pieces = static_cast<int>(best & 31u);
+    pl.shares = max(1, pl.pieces ? pl.pieces * tiles : min(grid, pl.units));
     pl.q = pl.units / pl.shares;
     pl.r = pl.units - pl.q * pl.shares;
 }
@@ -256,33 +254,34 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
 // are then the first thing its shares do, and joining them hides behind the whole tiles.
 template <int kMode>
 struct StreamWalk {
-    int u, end, tail, tail_end, tt;      // [u, end) is left; before it [tail, tail_end) if tail >= 0
-    __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share) : u(0), end(0), tail(-1), tail_end(0), tt(0) {
+    int u, end, tail, tail_end;          // [u, end) is left; before it [tail, tail_end) if tail >= 0
+    int tile, tt, first, nk;             // the tile of unit u
+    int tail_tile, tail_tt, tail_nk;
+    __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share)
+        : u(0), end(0), tail(-1), tail_end(0), tile(0), tt(0), first(0), nk(1), tail_tile(0), tail_tt(0), tail_nk(1) {
         if (share >= pl.shares) return;
         u = share_begin(pl, share);
         end = tail_end = share_begin(pl, share + 1);
-        StreamSeg s;
-        locate(pl, end - 1, s);
-        tt = 0;
-        if (s.first_unit + s.nk != end && s.first_unit > u) end = tail = s.first_unit;
-    }
-    // the tile of unit v (token tiles are searched from tt on)
-    __device__ __forceinline__ void locate(const StreamPlan& pl, int v, StreamSeg& s) {
-        int base = 0;
-        s.nk = pl.nk;
-        if (kMode == kProj) {
-            while (v >= pl.pre[tt + 1]) ++tt;
-            base = pl.pre[tt];
-            s.nk = (pl.pre[tt + 1] - base) / pl.row_tiles;
-        }
-        s.tt = tt;
-        s.tile = (v - base) / s.nk;
-        s.first_unit = base + s.tile * s.nk;
+        int a = 0, base = 0;
+        auto locate = [&](int v, int& at_tile, int& at_tt, int& at_nk) {
+            at_nk = pl.nk;
+            if (kMode == kProj) {
+                while (v >= pl.pre[a + 1]) ++a;
+                base = pl.pre[a];
+                at_nk = (pl.pre[a + 1] - base) / pl.row_tiles;
+            }
+            at_tt = a;
+            at_tile = (v - base) / at_nk;
+            return base + at_tile * at_nk;
+        };
+        if (u >= end) return;
+        first = locate(u, tile, tt, nk);
+        const int last = locate(end - 1, tail_tile, tail_tt, tail_nk);
+        if (last + tail_nk != end && last > u) end = tail = last;
     }
     __device__ __forceinline__ bool next(const StreamPlan& pl, StreamSeg& s) {
         if (tail >= 0) {
-            locate(pl, tail, s);
-            tt = 0;
+            s.tile = tail_tile; s.tt = tail_tt; s.nk = tail_nk; s.first_unit = tail;
             s.k0 = 0;
             s.k1 = tail_end - tail;
             s.whole = false;
@@ -290,11 +289,18 @@ struct StreamWalk {
             return true;
         }
         if (u >= end) return false;
-        locate(pl, u, s);
-        s.k0 = u - s.first_unit;
-        s.k1 = min(s.nk, s.k0 + (end - u));
-        s.whole = s.k0 == 0 && s.k1 == s.nk;
+        s.tile = tile; s.tt = tt; s.nk = nk; s.first_unit = first;
+        s.k0 = u - first;
+        s.k1 = min(nk, s.k0 + (end - u));
+        s.whole = s.k0 == 0 && s.k1 == nk;
         u += s.k1 - s.k0;
+        // the tile behind it
+        first += nk;
+        if (++tile == pl.row_tiles && kMode == kProj) {
+            tile = 0;
+            ++tt;
+            if (u < end) nk = (pl.pre[tt + 1] - pl.pre[tt]) / pl.row_tiles;
+        }
         return true;
     }
     __device__ __forceinline__ bool done() const { return tail < 0 && u >= end; }
@@ -308,8 +314,8 @@ struct StreamCursor {
     StreamSeg sg;
     int k, li, kl, per;
     bool valid;
-    __device__ __forceinline__ StreamCursor(const StreamPlan& pl, int share, int per_expert)
-        : walk(pl, share), k(0), li(0), kl(0), per(per_expert) { enter(pl); }
+    __device__ __forceinline__ StreamCursor(const StreamPlan& pl, const StreamWalk<kMode>& from, int per_expert)
+        : walk(from), k(0), li(0), kl(0), per(per_expert) { enter(pl); }
     __device__ __forceinline__ void enter(const StreamPlan& pl) {
         valid = walk.next(pl, sg);
         if (!valid) return;
@@ -469,10 +475,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     pl.pre = pre;
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
-    pl.light = one_tile ? p.nk : pl.nk;
     plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
                 kMoe || one_tile);
     const int share = static_cast<int>(blockIdx.x);
+    StreamWalk<kMode>& share_walk = *reinterpret_cast<StreamWalk<kMode>*>(smem + C::kOffWalk);   // each role's copy starts from it
+    if (threadIdx.x == 0) share_walk = StreamWalk<kMode>(pl, share);
+    __syncthreads();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
     // kProj: adapter units behind the K-groups
@@ -487,7 +495,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             int s = 0;
             uint32_t ph = 0, n = 0, armed = 0, armed_par = 0;
             bool stall = p.debug_stall != 0 && par == 0, aborted = false;
-            StreamCursor<kMode> c(pl, share, p.nk);
+            StreamCursor<kMode> c(pl, share_walk, p.nk);
             for (; c.valid; c.step(pl), ++n) {
                 if ((n & 1u) == par) {
                     if (!wait_bar(empty_bar(s), ph ^ 1u, wctl, kWaitProducer)) { aborted = true; break; }
@@ -541,7 +549,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         int s = 0;
         uint32_t ph = 0, armed = 0, armed_par = 0;
         bool aborted = false, waited = !one_tile;
-        StreamCursor<kMode> c(pl, share, p.nk);
+        StreamCursor<kMode> c(pl, share_walk, p.nk);
         for (; c.valid; c.step(pl)) {
             if (kMode == kProj && !waited && c.k >= p.nk) {      // x @ A^T from here on
                 grid_dependency_wait();
@@ -618,7 +626,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             auto wait_all = [&](uint32_t bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, wait_bar(bar, parity, wctl, kWaitMma)) != 0;
             };
-            StreamWalk<kMode> walk(pl, share);
+            StreamWalk<kMode> walk(share_walk);
             StreamSeg sg;
             while (!aborted && walk.next(pl, sg)) {
                 if (!wait_all(acce_bar(acc), acc_ph ^ 1u)) { aborted = true; break; }
@@ -714,7 +722,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         const uint32_t par = warp == 8 ? 0u : 1u;
         int s = 0;
         uint32_t ph = 0, n = 0;
-        StreamCursor<kMode> c(pl, share, p.nk), ahead(pl, share, p.nk);
+        StreamCursor<kMode> c(pl, share_walk, p.nk), ahead(c);
         auto words_of = [&](const StreamCursor<kMode>& at) {
             const int e = kMode == kGateUp ? list[at.sg.tile / p.row_tiles] : (kMode == kDown ? list[at.li] : 0);
             return p.sfw + e * p.sfw_gstride + (long long)(kFp4 ? at.kl : at.kl >> 2) * p.sfw_ld;
@@ -794,7 +802,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         const int my_part = grp * 2 * kHalf * 128 + row;
         int acc = 0;
         uint32_t acc_ph = 0;
-        StreamWalk<kMode> walk(pl, share);
+        StreamWalk<kMode> walk(share_walk);
         StreamSeg sg;
         while (walk.next(pl, sg)) {
             if constexpr (kMode == kGateUp) {
@@ -887,7 +895,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             // products were its last): pieces (chunk, share) in order, kJoinSlots in flight, issued by
             // the four warps in turn (one thread's bulk copies complete one after another).  Those of
             // an earlier tile, joined while others stream, come into registers.
-            const bool by_ring = !sg.whole && walk.done();
+            const bool few = cols <= 2;
+            const bool by_ring = !sg.whole && !few && walk.done();
             const int n_parts = c_last - c_first + 1;
             const int pieces_all = by_ring ? (cols + kChunk - 1) / kChunk * n_parts : 0;
             const uint32_t jbuf = sbase + grp * C::kJoinSlots * C::kPieceBytes;
@@ -931,6 +940,29 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             esync();                                   // the slot is free
                             if (lane == 0 && ((piece + C::kJoinSlots) & 3) == q && !lost) fetch(piece + C::kJoinSlots);
                         }
+                    }
+                } else if (few) {
+                    // one or two columns: eight partials in flight
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v0[i] = v1[i] = 0.0f;
+                    for (int c = c_first; c <= c_last; c += 8) {
+                        float x[8][4];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float* src = part_of(min(c + u, c_last)) + row;
+                            x[u][0] = __ldcg(src);
+                            x[u][1] = __ldcg(src + kChunk * 128);
+                            x[u][2] = __ldcg(src + (cols - 1) * 128);
+                            x[u][3] = __ldcg(src + (kChunk + cols - 1) * 128);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (c + u <= c_last) {
+                                v0[0] += x[u][0];
+                                v1[0] += x[u][1];
+                                v0[1] += x[u][2];
+                                v1[1] += x[u][3];
+                            }
                     }
                 } else {
                     // the partials in share order, kJoin of them in flight
