@@ -1,5 +1,6 @@
 // fg_moe.cu - the whole MoE MLP of a decode step in two launches (fg_stream.cuh): gate-up +
-// SwiGLU + requantisation, then the down projection summed over the experts.
+// SwiGLU + requantisation, then the down projection summed over the experts (from 33 tokens on a
+// third one adds up its parts).
 #include <cstdio>
 #include <cstring>
 
@@ -112,7 +113,9 @@ int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t
         p.ctr = reinterpret_cast<unsigned*>(ws) + fg::kMaxCounters;
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = 0;
-        if (fg::launch_stream<fg::kDown, kFp4>(bn, p, m, dim3(grid), s) != cudaSuccess) {
+        if (bn >= 64 && p.row_tiles <= grid) p.spread = reinterpret_cast<int*>(ws) + 2 * fg::kMaxCounters;
+        if (fg::launch_stream<fg::kDown, kFp4>(bn, p, m, dim3(grid), s) != cudaSuccess ||
+            (p.spread && fg::launch_reduce(bn, p, s) != cudaSuccess)) {
             cudaGetLastError();
             return FG_ERR_CUDA;
         }

@@ -46,7 +46,7 @@ constexpr int kMaxListed = 1024;         // experts of a shard, adapters of a ca
 constexpr int kMaxTokenTiles = 512;      // kProj: token tiles of one call
 constexpr int kMaxStreamCtas = 256;      // shares of a launch (partial slots in the workspace)
 constexpr int kMaxCounters = 512;        // of one launch: two per share, one for each half of the columns
-constexpr int kCounterBytes = 2 * kMaxCounters * 4;   // head of a workspace: both launches' counters
+constexpr int kCounterBytes = 2 * kMaxCounters * 4 + 256;   // head of a workspace: both launches' counters, a spread plan
 
 struct StreamMaps {
     CUtensorMap w;       // weights
@@ -74,6 +74,8 @@ struct StreamParams {
     unsigned* ctr;               // [kMaxCounters]
     void* d;
     int d_f32;
+    int* spread;                 // not null: every tile's parts go to the workspace, and a third launch adds
+                                 // them up (stream_reduce_kernel), told here how the units were dealt
     // adapters
     int lora_rp, lora_count, max_slots, token_tiles;
     int parts, unit_cols;        // BF16 parts of x @ A^T; rank columns of a unit
@@ -226,11 +228,11 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 // when HBM keeps up, all SMs together 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM; counting in takes
 // 2 us and a partial's chunk 0.25 us.
 __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int early,
-                                            bool even_ok) {
+                                            bool even_ok, bool spread) {
     const float unit_hbm = fp4 ? 0.0025f : 0.00475f;
     auto time = [&](int shares, int per, int n) {
         const float t = fmaxf(per * 0.3f, (pl.units - min(pl.units, early * shares)) * unit_hbm);
-        return t + (n > 1 ? 2.0f + 0.25f * n * chunks : 0.0f);
+        return t + (spread ? 0.1f * n : n > 1 ? 2.0f + 0.25f * n * chunks : 0.0f);
     };
     // lane s > 0 looks at s pieces per tile, lane 0 at equal shares; the least time (its bits, the
     // lane in the low five) wins
@@ -238,7 +240,7 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
     float t = 1e30f;
     if (s == 0) {
         const int per = (pl.units + grid - 1) / grid;
-        t = time(min(grid, pl.units), per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + 2.0f;
+        t = time(min(grid, pl.units), per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + (spread ? 0.0f : 2.0f);
     } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.nk) {
         t = time(s * tiles, (pl.nk + s - 1) / s, s);
     }
@@ -248,6 +250,9 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
     pl.q = pl.units / pl.shares;
     pl.r = pl.units - pl.q * pl.shares;
 }
+
+// What stream_reduce_kernel has to know of a plan.
+enum : int { kSpreadUnits = 0, kSpreadShares, kSpreadNk, kSpreadPieces, kSpreadWords };
 
 // The pieces of one share: first the tile that goes on into the next share, then the others in
 // order (so a tile that the share before began comes next, whole tiles last).  A cut tile's parts
@@ -476,7 +481,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
     plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
-                kMoe || one_tile);
+                kMoe || one_tile, p.spread != nullptr);
     const int share = static_cast<int>(blockIdx.x);
     StreamWalk<kMode>& share_walk = *reinterpret_cast<StreamWalk<kMode>*>(smem + C::kOffWalk);   // each role's copy starts from it
     if (threadIdx.x == 0) share_walk = StreamWalk<kMode>(pl, share);
@@ -777,7 +782,13 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         const int te = row;                                            // 0..127 over the group
         if (kMode == kDown || one_tile) grid_dependency_wait();
         if (one_tile && threadIdx.x == 128) grid_launch_dependents();
-        if (kMode == kDown && nlist == 0) {
+        if (p.spread && share == 0 && threadIdx.x == 128) {
+            p.spread[kSpreadUnits] = pl.units;
+            p.spread[kSpreadShares] = pl.shares;
+            p.spread[kSpreadNk] = pl.nk;
+            p.spread[kSpreadPieces] = pl.pieces;
+        }
+        if (kMode == kDown && nlist == 0 && !p.spread) {
             // no token uses an expert of this shard: the sum is empty
             const long long n = (long long)p.tokens * p.out_rows;
             for (long long i = ((long long)blockIdx.x * 2 + grp) * 128 + te; i < n; i += (long long)gridDim.x * 256) {
@@ -856,7 +867,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 for (int i = 0; i < kChunk; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
             };
             int c_first = share, c_last = share;
-            if (!sg.whole) {
+            if (!sg.whole || p.spread) {
                 // this share's part of the tile: 0 where the tile began in an earlier share, else 1
                 float* mine = p.part + (2LL * share + (sg.k0 > 0 ? 0 : 1)) * part_tile + my_part;
                 for (int c0 = 0; c0 < cols; c0 += kChunk) {
@@ -870,7 +881,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     }
                 }
                 release();
-                if (cols <= 0) {
+                if (cols <= 0 || p.spread) {
                     if (++acc == C::kNumAcc) { acc = 0; acc_ph ^= 1u; }
                     continue;
                 }
@@ -1051,6 +1062,82 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         tc_fence_after();
         tmem_dealloc(tmem_base, C::kTmemCols);
     }
+}
+
+// Adds up the parts of every tile (spread joins).  With 64 or more token columns a part is 64 KB or
+// more, and one SM reads about 55 GB/s: the last arrival of nine would take 11 us to join them,
+// while all SMs together read all tiles' parts in about 2.  One CTA per (tile, kSpreadCols columns),
+// thread = row of the tile; the parts are added in share order, eight in flight.
+constexpr int kSpreadCols = 4;
+template <int BN>
+__global__ void __launch_bounds__(256) stream_reduce_kernel(const int* spread, const float* part, int tokens, int out_rows,
+                                                            void* d, int d_f32) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int kChunk = 16, kHalf = BN / 2;
+    StreamPlan pl;
+    pl.units = __ldcg(spread + kSpreadUnits);
+    pl.shares = __ldcg(spread + kSpreadShares);
+    pl.nk = __ldcg(spread + kSpreadNk);
+    pl.pieces = __ldcg(spread + kSpreadPieces);
+    pl.q = pl.units / pl.shares;
+    pl.r = pl.units - pl.q * pl.shares;
+    const int tile = blockIdx.x, c0 = blockIdx.y * kSpreadCols;
+    const int row = threadIdx.x & 127, blk = threadIdx.x >> 7;
+    const int cols = min(kSpreadCols, tokens - c0);
+    float v[kSpreadCols] = {};
+    if (pl.units > 0) {
+        int first, last;
+        const int first_unit = tile * pl.nk;
+        shares_of(pl, first_unit, pl.nk, first, last);
+        // [half][chunk][block][column][row] within a part
+        const int in_half = c0 % kHalf;
+        const float* at = part + (c0 / kHalf) * 2 * kHalf * 128 +
+                          (2 * (in_half / kChunk * kChunk) + blk * kChunk + in_half % kChunk) * 128 + row;
+        for (int c = first; c <= last; c += 8) {
+            float x[8][kSpreadCols];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int cc = min(c + u, last);
+                const float* src = at + (2LL * cc + (share_begin(pl, cc) > first_unit ? 0 : 1)) * 2 * BN * 128;
+#pragma unroll
+                for (int i = 0; i < kSpreadCols; ++i) x[u][i] = i < cols ? __ldcg(src + i * 128) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u <= last) {
+#pragma unroll
+                    for (int i = 0; i < kSpreadCols; ++i) v[i] += x[u][i];
+                }
+        }
+    }
+    const int r = tile * 256 + blk * 128 + row;
+    if (r >= out_rows) return;
+    const long long out = (long long)c0 * out_rows + r;
+#pragma unroll
+    for (int i = 0; i < kSpreadCols; ++i) {
+        if (i >= cols) break;
+        if (d_f32) static_cast<float*>(d)[out + (long long)i * out_rows] = v[i];
+        else static_cast<__nv_bfloat16*>(d)[out + (long long)i * out_rows] = __float2bfloat16(v[i]);
+    }
+}
+
+inline cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_tiles), static_cast<unsigned>((p.tokens + kSpreadCols - 1) / kSpreadCols));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (p.pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const int* spread = p.spread;
+    const float* part = p.part;
+    return bn == 64 ? cudaLaunchKernelEx(&cfg, stream_reduce_kernel<64>, spread, part, p.tokens, p.out_rows, p.d, p.d_f32)
+                    : cudaLaunchKernelEx(&cfg, stream_reduce_kernel<128>, spread, part, p.tokens, p.out_rows, p.d, p.d_f32);
 }
 
 template <int kMode, int BN, bool kFp4>
