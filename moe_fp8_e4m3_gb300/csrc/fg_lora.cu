@@ -46,14 +46,22 @@ bool shapes_ok(int M, int N, int K, int R) {
 }
 
 // ---------------------------------------------------------------- v = scaling * x @ A^T
-// A work item is (distinct adapter of a token tile, 8 * NB of the tokens that use it); a token
-// tile's CTAs share its items.  The adapter's rows are the M operand of mma.sync (MB blocks of
-// 16), its tokens the N operand (NB blocks of 8), gathered by their row numbers.  The 16 warps split K and read both operands
+// Two ways through one kernel, taken per token tile by how many tokens share an adapter.
+//
+// Few (a decode batch): a work item is (distinct adapter, 8 of the tokens that use it), dealt to
+// the tile's CTAs.  The adapter's rows are the M operand of mma.sync (MB blocks of 16), its tokens
+// the N operand, gathered by their row numbers.  The 16 warps split K and read both operands
 // straight into registers, 16 bytes (8 consecutive k) per row and lane: k is summed over, so a
 // lane's 8 values may stand for any k as long as A and x agree; they feed two 16-wide steps.
-// There is nothing to stage: each A element is used by one CTA (latency-bound: its bytes in
-// flight are what counts, U blocks of 32 k per warp), and tcgen05's 128 rows would be mostly
-// empty.  The partial sums meet in shared memory, in warp order.
+// There is nothing to stage: each A element is used once (latency-bound: its bytes in flight are
+// what counts, U blocks of 32 k per warp), and tcgen05's 128 rows would be mostly empty.  The
+// partial sums meet in shared memory, in warp order.
+//
+// Many (a prompt's tile of 128 tokens, from 8 tokens per adapter): tcgen05 with the tokens as 128
+// rows and up to 256 rank columns of the tile's adapters.  K is split over a cluster of CTAs
+// (each streams its few 64-wide chunks through a TMA ring), the partial sums meet through
+// distributed shared memory: the CTAs take four tokens in turn and add them up in rank order.  (2048 tokens x
+// 4096, rank 64, five prompts: 36 us by the first way, each 32 tokens re-reading their adapter.)
 struct ShrinkParams {
     int tokens, bn, K, R, rp, L, max_slots, parts;
     const int32_t* ids;
@@ -64,9 +72,19 @@ struct ShrinkParams {
     int* slot_ids;
     int* slot_count;
     int* status;
+    unsigned long long timeout_ns;
+};
+struct ShrinkMaps {
+    CUtensorMap x;              // [tokens][K], boxes of 128 rows x 64
+    CUtensorMap a;              // [L][R][K], boxes of rp rows x 64
 };
 
 constexpr int kShrinkWarps = 16;
+constexpr int kShrinkCluster = 6;                 // measured on GB300: of 16 clusters of 8 one waits for SMs, of 6 none
+constexpr int kTcStages = 4, kTcXBytes = 128 * 128, kTcABytes = 256 * 128;
+constexpr int kTcPitch = 132;                     // floats per column of the exchange buffer (128 tokens + 4)
+constexpr int kTcSmem = kTcStages * (kTcXBytes + kTcABytes) + 1024;
+static_assert(256 * kTcPitch * 4 <= kTcStages * (kTcXBytes + kTcABytes), "the exchange buffer takes the ring's place");
 
 __device__ __forceinline__ void mma_bf16_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                  uint32_t b0, uint32_t b1) {
@@ -85,47 +103,29 @@ __device__ __forceinline__ void store_parts(uint16_t* dst, long long stride, int
     }
 }
 
-template <int MB, int NB, int U>
-__global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const ShrinkParams p) {
-    constexpr int kTok = 8 * NB;
-    __shared__ uint32_t bits[32];
-    __shared__ uint16_t list[fg::kMaxListed];
-    __shared__ int listed;
-    __shared__ int16_t slot_of[128];              // of each token of the tile, -1 without an adapter
-    __shared__ int count[128], first_item[129];   // tokens of each slot, items before it
-    __shared__ int16_t member[128];               // tokens that use the item's adapter, in order
-    __shared__ float red[kShrinkWarps / 2][MB * 16][kTok];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tt = blockIdx.y;
-    fg::grid_dependency_wait();
-    if (threadIdx.x == 0) fg::grid_launch_dependents();
-    const int n = min(p.bn, p.tokens - tt * p.bn);
-    const int32_t* ids = p.ids + (long long)tt * p.bn;
-    const int my_id = threadIdx.x < static_cast<unsigned>(n) ? __ldcg(ids + threadIdx.x) : -1;
-    if (threadIdx.x < 128) count[threadIdx.x] = 0;
-    fg::list_distinct(ids, n, 0, p.L, bits, list, &listed);
-    const int slots = listed;
-    if (threadIdx.x < 128) {
-        int slot = -1;
-        if (my_id >= 0 && my_id < p.L)            // its rank in the list
-            for (int lo = 0, hi = slots; lo < hi;) {
-                const int mid = (lo + hi) / 2;
-                if (list[mid] <= my_id) { slot = mid; lo = mid + 1; }
-                else hi = mid;
-            }
-        slot_of[threadIdx.x] = static_cast<int16_t>(slot);
-        if (slot >= 0) atomicAdd(count + slot, 1);
-    }
-    if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < slots; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = list[i];
-        if (threadIdx.x == 0) p.slot_count[tt] = slots;
-        if (my_id >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
-    }
-    __syncthreads();
+// What both ways know of the tile: its distinct adapters and each token's place among them.
+struct TileShared {
+    uint32_t bits[32];
+    uint16_t list[fg::kMaxListed];
+    int listed;
+    int16_t slot_of[128];               // of each token of the tile, -1 without an adapter
+    int count[128], first_item[129];    // tokens of each slot, work items before it
+    int16_t member[128];                // tokens that use the item's adapter, in order
+    float scale[128];                   // of each slot's adapter
+};
+
+// The few-tokens way: items first, first + stride, ...
+template <int MB, int U>
+__device__ __forceinline__ void shrink_items(const ShrinkParams& p, TileShared& sh,
+                                             float (&red)[kShrinkWarps / 2][MB * 16][8], int tt, int n, int first_of_cta,
+                                             int stride) {
+    constexpr int kTok = 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = sh.listed;
     if (warp == 0) {                              // items of each slot, four slots a lane, and their prefix sums
         int c[4], sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            c[i] = (count[4 * lane + i] + kTok - 1) / kTok;
+            c[i] = (sh.count[4 * lane + i] + kTok - 1) / kTok;
             sum += c[i];
         }
         int incl = sum;
@@ -137,138 +137,330 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
         int at = incl - sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            first_item[4 * lane + i] = at;
+            sh.first_item[4 * lane + i] = at;
             at += c[i];
         }
-        if (lane == 31) first_item[128] = at;
+        if (lane == 31) sh.first_item[128] = at;
     }
     __syncthreads();
-    const int items = first_item[128];
+    const int items = sh.first_item[128];
     const long long part = (long long)p.bn * p.rp;
     const int g = lane >> 2, q = lane & 3;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    int slot = 0;
-    for (int lo = 0, hi = slots; lo < hi;) {      // the last slot whose first item is not behind `item`
-        const int mid = (lo + hi) / 2;
-        if (first_item[mid] <= item) { slot = mid; lo = mid + 1; }
-        else hi = mid;
-    }
-    const int first = (item - first_item[slot]) * kTok, id = list[slot];
-    uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
-    __syncthreads();                              // the item before is done with member
-    if (warp == 0) {
-        int members = 0;
-        for (int t0 = 0; t0 < p.bn; t0 += 32) {
-            const bool mine = t0 + lane < n && slot_of[t0 + lane] == slot;
-            const uint32_t m = __ballot_sync(0xffffffffu, mine);
-            if (mine) member[members + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(t0 + lane);
-            members += __popc(m);
+    for (int item = first_of_cta; item < items; item += stride) {
+        int slot = 0;
+        for (int lo = 0, hi = slots; lo < hi;) {      // the last slot whose first item is not behind `item`
+            const int mid = (lo + hi) / 2;
+            if (sh.first_item[mid] <= item) { slot = mid; lo = mid + 1; }
+            else hi = mid;
         }
-    } else {
-        // the other tokens' rows are zero: they are multiplied with this adapter's B too
-        if (first == 0) {
-            const int per = p.rp / 8;             // 16-byte pieces of a row
+        const int first = (item - sh.first_item[slot]) * kTok, id = sh.list[slot];
+        uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * p.bn * p.rp;
+        __syncthreads();                              // the item before is done with member
+        if (warp == 0) {
+            int members = 0;
+            for (int t0 = 0; t0 < p.bn; t0 += 32) {
+                const bool mine = t0 + lane < n && sh.slot_of[t0 + lane] == slot;
+                const uint32_t m = __ballot_sync(0xffffffffu, mine);
+                if (mine) sh.member[members + __popc(m & ((1u << lane) - 1))] = static_cast<int16_t>(t0 + lane);
+                members += __popc(m);
+            }
+        } else if (first == 0) {
+            // the other tokens' rows are zero: they are multiplied with this adapter's B too
+            const int per = p.rp / 8;                 // 16-byte pieces of a row
             for (int i = threadIdx.x - 32; i < p.parts * p.bn * per; i += blockDim.x - 32) {
-                const int row = i / per, t = row % p.bn;
-                if (t >= n || slot_of[t] != slot) *reinterpret_cast<uint4*>(v + (long long)i * 8) = zero;
+                const int t = i / per % p.bn;
+                if (t >= n || sh.slot_of[t] != slot) *reinterpret_cast<uint4*>(v + (long long)i * 8) = zero;
             }
         }
-    }
-    __syncthreads();
-    const int mine = min(kTok, count[slot] - first);
-    const float scale = __ldg(p.scaling + id);
-    // rows by their offset in 16-byte pieces from the tile's and the adapter's first, -1: none
-    const uint4* xb = reinterpret_cast<const uint4*>(p.x + (long long)tt * p.bn * p.K) + q;
-    const uint4* ab = reinterpret_cast<const uint4*>(p.lora_a + (long long)id * p.R * p.K) + q;
-    int xrow[NB];
+        __syncthreads();
+        const int mine = min(kTok, sh.count[slot] - first);
+        const float scale = sh.scale[slot];
+        // rows by their offset in 16-byte pieces from the tile's and the adapter's first, -1: none
+        const uint4* xb = reinterpret_cast<const uint4*>(p.x + (long long)tt * p.bn * p.K) + q;
+        const uint4* ab = reinterpret_cast<const uint4*>(p.lora_a + (long long)id * p.R * p.K) + q;
+        const int xrow = g < mine ? sh.member[first + g] * (p.K / 8) : -1;
+        const int blocks = p.K / 32;                  // 64 bytes of a row each: four lanes' 16
+        for (int m0 = 0; m0 < p.rp; m0 += 16 * MB) {
+            float acc[MB][4] = {};
+            int arow[MB][2];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) xrow[j] = 8 * j + g < mine ? member[first + 8 * j + g] * (p.K / 8) : -1;
-    const int blocks = p.K / 32;                   // 64 bytes of a row each: four lanes' 16
-    for (int m0 = 0; m0 < p.rp; m0 += 16 * MB) {
-        float acc[MB][NB][4] = {};
-        int arow[MB][2];
+            for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+                for (int h = 0; h < 2; ++h) {
+                    const int r = m0 + 16 * i + 8 * h + g;
+                    arow[i][h] = r < p.R ? r * (p.K / 8) : -1;
+                }
+            for (int b0 = warp; b0 < blocks; b0 += kShrinkWarps * U) {
+                uint4 a[U][MB][2], x[U];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = m0 + 16 * i + 8 * h + g;
-                arow[i][h] = r < p.R ? r * (p.K / 8) : -1;
-            }
-        for (int b0 = warp; b0 < blocks; b0 += kShrinkWarps * U) {
-            uint4 a[U][MB][2], x[U][NB];
+                for (int u = 0; u < U; ++u) {
+                    const int b = b0 + u * kShrinkWarps;
+                    const bool in = b < blocks;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int b = b0 + u * kShrinkWarps;
-                const bool in = b < blocks;
+                    for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int i = 0; i < MB; ++i)
+                        for (int h = 0; h < 2; ++h) a[u][i][h] = in && arow[i][h] >= 0 ? __ldg(ab + arow[i][h] + b * 4) : zero;
+                    x[u] = in && xrow >= 0 ? __ldg(xb + xrow + b * 4) : zero;
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) a[u][i][h] = in && arow[i][h] >= 0 ? __ldg(ab + arow[i][h] + b * 4) : zero;
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) x[u][j] = in && xrow[j] >= 0 ? __ldg(xb + xrow[j] + b * 4) : zero;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < MB; ++i)
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        mma_bf16_16x8x16(acc[i][j], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, x[u][j].x, x[u][j].y);
-                        mma_bf16_16x8x16(acc[i][j], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, x[u][j].z, x[u][j].w);
+                    for (int i = 0; i < MB; ++i) {
+                        mma_bf16_16x8x16(acc[i], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, x[u].x, x[u].y);
+                        mma_bf16_16x8x16(acc[i], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, x[u].z, x[u].w);
                     }
-        }
-        // the upper eight warps' sums first, then the lower eight add theirs
+            }
+            // the upper eight warps' sums first, then the lower eight add theirs
 #pragma unroll
-        for (int pass = 1; pass >= 0; --pass) {
-            if (warp / 8 == pass) {
+            for (int pass = 1; pass >= 0; --pass) {
+                if (warp / 8 == pass) {
 #pragma unroll
-                for (int i = 0; i < MB; ++i)
-#pragma unroll
-                    for (int j = 0; j < NB; ++j)
+                    for (int i = 0; i < MB; ++i)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            float& at = red[warp & 7][16 * i + g + 8 * (c >> 1)][8 * j + 2 * q + (c & 1)];
-                            at = pass ? acc[i][j][c] : at + acc[i][j][c];
+                            float& at = red[warp & 7][16 * i + g + 8 * (c >> 1)][2 * q + (c & 1)];
+                            at = pass ? acc[i][c] : at + acc[i][c];
                         }
+                }
+                __syncthreads();
+            }
+            for (int o = threadIdx.x; o < MB * 16 * mine; o += blockDim.x) {
+                const int r = o % (MB * 16), t = o / (MB * 16);
+                float sum = red[0][r][t];
+#pragma unroll
+                for (int w = 1; w < kShrinkWarps / 2; ++w) sum += red[w][r][t];
+                if (m0 + r < p.rp) store_parts(v + (long long)sh.member[first + t] * p.rp + m0 + r, part, p.parts, scale * sum);
             }
             __syncthreads();
         }
-        for (int o = threadIdx.x; o < MB * 16 * mine; o += blockDim.x) {
-            const int r = o % (MB * 16), t = o / (MB * 16);
-            float sum = red[0][r][t];
-#pragma unroll
-            for (int w = 1; w < kShrinkWarps / 2; ++w) sum += red[w][r][t];
-            if (m0 + r < p.rp) store_parts(v + (long long)member[first + t] * p.rp + m0 + r, part, p.parts, scale * sum);
-        }
-        __syncthreads();
     }
+}
+
+// The many-tokens way: groups of up to 256 rank columns, one per cluster and round.
+__device__ __forceinline__ void shrink_tcgen05(const ShrinkParams& p, const ShrinkMaps& maps, TileShared& sh, uint8_t* ring,
+                                               uint64_t* bars, uint32_t* tmem_slot, int* abort_word, int tt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = sh.listed;
+    const int rank = static_cast<int>(fg::cluster_ctarank()), cluster = blockIdx.x / kShrinkCluster;
+    const int clusters = gridDim.x / kShrinkCluster;
+    const int per_group = 256 / p.rp, groups = (slots + per_group - 1) / per_group;
+    const int nk = p.K / 64, k0 = rank * nk / kShrinkCluster, k1 = (rank + 1) * nk / kShrinkCluster;
+    const uint32_t rbase = fg::smem_u32(ring), b0 = fg::smem_u32(bars);
+    auto full_bar = [&](int s) { return b0 + 8u * s; };
+    auto empty_bar = [&](int s) { return b0 + 8u * (kTcStages + s); };
+    const uint32_t done_bar = b0 + 8u * (2 * kTcStages);
+    volatile int* abort_flag = abort_word;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kTcStages; ++s) {
+            fg::mbar_init(full_bar(s), 1);
+            fg::mbar_init(empty_bar(s), 1);
+        }
+        fg::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fg::fence_mbar_init();
+        fg::tma_prefetch_map(&maps.x);
+        fg::tma_prefetch_map(&maps.a);
+    }
+    if (warp == 1) {
+        fg::tmem_alloc(fg::smem_u32(tmem_slot), 256);
+        fg::tmem_relinquish();
+    }
+    fg::tc_fence_before();
+    __syncthreads();
+    fg::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const fg::WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
+    // four TMA producers (warps 0, 2, 3, 8; one thread's loads complete one after another), one per stage
+    const int producer = warp == 0 ? 0 : (warp == 2 || warp == 3 ? warp - 1 : (warp == 8 ? 3 : -1));
+    int s = 0, loads = 0;
+    uint32_t ph = 0, done_ph = 0;
+    int before = 0;                                   // chunks of the groups before: stage of chunk c is (before + c) mod 4
+    for (int grp = cluster; grp < groups; grp += clusters) {
+        const int slot0 = grp * per_group, cnt = min(per_group, slots - slot0), cols = cnt * p.rp;
+        if (producer >= 0) {
+            if (lane == 0 && !*abort_flag)
+                for (int k = k0; k < k1; ++k) {
+                    if (((before + k - k0) & (kTcStages - 1)) != producer) continue;
+                    if (!fg::wait_bar(empty_bar(producer), (loads & 1) ^ 1, wctl, fg::kWaitProducer)) break;
+                    const uint32_t dst = rbase + producer * (kTcXBytes + kTcABytes), fb = full_bar(producer);
+                    fg::mbar_arrive_expect_tx(fb, kTcXBytes + cols * 128);
+                    fg::tma_load_2d(dst, &maps.x, fb, k * 64, tt * p.bn);
+                    for (int i = 0; i < cnt; ++i)
+                        fg::tma_load_3d(dst + kTcXBytes + i * p.rp * 128, &maps.a, fb, k * 64, 0, sh.list[slot0 + i]);
+                    ++loads;
+                }
+            __syncwarp();
+        } else if (warp == 1) {
+            const uint32_t idesc = fg::make_idesc_bf16(128, 0) | static_cast<uint32_t>(cols >> 3) << 17;
+            bool ok = true;
+            for (int k = k0; k < k1; ++k) {
+                ok = __all_sync(0xffffffffu, fg::wait_bar(full_bar(s), ph, wctl, fg::kWaitMma)) != 0;
+                if (!ok) break;
+                fg::tc_fence_after();
+                if (fg::elect_one()) {
+                    const uint32_t at = rbase + s * (kTcXBytes + kTcABytes);
+                    const uint64_t xd = fg::make_sdesc(at, 0, 1024, fg::kLayoutSw128);
+                    const uint64_t ad = fg::make_sdesc(at + kTcXBytes, 0, 1024, fg::kLayoutSw128);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) fg::tc_mma_bf16(tmem, xd + 2 * j, ad + 2 * j, idesc, (k > k0 || j) ? 1u : 0u);
+                    fg::tc_commit(empty_bar(s));
+                }
+                __syncwarp();
+                if (++s == kTcStages) { s = 0; ph ^= 1u; }
+            }
+            // also on the way out: no product of this CTA is in flight behind this
+            if (fg::elect_one()) fg::tc_commit(done_bar);
+            __syncwarp();
+        }
+        before += k1 - k0;
+        const bool ok = fg::wait_bar(done_bar, done_ph, wctl, fg::kWaitEpilogue);
+        done_ph ^= 1u;
+        (void)ok;                                     // on a time-out the sums are wrong, and reported
+        fg::tc_fence_after();
+        float* xch = reinterpret_cast<float*>(ring);  // [column][token], pitch kTcPitch
+        if (warp >= 4 && warp < 8 && k1 > k0) {
+            const int row = (warp & 3) * 32 + lane;
+            for (int c0 = 0; c0 < cols; c0 += 16) {
+                uint32_t r[16];
+                fg::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, r);
+                fg::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) xch[(c0 + i) * kTcPitch + row] = __uint_as_float(r[i]);
+            }
+        }
+        fg::tc_fence_before();
+        __syncwarp();
+        fg::cluster_sync();
+        // four tokens at a time, rank's: thread = (column, four tokens), the partials in rank order
+        const uint32_t xbase = fg::smem_u32(xch);
+        const long long part = (long long)p.bn * p.rp;
+        for (int o = threadIdx.x; o < cols * ((31 - rank) / kShrinkCluster + 1); o += blockDim.x) {
+            const int col = o % cols, t0 = (rank + o / cols * kShrinkCluster) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 x[kShrinkCluster];
+#pragma unroll
+            for (int r = 0; r < kShrinkCluster; ++r)
+                x[r] = r * nk / kShrinkCluster < (r + 1) * nk / kShrinkCluster
+                           ? fg::ld_dsmem_f32x4(fg::map_shared_rank(xbase + (col * kTcPitch + t0) * 4, r))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kShrinkCluster; ++r) {
+                sum.x += x[r].x; sum.y += x[r].y; sum.z += x[r].z; sum.w += x[r].w;
+            }
+            const int i = col / p.rp, rr = col - i * p.rp, slot = slot0 + i;
+            const float scale = sh.scale[slot];
+            const float val[4] = {sum.x, sum.y, sum.z, sum.w};
+            uint16_t* v = p.v + ((long long)tt * p.max_slots + slot) * p.parts * part + rr;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)               // another adapter's tokens are zero rows
+                store_parts(v + (long long)(t0 + t) * p.rp, part, p.parts, sh.slot_of[t0 + t] == slot ? scale * val[t] : 0.0f);
+        }
+        fg::fence_proxy_async_smem();                 // the ring is TMA's again
+        __syncwarp();
+        fg::cluster_sync();
+    }
+    if (producer >= 0 && lane == 0 && *abort_flag && loads > 0)
+        fg::drain_bar(full_bar(producer), (loads - 1) & 1, 20000000ull);
+    __syncthreads();
+    if (warp == 1) {
+        fg::tc_fence_after();
+        fg::tmem_dealloc(tmem, 256);
+    }
+}
+
+template <int MB, int U, bool kClusters>
+__global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const ShrinkParams p, const __grid_constant__ ShrinkMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TileShared sh;
+    __shared__ float red[kShrinkWarps / 2][MB * 16][8];
+    __shared__ uint64_t bars[2 * kTcStages + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    const int tt = blockIdx.y;
+    fg::grid_dependency_wait();
+    if (threadIdx.x == 0) fg::grid_launch_dependents();
+    const int n = min(p.bn, p.tokens - tt * p.bn);
+    const int32_t* ids = p.ids + (long long)tt * p.bn;
+    const int my_id = static_cast<int>(threadIdx.x) < n ? __ldcg(ids + threadIdx.x) : -1;
+    if (threadIdx.x < 128) sh.count[threadIdx.x] = 0;
+    fg::list_distinct(ids, n, 0, p.L, sh.bits, sh.list, &sh.listed);
+    const int slots = sh.listed;
+    if (threadIdx.x < 128) {
+        int slot = -1;
+        if (my_id >= 0 && my_id < p.L)            // its rank in the list
+            for (int lo = 0, hi = slots; lo < hi;) {
+                const int mid = (lo + hi) / 2;
+                if (sh.list[mid] <= my_id) { slot = mid; lo = mid + 1; }
+                else hi = mid;
+            }
+        sh.slot_of[threadIdx.x] = static_cast<int16_t>(slot);
+        if (slot >= 0) atomicAdd(sh.count + slot, 1);
+        if (static_cast<int>(threadIdx.x) < slots) sh.scale[threadIdx.x] = __ldg(p.scaling + sh.list[threadIdx.x]);
+    }
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < slots; i += blockDim.x) p.slot_ids[tt * p.max_slots + i] = sh.list[i];
+        if (threadIdx.x == 0) p.slot_count[tt] = slots;
+        if (my_id >= p.L) fg::record_status(p.status, fg::kErrContract | fg::kChkAdapter);
+    }
+    __syncthreads();
+    if (kClusters && n >= 8 * slots) {
+        uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+        shrink_tcgen05(p, maps, sh, ring, bars, &tmem_slot, &abort_word, tt);
+    } else {
+        shrink_items<MB, U>(p, sh, red, tt, n, blockIdx.x, gridDim.x);
     }
     fg::fence_proxy_async_global();
 }
 
-cudaError_t launch_shrink(const ShrinkParams& p, int tiles, int sms, int pdl, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(32 * kShrinkWarps);
-    cfg.stream = stream;
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+template <int MB, int U, bool kClusters>
+cudaError_t launch_shrink_as(const ShrinkParams& p, const ShrinkMaps& maps, dim3 grid, int pdl, cudaStream_t stream) {
+    static bool configured[256] = {};        // set once per device; setting it again is harmless
+    const int smem = kClusters ? kTcSmem : 0;
+    if (kClusters) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
+        if (!configured[dev]) {
+            err = cudaFuncSetAttribute(lora_shrink_kernel<MB, U, kClusters>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (err != cudaSuccess) return err;
+            configured[dev] = true;
+        }
     }
-    auto go = [&](auto kernel, int tok) {
-        // a tile has at most min(bn, L) + bn / tok items; one CTA an item, as far as one wave of SMs goes
-        const int most = (p.L < p.bn ? p.L : p.bn) + p.bn / tok;
-        const int share = sms / tiles > 1 ? sms / tiles : 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(tiles));
-        return cudaLaunchKernelEx(&cfg, kernel, p);
-    };
-    // 8 tokens at a time where there are few per adapter (small tiles), 32 in a prompt's tiles
-    if (p.bn <= 64)
-        return p.rp <= 16 ? go(lora_shrink_kernel<1, 1, 8>, 8) : go(lora_shrink_kernel<2, 1, 4>, 8);
-    return p.rp <= 16 ? go(lora_shrink_kernel<1, 4, 2>, 32) : go(lora_shrink_kernel<2, 4, 2>, 32);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * kShrinkWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (kClusters) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = kShrinkCluster;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (pdl) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<MB, U, kClusters>, p, maps);
+}
+
+cudaError_t launch_shrink(const ShrinkParams& p, const ShrinkMaps& maps, int tiles, int sms, int pdl, cudaStream_t stream) {
+    if (tiles > 1) {                              // whole clusters per tile, as far as one wave of SMs goes
+        const int clusters = sms / (kShrinkCluster * tiles) > 1 ? sms / (kShrinkCluster * tiles) : 1;
+        const dim3 grid(static_cast<unsigned>(clusters * kShrinkCluster), static_cast<unsigned>(tiles));
+        return p.rp <= 16 ? launch_shrink_as<1, 8, true>(p, maps, grid, pdl, stream)
+                          : launch_shrink_as<2, 4, true>(p, maps, grid, pdl, stream);
+    }
+    // at most min(bn, L) + bn / 8 items; one CTA an item, as far as one wave of SMs goes
+    const int most = (p.L < p.bn ? p.L : p.bn) + p.bn / 8;
+    const dim3 grid(static_cast<unsigned>(most < sms ? most : sms));
+    return p.rp <= 16 ? launch_shrink_as<1, 8, false>(p, maps, grid, pdl, stream)
+                      : launch_shrink_as<2, 4, false>(p, maps, grid, pdl, stream);
 }
 
 }  // namespace
@@ -306,8 +498,18 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
                      l.rp, grid);
     const ShrinkParams sp{M, l.bn, K, R, l.rp, L, l.bn, parts, ids, static_cast<const uint16_t*>(x),
                           static_cast<const uint16_t*>(lora_a), scaling, reinterpret_cast<uint16_t*>(ws + l.v),
-                          reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<int*>(ws + l.count), st.status};
-    if (launch_shrink(sp, l.tiles, st.sms, st.pdl, s) != cudaSuccess) {
+                          reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<int*>(ws + l.count), st.status, st.timeout_ns};
+    ShrinkMaps sm;
+    std::memset(&sm, 0, sizeof(sm));
+    if (l.tiles > 1) {
+        const uint64_t xd[2] = {(uint64_t)K, (uint64_t)M}, xp[1] = {(uint64_t)K * 2};
+        const uint64_t ad[3] = {(uint64_t)K, (uint64_t)R, (uint64_t)L}, ap[2] = {(uint64_t)K * 2, (uint64_t)K * 2 * R};
+        const uint32_t xb[2] = {64, 128}, ab[3] = {64, (uint32_t)l.rp, 1};
+        if (!fg::encode_tiled(&sm.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xp, xb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !fg::encode_tiled(&sm.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_a, ad, ap, ab, CU_TENSOR_MAP_SWIZZLE_128B))
+            return FG_ERR_INVALID_ARG;
+    }
+    if (launch_shrink(sp, sm, l.tiles, st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
         return FG_ERR_CUDA;
     }
