@@ -536,7 +536,8 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         const uint64_t ld[3] = {(uint64_t)R, (uint64_t)N, (uint64_t)L}, lp[2] = {(uint64_t)R * 2, (uint64_t)R * 2 * N};
         const uint32_t lb[3] = {cols, 256, 1};
         const uint64_t vd[2] = {(uint64_t)l.rp, (uint64_t)l.tiles * l.bn * p.parts * l.bn}, vp[1] = {(uint64_t)l.rp * 2};
-        const uint32_t vb[2] = {cols, (uint32_t)l.bn};
+        const int v_rows = (unit_cols / l.rp > 1 ? unit_cols / l.rp : 1) * parts * l.bn;   // of a unit
+        const uint32_t vb[2] = {cols, (uint32_t)(v_rows <= 256 ? v_rows : v_rows / 2)};
         if (!fg::encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, b, wd, wp, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !fg::encode_tiled(&m.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, xd, xp, xb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !fg::encode_tiled(&m.lb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_b, ld, lp, lb, sw) ||

@@ -184,10 +184,13 @@ struct StreamCfg {
     static_assert(kStages >= 3 && kSmemBytes <= kSmemLimit, "shared memory");
 };
 
-// One share's piece of one tile: units [k0, k1) of nk.
+// One share's piece of one tile: units [k0, k1) of nk.  kProj deals a tile's FP8 units and its
+// adapter units to its pieces separately (the adapter units wait for x @ A^T and take longer):
+// unit k0 + j is FP8 unit f0 + j for j < nf, then adapter unit l0 + j - nf.
 struct StreamSeg {
     int tile, tt, k0, k1, nk;
     int first_unit;      // of the tile
+    int f0, nf, l0;
     bool whole;
 };
 
@@ -195,13 +198,15 @@ struct StreamPlan {
     int units, shares, nk, row_tiles;
     int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares
     int q, r;            // equal shares: r shares of q + 1 units, then shares of q
+    int fp8;             // kProj: FP8 units of a tile
     const int* pre;      // kProj: units before each token tile
 };
 
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
     if (pl.pieces) {
         const int t = c / pl.pieces;
-        return t * pl.nk + (c - t * pl.pieces) * pl.nk / pl.pieces;
+        const int i = c - t * pl.pieces;
+        return t * pl.nk + i * pl.fp8 / pl.pieces + i * (pl.nk - pl.fp8) / pl.pieces;
     }
     return c * pl.q + min(c, pl.r);
 }
@@ -241,7 +246,7 @@ __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid,
     if (s == 0) {
         const int per = (pl.units + grid - 1) / grid;
         t = time(min(grid, pl.units), per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + (spread ? 0.0f : 2.0f);
-    } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.nk) {
+    } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.fp8) {      // (no piece is empty)
         t = time(s * tiles, (pl.nk + s - 1) / s, s);
     }
     const uint32_t best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | s);
@@ -291,6 +296,7 @@ struct StreamWalk {
             s.k1 = tail_end - tail;
             s.whole = false;
             tail = -1;
+            deal(pl, s);
             return true;
         }
         if (u >= end) return false;
@@ -299,6 +305,7 @@ struct StreamWalk {
         s.k1 = min(nk, s.k0 + (end - u));
         s.whole = s.k0 == 0 && s.k1 == nk;
         u += s.k1 - s.k0;
+        deal(pl, s);
         // the tile behind it
         first += nk;
         if (++tile == pl.row_tiles && kMode == kProj) {
@@ -308,35 +315,52 @@ struct StreamWalk {
         }
         return true;
     }
+    __device__ __forceinline__ void deal(const StreamPlan& pl, StreamSeg& s) const {
+        if (kMode != kProj) return;
+        if (pl.pieces) {
+            // k0 is the sum of both kinds' shares before piece i (the share is one piece)
+            const int i = static_cast<int>(blockIdx.x) % pl.pieces;
+            s.f0 = i * pl.fp8 / pl.pieces;
+            s.nf = (i + 1) * pl.fp8 / pl.pieces - s.f0;
+            s.l0 = i * (pl.nk - pl.fp8) / pl.pieces;
+        } else {
+            s.f0 = min(s.k0, pl.fp8);
+            s.nf = min(s.k1, pl.fp8) - s.f0;
+            s.l0 = max(s.k0, pl.fp8) - pl.fp8;
+        }
+    }
     __device__ __forceinline__ bool done() const { return tail < 0 && u >= end; }
 };
 
-// Walks a share unit by unit.  li, kl: kDown's expert (list index) and K-group within it (else
-// kl == k); no division per unit.
+// Walks a share unit by unit.  k: K-group, from `fp8` on adapter units (kProj).  li, kl: kDown's
+// expert (list index) and K-group within it (else kl == k); no division per unit.
 template <int kMode>
 struct StreamCursor {
     StreamWalk<kMode> walk;
     StreamSeg sg;
-    int k, li, kl, per;
+    int at, k, li, kl, per;
     bool valid;
     __device__ __forceinline__ StreamCursor(const StreamPlan& pl, const StreamWalk<kMode>& from, int per_expert)
-        : walk(from), k(0), li(0), kl(0), per(per_expert) { enter(pl); }
+        : walk(from), at(0), k(0), li(0), kl(0), per(per_expert) { enter(pl); }
     __device__ __forceinline__ void enter(const StreamPlan& pl) {
         valid = walk.next(pl, sg);
         if (!valid) return;
-        k = kl = sg.k0;
+        at = k = kl = sg.k0;
         if (kMode == kDown) { li = k / per; kl = k - li * per; }
+        if (kMode == kProj) { at = 0; k = kl = sg.nf > 0 ? sg.f0 : pl.fp8 + sg.l0; }
     }
     __device__ __forceinline__ void step(const StreamPlan& pl) {
+        ++at;
         ++k;
         ++kl;
         if (kMode == kDown && kl == per) { kl = 0; ++li; }
-        if (k == sg.k1) enter(pl);
+        if (kMode == kProj && at == sg.nf) k = kl = pl.fp8 + sg.l0;
+        if (at == (kMode == kProj ? sg.k1 - sg.k0 : sg.k1)) enter(pl);
     }
     // the unit brings new scale words: FP4 weights every K-group, else at the segment's first and
     // every fourth K-group
     __device__ __forceinline__ bool new_words(bool fp4, int fp8_units) const {
-        return (kMode != kProj || k < fp8_units) && (fp4 || k == sg.k0 || (kl & 3) == 0);
+        return (kMode != kProj || k < fp8_units) && (fp4 || at == (kMode == kProj ? 0 : sg.k0) || (kl & 3) == 0);
     }
 };
 
@@ -480,6 +504,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     pl.pre = pre;
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
+    pl.fp8 = kMode == kProj ? p.nk : pl.nk;
     plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
                 kMoe || one_tile, p.spread != nullptr);
     const int share = static_cast<int>(blockIdx.x);
@@ -569,13 +594,14 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 armed_par = (armed_par & ~(1u << s)) | (ph << s);
                 if (kMode == kProj && c.k >= p.nk) {
                     const int u = c.k - p.nk;
-                    const int nslots = slots_of(c.sg.tt);
                     const int s0 = pieces > 1 ? u / pieces : u * per_unit;
-                    const int cnt = min(per_unit, nslots - s0);
-                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cnt * p.parts * BN * rb));
-                    for (int j = 0; j < cnt * p.parts; ++j)      // an adapter's parts follow one another
-                        tma_load_2d(dst + j * BN * rb, &maps.v, fb, pieces > 1 ? (u % pieces) * ucols : 0,
-                                    ((c.sg.tt * p.max_slots + s0) * p.parts + j) * BN);
+                    // an adapter's parts follow one another, and the adapters: one piece of v (past
+                    // the last adapter it is not used)
+                    const int rows = per_unit * p.parts * BN, box = rows <= 256 ? rows : rows / 2;
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(rows * rb));
+                    for (int j = 0; j < rows; j += box)
+                        tma_load_2d(dst + j * rb, &maps.v, fb, pieces > 1 ? (u % pieces) * ucols : 0,
+                                    (c.sg.tt * p.max_slots + s0) * p.parts * BN + j);
                 } else {
                     mbar_arrive_expect_tx(fb, BN * 128);
                     if constexpr (kMode == kDown) tma_load_2d(dst, &maps.x, fb, c.kl * 128, c.li * BN);
@@ -638,14 +664,15 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 tc_fence_after();
                 const uint32_t dt = tmem_base + (acc * 2 + blk) * BN;
                 uint32_t add = 0;                     // 0: the first product of the segment overwrites
-                int kl = kMode == kDown ? sg.k0 % p.nk : sg.k0;      // K-group (kDown: within the expert)
-                for (int k = sg.k0; k < sg.k1; ++k) {
+                int kl = kMode == kDown ? sg.k0 % p.nk : (kMode == kProj ? sg.f0 : sg.k0);   // K-group (kDown: within the expert)
+                for (int i = 0; i < sg.k1 - sg.k0; ++i) {
+                    const bool lora_unit = kMode == kProj && i >= sg.nf;
                     if (!wait_all(full_bar(s), ph)) { aborted = true; break; }
                     tc_fence_after();
                     const uint64_t ad = a0 + static_cast<uint64_t>((s * C::kABytes) >> 4);
                     const uint64_t bd = b0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
-                    if (kMode == kProj && k >= p.nk) {
-                        if (k == p.nk && add) {
+                    if (lora_unit) {
+                        if (i == sg.nf && add) {
                             // let the scaled FP8 products finish before another kind adds to their sums
                             if (elect_one()) tc_commit(turn_of(blk));
                             __syncwarp();
@@ -653,7 +680,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             turn_ph ^= 1u;
                             tc_fence_after();
                         }
-                        const int u = k - p.nk;
+                        const int u = sg.l0 + i - sg.nf;
                         const int nslots = slots_of(sg.tt);
                         const int cnt = pieces > 1 ? 1 : min(per_unit, nslots - u * per_unit);
                         if (elect_one()) {
@@ -661,8 +688,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             uint64_t bj = lb0 + static_cast<uint64_t>((s * C::kBBytes) >> 4);
                             uint32_t keep = add;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (i >= cnt) break;
+                            for (int n = 0; n < 4; ++n) {
+                                if (n >= cnt) break;
 #pragma unroll
                                 for (int o = 0; o < 3; ++o) {
                                     if (o >= p.parts) break;
@@ -681,7 +708,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         add = 1;
                     } else {
                         const uint32_t sf_id = static_cast<uint32_t>(kl) & 3u;
-                        const bool words = kFp4 || k == sg.k0 || sf_id == 0;
+                        const bool words = kFp4 || i == 0 || sf_id == 0;
                         if (words) ++kcount;
                         const uint32_t t = sf0 + (kcount % kSfSlots) * 16;
                         if (elect_one()) {
@@ -1082,6 +1109,7 @@ __global__ void __launch_bounds__(256) stream_reduce_kernel(const int* spread, c
     pl.pieces = __ldcg(spread + kSpreadPieces);
     pl.q = pl.units / pl.shares;
     pl.r = pl.units - pl.q * pl.shares;
+    pl.fp8 = pl.nk;
     const int tile = blockIdx.x, c0 = blockIdx.y * kSpreadCols;
     const int row = threadIdx.x & 127, blk = threadIdx.x >> 7;
     const int cols = min(kSpreadCols, tokens - c0);
