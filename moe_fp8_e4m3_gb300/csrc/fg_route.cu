@@ -1,11 +1,13 @@
 // fg_route.cu - MoE router: logits -> top-k expert ids and routing weights.
 //
-// One warp per token, the token's E logits in its registers (E / 32 per lane).  The k-th best
-// expert is found k times: each lane keeps its best key, one warp-wide integer maximum over
-// order-preserving bits finds the winner, one minimum over the winners' indices breaks ties to
-// the lowest expert, and only the winning lane looks for its next best.  Bound: latency for few
-// tokens, instruction issue (about 60 warp instructions per chosen expert) for many; the bytes,
-// 4 E per token, are read once.
+// One warp per token, the token's E logits in its registers (E / 32 per lane) as keys whose
+// unsigned order is the floats'.  The k-th best expert is found k times: each lane keeps its best
+// key, one warp-wide integer maximum finds the winner, the lowest of the winners' indices breaks a
+// tie, and the winning lane looks for its next best.  Scores of all experts are worked out only
+// where something needs them (a bias, or softmax weights that are not renormalised): else the
+// chosen logits, one per lane, are enough, since a common factor cancels.
+// Bound: latency for few tokens, instruction issue for many; the bytes, 4 E per token, are read
+// once.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -40,7 +42,12 @@ __device__ __forceinline__ uint32_t ordered_any(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-template <int V>
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return k == 0 ? kNegInf : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// kScores: every expert's score is needed (see above).
+template <int V, bool kScores>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p) {
     extern __shared__ float keys_s[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -50,97 +57,116 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p)
     if (t >= p.T) return;
     constexpr uint32_t kAll = 0xffffffffu;
     float s[V];
+    uint32_t key[V];
     const float* row = p.logits + (long long)t * p.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         s[i] = e < p.E ? __ldcg(row + e) : kNegInf;
-        if (!(s[i] == s[i])) s[i] = kNegInf;               // NaN: never chosen, no share of the softmax
     }
-    uint32_t key[V];
-    float top = kNegInf;
+    float bias[V];                                            // loaded beside the logits
+    if (kScores && p.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        top = fmaxf(top, s[i]);
-        key[i] = ordered(s[i]);
+        for (int i = 0; i < V; ++i) bias[i] = i * 32 + lane < p.E ? __ldg(p.bias + i * 32 + lane) : 0.0f;
     }
-    if (p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = 1.0f / (1.0f + expf(-s[i]));       // 0 for -inf
-    } else {
+    for (int i = 0; i < V; ++i) key[i] = ordered(s[i]);       // NaN and -inf: never chosen
+    if constexpr (kScores) {
+        if (p.sigmoid) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        float sum = 0.0f;
+            for (int i = 0; i < V; ++i) s[i] = key[i] ? 1.0f / (1.0f + expf(-s[i])) : 0.0f;
+        } else {
+            uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s[i] = s[i] > kNegInf ? expf(s[i] - top) : 0.0f;
-            sum += s[i];
+            for (int i = 0; i < V; ++i) best = max(best, key[i]);
+            const float top = value_of(__reduce_max_sync(kAll, best));
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = key[i] ? expf(s[i] - top) : 0.0f;
+                sum += s[i];
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = sum > 0.0f ? s[i] / sum : (sum == sum ? 0.0f : sum);
         }
+        if (p.bias) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = sum > 0.0f ? s[i] / sum : (sum == sum ? 0.0f : sum);
-    }
-    if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i]) key[i] = ordered(s[i] + __ldg(p.bias + i * 32 + lane));
+            for (int i = 0; i < V; ++i)
+                if (key[i]) key[i] = ordered(s[i] + bias[i]);
+        }
     }
     if (p.groups > 1) {
-        // group score: its largest key, or with a bias the sum of its two largest; lane g looks at group g
+        // group score: its largest key, or with a bias the sum of its two largest.  `per_lanes` lanes
+        // (a power of two) share a group and join their two largest.
         uint32_t* ks = reinterpret_cast<uint32_t*>(keys_s) + warp * p.E;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (i * 32 + lane < p.E) ks[i * 32 + lane] = key[i];
         __syncwarp();
         const int per = p.E / p.groups;
+        const int per_lanes = 1 << (31 - __clz(32 / p.groups));
+        const int g = lane / per_lanes;
         uint32_t a = 0, b = 0;                                // two largest
-        if (lane < p.groups)
-            for (int j = 0; j < per; ++j) {
-                const uint32_t k = ks[lane * per + j];
-                if (k > a) { b = a; a = k; }
-                else if (k > b) b = k;
+        if (g < p.groups)
+            for (int j = lane & (per_lanes - 1); j < per; j += per_lanes) {
+                const uint32_t k = ks[g * per + j];
+                b = max(b, min(a, k));
+                a = max(a, k);
             }
-        auto value = [](uint32_t k) {
-            return k == 0 ? kNegInf : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-        };
-        const uint32_t score = ordered_any(p.bias && per > 1 ? value(a) + value(b) : value(a));
-        int rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const uint32_t other = __shfl_sync(kAll, score, g);
-            rank += other > score || (other == score && g < lane);
+        for (int o = 1; o < per_lanes; o <<= 1) {
+            const uint32_t a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+            b = max(min(a, a2), max(b, b2));
+            a = max(a, a2);
         }
-        const uint32_t kept = __ballot_sync(kAll, lane < p.groups && rank < p.keep);
+        const uint32_t score = ordered_any(p.bias && per > 1 ? value_of(a) + value_of(b) : value_of(a));
+        int rank = 0;
+        for (int h = 0; h < p.groups; ++h) {
+            const uint32_t other = __shfl_sync(kAll, score, h * per_lanes);
+            rank += other > score || (other == score && h < g);
+        }
+        const uint32_t kept = __ballot_sync(kAll, g < p.groups && rank < p.keep);   // bit g * per_lanes: group g
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i * 32 + lane < p.E && !(kept >> ((i * 32 + lane) / per) & 1u)) key[i] = 0;
+            if (i * 32 + lane < p.E && !(kept >> ((i * 32 + lane) / per * per_lanes) & 1u)) key[i] = 0;
     }
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
     int my_id = -1;
+    uint32_t my_key = 0;
     float my_w = 0.0f;
     for (int j = 0; j < p.topk; ++j) {
         const uint32_t m = __reduce_max_sync(kAll, best);
         if (m == 0) break;                                    // nothing left: the slots stay -1
-        uint32_t e = 0xffffffffu;
+        const uint32_t who = __ballot_sync(kAll, best == m);
+        int e = 0x7fffffff;
         if (best == m) {
 #pragma unroll
             for (int i = V - 1; i >= 0; --i)
                 if (key[i] == m) e = i * 32 + lane;
         }
-        const uint32_t win = __reduce_min_sync(kAll, e);
+        const int win = (who & (who - 1)) == 0 ? __shfl_sync(kAll, e, __ffs(who) - 1) : __reduce_min_sync(kAll, e);
         float w = 0.0f;
         if (e == win) {
             best = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (i * 32 + lane == win) { w = s[i]; key[i] = 0; }
+                if (i * 32 + lane == win) {
+                    if (kScores) w = s[i];
+                    key[i] = 0;
+                }
                 best = max(best, key[i]);
             }
         }
-        w = __shfl_sync(kAll, w, win & 31);
-        if (lane == j) { my_id = static_cast<int>(win); my_w = w; }
+        if (kScores) w = __shfl_sync(kAll, w, win & 31);
+        if (lane == j) { my_id = win; my_key = m; my_w = w; }
+    }
+    if constexpr (!kScores) {
+        // the key is the logit; the first chosen one is the largest
+        const float l = value_of(my_key), top = value_of(__shfl_sync(kAll, my_key, 0));
+        if (my_id >= 0) my_w = p.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
     }
     if (p.renormalize) {
         float sum = my_w;
@@ -168,7 +194,8 @@ cudaError_t launch(const RouteParams& p, int pdl, cudaStream_t stream) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, route_kernel<V>, p);
+    return p.bias || !(p.sigmoid || p.renormalize) ? cudaLaunchKernelEx(&cfg, route_kernel<V, true>, p)
+                                                   : cudaLaunchKernelEx(&cfg, route_kernel<V, false>, p);
 }
 
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
