@@ -84,6 +84,7 @@ struct StreamParams {
     int* status;
     unsigned long long timeout_ns;
     int debug_stall, pdl;
+    int cluster;                 // kDown, kProj: > 1: a tile's pieces, one a CTA of a cluster that joins them itself
 };
 
 // D(tmem) (+)= A(smem) x B(smem)^T, BF16 inputs, FP32 accumulation in TMEM.
@@ -144,6 +145,11 @@ template <int C>
 __device__ __forceinline__ int column_of(int lane) {
     return lane / (32 / C);          // the lane bits from the top choose the halves in turn
 }
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
 // Orders generic-proxy global writes (the codes that the next kernel loads by TMA).
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
@@ -170,7 +176,7 @@ struct StreamCfg {
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSf = kOffB + kStages * kBBytes;
     static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 4 + 2 * kJoinSlots;
+    static constexpr int kNumBars = 2 * kStages + 2 * kNumAcc + 5 + 2 * kJoinSlots;
     static constexpr int kOffMisc = kOffBar + 512 - 64;                     // TMEM address, abort flag, count, last flag
     static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
     static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
@@ -409,6 +415,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     // per issuer: its MMAs done, on the way out and before products of another kind
     auto drain_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + b); };
     auto turn_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 2 + b); };
+    const uint32_t xfull_bar = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + 2 * C::kJoinSlots);   // cluster: all parts ready
+    const int cl = kMode == kGateUp ? 1 : p.cluster;
     // a group's pieces of partials on their way into the ring
     auto join_bar = [&](int g, int i) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g * C::kJoinSlots + i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -435,6 +443,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             mbar_init(turn_of(b), 1);
             for (int i = 0; i < C::kJoinSlots; ++i) mbar_init(join_bar(b, i), 1);
         }
+        mbar_init(xfull_bar, 8 * cl);             // every epilogue warp of the cluster
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.w);
@@ -445,7 +454,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         tmem_relinquish();
     }
     tc_fence_before();
-    __syncthreads();
+    // a cluster's barriers are initialised before any CTA of it arrives on them from afar
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
     // kDown runs behind its own kGateUp launch, and kProj behind x @ A^T, which let it start only
     // after their own wait: the ids, weights and adapters they read before this launch's wait were
@@ -505,8 +516,14 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
     if (one_tile) pl.nk = pl.units / p.row_tiles;
     pl.fp8 = kMode == kProj ? p.nk : pl.nk;
-    plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
-                kMoe || one_tile, p.spread != nullptr);
+    if (cl > 1) {
+        pl.pieces = cl;
+        pl.shares = cl * p.row_tiles;
+        pl.q = pl.r = 0;
+    } else {
+        plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
+                    kMoe || one_tile, p.spread != nullptr);
+    }
     const int share = static_cast<int>(blockIdx.x);
     StreamWalk<kMode>& share_walk = *reinterpret_cast<StreamWalk<kMode>*>(smem + C::kOffWalk);   // each role's copy starts from it
     if (threadIdx.x == 0) share_walk = StreamWalk<kMode>(pl, share);
@@ -815,7 +832,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             p.spread[kSpreadNk] = pl.nk;
             p.spread[kSpreadPieces] = pl.pieces;
         }
-        if (kMode == kDown && nlist == 0 && !p.spread) {
+        if (kMode == kDown && nlist == 0 && !p.spread && cl == 1) {
             // no token uses an expert of this shard: the sum is empty
             const long long n = (long long)p.tokens * p.out_rows;
             for (long long i = ((long long)blockIdx.x * 2 + grp) * 128 + te; i < n; i += (long long)gridDim.x * 256) {
@@ -842,6 +859,73 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         uint32_t acc_ph = 0;
         StreamWalk<kMode> walk(share_walk);
         StreamSeg sg;
+        if (kMode != kGateUp && cl > 1) {
+            // A tile's pieces are the CTAs of a cluster: each leaves its part in its own ring (idle: its
+            // only tile's products are done), and each adds up every cl-th (column, 32 rows) of the
+            // tile over the cluster, in piece order.
+            float* xch = reinterpret_cast<float*>(smem);               // [column][block][row]
+            const int cols_all = min(BN, p.tokens);
+            bool ok = true;
+            if (walk.next(pl, sg)) {
+                ok = evote(wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue));
+                tc_fence_after();
+                if (ok) {
+                    const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + grp * kHalf;
+                    const int cols = min(kHalf, cols_all - grp * kHalf);
+                    for (int c0 = 0; c0 < cols; c0 += kChunk) {
+                        uint32_t r0[kChunk], r1[kChunk];
+                        if constexpr (kChunk == 16) {
+                            tmem_ld_32x32b_x16(ta + c0, r0);
+                            tmem_ld_32x32b_x16(ta + BN + c0, r1);
+                        } else {
+                            tmem_ld_32x32b_x8(ta + c0, r0);
+                            tmem_ld_32x32b_x8(ta + BN + c0, r1);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            if (c0 + i >= cols) break;
+                            xch[(grp * kHalf + c0 + i) * 256 + row] = __uint_as_float(r0[i]);
+                            xch[(grp * kHalf + c0 + i) * 256 + 128 + row] = __uint_as_float(r1[i]);
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane < cl) mbar_arrive_remote(map_shared_rank(xfull_bar, lane));
+            ok = wait_bar<true>(xfull_bar, 0, wctl, kWaitExchange) && ok;
+            const int rank = share % cl, tile = share / cl;
+            uint32_t full = 0;                                         // pieces that are not empty
+            for (int c = 0; c < cl; ++c)
+                if (share_begin(pl, tile * cl + c + 1) > share_begin(pl, tile * cl + c)) full |= 1u << c;
+            const uint32_t xbase = smem_u32(xch) + lane * 4;
+            const int w = grp * 4 + q;
+            if (__all_sync(0xffffffffu, ok)) {
+                constexpr int kItems = BN >= 64 ? 4 : 1;               // at a time
+                for (int i0 = rank + cl * w; i0 < cols_all * 8; i0 += cl * 8 * kItems) {
+                    float v[kItems], x[kItems][8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int n = 0; n < kItems; ++n) {
+                            const int it = i0 + cl * 8 * n;
+                            x[n][c] = (full >> c & 1u) && it < cols_all * 8 ? ld_dsmem_f32(map_shared_rank(xbase + it * 128, c)) : 0.0f;
+                        }
+#pragma unroll
+                    for (int n = 0; n < kItems; ++n) {
+                        v[n] = x[n][0];
+#pragma unroll
+                        for (int c = 1; c < 8; ++c) v[n] += x[n][c];
+                        const int it = i0 + cl * 8 * n, t = it >> 3, r = tile * 256 + (it & 7) * 32 + lane;
+                        if (it < cols_all * 8 && r < p.out_rows) {
+                            if (p.d_f32) static_cast<float*>(p.d)[(long long)t * p.out_rows + r] = v[n];
+                            else static_cast<__nv_bfloat16*>(p.d)[(long long)t * p.out_rows + r] = __float2bfloat16(v[n]);
+                        }
+                    }
+                }
+            }
+        }
         while (walk.next(pl, sg)) {
             if constexpr (kMode == kGateUp) {
                 // the tile's routing weights, while its weights stream
@@ -1084,7 +1168,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         if (kMode == kGateUp) fence_proxy_async_global();
     }
     tc_fence_before();
-    __syncthreads();
+    // a cluster's parts stay in place until all its CTAs have read them
+    __syncwarp();
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::kTmemCols);
@@ -1169,42 +1256,98 @@ inline cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t str
 }
 
 template <int kMode, int BN, bool kFp4>
-cudaError_t launch_stream_bn(const StreamParams& p, const StreamMaps& maps, dim3 grid, cudaStream_t stream) {
+struct StreamLaunch {
     using C = StreamCfg<kMode, BN>;
-    static bool configured[256] = {};        // set once per device; setting it again is harmless
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
-        err = cudaFuncSetAttribute(fg_stream_kernel<kMode, BN, kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   C::kSmemBytes);
+    // The current device, its kernel's shared memory allowed (again is harmless).
+    static cudaError_t device(int* dev) {
+        static bool configured[256] = {};
+        cudaError_t err = cudaGetDevice(dev);
         if (err != cudaSuccess) return err;
-        configured[dev] = true;
+        if (*dev < 0 || *dev >= 256) return cudaErrorInvalidDevice;
+        if (!configured[*dev]) {
+            err = cudaFuncSetAttribute(fg_stream_kernel<kMode, BN, kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kSmemBytes);
+            if (err != cudaSuccess) return err;
+            configured[*dev] = true;
+        }
+        return cudaSuccess;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (p.pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    static void config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid, int cluster, int pdl, cudaStream_t stream) {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = C::kSmemBytes;
+        cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 0;
+        if (cluster > 1) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(cluster);
+            attr[cfg.numAttrs].val.clusterDim.y = 1;
+            attr[cfg.numAttrs].val.clusterDim.z = 1;
+            ++cfg.numAttrs;
+        }
+        if (pdl) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+            ++cfg.numAttrs;
+        }
     }
-    return cudaLaunchKernelEx(&cfg, fg_stream_kernel<kMode, BN, kFp4>, p, maps);
-}
+    static cudaError_t launch(const StreamParams& p, const StreamMaps& maps, dim3 grid, cudaStream_t stream) {
+        int dev = 0;
+        const cudaError_t err = device(&dev);
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        config(cfg, attr, grid, p.cluster, p.pdl, stream);
+        return cudaLaunchKernelEx(&cfg, fg_stream_kernel<kMode, BN, kFp4>, p, maps);
+    }
+    // How many clusters of `cluster` CTAs run at once (0: unknown).
+    static int resident(int cluster) {
+        static int known[256][9] = {};           // + 1; asked again at worst
+        int dev = 0;
+        if (device(&dev) != cudaSuccess) return 0;
+        if (!known[dev][cluster]) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[2];
+            int n = 0;
+            config(cfg, attr, dim3(static_cast<unsigned>(cluster)), cluster, 0, nullptr);
+            if (cudaOccupancyMaxActiveClusters(&n, fg_stream_kernel<kMode, BN, kFp4>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            known[dev][cluster] = n + 1;
+        }
+        return known[dev][cluster] - 1;
+    }
+};
 
 template <int kMode, bool kFp4>
 cudaError_t launch_stream(int bn, const StreamParams& p, const StreamMaps& maps, dim3 grid, cudaStream_t stream) {
     switch (bn) {
-        case 16: return launch_stream_bn<kMode, 16, kFp4>(p, maps, grid, stream);
-        case 32: return launch_stream_bn<kMode, 32, kFp4>(p, maps, grid, stream);
-        case 64: return launch_stream_bn<kMode, 64, kFp4>(p, maps, grid, stream);
-        default: return launch_stream_bn<kMode, 128, kFp4>(p, maps, grid, stream);
+        case 16: return StreamLaunch<kMode, 16, kFp4>::launch(p, maps, grid, stream);
+        case 32: return StreamLaunch<kMode, 32, kFp4>::launch(p, maps, grid, stream);
+        case 64: return StreamLaunch<kMode, 64, kFp4>::launch(p, maps, grid, stream);
+        default: return StreamLaunch<kMode, 128, kFp4>::launch(p, maps, grid, stream);
     }
+}
+
+// CTAs that share a tile of `tiles` as a cluster: the most whose clusters are all resident at once
+// on `sms` SMs; 1 where not even three are (the shares are then dealt and joined through the
+// workspace).
+template <int kMode, bool kFp4>
+int stream_cluster(int bn, int tiles, int sms) {
+    for (int s = 8; s > 2; --s) {
+        if (tiles * s > sms) continue;
+        int n = 0;
+        switch (bn) {
+            case 16: n = StreamLaunch<kMode, 16, kFp4>::resident(s); break;
+            case 32: n = StreamLaunch<kMode, 32, kFp4>::resident(s); break;
+            case 64: n = StreamLaunch<kMode, 64, kFp4>::resident(s); break;
+            default: n = StreamLaunch<kMode, 128, kFp4>::resident(s); break;
+        }
+        if (tiles <= n) return s;
+    }
+    return 1;
 }
 
 // Token columns of a tile: the smallest width that holds them.
