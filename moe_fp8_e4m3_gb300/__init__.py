@@ -380,7 +380,8 @@ _NAMES = {"q": "uint8/float8_e4m3fn", "i": "int32", "f": "float32", "b": "bfloat
 
 def _check_all(*args):
     """(tensor, name, letter) triples in a row: contiguous CUDA tensors of the letter's dtype.  A
-    decode step's calls are short, so their checks are one pass (0.2 us a tensor)."""
+    decode step's calls are short on the GPU, so those with many tensors look at them in one
+    expression first and come here to name the one that is wrong."""
     kinds = _DTYPES or _dtypes()
     for k in range(0, len(args), 3):
         t = args[k]
@@ -422,8 +423,17 @@ def moe_mlp_workspace(t, h, i, e, device="cuda"):
 
 
 def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, workspace, expert_base, stream):
-    _check_all(a, "a", "q", sfa, "sfa", "i", w13, "w13", letter, sf13, "sf13", "i", w2, "w2", letter, sf2, "sf2", "i",
-               topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f", d, "d", "o")
+    kinds = _DTYPES or _dtypes()
+    q, w, i32 = kinds["q"], kinds[letter], kinds["i"]
+    if not (a.dtype in q and sfa.dtype in i32 and w13.dtype in w and sf13.dtype in i32 and w2.dtype in w and
+            sf2.dtype in i32 and topk_ids.dtype in i32 and topk_weights.dtype in kinds["f"] and d.dtype in kinds["o"] and
+            a.is_cuda and sfa.is_cuda and w13.is_cuda and sf13.is_cuda and w2.is_cuda and sf2.is_cuda and
+            topk_ids.is_cuda and topk_weights.is_cuda and d.is_cuda and
+            a.is_contiguous() and sfa.is_contiguous() and w13.is_contiguous() and sf13.is_contiguous() and
+            w2.is_contiguous() and sf2.is_contiguous() and topk_ids.is_contiguous() and topk_weights.is_contiguous() and
+            d.is_contiguous()):
+        _check_all(a, "a", "q", sfa, "sfa", "i", w13, "w13", letter, sf13, "sf13", "i", w2, "w2", letter, sf2, "sf2", "i",
+                   topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f", d, "d", "o")
     t, h = a.shape
     e, i2, _ = w13.shape
     i = i2 // 2
@@ -466,8 +476,18 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
     """D[m] = A[m] @ B.T + scaling[l] * (x[m] @ lora_a[l].T) @ lora_b[l].T with l = ids[m] (-1: no
     adapter).  a, sfa, b, sfb as fp8_gemm_nt; x [M,K], lora_a [L,R,K], lora_b [L,N,R] BF16; scaling
     float32 [L]; ids int32 [M]; d [M,N] BF16/FP32 (out).  workspace from lora_workspace."""
-    _check_all(a, "a", "q", sfa, "sfa", "i", b, "b", "q", sfb, "sfb", "i", x, "x", "b", lora_a, "lora_a", "b",
-               lora_b, "lora_b", "b", scaling, "scaling", "f", ids, "ids", "i", d, "d", "o")
+    kinds = _DTYPES or _dtypes()
+    q, i32, bf = kinds["q"], kinds["i"], kinds["b"]
+    if not (a.dtype in q and sfa.dtype in i32 and b.dtype in q and sfb.dtype in i32 and x.dtype in bf and
+            lora_a.dtype in bf and lora_b.dtype in bf and scaling.dtype in kinds["f"] and ids.dtype in i32 and
+            d.dtype in kinds["o"] and
+            a.is_cuda and sfa.is_cuda and b.is_cuda and sfb.is_cuda and x.is_cuda and lora_a.is_cuda and
+            lora_b.is_cuda and scaling.is_cuda and ids.is_cuda and d.is_cuda and
+            a.is_contiguous() and sfa.is_contiguous() and b.is_contiguous() and sfb.is_contiguous() and
+            x.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous() and scaling.is_contiguous() and
+            ids.is_contiguous() and d.is_contiguous()):
+        _check_all(a, "a", "q", sfa, "sfa", "i", b, "b", "q", sfb, "sfb", "i", x, "x", "b", lora_a, "lora_a", "b",
+                   lora_b, "lora_b", "b", scaling, "scaling", "f", ids, "ids", "i", d, "d", "o")
     m, k = a.shape
     n, kb = b.shape
     l, r, ka = lora_a.shape

@@ -208,11 +208,14 @@ struct StreamPlan {
     const int* pre;      // kProj: units before each token tile
 };
 
+// Units of a tile before its piece i.
+__device__ __forceinline__ int piece_begin(const StreamPlan& pl, int i) {
+    return i == 0 ? 0 : i * pl.fp8 / pl.pieces + (pl.nk == pl.fp8 ? 0 : i * (pl.nk - pl.fp8) / pl.pieces);
+}
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
     if (pl.pieces) {
         const int t = c / pl.pieces;
-        const int i = c - t * pl.pieces;
-        return t * pl.nk + i * pl.fp8 / pl.pieces + i * (pl.nk - pl.fp8) / pl.pieces;
+        return t * pl.nk + piece_begin(pl, c - t * pl.pieces);
     }
     return c * pl.q + min(c, pl.r);
 }
@@ -276,6 +279,15 @@ struct StreamWalk {
     __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share)
         : u(0), end(0), tail(-1), tail_end(0), tile(0), tt(0), first(0), nk(1), tail_tile(0), tail_tt(0), tail_nk(1) {
         if (share >= pl.shares) return;
+        if (pl.pieces) {                  // one piece of one tile
+            const int i = pl.pieces == 1 ? 0 : share % pl.pieces;
+            tile = pl.pieces == 1 ? share : share / pl.pieces;
+            nk = pl.nk;
+            first = tile * nk;
+            u = first + piece_begin(pl, i);
+            end = first + (i + 1 == pl.pieces ? nk : piece_begin(pl, i + 1));
+            return;
+        }
         u = share_begin(pl, share);
         end = tail_end = share_begin(pl, share + 1);
         int a = 0, base = 0;
@@ -865,6 +877,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             // tile over the cluster, in piece order.
             float* xch = reinterpret_cast<float*>(smem);               // [column][block][row]
             const int cols_all = min(BN, p.tokens);
+            const int rank = static_cast<int>(cluster_ctarank()), tile = share_walk.tile;
+            uint32_t full = 0;                                         // pieces that are not empty
+            for (int c = 0; c < cl; ++c)
+                if (pl.fp8 >= cl || (c + 1 == cl ? pl.nk : piece_begin(pl, c + 1)) > piece_begin(pl, c)) full |= 1u << c;
             bool ok = true;
             if (walk.next(pl, sg)) {
                 ok = evote(wait_bar(accf_bar(acc), acc_ph, wctl, kWaitEpilogue));
@@ -895,10 +911,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             __syncwarp();
             if (lane < cl) mbar_arrive_remote(map_shared_rank(xfull_bar, lane));
             ok = wait_bar<true>(xfull_bar, 0, wctl, kWaitExchange) && ok;
-            const int rank = share % cl, tile = share / cl;
-            uint32_t full = 0;                                         // pieces that are not empty
-            for (int c = 0; c < cl; ++c)
-                if (share_begin(pl, tile * cl + c + 1) > share_begin(pl, tile * cl + c)) full |= 1u << c;
             const uint32_t xbase = smem_u32(xch) + lane * 4;
             const int w = grp * 4 + q;
             if (__all_sync(0xffffffffu, ok)) {
