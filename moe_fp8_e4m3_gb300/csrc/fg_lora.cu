@@ -105,7 +105,7 @@ __device__ __forceinline__ void store_parts(uint16_t* dst, long long stride, int
 
 // What both ways know of the tile: its distinct adapters and each token's place among them.
 struct TileShared {
-    uint32_t bits[32];
+    alignas(16) uint8_t marks[fg::kMaxListed];
     uint16_t list[fg::kMaxListed];
     int listed;
     int16_t slot_of[128];               // of each token of the tile, -1 without an adapter
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     const int32_t* ids = p.ids + (long long)tt * p.bn;
     const int my_id = static_cast<int>(threadIdx.x) < n ? __ldcg(ids + threadIdx.x) : -1;
     if (threadIdx.x < 128) sh.count[threadIdx.x] = 0;
-    fg::list_distinct(ids, n, 0, p.L, sh.bits, sh.list, &sh.listed);
+    fg::list_distinct(ids, n, 0, p.L, sh.marks, sh.list, &sh.listed);
     const int slots = sh.listed;
     if (threadIdx.x < 128) {
         int slot = -1;

@@ -159,7 +159,7 @@ struct StreamCfg {
     static constexpr int kBBytes = BN * 128;                                // kProj: also the parts of an adapter unit
     static constexpr int kSfBytes = 3 * 512;                                // weight block 0, 1, tokens
     static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + 128 + 64 + 2 * kMaxListed +
+    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + kMaxListed + 64 + 2 * kMaxListed +
                                       (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
     static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
@@ -181,7 +181,7 @@ struct StreamCfg {
     static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
     static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
     static constexpr int kOffBits = kOffTok + BN * 8;
-    static constexpr int kOffWalk = kOffBits + 128;
+    static constexpr int kOffWalk = kOffBits + kMaxListed;
     static constexpr int kOffList = kOffWalk + 64;
     static constexpr int kOffPre = kOffList + 2 * kMaxListed;
     static constexpr int kSmemBytes = kOffBar + kMiscBytes + 1024;          // + alignment slack
@@ -244,19 +244,20 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 __device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int early,
                                             bool even_ok, bool spread) {
     const float unit_hbm = fp4 ? 0.0025f : 0.00475f;
-    auto time = [&](int shares, int per, int n) {
-        const float t = fmaxf(per * 0.3f, (pl.units - min(pl.units, early * shares)) * unit_hbm);
-        return t + (spread ? 0.1f * n : n > 1 ? 2.0f + 0.25f * n * chunks : 0.0f);
+    const float units = pl.units, nk = pl.nk;
+    auto time = [&](float shares, float per, float n) {
+        const float t = fmaxf(per * 0.3f, fmaxf(units - early * shares, 0.0f) * unit_hbm);
+        return t + (spread ? 0.1f * n : n > 1.0f ? 2.0f + 0.25f * n * chunks : 0.0f);
     };
     // lane s > 0 looks at s pieces per tile, lane 0 at equal shares; the least time (its bits, the
     // lane in the low five) wins
     const int s = static_cast<int>(threadIdx.x & 31);
     float t = 1e30f;
     if (s == 0) {
-        const int per = (pl.units + grid - 1) / grid;
-        t = time(min(grid, pl.units), per, per > 0 ? (pl.nk + per - 1) / per + 1 : 1) + (spread ? 0.0f : 2.0f);
+        const float per = fmaxf(__fdividef(units, static_cast<float>(grid)), 1.0f);
+        t = time(fminf(grid, units), per, __fdividef(nk, per) + 1.0f) + (spread ? 0.0f : 2.0f);
     } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.fp8) {      // (no piece is empty)
-        t = time(s * tiles, (pl.nk + s - 1) / s, s);
+        t = time(s * tiles, __fdividef(nk, static_cast<float>(s)), s);
     }
     const uint32_t best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | s);
     pl.pieces = static_cast<int>(best & 31u);
@@ -280,8 +281,8 @@ struct StreamWalk {
         : u(0), end(0), tail(-1), tail_end(0), tile(0), tt(0), first(0), nk(1), tail_tile(0), tail_tt(0), tail_nk(1) {
         if (share >= pl.shares) return;
         if (pl.pieces) {                  // one piece of one tile
-            const int i = pl.pieces == 1 ? 0 : share % pl.pieces;
             tile = pl.pieces == 1 ? share : share / pl.pieces;
+            const int i = share - tile * pl.pieces;
             nk = pl.nk;
             first = tile * nk;
             u = first + piece_begin(pl, i);
@@ -382,19 +383,28 @@ struct StreamCursor {
     }
 };
 
-// Ascending list of the distinct ids in [base, base + count) among ids[0, n); all threads.
-__device__ __forceinline__ void list_distinct(const int32_t* ids, int n, int base, int count, uint32_t* bits,
+// Ascending list of the distinct ids in [base, base + count) among ids[0, n); all threads.  An id
+// marks its byte (plain stores: with few experts, atomics on one word's bits would queue up).
+__device__ __forceinline__ void list_distinct(const int32_t* ids, int n, int base, int count, uint8_t* marks,
                                               uint16_t* list, int* listed) {
     const int t = threadIdx.x, lane = t & 31;
-    if (t < 32) bits[t] = 0;
+    for (int i = t; i < kMaxListed / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(marks)[i] = 0;
     __syncthreads();
     for (int i = t; i < n; i += blockDim.x) {
         const unsigned v = static_cast<unsigned>(__ldcg(ids + i)) - static_cast<unsigned>(base);
-        if (v < static_cast<unsigned>(count)) atomicOr(bits + (v >> 5), 1u << (v & 31));
+        if (v < static_cast<unsigned>(count)) marks[v] = 1;
     }
     __syncthreads();
     if (t < 32) {
-        uint32_t m = bits[lane];
+        // lane's 32 bytes to bits: four at a time, byte k of a word to bit k
+        uint32_t m = 0;
+        const uint4* own = reinterpret_cast<const uint4*>(marks) + lane * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = own[i];
+            m |= ((w.x * 0x10204080u) >> 28) << (16 * i) | ((w.y * 0x10204080u) >> 28) << (16 * i + 4) |
+                 ((w.z * 0x10204080u) >> 28) << (16 * i + 8) | ((w.w * 0x10204080u) >> 28) << (16 * i + 12);
+        }
         const int c = __popc(m);
         int incl = c;
 #pragma unroll
@@ -437,7 +447,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [2]
     // per token: routing weight of the tile's expert, 1 where the token uses it
     float2* tok = reinterpret_cast<float2*>(smem + C::kOffTok);
-    uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::kOffBits);
+    uint8_t* marks = smem + C::kOffBits;
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
     int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
 
@@ -481,12 +491,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     StreamPlan pl;
     int nlist = 0;
     if constexpr (kMoe) {
-        list_distinct(p.ids, p.tokens * p.topk, p.expert_base, p.experts, bits, list, listed);
+        list_distinct(p.ids, p.tokens * p.topk, p.expert_base, p.experts, marks, list, listed);
         nlist = *listed;
         pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
         pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
     } else if (one_tile) {
-        list_distinct(p.ids, p.tokens, 0, p.lora_count, bits, list, listed);
+        list_distinct(p.ids, p.tokens, 0, p.lora_count, marks, list, listed);
         nlist = *listed;
         if (threadIdx.x == 0) {
             pre[0] = 0;
