@@ -30,8 +30,9 @@ Other workloads (--workload prefill | decode | small | contiguous | masked | k_g
 the other operand layouts prefill_nn | prefill_tn | prefill_tt | contiguous_nn, the fused
 gate-up GEMM contiguous_swiglu, the indexer's mqa_logits, the quantisers quant, the FP8 x
 FP4 forms fp4_dense_pair | fp4_prefill | fp4_decode | fp4_contiguous | fp4_masked |
-fp4_contiguous_swiglu, and the MoE expert MLP moe_mlp | fp4_moe_mlp) time them on the same
-rules; they are measurement aids, the default line is the headline (its config.kernels also
+fp4_contiguous_swiglu, the MoE expert MLP moe_mlp | fp4_moe_mlp, and the MoE layer's decode
+step decode_step | fp4_decode_step: projection with adapters, quantiser, router, whole MoE
+MLP) time them on the same rules; they are measurement aids, the default line is the headline (its config.kernels also
 records small, contiguous, masked, k_grouped, quant and the FP8 x FP4 dense pair,
 contiguous and masked).
 
@@ -738,6 +739,88 @@ class MqaLogits:
         return ins, [(self.out, self.torch.empty_like(self.out, device="cpu").pin_memory())]
 
 
+class DecodeStep:
+    """The tail of one decode step of an MoE layer for 64 requests: the FP8 output projection
+    (K = N = 4096) with each request's own rank-16 adapter, the activation quantiser, the router
+    (top-6 of 32 experts) and the whole MoE MLP (H = 4096, I = 2048) with E4M3 weights."""
+    name = "decode_step"
+    fp4 = False
+    T, K, H, I, E, TOPK, L, R = 64, 4096, 4096, 2048, 32, 6, 48, 16
+    description = ("decode step of an MoE layer, 64 tokens: FP8 projection 4096 x 4096 with per-token rank-16 adapters "
+                   "(48 of them), 1x128 quantiser, router top-6 of 32, MoE MLP H=4096 I=2048 over all its experts")
+
+    def __init__(self, torch, fg, seed):
+        import workloads
+        self.torch, self.fg = torch, fg
+        t, k, h, i, e, topk, l, r = self.T, self.K, self.H, self.I, self.E, self.TOPK, self.L, self.R
+        u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+
+        def empty(*shape, dtype=u8):
+            return torch.zeros(shape, dtype=dtype, device="cuda")
+
+        x = workloads.device_normal(seed, (t, k))
+        self.x = x.to(bf)
+        self.a, self.sfa = empty(t, k), empty(cdiv(k, 512), align4(t), dtype=i32)
+        fg.quantize_1x128_rows(self.x.float(), self.a, self.sfa)
+        self.w, self.sfw = empty(h, k), empty(1, cdiv(k, 512), align4(cdiv(h, 128)), dtype=i32)
+        fg.quantize_128x128_blocks(workloads.device_normal(seed + 1, (h, k), std=0.02), self.w, self.sfw)
+        self.la = workloads.device_normal(seed + 2, (l, r, k), std=k ** -0.5).to(bf)
+        self.lb = workloads.device_normal(seed + 3, (l, h, r), std=0.1).to(bf)
+        self.scaling = torch.ones(l, device="cuda")
+        self.ids = torch.randint(0, l, (t,), generator=gen, device="cuda", dtype=i32)
+        self.y = empty(t, h, dtype=torch.float32)
+        self.b, self.sfb = empty(t, h), empty(cdiv(h, 512), align4(t), dtype=i32)
+        self.logits = workloads.device_normal(seed + 4, (t, e), std=2.0)
+        self.topk_ids, self.topk_w = empty(t, topk, dtype=i32), empty(t, topk, dtype=torch.float32)
+        if self.fp4:
+            self.w13, self.sf13 = empty(e, 2 * i, h // 2), empty(e, h // 128, align4(2 * i), dtype=i32)
+            self.w2, self.sf2 = empty(e, h, i // 2), empty(e, i // 128, align4(h), dtype=i32)
+            quant, self.moe = fg.quantize_mxfp4, fg.fp8_fp4_moe_mlp
+        else:
+            self.w13, self.sf13 = empty(e, 2 * i, h), empty(e, cdiv(h, 512), align4(2 * i // 128), dtype=i32)
+            self.w2, self.sf2 = empty(e, h, i), empty(e, cdiv(i, 512), align4(h // 128), dtype=i32)
+            quant, self.moe = fg.quantize_128x128_blocks, fg.fp8_moe_mlp
+        quant(workloads.device_normal(seed + 5, (e, 2 * i, h), std=0.02), self.w13, self.sf13)
+        quant(workloads.device_normal(seed + 6, (e, h, i), std=0.02), self.w2, self.sf2)
+        self.out = empty(t, h, dtype=bf)
+        self.lora_ws, self.moe_ws = fg.lora_workspace(t, h, k, r), fg.moe_mlp_workspace(t, h, i, e)
+        for fn in self.launches():
+            fn()
+        torch.cuda.synchronize()
+        experts = len(set(self.topk_ids.flatten().tolist()))
+        adapters = len(set(self.ids.tolist()))
+        per = 3 * h * i * (0.5 + 1 / 32 if self.fp4 else 1 + 1 / 16384)
+        self.parts = [
+            {"name": "lora_projection", "flops": 2.0 * t * h * k + 2.0 * t * r * (h + k), "bound": "hbm",
+             "bytes": int(h * k + t * k * 3 + adapters * r * (h + k) * 2 + t * h * 4)},
+            {"name": "quantise", "flops": 0.0, "bound": "hbm", "bytes": t * h * 5},
+            {"name": "route", "flops": 0.0, "bound": "hbm", "bytes": t * e * 4 + t * topk * 8},
+            {"name": "moe_mlp", "flops": 6.0 * t * topk * h * i, "bound": "hbm", "bytes": int(experts * per + t * h * 3)},
+        ]
+
+    def launches(self):
+        fg = self.fg
+        return [
+            lambda: fg.fp8_gemm_nt_lora(self.a, self.sfa, self.w, self.sfw[0], self.x, self.la, self.lb, self.scaling, self.ids,
+                                        self.y, self.lora_ws),
+            lambda: fg.quantize_1x128_rows(self.y, self.b, self.sfb),
+            lambda: fg.moe_route(self.logits, self.topk_ids, self.topk_w),
+            lambda: self.moe(self.b, self.sfb, self.w13, self.sf13, self.w2, self.sf2, self.topk_ids, self.topk_w, self.out,
+                             self.moe_ws),
+        ]
+
+    def e2e_io(self):
+        ins = [(x, x.cpu().pin_memory()) for x in (self.a, self.sfa, self.x, self.logits)]
+        return ins, [(self.out, self.torch.empty_like(self.out, device="cpu").pin_memory())]
+
+
+class Fp4DecodeStep(DecodeStep):
+    name = "fp4_decode_step"
+    fp4 = True
+    description = DecodeStep.description + ", MXFP4 expert weights"
+
+
 class ContiguousNN(Contiguous):
     """The contiguous workload with each expert's weights stored [K, N]."""
     name = "contiguous_nn"
@@ -756,7 +839,7 @@ class ContiguousNN(Contiguous):
 WORKLOADS = {w.name: w for w in (DensePair, Prefill, Decode, Small, Contiguous, Masked, KGrouped, KGroupedSeparate, Quant, PrefillNN,
                                  PrefillTN, PrefillTT, ContiguousNN, ContiguousSwiGLU, MqaLogits, Fp4DensePair,
                                  Fp4Prefill, Fp4Decode, Fp4Contiguous, Fp4Masked, Fp4ContiguousSwiGLU, MoeMlp,
-                                 Fp4MoeMlp)}
+                                 Fp4MoeMlp, DecodeStep, Fp4DecodeStep)}
 
 # The benchmark configurations beside the headline pair (recorded in config.kernels of
 # the default run): (configuration number, workload).
