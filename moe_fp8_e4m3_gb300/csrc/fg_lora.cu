@@ -449,9 +449,7 @@ cudaError_t launch_shrink_as(const ShrinkParams& p, const ShrinkMaps& maps, dim3
     return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<MB, U, kClusters>, p, maps);
 }
 
-// One token tile: one CTA an item, of which there are at most min(bn, L) + bn / 8.
-int shrink_ctas(const ShrinkParams& p) { return (p.L < p.bn ? p.L : p.bn) + p.bn / 8; }
-
+// sms: how many the launch may take.
 cudaError_t launch_shrink(const ShrinkParams& p, const ShrinkMaps& maps, int tiles, int sms, int pdl, cudaStream_t stream) {
     if (tiles > 1) {                              // whole clusters per tile, as far as one wave of SMs goes
         const int clusters = sms / (kShrinkCluster * tiles) > 1 ? sms / (kShrinkCluster * tiles) : 1;
@@ -459,7 +457,8 @@ cudaError_t launch_shrink(const ShrinkParams& p, const ShrinkMaps& maps, int til
         return p.rp <= 16 ? launch_shrink_as<1, 8, true>(p, maps, grid, pdl, stream)
                           : launch_shrink_as<2, 4, true>(p, maps, grid, pdl, stream);
     }
-    const int most = shrink_ctas(p);
+    // one CTA an item, of which there are at most min(bn, L) + bn / 8
+    const int most = (p.L < p.bn ? p.L : p.bn) + p.bn / 8;
     const dim3 grid(static_cast<unsigned>(most < sms ? most : sms));
     return p.rp <= 16 ? launch_shrink_as<1, 8, false>(p, maps, grid, pdl, stream)
                       : launch_shrink_as<2, 4, false>(p, maps, grid, pdl, stream);
@@ -511,7 +510,13 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
             !fg::encode_tiled(&sm.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_a, ad, ap, ab, CU_TENSOR_MAP_SWIZZLE_128B))
             return FG_ERR_INVALID_ARG;
     }
-    if (launch_shrink(sp, sm, l.tiles, st.sms, st.pdl, s) != cudaSuccess) {
+    // A single token tile's projection runs in clusters that start beside this launch and stream the
+    // FP8 weights meanwhile: this launch leaves them their SMs, they leave it at least 40.  Measured
+    // on GB300 (64 x 7168, 52 adapters): 4 CTAs a cluster and 40 here 21.0 us, 72 here 22.4 (some
+    // clusters start late), no clusters 25.0; 64 x 4096, 6 a cluster 16.4, none 23.0.
+    const int row_tiles = ceil_div(N, 256);
+    const int cluster = l.tiles == 1 ? fg::stream_cluster<fg::kProj, false>(l.bn, row_tiles, grid - 40) : 1;
+    if (launch_shrink(sp, sm, l.tiles, cluster > 1 ? grid - cluster * row_tiles : st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
         return FG_ERR_CUDA;
     }
@@ -545,7 +550,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
             !fg::encode_tiled(&m.lb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_b, ld, lp, lb, sw) ||
             !fg::encode_tiled(&m.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, sp.v, vd, vp, vb, sw))
             return FG_ERR_INVALID_ARG;
-        p.nk = K / 128; p.row_tiles = ceil_div(N, 256); p.out_rows = N;
+        p.nk = K / 128; p.row_tiles = row_tiles; p.out_rows = N;
         p.sfw = sfb;
         p.sfw_rows = ceil_div(N, 128);
         p.sfw_ld = align4(p.sfw_rows);
@@ -553,9 +558,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         p.ctr = reinterpret_cast<unsigned*>(ws) + fg::kMaxCounters;
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = st.debug_stall;
-        // Clusters where they find room beside the launch before, whose end they would wait for else
-        // (33 x 1008: 12.6 us in clusters, 16.3 without; 64 x 7168 with 72 CTAs before: 30.4, 24.4).
-        p.cluster = l.tiles == 1 ? fg::stream_cluster<fg::kProj, false>(l.bn, p.row_tiles, grid - shrink_ctas(sp)) : 1;
+        p.cluster = cluster;
         const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles : grid);
         if (fg::launch_stream<fg::kProj, false>(l.bn, p, m, ctas, s) != cudaSuccess) {
             cudaGetLastError();

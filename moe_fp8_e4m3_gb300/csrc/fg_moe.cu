@@ -114,11 +114,12 @@ int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t
         p.ctr = reinterpret_cast<unsigned*>(ws) + fg::kMaxCounters;
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = 0;
-        // Up to 32 tokens a tile's pieces meet in a cluster (from 11 units a tile: fewer run uncut in the
-        // time a join takes); wider parts leave it idle SMs to stream
-        // with and take the third launch (128 x 7168: 276 us in clusters, 255 with it; 37 x 4096: 95, 94;
-        // 16 x 4096: 50.7 in clusters, 52.0 through the workspace; 1 x 4096: 35.6, 38.1).
-        p.cluster = bn <= 32 && slots * p.nk > 10 ? fg::stream_cluster<fg::kDown, kFp4>(bn, p.row_tiles, grid) : 1;
+        // Up to 32 tokens a tile's pieces meet in a cluster, on three quarters of the SMs (of more, some
+        // clusters wait for SMs of one GPC).  Wider parts take the third launch.  Measured on GB300, us
+        // in clusters (CTAs each), through the workspace: 1 x 1024 11.0 (8), 12.8; 1 x 4096 34.4 (6),
+        // 39.2; 16 x 4096 49.7 (6), 53.0; 4 x 7168 127.1 (4), 140.9 (5), 129.6; 128 x 7168 276 (4), 255
+        // with the third launch.
+        p.cluster = bn <= 32 ? fg::stream_cluster<fg::kDown, kFp4>(bn, p.row_tiles, grid * 3 / 4) : 1;
         if (p.cluster == 1 && bn >= 64 && p.row_tiles <= grid) p.spread = reinterpret_cast<int*>(ws) + 2 * fg::kMaxCounters;
         const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles : grid);
         if (fg::launch_stream<fg::kDown, kFp4>(bn, p, m, ctas, s) != cudaSuccess ||
