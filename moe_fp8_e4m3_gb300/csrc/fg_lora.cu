@@ -383,7 +383,12 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     const int32_t* ids = p.ids + (long long)tt * p.bn;
     const int my_id = static_cast<int>(threadIdx.x) < n ? __ldcg(ids + threadIdx.x) : -1;
     if (threadIdx.x < 128) sh.count[threadIdx.x] = 0;
-    fg::list_distinct(ids, n, 0, p.L, sh.marks, sh.list, &sh.listed);
+    fg::mark_ids(ids, n, 0, p.L, sh.marks);
+    if (threadIdx.x < 32) {
+        const int found = fg::list_marked(sh.marks, sh.list);
+        if (threadIdx.x == 0) sh.listed = found;
+    }
+    __syncthreads();
     const int slots = sh.listed;
     if (threadIdx.x < 128) {
         int slot = -1;

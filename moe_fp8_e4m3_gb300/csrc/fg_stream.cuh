@@ -159,7 +159,7 @@ struct StreamCfg {
     static constexpr int kBBytes = BN * 128;                                // kProj: also the parts of an adapter unit
     static constexpr int kSfBytes = 3 * 512;                                // weight block 0, 1, tokens
     static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + kMaxListed + 64 + 2 * kMaxListed +
+    static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + kMaxListed + 128 + 2 * kMaxListed +
                                       (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
     static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
@@ -181,8 +181,8 @@ struct StreamCfg {
     static constexpr int kOffRed = kOffBar + 512;                           // [group][2][4 warps][16] amax words
     static constexpr int kOffTok = kOffRed + 1024;                          // [BN] routing weights, [BN] flags
     static constexpr int kOffBits = kOffTok + BN * 8;
-    static constexpr int kOffWalk = kOffBits + kMaxListed;
-    static constexpr int kOffList = kOffWalk + 64;
+    static constexpr int kOffSetup = kOffBits + kMaxListed;
+    static constexpr int kOffList = kOffSetup + 128;
     static constexpr int kOffPre = kOffList + 2 * kMaxListed;
     static constexpr int kSmemBytes = kOffBar + kMiscBytes + 1024;          // + alignment slack
     static_assert(kNumBars * 8 <= 512 - 64, "barrier area");
@@ -277,6 +277,7 @@ struct StreamWalk {
     int u, end, tail, tail_end;          // [u, end) is left; before it [tail, tail_end) if tail >= 0
     int tile, tt, first, nk;             // the tile of unit u
     int tail_tile, tail_tt, tail_nk;
+    StreamWalk() = default;
     __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share)
         : u(0), end(0), tail(-1), tail_end(0), tile(0), tt(0), first(0), nk(1), tail_tile(0), tail_tt(0), tail_nk(1) {
         if (share >= pl.shares) return;
@@ -383,11 +384,10 @@ struct StreamCursor {
     }
 };
 
-// Ascending list of the distinct ids in [base, base + count) among ids[0, n); all threads.  An id
-// marks its byte (plain stores: with few experts, atomics on one word's bits would queue up).
-__device__ __forceinline__ void list_distinct(const int32_t* ids, int n, int base, int count, uint8_t* marks,
-                                              uint16_t* list, int* listed) {
-    const int t = threadIdx.x, lane = t & 31;
+// Marks the byte of every id in [base, base + count) among ids[0, n) (plain stores: with few
+// experts, atomics on one word's bits would queue up); all threads.
+__device__ __forceinline__ void mark_ids(const int32_t* ids, int n, int base, int count, uint8_t* marks) {
+    const int t = threadIdx.x;
     for (int i = t; i < kMaxListed / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(marks)[i] = 0;
     __syncthreads();
     for (int i = t; i < n; i += blockDim.x) {
@@ -395,34 +395,44 @@ __device__ __forceinline__ void list_distinct(const int32_t* ids, int n, int bas
         if (v < static_cast<unsigned>(count)) marks[v] = 1;
     }
     __syncthreads();
-    if (t < 32) {
-        // lane's 32 bytes to bits: four at a time, byte k of a word to bit k
-        uint32_t m = 0;
-        const uint4* own = reinterpret_cast<const uint4*>(marks) + lane * 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 w = own[i];
-            m |= ((w.x * 0x10204080u) >> 28) << (16 * i) | ((w.y * 0x10204080u) >> 28) << (16 * i + 4) |
-                 ((w.z * 0x10204080u) >> 28) << (16 * i + 8) | ((w.w * 0x10204080u) >> 28) << (16 * i + 12);
-        }
-        const int c = __popc(m);
-        int incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        int pos = incl - c;
-        for (; m; m &= m - 1) list[pos++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
-        if (lane == 31) *listed = incl;
-    }
-    __syncthreads();
 }
+// The marked ids in ascending order, and their number; one warp.
+__device__ __forceinline__ int list_marked(const uint8_t* marks, uint16_t* list) {
+    const int lane = threadIdx.x & 31;
+    // lane's 32 bytes to bits: four at a time, byte k of a word to bit k
+    uint32_t m = 0;
+    const uint4* own = reinterpret_cast<const uint4*>(marks) + lane * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 w = own[i];
+        m |= ((w.x * 0x10204080u) >> 28) << (16 * i) | ((w.y * 0x10204080u) >> 28) << (16 * i + 4) |
+             ((w.z * 0x10204080u) >> 28) << (16 * i + 8) | ((w.w * 0x10204080u) >> 28) << (16 * i + 12);
+    }
+    const int c = __popc(m);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    int pos = incl - c;
+    for (; m; m &= m - 1) list[pos++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
+    return __shfl_sync(0xffffffffu, incl, 31);
+}
+
+// What warp 0 works out for a CTA before its roles begin.
+template <int kMode>
+struct StreamSetup {
+    StreamPlan pl;
+    int listed;              // distinct experts or adapters
+    StreamWalk<kMode> walk;
+};
 
 template <int kMode, int BN, bool kFp4>
 __global__ void __launch_bounds__(StreamCfg<kMode, BN>::kThreads, 1)
 fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) {
     using C = StreamCfg<kMode, BN>;
+    static_assert(sizeof(StreamSetup<kMode>) <= 128, "set-up area");
     constexpr bool kMoe = kMode == kGateUp || kMode == kDown;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -443,7 +453,6 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     auto join_bar = [&](int g, int i) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g * C::kJoinSlots + i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    int* listed = reinterpret_cast<int*>(smem + C::kOffMisc + 8);
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [2]
     // per token: routing weight of the tile's expert, 1 where the token uses it
     float2* tok = reinterpret_cast<float2*>(smem + C::kOffTok);
@@ -488,31 +497,31 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         grid_dependency_wait();
         if (threadIdx.x == 0) grid_launch_dependents();
     }
-    StreamPlan pl;
-    int nlist = 0;
-    if constexpr (kMoe) {
-        list_distinct(p.ids, p.tokens * p.topk, p.expert_base, p.experts, marks, list, listed);
-        nlist = *listed;
-        pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
-        pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
-    } else if (one_tile) {
-        list_distinct(p.ids, p.tokens, 0, p.lora_count, marks, list, listed);
-        nlist = *listed;
-        if (threadIdx.x == 0) {
-            pre[0] = 0;
-            pre[1] = p.row_tiles * (p.nk + (nlist * p.lora_rp + p.unit_cols - 1) / p.unit_cols);
-        }
-        __syncthreads();
+    if (kMoe) mark_ids(p.ids, p.tokens * p.topk, p.expert_base, p.experts, marks);
+    else if (one_tile) mark_ids(p.ids, p.tokens, 0, p.lora_count, marks);
+    StreamSetup<kMode>& setup = *reinterpret_cast<StreamSetup<kMode>*>(smem + C::kOffSetup);
+    const int share = static_cast<int>(blockIdx.x);
+    if (warp == 0) {
+        StreamPlan pl;
+        int nlist = 0;
+        pl.row_tiles = p.row_tiles;
+        pl.pre = pre;
         pl.nk = p.nk;
-        pl.units = pre[1];
-    } else {
-        // units of a token tile: row tiles x (K-groups + adapter units of unit_cols rank columns)
-        if (warp == 0) {
+        if (kMoe || one_tile) nlist = list_marked(marks, list);
+        auto tile_units = [&](int adapters) { return p.nk + (adapters * p.lora_rp + p.unit_cols - 1) / p.unit_cols; };
+        if constexpr (kMoe) {
+            pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
+            pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
+        } else if (one_tile) {
+            pl.nk = tile_units(nlist);
+            pl.units = p.row_tiles * pl.nk;
+            if (lane < 2) pre[lane] = lane * pl.units;
+        } else {
+            // units of a token tile: row tiles x (K-groups + adapter units of unit_cols rank columns)
             int run = 0;
             for (int i0 = 0; i0 < p.token_tiles; i0 += 32) {
                 const int i = i0 + lane;
-                const int c = i < p.token_tiles ? __ldcg(p.slot_count + i) : 0;
-                const int v = i < p.token_tiles ? p.row_tiles * (p.nk + (c * p.lora_rp + p.unit_cols - 1) / p.unit_cols) : 0;
+                const int v = i < p.token_tiles ? p.row_tiles * tile_units(__ldcg(p.slot_count + i)) : 0;
                 int incl = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -523,33 +532,31 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 run += __shfl_sync(0xffffffffu, incl, 31);
             }
             if (lane == 0) pre[p.token_tiles] = run;
+            pl.units = run;
         }
-        __syncthreads();
-        pl.nk = p.nk;
-        pl.units = pre[p.token_tiles];
+        pl.fp8 = kMode == kProj ? p.nk : pl.nk;
+        if (cl > 1) {
+            pl.pieces = cl;
+            pl.shares = cl * p.row_tiles;
+            pl.q = pl.r = 0;
+        } else {
+            const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
+            plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
+                        kMoe || one_tile, p.spread != nullptr);
+        }
+        __syncwarp();
+        if (lane == 0) {
+            setup.pl = pl;
+            setup.listed = nlist;
+            setup.walk = StreamWalk<kMode>(pl, share);
+        }
     }
+    __syncthreads();
+    const StreamPlan pl = setup.pl;
+    const StreamWalk<kMode>& share_walk = setup.walk;      // each role's copy starts from it
+    const int nlist = setup.listed;
     auto slots_of = [&](int tt) { return one_tile ? nlist : __ldcg(p.slot_count + tt); };
     auto adapter_of = [&](int tt, int slot) { return one_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
-    pl.units = __shfl_sync(0xffffffffu, pl.units, 0);
-    nlist = __shfl_sync(0xffffffffu, nlist, 0);
-    pl.nk = __shfl_sync(0xffffffffu, pl.nk, 0);
-    pl.row_tiles = p.row_tiles;
-    pl.pre = pre;
-    const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
-    if (one_tile) pl.nk = pl.units / p.row_tiles;
-    pl.fp8 = kMode == kProj ? p.nk : pl.nk;
-    if (cl > 1) {
-        pl.pieces = cl;
-        pl.shares = cl * p.row_tiles;
-        pl.q = pl.r = 0;
-    } else {
-        plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
-                    kMoe || one_tile, p.spread != nullptr);
-    }
-    const int share = static_cast<int>(blockIdx.x);
-    StreamWalk<kMode>& share_walk = *reinterpret_cast<StreamWalk<kMode>*>(smem + C::kOffWalk);   // each role's copy starts from it
-    if (threadIdx.x == 0) share_walk = StreamWalk<kMode>(pl, share);
-    __syncthreads();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
     // kProj: adapter units behind the K-groups
