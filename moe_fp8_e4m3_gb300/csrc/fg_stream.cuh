@@ -11,12 +11,24 @@
 //
 // Work split: the units of one launch - (tile, K-group) pairs, tile by tile - form one line
 // that is cut into equal shares, one per CTA, wherever the cuts fall ("stream-K"): every SM
-// streams the same number of bytes whatever the number of experts, tiles and K-groups.  A
-// tile cut by a share's border is accumulated by several CTAs: each writes its FP32 partial
-// to the workspace and counts itself in; the one that arrives last adds the partials up in
-// CTA order (so the result does not depend on which came last) and finishes the tile.  No
-// CTA ever waits for another.  The counters wrap to zero by themselves (atomicInc).  Where the
-// tiles fit the SMs, whole tiles or equal pieces of each are dealt instead (plan_shares).
+// streams the same number of bytes whatever the number of experts, tiles and K-groups.  Where
+// the tiles fit the SMs, whole tiles or equal pieces of each are dealt instead (plan_shares).
+// A cut tile is accumulated by several CTAs, whose FP32 parts are added up in share order (so
+// the result does not depend on who comes last), in one of three ways that the host chooses:
+//   through the workspace: each CTA writes its part and counts itself in, the last to arrive
+//     adds them up and finishes the tile; no CTA waits for another, and the counters wrap to
+//     zero by themselves (atomicInc);
+//   in a cluster (few columns, tiles x pieces within the SMs): the parts stay in the CTAs' shared
+//     memory, and each CTA adds up its share of the tile over the cluster;
+//   spread (kDown with 64 or more columns): all parts go to the workspace and a third launch adds
+//     them up on all SMs (stream_reduce_kernel).
+//
+// Bound: HBM, whose time for the weights is the floor.  Measured on GB300, the whole MoE MLP, its
+// launches included: 128 tokens x 7168 x 2048, 32 experts, E4M3 253 us (5.6 TB/s, 0.82 of a copy's
+// 6.8), 16 x 4096 49.5 us (0.76), 37 x 4096 with FP4 weights 93 us (0.68; half the bytes in the
+// same ring), 1 x 4096 34 us (0.65).  Within a launch the weights stream at 6.3 to 6.6 TB/s; what
+// is left are the ends: 3 us until the first loads are out and 2 us until they are back, 4 to 5 us
+// from the first launch's last product to the second's first, and the joins.
 //
 // Modes
 //   kGateUp  tile = 128 gate rows + the 128 up rows of one expert; epilogue: SiLU(gate) * up *
@@ -678,9 +690,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         __syncwarp();
     } else if (warp == 1 || warp == 9) {
         // ------------------------------------------------------------- MMA issuers
-        // One for each 128-row block of the tile: a thread needs ~80 clocks to issue a
-        // tcgen05.mma, so one issuer's eight per unit (~0.45 us with the waits) would pace the
-        // FP4 weights, whose unit takes HBM 0.38 us.
+        // One for each 128-row block of the tile.  The whole warp takes the loop and the waits, one
+        // elected lane issues: measured 0.14 us for a unit's four products and copies where a
+        // single-lane loop takes 0.29, which, twice for one issuer, would pace the FP4 weights
+        // (HBM 0.38 us a unit).
         {
             const int blk = warp == 1 ? 0 : 1;
             constexpr uint32_t kIdesc = make_idesc_stream(BN, kFp4);
