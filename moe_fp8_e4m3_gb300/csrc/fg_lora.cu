@@ -5,7 +5,7 @@
 // prompt by the projection's units (0.33 us each where nothing waits, their products' time).
 // Measured on GB300, both launches: 1 token x 4096 x 4096, rank 16 10.2 us; 64 x 7168 x 4096 with
 // 52 adapters of rank 16 21.2 us (2.2 TB/s); 33 x 1008 x 2048, rank 8, FP32 10.6 us; 2048 x 4096 x
-// 4096, rank 64, five prompts 65 us, 46 of them the projection (1.5 PFLOP/s).
+// 4096, rank 64, five prompts 61 us, 42 of them the projection (1.7 PFLOP/s).
 #include <cuda_bf16.h>
 
 #include <cstdio>
@@ -524,9 +524,19 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
     // FP8 weights meanwhile: this launch leaves them their SMs, they leave it at least 40.  Measured
     // on GB300 (64 x 7168, 52 adapters): 4 CTAs a cluster and 40 here 21.0 us, 72 here 22.4 (some
     // clusters start late), no clusters 25.0; 64 x 4096, 6 a cluster 16.4, none 23.0.
+    // Several token tiles take clusters too where they are few and long enough for the join to pay
+    // (~4 us; of the adapters in a tile the host knows at most how many there are, and counts on 16):
+    // 180 x 544 x 640, 113 adapters of rank 128 46.0 us (8 a cluster), 94 in equal shares, 177 in whole
+    // tiles; 275 x 464 x 2304, rank 8 20.2 (6), 54.6, 22.1; 350 x 1456 x 640, one adapter 20.9 (5), 31.4,
+    // 18.1.
     const int row_tiles = ceil_div(N, 256);
-    const int cluster = l.tiles == 1 ? fg::stream_cluster<fg::kProj, false>(l.bn, row_tiles, grid - 40) : 1;
-    if (launch_shrink(sp, sm, l.tiles, cluster > 1 ? grid - cluster * row_tiles : st.sms, st.pdl, s) != cudaSuccess) {
+    int cluster = fg::stream_cluster<fg::kProj, false>(l.bn, row_tiles * l.tiles, l.tiles == 1 ? grid - 40 : grid * 3 / 4);
+    if (l.tiles > 1) {
+        const float units = K / 128 + static_cast<float>((L < 16 ? L : 16) * l.rp) / unit_cols;
+        if (units * 0.33f * (cluster - 1) < 4.0f * cluster) cluster = 1;
+    }
+    const int beside = l.tiles == 1 && cluster > 1 ? cluster * row_tiles : 0;
+    if (launch_shrink(sp, sm, l.tiles, beside ? grid - beside : st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
         return FG_ERR_CUDA;
     }
@@ -569,7 +579,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = st.debug_stall;
         p.cluster = cluster;
-        const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles : grid);
+        const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles * l.tiles : grid);
         if (fg::launch_stream<fg::kProj, false>(l.bn, p, m, ctas, s) != cudaSuccess) {
             cudaGetLastError();
             return FG_ERR_CUDA;

@@ -12,14 +12,15 @@
 // Work split: the units of one launch - (tile, K-group) pairs, tile by tile - form one line
 // that is cut into equal shares, one per CTA, wherever the cuts fall ("stream-K"): every SM
 // streams the same number of bytes whatever the number of experts, tiles and K-groups.  Where
-// the tiles fit the SMs, whole tiles or equal pieces of each are dealt instead (plan_shares).
+// cuts cost more than they balance, whole tiles or equal pieces of each are dealt instead
+// (plan_shares, plan_prompt).
 // A cut tile is accumulated by several CTAs, whose FP32 parts are added up in share order (so
 // the result does not depend on who comes last), in one of three ways that the host chooses:
 //   through the workspace: each CTA writes its part and counts itself in, the last to arrive
 //     adds them up and finishes the tile; no CTA waits for another, and the counters wrap to
 //     zero by themselves (atomicInc);
-//   in a cluster (few columns, tiles x pieces within the SMs): the parts stay in the CTAs' shared
-//     memory, and each CTA adds up its share of the tile over the cluster;
+//   in a cluster (few columns or a prompt's few tiles, tiles x pieces within the SMs): the parts stay
+//     in the CTAs' shared memory, and each CTA adds up its share of the tile over the cluster;
 //   spread (kDown with 64 or more columns): all parts go to the workspace and a third launch adds
 //     them up on all SMs (stream_reduce_kernel).
 //
@@ -214,8 +215,9 @@ struct StreamSeg {
 
 struct StreamPlan {
     int units, shares, nk, row_tiles;
-    int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares
-    int q, r;            // equal shares: r shares of q + 1 units, then shares of q
+    int pieces;          // > 0: every tile is cut into that many pieces, one a share; 0: equal shares;
+                         // -1: whole tiles, equally many to a share
+    int q, r;            // the last two: r shares of q + 1 units (tiles), then shares of q
     int fp8;             // kProj: FP8 units of a tile
     const int* pre;      // kProj: units before each token tile
 };
@@ -225,7 +227,7 @@ __device__ __forceinline__ int piece_begin(const StreamPlan& pl, int i) {
     return i == 0 ? 0 : i * pl.fp8 / pl.pieces + (pl.nk == pl.fp8 ? 0 : i * (pl.nk - pl.fp8) / pl.pieces);
 }
 __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
-    if (pl.pieces) {
+    if (pl.pieces > 0) {
         const int t = c / pl.pieces;
         return t * pl.nk + piece_begin(pl, c - t * pl.pieces);
     }
@@ -233,7 +235,7 @@ __device__ __forceinline__ int share_begin(const StreamPlan& pl, int c) {
 }
 // The first and the last share of the tile of units [u0, u0 + nk).
 __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, int& first, int& last) {
-    if (pl.pieces) {
+    if (pl.pieces > 0) {
         first = u0 / pl.nk * pl.pieces;
         last = first + pl.pieces - 1;
         return;
@@ -246,36 +248,64 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
     last = of(u0 + nk - 1);
 }
 
+__device__ __forceinline__ void deal_shares(StreamPlan& pl, int tiles, int grid) {
+    pl.shares = max(1, pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units));
+    const int n = pl.pieces < 0 ? tiles : pl.units;
+    pl.q = n / pl.shares;
+    pl.r = n - pl.q * pl.shares;
+}
 // How `tiles` tiles of nk units each become shares for at most `grid` CTAs: s pieces per tile
-// (s = 1: no cut), where all pieces find a CTA, or equal shares cut anywhere.  A tile's time is
-// the larger of a CTA's units at the pace of its MMA issuers and all units at HBM's (less `early`
-// units per share, which stream before the launch can begin), plus the join of a cut tile;
-// equal shares cut a tile at both ends of a share.  Measured on GB300: a unit takes an SM 0.3 us
-// when HBM keeps up, all SMs together 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM; counting in takes
-// 2 us and a partial's chunk 0.25 us.
-__device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int early,
-                                            bool even_ok, bool spread) {
+// (s = 1: no cut), where all pieces find a CTA, whole tiles in several rounds, or equal shares cut
+// anywhere.  The time is the larger of a CTA's units at the pace of its MMA issuers and all units
+// at HBM's (less `early` units per share, which stream before the launch can begin; in the last
+// round of whole tiles only some CTAs ask for theirs), plus the join of a cut tile.  Equal shares
+// cut a tile at both ends of a share; with more than a tile to a share the join hides behind the
+// rest of it.  Measured on GB300: a unit takes an SM 0.3 us when HBM keeps up, all SMs together
+// 4.75 ns (E4M3) or 2.5 ns (FP4) of HBM; counting in takes 2 us and a partial's chunk 0.25 us, and
+// what equal shares lose against whole tiles with the same bytes 8 us at 64 columns and 11 us of
+// streaming, 6 at 128 and 19, 4 at 128 and 46, nothing at 128 and 136, 3 to 4 at 32 and 15.  The
+// whole MoE MLP, equal shares and whole tiles: 59 x 1408 x 1280, 24 experts 52.6 and 44.6 us; 88 x
+// 2048 x 1920, 17 experts 71.1 and 65.0; 29 x 1920 x 1536, 37 experts, FP4 54.8 and 51.6; 128 x 7168
+// x 2048, 32 experts 255 and 263; 37 x 4096 x 2048, 32 experts, FP4 94.4 and 98.7.
+__device__ __forceinline__ void plan_shares(StreamPlan& pl, int tiles, int grid, bool fp4, int chunks, int early, bool spread) {
     const float unit_hbm = fp4 ? 0.0025f : 0.00475f;
     const float units = pl.units, nk = pl.nk;
     auto time = [&](float shares, float per, float n) {
         const float t = fmaxf(per * 0.3f, fmaxf(units - early * shares, 0.0f) * unit_hbm);
         return t + (spread ? 0.1f * n : n > 1.0f ? 2.0f + 0.25f * n * chunks : 0.0f);
     };
-    // lane s > 0 looks at s pieces per tile, lane 0 at equal shares; the least time (its bits, the
-    // lane in the low five) wins
+    // lane s > 0 looks at s pieces per tile, lane 0 at equal shares, lane 31 at whole tiles; the least
+    // time (its bits, the lane in the low five) wins
     const int s = static_cast<int>(threadIdx.x & 31);
     float t = 1e30f;
     if (s == 0) {
         const float per = fmaxf(__fdividef(units, static_cast<float>(grid)), 1.0f);
-        t = time(fminf(grid, units), per, __fdividef(nk, per) + 1.0f) + (spread ? 0.0f : 2.0f);
-    } else if (even_ok && s <= 16 && s * tiles <= grid && s <= pl.fp8) {      // (no piece is empty)
+        const float n = __fdividef(nk, per) + 1.0f, all = time(fminf(grid, units), per, 1.0f);
+        t = spread ? time(fminf(grid, units), per, n)
+                   : all + fmaxf(n > 2.0f ? 4.0f + 0.25f * n * chunks : 0.0f, (chunks > 1 ? 9.0f : 5.0f) - 0.125f * all);
+    } else if (s <= 16 && s * tiles <= grid && s <= pl.fp8) {                 // (no piece is empty)
         t = time(s * tiles, __fdividef(nk, static_cast<float>(s)), s);
+    } else if (s == 31 && tiles > grid) {
+        const int rounds = tiles / grid;
+        t = nk * (rounds * fmaxf(0.3f, grid * unit_hbm) +
+                  (tiles > rounds * grid ? fmaxf(0.33f, (tiles - rounds * grid) * unit_hbm) : 0.0f));
     }
     const uint32_t best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | s);
-    pl.pieces = static_cast<int>(best & 31u);
-    pl.shares = max(1, pl.pieces ? pl.pieces * tiles : min(grid, pl.units));
-    pl.q = pl.units / pl.shares;
-    pl.r = pl.units - pl.q * pl.shares;
+    pl.pieces = (best & 31u) == 31u ? -1 : static_cast<int>(best & 31u);
+    deal_shares(pl, tiles, grid);
+}
+// The same for a projection of several token tiles (128 columns each, `most` units in the largest
+// one), whose products bound it: whole tiles, or equal shares where that leaves too many CTAs idle in
+// the last round.  Measured on GB300: a unit takes 0.33 us, a tile's epilogue or part 3 us, counting
+// in and waiting for the last arrival 6, adding a part of 128 KB 2.2.  Whole tiles and equal shares:
+// 2048 x 4096 x 4096, rank 64 60.4 and 66.8 us; 664 x 4224 x 1280 23.4 and 35.2; 1037 x 416 x 1408
+// 28.2 and 51.0; 180 x 544 x 640, 113 adapters of rank 128 177 and 93.7.
+__device__ __forceinline__ void plan_prompt(StreamPlan& pl, int tiles, int grid, int most) {
+    const float nk = __fdividef(pl.units, tiles), per = __fdividef(pl.units, static_cast<float>(min(grid, pl.units)));
+    const float whole = ((tiles + grid - 1) / grid) * (0.33f * most + 3.0f);
+    const float equal = 0.33f * per + 3.0f * (__fdividef(per, nk) + 1.0f) + 6.0f + 2.2f * (__fdividef(nk, per) + 1.0f);
+    pl.pieces = whole <= equal ? -1 : 0;
+    deal_shares(pl, tiles, grid);
 }
 
 // What stream_reduce_kernel has to know of a plan.
@@ -293,9 +323,29 @@ struct StreamWalk {
     __device__ __forceinline__ StreamWalk(const StreamPlan& pl, int share)
         : u(0), end(0), tail(-1), tail_end(0), tile(0), tt(0), first(0), nk(1), tail_tile(0), tail_tt(0), tail_nk(1) {
         if (share >= pl.shares) return;
-        if (pl.pieces) {                  // one piece of one tile
+        if (pl.pieces < 0) {
+            auto first_of = [&](int t) {
+                tile = t;
+                nk = pl.nk;
+                if (kMode != kProj) return t * nk;
+                tt = t / pl.row_tiles;
+                tile = t - tt * pl.row_tiles;
+                nk = (pl.pre[tt + 1] - pl.pre[tt]) / pl.row_tiles;
+                return pl.pre[tt] + tile * nk;
+            };
+            const int t = share * pl.q + min(share, pl.r);
+            const int last = first_of(t + pl.q - (share < pl.r ? 0 : 1));
+            end = last + nk;
+            u = first = first_of(t);
+            return;
+        }
+        if (pl.pieces > 0) {              // one piece of one tile
             tile = pl.pieces == 1 ? share : share / pl.pieces;
             const int i = share - tile * pl.pieces;
+            if (kMode == kProj) {         // (in a cluster, pl.nk is this tile's)
+                tt = tile / pl.row_tiles;
+                tile -= tt * pl.row_tiles;
+            }
             nk = pl.nk;
             first = tile * nk;
             u = first + piece_begin(pl, i);
@@ -349,7 +399,7 @@ struct StreamWalk {
     }
     __device__ __forceinline__ void deal(const StreamPlan& pl, StreamSeg& s) const {
         if (kMode != kProj) return;
-        if (pl.pieces) {
+        if (pl.pieces > 0) {
             // k0 is the sum of both kinds' shares before piece i (the share is one piece)
             const int i = static_cast<int>(blockIdx.x) % pl.pieces;
             s.f0 = i * pl.fp8 / pl.pieces;
@@ -515,7 +565,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const int share = static_cast<int>(blockIdx.x);
     if (warp == 0) {
         StreamPlan pl;
-        int nlist = 0;
+        int nlist = 0, most = 0;              // (units of the largest token tile)
         pl.row_tiles = p.row_tiles;
         pl.pre = pre;
         pl.nk = p.nk;
@@ -534,6 +584,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             for (int i0 = 0; i0 < p.token_tiles; i0 += 32) {
                 const int i = i0 + lane;
                 const int v = i < p.token_tiles ? p.row_tiles * tile_units(__ldcg(p.slot_count + i)) : 0;
+                most = max(most, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v))));
                 int incl = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -544,17 +595,24 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                 run += __shfl_sync(0xffffffffu, incl, 31);
             }
             if (lane == 0) pre[p.token_tiles] = run;
+            __syncwarp();
             pl.units = run;
         }
         pl.fp8 = kMode == kProj ? p.nk : pl.nk;
         if (cl > 1) {
             pl.pieces = cl;
-            pl.shares = cl * p.row_tiles;
+            pl.shares = cl * p.row_tiles * (kMode == kProj ? p.token_tiles : 1);
             pl.q = pl.r = 0;
+            if (kMode == kProj && !one_tile) {
+                const int tt = share / cl / p.row_tiles;
+                pl.nk = (pre[tt + 1] - pre[tt]) / p.row_tiles;
+            }
+        } else if (kMode == kProj && !one_tile) {
+            plan_prompt(pl, p.token_tiles * p.row_tiles, static_cast<int>(gridDim.x), most / p.row_tiles);
         } else {
             const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
             plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
-                        kMoe || one_tile, p.spread != nullptr);
+                        p.spread != nullptr);
         }
         __syncwarp();
         if (lane == 0) {
@@ -906,8 +964,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             // only tile's products are done), and each adds up every cl-th (column, 32 rows) of the
             // tile over the cluster, in piece order.
             float* xch = reinterpret_cast<float*>(smem);               // [column][block][row]
-            const int cols_all = min(BN, p.tokens);
-            const int rank = static_cast<int>(cluster_ctarank()), tile = share_walk.tile;
+            const int rank = static_cast<int>(cluster_ctarank()), tile = share_walk.tile, token0 = share_walk.tt * BN;
+            const int cols_all = min(BN, p.tokens - token0);
             uint32_t full = 0;                                         // pieces that are not empty
             for (int c = 0; c < cl; ++c)
                 if (pl.fp8 >= cl || (c + 1 == cl ? pl.nk : piece_begin(pl, c + 1)) > piece_begin(pl, c)) full |= 1u << c;
@@ -961,8 +1019,9 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                         for (int c = 1; c < 8; ++c) v[n] += x[n][c];
                         const int it = i0 + cl * 8 * n, t = it >> 3, r = tile * 256 + (it & 7) * 32 + lane;
                         if (it < cols_all * 8 && r < p.out_rows) {
-                            if (p.d_f32) static_cast<float*>(p.d)[(long long)t * p.out_rows + r] = v[n];
-                            else static_cast<__nv_bfloat16*>(p.d)[(long long)t * p.out_rows + r] = __float2bfloat16(v[n]);
+                            const long long at = (long long)(token0 + t) * p.out_rows + r;
+                            if (p.d_f32) static_cast<float*>(p.d)[at] = v[n];
+                            else static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16(v[n]);
                         }
                     }
                 }

@@ -432,3 +432,31 @@ def test_stalled_pipeline_times_out_and_context_survives(fg, which):
         check(run_moe(fg, c, ws=ws, args=args), moe_ref(c))
     else:
         check(run_lora(fg, c, ws=ws, args=args), lora_ref(c))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k,l,r,sms", [
+    # several token tiles in clusters: many adapters, a last tile of 44 tokens, a last block of 16 rows, more
+    # pieces than FP8 units
+    (200, 272, 640, 60, 128, 0), (300, 528, 2304, 3, 16, 0), (129, 144, 128, 40, 64, 0),
+    # whole tiles, one round and several; equal shares
+    (400, 272, 128, 2, 8, 0), (400, 528, 256, 2, 16, 5), (200, 528, 384, 60, 128, 20)])
+def test_lora_prompt_shares(fg, m, n, k, l, r, sms, out):
+    c = D.lora_case(m + n + l, m, n, k, l, r)
+    try:
+        fg.set_num_sms(sms)
+        check(run_lora(fg, c, out), lora_ref(c, out), out)
+    finally:
+        fg.set_num_sms(0)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t,sms", [(9, 0), (40, 0), (70, 0), (20, 37)])
+def test_moe_more_tiles_than_sms(fg, t, sms, fp4):
+    """Whole tiles in several rounds."""
+    c = D.moe_case(31 + t, t, 256, 128, 170, 16, 170, fp4)
+    try:
+        fg.set_num_sms(sms)
+        check(run_moe(fg, c), moe_ref(c))
+    finally:
+        fg.set_num_sms(0)
