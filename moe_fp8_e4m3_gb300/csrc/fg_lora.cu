@@ -382,13 +382,15 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) lora_shrink_kernel(const Sh
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     const int tt = blockIdx.y;
-    fg::grid_dependency_wait();
-    if (threadIdx.x == 0) fg::grid_launch_dependents();
     const int n = min(p.bn, p.tokens - tt * p.bn);
     const int32_t* ids = p.ids + (long long)tt * p.bn;
-    const int my_id = static_cast<int>(threadIdx.x) < n ? __ldcg(ids + threadIdx.x) : -1;
     if (threadIdx.x < 128) sh.count[threadIdx.x] = 0;
-    fg::mark_ids(ids, n, 0, p.L, sh.marks);
+    fg::clear_marks(sh.marks);
+    fg::grid_dependency_wait();
+    if (threadIdx.x == 0) fg::grid_launch_dependents();
+    const int my_id = fg::load_id(ids, n);
+    __syncthreads();
+    fg::mark_ids(ids, n, my_id, 0, p.L, sh.marks);
     if (threadIdx.x < 32) {
         const int found = fg::list_marked(sh.marks, sh.list);
         if (threadIdx.x == 0) sh.listed = found;

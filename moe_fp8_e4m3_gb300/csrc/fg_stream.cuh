@@ -447,14 +447,19 @@ struct StreamCursor {
 };
 
 // Marks the byte of every id in [base, base + count) among ids[0, n) (plain stores: with few
-// experts, atomics on one word's bits would queue up); all threads.
-__device__ __forceinline__ void mark_ids(const int32_t* ids, int n, int base, int count, uint8_t* marks) {
-    const int t = threadIdx.x;
-    for (int i = t; i < kMaxListed / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(marks)[i] = 0;
-    __syncthreads();
-    for (int i = t; i < n; i += blockDim.x) {
-        const unsigned v = static_cast<unsigned>(__ldcg(ids + i)) - static_cast<unsigned>(base);
+// experts, atomics on one word's bits would queue up); all threads, behind a barrier after
+// clear_marks.  own: what load_id gave the thread, so that the load can run ahead of the barrier.
+__device__ __forceinline__ void clear_marks(uint8_t* marks) {
+    for (int i = threadIdx.x; i < kMaxListed / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(marks)[i] = 0;
+}
+__device__ __forceinline__ int load_id(const int32_t* ids, int n) {
+    return static_cast<int>(threadIdx.x) < n ? __ldcg(ids + threadIdx.x) : -1;
+}
+__device__ __forceinline__ void mark_ids(const int32_t* ids, int n, int own, int base, int count, uint8_t* marks) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const unsigned v = static_cast<unsigned>(own) - static_cast<unsigned>(base);
         if (v < static_cast<unsigned>(count)) marks[v] = 1;
+        if (i + blockDim.x < n) own = __ldcg(ids + i + blockDim.x);
     }
     __syncthreads();
 }
@@ -522,6 +527,13 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
     int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
 
+    // kDown runs behind its own kGateUp launch, and kProj behind x @ A^T, which let it start only
+    // after their own wait: the ids, weights and adapters they read before this launch's wait were
+    // complete before that.  Only the roles that touch what the launch before writes wait.
+    const bool one_tile = kMode == kProj && p.token_tiles == 1;
+    const int n_ids = kMoe ? p.tokens * p.topk : (one_tile ? p.tokens : 0);
+    int own_id = kMode == kGateUp ? -1 : load_id(p.ids, n_ids);
+    clear_marks(marks);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(full_bar(s), 66);          // two TMA producers; the lanes of the scale loader and of warp 3
@@ -551,16 +563,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     if (cl > 1) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    // kDown runs behind its own kGateUp launch, and kProj behind x @ A^T, which let it start only
-    // after their own wait: the ids, weights and adapters they read before this launch's wait were
-    // complete before that.  Only the roles that touch what the launch before writes wait.
-    const bool one_tile = kMode == kProj && p.token_tiles == 1;
     if (kMode == kGateUp || (kMode == kProj && !one_tile)) {
         grid_dependency_wait();
         if (threadIdx.x == 0) grid_launch_dependents();
     }
-    if (kMoe) mark_ids(p.ids, p.tokens * p.topk, p.expert_base, p.experts, marks);
-    else if (one_tile) mark_ids(p.ids, p.tokens, 0, p.lora_count, marks);
+    if (kMode == kGateUp) own_id = load_id(p.ids, n_ids);
+    if (kMoe || one_tile) mark_ids(p.ids, n_ids, own_id, kMoe ? p.expert_base : 0, kMoe ? p.experts : p.lora_count, marks);
     StreamSetup<kMode>& setup = *reinterpret_cast<StreamSetup<kMode>*>(smem + C::kOffSetup);
     const int share = static_cast<int>(blockIdx.x);
     if (warp == 0) {
