@@ -8,6 +8,7 @@ built (``moe_fp8_e4m3_gb300.build.build()``)."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +80,9 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+# bytes a workspace needs, by sizes: a call through ctypes (0.6 us) once per size, not once per step
+_moe_mlp_bytes = functools.lru_cache(1024)(lib.fg_moe_mlp_workspace)
+_lora_bytes = functools.lru_cache(1024)(lib.fg_lora_workspace)
 
 
 class FgError(RuntimeError):
@@ -441,7 +445,7 @@ def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weight
     e2, h2, _ = w2.shape
     if e2 != e or h2 != h or len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape:
         raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I], topk_ids and topk_weights [T,topk]")
-    if not workspace.is_cuda or workspace.nbytes < lib.fg_moe_mlp_workspace(t, h, i, e):
+    if not workspace.is_cuda or workspace.nbytes < _moe_mlp_bytes(t, h, i, e):
         raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
     st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
             sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), d.data_ptr(),
@@ -495,7 +499,7 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
     if (kb != k or x.shape != a.shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
             ids.numel() != m or d.shape != (m, n)):
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
-    if not workspace.is_cuda or workspace.nbytes < lib.fg_lora_workspace(m, n, k, r):
+    if not workspace.is_cuda or workspace.nbytes < _lora_bytes(m, n, k, r):
         raise ValueError("workspace is smaller than lora_workspace(m, n, k, r)")
     st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
                                  lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), ids.data_ptr(), d.data_ptr(),
