@@ -543,7 +543,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         const float units = K / 128 + static_cast<float>((L < 16 ? L : 16) * l.rp) / unit_cols;
         if (units * 0.33f * (cluster - 1) < 4.0f * cluster) cluster = 1;
     }
-    const int beside = l.tiles == 1 && cluster > 1 ? cluster * row_tiles : 0;
+    const int beside = cluster > 1 ? cluster * row_tiles * l.tiles : 0;
     if (launch_shrink(sp, sm, l.tiles, beside ? grid - beside : st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
         return FG_ERR_CUDA;

@@ -530,9 +530,13 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     // kDown runs behind its own kGateUp launch, and kProj behind x @ A^T, which let it start only
     // after their own wait: the ids, weights and adapters they read before this launch's wait were
     // complete before that.  Only the roles that touch what the launch before writes wait.
-    const bool one_tile = kMode == kProj && p.token_tiles == 1;
-    const int n_ids = kMoe ? p.tokens * p.topk : (one_tile ? p.tokens : 0);
-    int own_id = kMode == kGateUp ? -1 : load_id(p.ids, n_ids);
+    // A CTA of one token tile (the only one, or its cluster's) finds its adapters by itself; one whose
+    // share crosses tiles reads what the launch before found.
+    const bool own_tile = kMode == kProj && (p.token_tiles == 1 || cl > 1);
+    const int own_tt = own_tile && p.token_tiles > 1 ? static_cast<int>(blockIdx.x) / cl / p.row_tiles : 0;
+    const int32_t* ids = p.ids + own_tt * BN;
+    const int n_ids = kMoe ? p.tokens * p.topk : (own_tile ? min(BN, p.tokens - own_tt * BN) : 0);
+    int own_id = kMode == kGateUp ? -1 : load_id(ids, n_ids);
     clear_marks(marks);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -563,12 +567,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     if (cl > 1) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    if (kMode == kGateUp || (kMode == kProj && !one_tile)) {
+    if (kMode == kGateUp || (kMode == kProj && !own_tile)) {
         grid_dependency_wait();
         if (threadIdx.x == 0) grid_launch_dependents();
     }
-    if (kMode == kGateUp) own_id = load_id(p.ids, n_ids);
-    if (kMoe || one_tile) mark_ids(p.ids, n_ids, own_id, kMoe ? p.expert_base : 0, kMoe ? p.experts : p.lora_count, marks);
+    if (kMode == kGateUp) own_id = load_id(ids, n_ids);
+    if (kMoe || own_tile) mark_ids(ids, n_ids, own_id, kMoe ? p.expert_base : 0, kMoe ? p.experts : p.lora_count, marks);
     StreamSetup<kMode>& setup = *reinterpret_cast<StreamSetup<kMode>*>(smem + C::kOffSetup);
     const int share = static_cast<int>(blockIdx.x);
     if (warp == 0) {
@@ -577,12 +581,12 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         pl.row_tiles = p.row_tiles;
         pl.pre = pre;
         pl.nk = p.nk;
-        if (kMoe || one_tile) nlist = list_marked(marks, list);
+        if (kMoe || own_tile) nlist = list_marked(marks, list);
         auto tile_units = [&](int adapters) { return p.nk + (adapters * p.lora_rp + p.unit_cols - 1) / p.unit_cols; };
         if constexpr (kMoe) {
             pl.nk = kMode == kDown ? nlist * p.nk : p.nk;
             pl.units = kMode == kDown ? p.row_tiles * pl.nk : nlist * p.row_tiles * pl.nk;
-        } else if (one_tile) {
+        } else if (own_tile) {
             pl.nk = tile_units(nlist);
             pl.units = p.row_tiles * pl.nk;
             if (lane < 2) pre[lane] = lane * pl.units;
@@ -611,11 +615,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             pl.pieces = cl;
             pl.shares = cl * p.row_tiles * (kMode == kProj ? p.token_tiles : 1);
             pl.q = pl.r = 0;
-            if (kMode == kProj && !one_tile) {
-                const int tt = share / cl / p.row_tiles;
-                pl.nk = (pre[tt + 1] - pre[tt]) / p.row_tiles;
-            }
-        } else if (kMode == kProj && !one_tile) {
+        } else if (kMode == kProj && !own_tile) {
             plan_prompt(pl, p.token_tiles * p.row_tiles, static_cast<int>(gridDim.x), most / p.row_tiles);
         } else {
             const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
@@ -633,8 +633,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     const StreamPlan pl = setup.pl;
     const StreamWalk<kMode>& share_walk = setup.walk;      // each role's copy starts from it
     const int nlist = setup.listed;
-    auto slots_of = [&](int tt) { return one_tile ? nlist : __ldcg(p.slot_count + tt); };
-    auto adapter_of = [&](int tt, int slot) { return one_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
+    auto slots_of = [&](int tt) { return own_tile ? nlist : __ldcg(p.slot_count + tt); };
+    auto adapter_of = [&](int tt, int slot) { return own_tile ? static_cast<int>(list[slot]) : __ldcg(p.slot_ids + tt * p.max_slots + slot); };
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
     // kProj: adapter units behind the K-groups
@@ -702,7 +702,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         }
         int s = 0;
         uint32_t ph = 0, armed = 0, armed_par = 0;
-        bool aborted = false, waited = !one_tile;
+        bool aborted = false, waited = !own_tile;
         StreamCursor<kMode> c(pl, share_walk, p.nk);
         for (; c.valid; c.step(pl)) {
             if (kMode == kProj && !waited && c.k >= p.nk) {      // x @ A^T from here on
@@ -932,8 +932,8 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         constexpr int kHalf = BN / 2, kChunk = C::kChunk, kJoin = C::kJoin;
         const int q = warp & 3, row = q * 32 + lane, grp = warp >= 8 ? 1 : 0;
         const int te = row;                                            // 0..127 over the group
-        if (kMode == kDown || one_tile) grid_dependency_wait();
-        if (one_tile && threadIdx.x == 128) grid_launch_dependents();
+        if (kMode == kDown || own_tile) grid_dependency_wait();
+        if (own_tile && threadIdx.x == 128) grid_launch_dependents();
         if (p.spread && share == 0 && threadIdx.x == 128) {
             p.spread[kSpreadUnits] = pl.units;
             p.spread[kSpreadShares] = pl.shares;
