@@ -528,21 +528,15 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
             !fg::encode_tiled(&sm.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lora_a, ad, ap, ab, CU_TENSOR_MAP_SWIZZLE_128B))
             return FG_ERR_INVALID_ARG;
     }
-    // A single token tile's projection runs in clusters that start beside this launch and stream the
-    // FP8 weights meanwhile: this launch leaves them their SMs, they leave it at least 40.  Measured
-    // on GB300 (64 x 7168, 52 adapters): 4 CTAs a cluster and 40 here 21.0 us, 72 here 22.4 (some
-    // clusters start late), no clusters 25.0; 64 x 4096, 6 a cluster 16.4, none 23.0.
-    // Several token tiles take clusters too where they are few and long enough for the join to pay
-    // (~4 us; of the adapters in a tile the host knows at most how many there are, and counts on 16):
-    // 180 x 544 x 640, 113 adapters of rank 128 46.0 us (8 a cluster), 94 in equal shares, 177 in whole
-    // tiles; 275 x 464 x 2304, rank 8 20.2 (6), 54.6, 22.1; 350 x 1456 x 640, one adapter 20.9 (5), 31.4,
-    // 18.1.
+    // Where a tile's pieces find SMs, the projection runs in clusters that start beside this launch,
+    // stream the FP8 weights meanwhile and join the pieces: this launch leaves them their SMs, they
+    // leave it 40.  Measured on GB300, one token tile: 64 x 7168 x 4096, 52 adapters 21.0 us with 4 CTAs a
+    // cluster and 40 SMs here, 22.4 with 72 here (some clusters start late), 25.0 without clusters; 64 x
+    // 4096 16.4 with 6, 23.0 without.  Several: 275 x 464 x 2304, rank 8 16.0 with 8, 22.1 in whole
+    // tiles, 54.6 in equal shares; 221 x 1984 x 2432, one adapter 17.8 with 7, 24.2, 40.4; 180 x 544 x
+    // 640, 113 adapters of rank 128 47 with 8, 177, 94.
     const int row_tiles = ceil_div(N, 256);
-    int cluster = fg::stream_cluster<fg::kProj, false>(l.bn, row_tiles * l.tiles, l.tiles == 1 ? grid - 40 : grid * 3 / 4);
-    if (l.tiles > 1) {
-        const float units = K / 128 + static_cast<float>((L < 16 ? L : 16) * l.rp) / unit_cols;
-        if (units * 0.33f * (cluster - 1) < 4.0f * cluster) cluster = 1;
-    }
+    const int cluster = fg::stream_cluster<fg::kProj, false>(l.bn, row_tiles * l.tiles, grid - 40);
     const int beside = cluster > 1 ? cluster * row_tiles * l.tiles : 0;
     if (launch_shrink(sp, sm, l.tiles, beside ? grid - beside : st.sms, st.pdl, s) != cudaSuccess) {
         cudaGetLastError();
