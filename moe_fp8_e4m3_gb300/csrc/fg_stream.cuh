@@ -173,7 +173,7 @@ struct StreamCfg {
     static constexpr int kSfBytes = 3 * 512;                                // weight block 0, 1, tokens
     static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
     static constexpr int kMiscBytes = 512 + 1024 + BN * 8 + kMaxListed + 128 + 2 * kMaxListed +
-                                      (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0);
+                                      (kMode == kProj ? 4 * (kMaxTokenTiles + 1) : 0) + (kMode == kGateUp && BN >= 32 ? 2 * 16 * 128 : 0);
     static constexpr int kStages0 = (kSmemLimit - 1024 - kMiscBytes) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
     static constexpr int kNumAcc = BN <= 64 ? 2 : 1;
@@ -197,6 +197,7 @@ struct StreamCfg {
     static constexpr int kOffSetup = kOffBits + kMaxListed;
     static constexpr int kOffList = kOffSetup + 128;
     static constexpr int kOffPre = kOffList + 2 * kMaxListed;
+    static constexpr int kOffCodes = kOffPre;                               // kGateUp, BN >= 32: [group][16 columns][128 rows] E4M3
     static constexpr int kSmemBytes = kOffBar + kMiscBytes + 1024;          // + alignment slack
     static_assert(kNumBars * 8 <= 512 - 64, "barrier area");
     static_assert(kSfCol0 + 64 <= 512, "TMEM columns");
@@ -1244,11 +1245,30 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                     if (q == 0 && lane < kChunk && c0 + lane < cols)
                         p.sfh[(((long long)li * ((p.row_tiles + 3) / 4) + (it >> 2)) * BN + t0 + lane) * 4 + (it & 3)] =
                             static_cast<uint8_t>(e + 127);
-                    uint8_t* hq = p.hq + ((long long)li * BN + t0) * p.out_rows + it * 128 + row;
+                    uint8_t* hq = p.hq + ((long long)li * BN + t0) * p.out_rows + it * 128;
+                    if constexpr (BN >= 32) {
+                        // the codes by way of shared memory, 16 bytes of a token a thread: a byte a row and
+                        // token takes 0.6 us of stores a chunk, of 1.7 (128 x 7168 255.5 -> 253.4 us; 1 x
+                        // 4096, where few columns are stored, 34.4 -> 34.5)
+                        uint8_t* codes = smem + C::kOffCodes + grp * 16 * 128;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        const float x = v0[i] * __shfl_sync(0xffffffffu, sc, i);
-                        if (c0 + i < cols) hq[(long long)i * p.out_rows] = static_cast<uint8_t>(e4m3(x));
+                        for (int i = 0; i < kChunk; i += 2) {
+                            const float x = v0[i] * __shfl_sync(0xffffffffu, sc, i), y = v0[i + 1] * __shfl_sync(0xffffffffu, sc, i + 1);
+                            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+                            codes[i * 128 + row] = static_cast<uint8_t>(two);
+                            codes[(i + 1) * 128 + row] = static_cast<uint8_t>(two >> 8);
+                        }
+                        esync();
+                        const int ct = te >> 3, cr = (te & 7) * 16;
+                        if (c0 + ct < cols)
+                            *reinterpret_cast<uint4*>(hq + (long long)ct * p.out_rows + cr) =
+                                *reinterpret_cast<const uint4*>(codes + ct * 128 + cr);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            const float x = v0[i] * __shfl_sync(0xffffffffu, sc, i);
+                            if (c0 + i < cols) hq[(long long)i * p.out_rows + row] = static_cast<uint8_t>(e4m3(x));
+                        }
                     }
                 } else {
 #pragma unroll
