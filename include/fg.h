@@ -368,10 +368,9 @@ int fg_moe_route(int T, int E, int topk, int n_group, int topk_group, int score,
  *   D[t,:]  = sum over the experts e that t uses of (q * s) @ w2[e]^T
  * accumulated in FP32 over all experts and rounded once.  Ids outside [expert_base,
  * expert_base + E) belong to other shards (or are -1) and are skipped; a token without an
- * expert here gets zeros whatever its row holds.  Non-finite activations of an expert make the
- * rows of the tokens that use it NaN, and no others.  Weights and their scales have to be finite:
- * w2 of an expert that any token uses is multiplied with every token (with zeros for those that do
- * not use it), so a NaN code or scale there reaches that output column of all T tokens.
+ * expert here gets zeros whatever its row holds.  Non-finite activations or weights of an expert
+ * reach the rows of the tokens that use it, and no others (an output that is not finite is worked
+ * out anew from its own token's experts, which takes milliseconds where there are many).
  *   a    [T][H] E4M3, sfa as for fg_fp8_gemm_nt      w13 [E][2I][H], sf13 [E][ceil(H/512)][align4(2I/128)]
  *   w2   [E][H][I], sf2 [E][ceil(I/512)][align4(H/128)]
  *   topk_ids [T][topk] int32, topk_weights [T][topk] FP32;  d [T][H] BF16 or FP32
@@ -401,9 +400,8 @@ int fg_fp8_fp4_moe_mlp(int T, int H, int I, int E, int topk, int expert_base, co
  * in the same FP32 accumulation, D is rounded once.  x @ lora_a^T enters the second product as
  * a sum of BF16 parts: two (16 mantissa bits) for a BF16 D, three (24) for an FP32 D.
  * ids[m] < 0: no adapter; ids[m] >= L: no adapter, and a device contract violation is recorded
- * (0x106).  lora_b has to be finite: rows of an adapter in use are multiplied with every token of
- * its tile of 16 to 128 tokens (with zeros for those of others), so an infinity or a NaN there
- * reaches that output column of the whole tile.  Non-finite x or lora_a stay with their tokens.
+ * (0x106).  Non-finite elements of x and of an adapter stay with the tokens that use them (outputs
+ * that are not finite are worked out anew, as above).
  *   x [M][K] BF16;  lora_a [L][R][K], lora_b [L][N][R] BF16 (smaller ranks zero-padded to R);
  *   scaling [L] FP32;  ids [M] int32;  d [M][N] BF16 or FP32
  *   workspace: fg_lora_workspace bytes, under the same rules as fg_moe_mlp_workspace

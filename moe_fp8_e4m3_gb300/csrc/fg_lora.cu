@@ -580,6 +580,9 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         p.ctr = reinterpret_cast<unsigned*>(ws) + fg::kMaxCounters;
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = st.debug_stall;
+        p.w_raw = b; p.x_raw = a;
+        p.lb_raw = static_cast<const uint16_t*>(lora_b); p.v_raw = sp.v;
+        p.lora_r = R;
         p.cluster = cluster;
         const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles * l.tiles : grid);
         if (fg::launch_stream<fg::kProj, false>(l.bn, p, m, ctas, s) != cudaSuccess) {

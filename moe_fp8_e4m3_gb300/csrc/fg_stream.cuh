@@ -26,7 +26,7 @@
 //
 // Bound: HBM, whose time for the weights is the floor.  Measured on GB300, the whole MoE MLP, its
 // launches included: 128 tokens x 7168 x 2048, 32 experts, E4M3 253 us (5.6 TB/s, 0.82 of a copy's
-// 6.8), 16 x 4096 49.5 us (0.76), 37 x 4096 with FP4 weights 93 us (0.68; half the bytes in the
+// 6.8), 16 x 4096 49.8 us (0.75), 37 x 4096 with FP4 weights 94 us (0.67; half the bytes in the
 // same ring), 1 x 4096 34 us (0.65).  Within a launch the weights stream at 6.3 to 6.6 TB/s; what
 // is left are the ends: 3 us until the first loads are out and 2 us until they are back, 4 to 5 us
 // from the first launch's last product to the second's first, and the joins.
@@ -47,6 +47,9 @@
 // roles wind down and the kernel returns.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
+
 #include "fg_gemm_kernel.cuh"
 
 namespace fg {
@@ -59,7 +62,8 @@ constexpr int kMaxListed = 1024;         // experts of a shard, adapters of a ca
 constexpr int kMaxTokenTiles = 512;      // kProj: token tiles of one call
 constexpr int kMaxStreamCtas = 256;      // shares of a launch (partial slots in the workspace)
 constexpr int kMaxCounters = 512;        // of one launch: two per share, one for each half of the columns
-constexpr int kCounterBytes = 2 * kMaxCounters * 4 + 256;   // head of a workspace: both launches' counters, a spread plan
+// head of a workspace: both launches' counters, a spread plan with its list of experts
+constexpr int kCounterBytes = 2 * kMaxCounters * 4 + 256 + 2 * kMaxListed;
 
 struct StreamMaps {
     CUtensorMap w;       // weights
@@ -98,6 +102,12 @@ struct StreamParams {
     unsigned long long timeout_ns;
     int debug_stall, pdl;
     int cluster;                 // kDown, kProj: > 1: a tile's pieces, one a CTA of a cluster that joins them itself
+    // the operands as plain arrays (mend_outputs): weights, token codes, adapters' B and x @ A^T
+    const uint8_t* w_raw;
+    const uint8_t* x_raw;
+    const uint16_t* lb_raw;
+    const uint16_t* v_raw;
+    int lora_r;
 };
 
 // D(tmem) (+)= A(smem) x B(smem)^T, BF16 inputs, FP32 accumulation in TMEM.
@@ -310,7 +320,7 @@ __device__ __forceinline__ void plan_prompt(StreamPlan& pl, int tiles, int grid,
 }
 
 // What stream_reduce_kernel has to know of a plan.
-enum : int { kSpreadUnits = 0, kSpreadShares, kSpreadNk, kSpreadPieces, kSpreadWords };
+enum : int { kSpreadUnits = 0, kSpreadShares, kSpreadNk, kSpreadPieces, kSpreadListed, kSpreadWords = 8 };
 
 // The pieces of one share: first the tile that goes on into the next share, then the others in
 // order (so a tile that the share before began comes next, whole tiles last).  A cut tile's parts
@@ -496,12 +506,111 @@ struct StreamSetup {
     StreamWalk<kMode> walk;
 };
 
+// ---------------------------------------------------------------- outputs that are not finite
+// Every weight tile is multiplied with every token of its tile, so a NaN weight or scale, or a
+// non-finite element of an adapter's B, makes a NaN of 0 * NaN for tokens that do not use it.  An
+// output that is not finite is therefore worked out again, from what its token uses alone: one
+// thread an output, the same products in FP32, in K order.  Slow, and only ever there; where all is
+// finite it costs an FMA an output, whose zero becomes a NaN behind an infinity or a NaN (37 x 4096
+// FP4 92.9 -> 93.9 us, 2048 x 4096 with adapters 60.1 -> 60.8, the others the same).
+__device__ __forceinline__ float ue8m0(uint32_t b) {
+    return b == 255u ? __int_as_float(0x7fc00000) : __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+__device__ __forceinline__ uint32_t scale_byte(const int32_t* word, int i) {
+    return static_cast<uint32_t>(__ldcg(word)) >> (8 * i) & 255u;
+}
+// One row of nk K-groups: x and w point at its codes, xs at its scale words (xs_ld words apart), ws
+// at the weight row's (FP4: a word a K-group, ws_ld apart; E4M3: one for four).
+template <bool kFp4>
+__device__ __forceinline__ float exact_dot(const uint8_t* x, const uint8_t* w, const int32_t* xs, int xs_ld, const int32_t* ws,
+                                           int ws_ld, int nk) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int g = 0; g < nk && sum == sum; ++g) {                        // (a NaN stays one)
+        const float sx = ue8m0(scale_byte(xs + (long long)(g >> 2) * xs_ld, g & 3));
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {                                   // 32 elements
+            const uint32_t* x4 = reinterpret_cast<const uint32_t*>(x + g * 128 + b * 32);
+            float part = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t xc = __ldcg(x4 + i);
+                const uint32_t wc = kFp4 ? __ldg(reinterpret_cast<const uint16_t*>(w + g * 64 + b * 16) + i)
+                                         : __ldg(reinterpret_cast<const uint32_t*>(w + g * 128 + b * 32) + i);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const __half_raw wv = kFp4 ? __nv_cvt_fp4_to_halfraw(static_cast<__nv_fp4_storage_t>(wc >> (4 * c) & 15u), __NV_E2M1)
+                                               : __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(wc >> (8 * c)), __NV_E4M3);
+                    const __half_raw xv = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(xc >> (8 * c)), __NV_E4M3);
+                    part += __half2float(__half(xv)) * __half2float(__half(wv));
+                }
+            }
+            const float sw = ue8m0(kFp4 ? scale_byte(ws + (long long)g * ws_ld, b) : scale_byte(ws + (long long)(g >> 2) * ws_ld, g & 3));
+            sum += part * sx * sw;
+        }
+    }
+    return sum;
+}
+__device__ __forceinline__ int place_of(const uint16_t* list, int n, int id) {
+    int lo = 0;
+    for (int hi = n; lo < hi;) {
+        const int mid = (lo + hi) / 2;
+        if (list[mid] < id) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+// Row r of D's tokens [t0, t0 + n) of token tile tt, where the stored value is not finite.
+template <int kMode, int BN, bool kFp4>
+__device__ __noinline__ void mend_outputs(const StreamParams& p, const uint16_t* list, int nlist, int tt, int t0, int n, int r) {
+    for (int t = t0; t < t0 + n; ++t) {
+        const int m = tt * BN + t;
+        const long long at = (long long)m * p.out_rows + r;
+        const float old = p.d_f32 ? static_cast<float*>(p.d)[at] : __bfloat162float(static_cast<__nv_bfloat16*>(p.d)[at]);
+        if (old - old == 0.0f) continue;
+        float sum = 0.0f;
+        if (kMode == kDown) {
+            const int32_t* ids = p.ids + (long long)m * p.topk;
+            for (int j = 0; j < p.topk; ++j) {
+                const int id = __ldg(ids + j), e = id - p.expert_base;
+                bool again = static_cast<unsigned>(e) >= static_cast<unsigned>(p.experts);
+                for (int i = 0; i < j; ++i) again |= __ldg(ids + i) == id;
+                if (again) continue;
+                const int li = place_of(list, nlist, e), words = (p.nk + 3) / 4;
+                const long long k = (long long)p.nk * 128, row = (long long)e * p.out_rows + r;
+                sum += exact_dot<kFp4>(p.x_raw + ((long long)li * BN + t) * k, p.w_raw + (kFp4 ? row * k / 2 : row * k),
+                                       p.sft + (long long)li * words * BN + t, BN,
+                                       p.sfw + e * p.sfw_gstride + (kFp4 ? r : r >> 7), p.sfw_ld, p.nk);
+            }
+        } else {
+            const long long k = (long long)p.nk * 128;
+            sum = exact_dot<kFp4>(p.x_raw + m * k, p.w_raw + r * k, p.sft + m, p.sft_ld, p.sfw + (r >> 7), p.sfw_ld, p.nk);
+            const int id = __ldg(p.ids + m);
+            if (id >= 0 && id < p.lora_count) {
+                int slot = 0;                     // its place among the tile's adapters
+                if (nlist > 0) slot = place_of(list, nlist, id);
+                else while (slot + 1 < p.max_slots && __ldcg(p.slot_ids + tt * p.max_slots + slot) != id) ++slot;
+                const long long part = (long long)BN * p.lora_rp;
+                const uint16_t* v = p.v_raw + ((long long)tt * p.max_slots + slot) * p.parts * part + (long long)t * p.lora_rp;
+                const uint16_t* lb = p.lb_raw + ((long long)id * p.out_rows + r) * p.lora_r;
+                for (int c = 0; c < p.lora_r; ++c)
+                    for (int o = 0; o < p.parts; ++o)
+                        sum += __bfloat162float(__ushort_as_bfloat16(__ldcg(v + o * part + c))) *
+                               __bfloat162float(__ushort_as_bfloat16(__ldg(lb + c)));
+            }
+        }
+        if (p.d_f32) static_cast<float*>(p.d)[at] = sum;
+        else static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16(sum);
+    }
+}
+
 template <int kMode, int BN, bool kFp4>
 __global__ void __launch_bounds__(StreamCfg<kMode, BN>::kThreads, 1)
-fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) {
+fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ StreamMaps maps) {
     using C = StreamCfg<kMode, BN>;
     static_assert(sizeof(StreamSetup<kMode>) <= 128, "set-up area");
     constexpr bool kMoe = kMode == kGateUp || kMode == kDown;
+    constexpr bool kClusters = kMode == kProj || (kMode == kDown && BN <= 32);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -516,7 +625,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
     auto drain_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + b); };
     auto turn_of = [&](int b) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 2 + b); };
     const uint32_t xfull_bar = bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + 2 * C::kJoinSlots);   // cluster: all parts ready
-    const int cl = kMode == kGateUp ? 1 : p.cluster;
+    const int cl = kClusters ? p.cluster : 1;
     // a group's pieces of partials on their way into the ring
     auto join_bar = [&](int g, int i) { return bar0 + 8u * (2 * C::kStages + 2 * C::kNumAcc + 4 + g * C::kJoinSlots + i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -940,7 +1049,10 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             p.spread[kSpreadShares] = pl.shares;
             p.spread[kSpreadNk] = pl.nk;
             p.spread[kSpreadPieces] = pl.pieces;
+            p.spread[kSpreadListed] = nlist;
         }
+        if (p.spread && share == 0 && grp == 0)
+            for (int i = te; i < nlist; i += 128) reinterpret_cast<uint16_t*>(p.spread + kSpreadWords)[i] = list[i];
         if (kMode == kDown && nlist == 0 && !p.spread && cl == 1) {
             // no token uses an expert of this shard: the sum is empty
             const long long n = (long long)p.tokens * p.out_rows;
@@ -968,7 +1080,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
         uint32_t acc_ph = 0;
         StreamWalk<kMode> walk(share_walk);
         StreamSeg sg;
-        if (kMode != kGateUp && cl > 1) {
+        if (kClusters && cl > 1) {
             // A tile's pieces are the CTAs of a cluster: each leaves its part in its own ring (idle: its
             // only tile's products are done), and each adds up every cl-th (column, 32 rows) of the
             // tile over the cluster, in piece order.
@@ -1012,6 +1124,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             const int w = grp * 4 + q;
             if (__all_sync(0xffffffffu, ok)) {
                 constexpr int kItems = BN >= 64 ? 4 : 1;               // at a time
+                float bad = 0.0f;                                      // NaN behind a value that is not finite
                 for (int i0 = rank + cl * w; i0 < cols_all * 8; i0 += cl * 8 * kItems) {
                     float v[kItems], x[kItems][8];
 #pragma unroll
@@ -1031,7 +1144,15 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                             const long long at = (long long)(token0 + t) * p.out_rows + r;
                             if (p.d_f32) static_cast<float*>(p.d)[at] = v[n];
                             else static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16(v[n]);
+                            bad = fmaf(v[n], 0.0f, bad);
                         }
+                    }
+                }
+                if (__builtin_expect(bad != 0.0f, 0) && cols_all > 1) {
+#pragma unroll 1
+                    for (int it = rank + cl * w; it < cols_all * 8; it += cl * 8) {
+                        const int r = tile * 256 + (it & 7) * 32 + lane;
+                        if (r < p.out_rows) mend_outputs<kMode, BN, kFp4>(p, list, nlist, share_walk.tt, it >> 3, 1, r);
                     }
                 }
             }
@@ -1150,6 +1271,7 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
             }
             int piece = 0;
             bool lost = false;
+            float bad = 0.0f, bad2 = 0.0f;               // NaN behind a value that is not finite
             for (int c0 = 0; c0 < cols; c0 += kChunk) {
                 const int t0 = grp * kHalf + c0;                       // first token column
                 float v0[kChunk], v1[kChunk];
@@ -1282,12 +1404,19 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
                                 const float x = b ? v1[i] : v0[i];
                                 if (p.d_f32) static_cast<float*>(p.d)[at + (long long)i * p.out_rows] = x;
                                 else static_cast<__nv_bfloat16*>(p.d)[at + (long long)i * p.out_rows] = __float2bfloat16(x);
+                                if (i & 1) bad = fmaf(x, 0.0f, bad);
+                                else bad2 = fmaf(x, 0.0f, bad2);
                             }
                         }
                     }
                 }
             }
             if (sg.whole && cols <= 0) release();
+            if (kMode != kGateUp && __builtin_expect(bad + bad2 != 0.0f, 0) && p.tokens > 1) {
+#pragma unroll 1
+                for (int r = sg.tile * 256 + row; r < min(p.out_rows, (sg.tile + 1) * 256); r += 128)
+                    mend_outputs<kMode, BN, kFp4>(p, list, nlist, sg.tt, grp * kHalf, cols, r);
+            }
             if (lost && lane == 0)     // pieces that may still be landing
                 for (int i = fetched - 1; i >= 0 && i >= fetched - C::kJoinSlots; i -= 4)
                     drain_bar(join_bar(grp, i % C::kJoinSlots), (i / C::kJoinSlots) & 1, 20000000ull);
@@ -1312,11 +1441,13 @@ fg_stream_kernel(const StreamParams p, const __grid_constant__ StreamMaps maps) 
 // while all SMs together read all tiles' parts in about 2.  One CTA per (tile, kSpreadCols columns),
 // thread = row of the tile; the parts are added in share order, eight in flight.
 constexpr int kSpreadCols = 4;
-template <int BN>
-__global__ void __launch_bounds__(256) stream_reduce_kernel(const int* spread, const float* part, int tokens, int out_rows,
-                                                            void* d, int d_f32) {
+template <int BN, bool kFp4>
+__global__ void __launch_bounds__(256) stream_reduce_kernel(const __grid_constant__ StreamParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
+    const int* spread = p.spread;
+    const float* part = p.part;
+    const int tokens = p.tokens, out_rows = p.out_rows;
     constexpr int kChunk = 16, kHalf = BN / 2;
     StreamPlan pl;
     pl.units = __ldcg(spread + kSpreadUnits);
@@ -1358,15 +1489,23 @@ __global__ void __launch_bounds__(256) stream_reduce_kernel(const int* spread, c
     const int r = tile * 256 + blk * 128 + row;
     if (r >= out_rows) return;
     const long long out = (long long)c0 * out_rows + r;
+    float bad = 0.0f;                             // NaN behind a value that is not finite
 #pragma unroll
     for (int i = 0; i < kSpreadCols; ++i) {
         if (i >= cols) break;
-        if (d_f32) static_cast<float*>(d)[out + (long long)i * out_rows] = v[i];
-        else static_cast<__nv_bfloat16*>(d)[out + (long long)i * out_rows] = __float2bfloat16(v[i]);
+        if (p.d_f32) static_cast<float*>(p.d)[out + (long long)i * out_rows] = v[i];
+        else static_cast<__nv_bfloat16*>(p.d)[out + (long long)i * out_rows] = __float2bfloat16(v[i]);
+        bad = fmaf(v[i], 0.0f, bad);
+    }
+    if (__builtin_expect(bad != 0.0f, 0)) {
+        const uint16_t* list = reinterpret_cast<const uint16_t*>(spread + kSpreadWords);
+        const int nlist = __ldcg(spread + kSpreadListed);
+        mend_outputs<kDown, BN, kFp4>(p, list, nlist, 0, c0, cols, r);
     }
 }
 
-inline cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
+template <bool kFp4>
+cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.row_tiles), static_cast<unsigned>((p.tokens + kSpreadCols - 1) / kSpreadCols));
     cfg.blockDim = dim3(256);
@@ -1378,10 +1517,8 @@ inline cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t str
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const int* spread = p.spread;
-    const float* part = p.part;
-    return bn == 64 ? cudaLaunchKernelEx(&cfg, stream_reduce_kernel<64>, spread, part, p.tokens, p.out_rows, p.d, p.d_f32)
-                    : cudaLaunchKernelEx(&cfg, stream_reduce_kernel<128>, spread, part, p.tokens, p.out_rows, p.d, p.d_f32);
+    return bn == 64 ? cudaLaunchKernelEx(&cfg, stream_reduce_kernel<64, kFp4>, p)
+                    : cudaLaunchKernelEx(&cfg, stream_reduce_kernel<128, kFp4>, p);
 }
 
 template <int kMode, int BN, bool kFp4>

@@ -460,3 +460,49 @@ def test_moe_more_tiles_than_sms(fg, t, sms, fp4):
         check(run_moe(fg, c), moe_ref(c))
     finally:
         fg.set_num_sms(0)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t,h,i,e,topk", [(6, 512, 256, 5, 2), (20, 384, 128, 6, 1), (40, 512, 256, 5, 2), (100, 640, 128, 6, 1),
+                                          (3, 1024, 128, 2, 1)])
+def test_moe_non_finite_weights_stay_with_their_tokens(fg, fp4, t, h, i, e, topk):
+    """A NaN code and NaN scales in one expert's weights reach the tokens that use it, and no others."""
+    c = D.moe_case(41 + t, t, h, i, e, topk, fp4=fp4)
+    ref = moe_ref(c)
+    bad = 1
+    if fp4:
+        c["sf13"][bad, 0, 3] |= 0xFF                          # K-block 0 of a gate row
+        c["sf2"][bad, 0, h - 1] |= 0xFF
+    else:
+        c["w2"][bad, h - 1, 5] = 0x7F
+        c["w2"][bad, 17, i - 1] = 0xFF
+        c["w13"][bad, 2 * i - 1, 0] = 0x7F
+    uses = (c["ids"] == bad).any(axis=1)
+    assert uses.any() and not uses.all()
+    for out in ("bf16", "f32"):
+        got = run_moe(fg, c, out)
+        assert np.isnan(got[uses]).any()
+        check(got[~uses], (ref[0][~uses], ref[1][~uses]), out)
+
+
+@pytest.mark.parametrize("m,n,k,l,r,sms", [(20, 272, 256, 4, 16, 0), (64, 528, 384, 12, 64, 0), (300, 272, 256, 4, 16, 0),
+                                           (400, 528, 256, 3, 16, 5), (200, 528, 384, 60, 128, 20)])
+def test_lora_non_finite_adapters_stay_with_their_tokens(fg, m, n, k, l, r, sms):
+    """Infinities and NaN in one adapter's A and B reach the tokens that use it, and no others."""
+    c = D.lora_case(51 + m, m, n, k, l, r)
+    refs = {out: lora_ref(c, out) for out in ("bf16", "f32")}
+    bad = 2
+    c["lb_bits"][bad, n - 1, 0] = 0x7F80
+    c["lb_bits"][bad, 3, r - 1] = 0x7FC0
+    c["la_bits"][bad, 1, k - 1] = 0xFF80
+    uses = c["ids"] == bad
+    assert uses.any() and not uses.all()
+    try:
+        fg.set_num_sms(sms)
+        for out, ref in refs.items():
+            got = run_lora(fg, c, out)
+            assert not np.isfinite(got[uses]).all()
+            check(got[~uses], (ref[0][~uses], ref[1][~uses]), out)
+    finally:
+        fg.set_num_sms(0)
+
