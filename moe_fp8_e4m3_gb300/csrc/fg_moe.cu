@@ -113,7 +113,7 @@ int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t
         p.sfw_ld = align4(p.sfw_rows);
         p.sfw_gstride = (long long)p.sfw_ld * (kFp4 ? I / 128 : (I + 511) / 512);
         p.sft = reinterpret_cast<const int32_t*>(p.sfh);
-        p.w_raw = w2; p.x_raw = p.hq;
+        p.w_raw = w2; p.x_raw = p.hq; p.w_fp4 = kFp4;
         p.ctr = reinterpret_cast<unsigned*>(ws) + fg::kMaxCounters;
         p.d = d; p.d_f32 = d_dtype == FG_F32;
         p.debug_stall = 0;
@@ -126,7 +126,7 @@ int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t
         if (p.cluster == 1 && bn >= 64 && p.row_tiles <= grid) p.spread = reinterpret_cast<int*>(ws) + 2 * fg::kMaxCounters;
         const dim3 ctas(p.cluster > 1 ? p.cluster * p.row_tiles : grid);
         if (fg::launch_stream<fg::kDown, kFp4>(bn, p, m, ctas, s) != cudaSuccess ||
-            (p.spread && fg::launch_reduce<kFp4>(bn, p, s) != cudaSuccess)) {
+            (p.spread && fg::launch_reduce(bn, p, s) != cudaSuccess)) {
             cudaGetLastError();
             return FG_ERR_CUDA;
         }

@@ -26,7 +26,7 @@
 //
 // Bound: HBM, whose time for the weights is the floor.  Measured on GB300, the whole MoE MLP, its
 // launches included: 128 tokens x 7168 x 2048, 32 experts, E4M3 253 us (5.6 TB/s, 0.82 of a copy's
-// 6.8), 16 x 4096 49.8 us (0.75), 37 x 4096 with FP4 weights 94 us (0.67; half the bytes in the
+// 6.8), 16 x 4096 49.8 us (0.75), 37 x 4096 with FP4 weights 93 us (0.68; half the bytes in the
 // same ring), 1 x 4096 34 us (0.65).  Within a launch the weights stream at 6.3 to 6.6 TB/s; what
 // is left are the ends: 3 us until the first loads are out and 2 us until they are back, 4 to 5 us
 // from the first launch's last product to the second's first, and the joins.
@@ -107,7 +107,7 @@ struct StreamParams {
     const uint8_t* x_raw;
     const uint16_t* lb_raw;
     const uint16_t* v_raw;
-    int lora_r;
+    int lora_r, w_fp4;
 };
 
 // D(tmem) (+)= A(smem) x B(smem)^T, BF16 inputs, FP32 accumulation in TMEM.
@@ -511,8 +511,10 @@ struct StreamSetup {
 // non-finite element of an adapter's B, makes a NaN of 0 * NaN for tokens that do not use it.  An
 // output that is not finite is therefore worked out again, from what its token uses alone: one
 // thread an output, the same products in FP32, in K order.  Slow, and only ever there; where all is
-// finite it costs an FMA an output, whose zero becomes a NaN behind an infinity or a NaN (37 x 4096
-// FP4 92.9 -> 93.9 us, 2048 x 4096 with adapters 60.1 -> 60.8, the others the same).
+// finite it costs an FMA an output, whose zero becomes a NaN behind an infinity or a NaN (at most 0.2
+// us a call: 1 x 4096 34.4 -> 34.6, 64 x 7168 with adapters 21.55 -> 21.75).  One function for both
+// weight types: with one each, the reduce kernel beside the FP4 one gets 48 registers instead of 61 and
+// keeps fewer loads in flight (37 x 4096 FP4 93.9 us instead of 92.9).
 __device__ __forceinline__ float ue8m0(uint32_t b) {
     return b == 255u ? __int_as_float(0x7fc00000) : __uint_as_float(b ? b << 23 : 0x00400000u);
 }
@@ -521,9 +523,8 @@ __device__ __forceinline__ uint32_t scale_byte(const int32_t* word, int i) {
 }
 // One row of nk K-groups: x and w point at its codes, xs at its scale words (xs_ld words apart), ws
 // at the weight row's (FP4: a word a K-group, ws_ld apart; E4M3: one for four).
-template <bool kFp4>
-__device__ __forceinline__ float exact_dot(const uint8_t* x, const uint8_t* w, const int32_t* xs, int xs_ld, const int32_t* ws,
-                                           int ws_ld, int nk) {
+__device__ __forceinline__ float exact_dot(bool fp4, const uint8_t* x, const uint8_t* w, const int32_t* xs, int xs_ld,
+                                           const int32_t* ws, int ws_ld, int nk) {
     float sum = 0.0f;
 #pragma unroll 1
     for (int g = 0; g < nk && sum == sum; ++g) {                        // (a NaN stays one)
@@ -535,17 +536,17 @@ __device__ __forceinline__ float exact_dot(const uint8_t* x, const uint8_t* w, c
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
                 const uint32_t xc = __ldcg(x4 + i);
-                const uint32_t wc = kFp4 ? __ldg(reinterpret_cast<const uint16_t*>(w + g * 64 + b * 16) + i)
+                const uint32_t wc = fp4 ? __ldg(reinterpret_cast<const uint16_t*>(w + g * 64 + b * 16) + i)
                                          : __ldg(reinterpret_cast<const uint32_t*>(w + g * 128 + b * 32) + i);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const __half_raw wv = kFp4 ? __nv_cvt_fp4_to_halfraw(static_cast<__nv_fp4_storage_t>(wc >> (4 * c) & 15u), __NV_E2M1)
+                    const __half_raw wv = fp4 ? __nv_cvt_fp4_to_halfraw(static_cast<__nv_fp4_storage_t>(wc >> (4 * c) & 15u), __NV_E2M1)
                                                : __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(wc >> (8 * c)), __NV_E4M3);
                     const __half_raw xv = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(xc >> (8 * c)), __NV_E4M3);
                     part += __half2float(__half(xv)) * __half2float(__half(wv));
                 }
             }
-            const float sw = ue8m0(kFp4 ? scale_byte(ws + (long long)g * ws_ld, b) : scale_byte(ws + (long long)(g >> 2) * ws_ld, g & 3));
+            const float sw = ue8m0(fp4 ? scale_byte(ws + (long long)g * ws_ld, b) : scale_byte(ws + (long long)(g >> 2) * ws_ld, g & 3));
             sum += part * sx * sw;
         }
     }
@@ -561,8 +562,9 @@ __device__ __forceinline__ int place_of(const uint16_t* list, int n, int id) {
     return lo;
 }
 // Row r of D's tokens [t0, t0 + n) of token tile tt, where the stored value is not finite.
-template <int kMode, int BN, bool kFp4>
+template <int kMode, int BN>
 __device__ __noinline__ void mend_outputs(const StreamParams& p, const uint16_t* list, int nlist, int tt, int t0, int n, int r) {
+    const bool fp4 = kMode == kDown && p.w_fp4;
     for (int t = t0; t < t0 + n; ++t) {
         const int m = tt * BN + t;
         const long long at = (long long)m * p.out_rows + r;
@@ -578,13 +580,13 @@ __device__ __noinline__ void mend_outputs(const StreamParams& p, const uint16_t*
                 if (again) continue;
                 const int li = place_of(list, nlist, e), words = (p.nk + 3) / 4;
                 const long long k = (long long)p.nk * 128, row = (long long)e * p.out_rows + r;
-                sum += exact_dot<kFp4>(p.x_raw + ((long long)li * BN + t) * k, p.w_raw + (kFp4 ? row * k / 2 : row * k),
+                sum += exact_dot(fp4, p.x_raw + ((long long)li * BN + t) * k, p.w_raw + (fp4 ? row * k / 2 : row * k),
                                        p.sft + (long long)li * words * BN + t, BN,
-                                       p.sfw + e * p.sfw_gstride + (kFp4 ? r : r >> 7), p.sfw_ld, p.nk);
+                                       p.sfw + e * p.sfw_gstride + (fp4 ? r : r >> 7), p.sfw_ld, p.nk);
             }
         } else {
             const long long k = (long long)p.nk * 128;
-            sum = exact_dot<kFp4>(p.x_raw + m * k, p.w_raw + r * k, p.sft + m, p.sft_ld, p.sfw + (r >> 7), p.sfw_ld, p.nk);
+            sum = exact_dot(false, p.x_raw + m * k, p.w_raw + r * k, p.sft + m, p.sft_ld, p.sfw + (r >> 7), p.sfw_ld, p.nk);
             const int id = __ldg(p.ids + m);
             if (id >= 0 && id < p.lora_count) {
                 int slot = 0;                     // its place among the tile's adapters
@@ -1152,7 +1154,7 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
 #pragma unroll 1
                     for (int it = rank + cl * w; it < cols_all * 8; it += cl * 8) {
                         const int r = tile * 256 + (it & 7) * 32 + lane;
-                        if (r < p.out_rows) mend_outputs<kMode, BN, kFp4>(p, list, nlist, share_walk.tt, it >> 3, 1, r);
+                        if (r < p.out_rows) mend_outputs<kMode, BN>(p, list, nlist, share_walk.tt, it >> 3, 1, r);
                     }
                 }
             }
@@ -1415,7 +1417,7 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
             if (kMode != kGateUp && __builtin_expect(bad + bad2 != 0.0f, 0) && p.tokens > 1) {
 #pragma unroll 1
                 for (int r = sg.tile * 256 + row; r < min(p.out_rows, (sg.tile + 1) * 256); r += 128)
-                    mend_outputs<kMode, BN, kFp4>(p, list, nlist, sg.tt, grp * kHalf, cols, r);
+                    mend_outputs<kMode, BN>(p, list, nlist, sg.tt, grp * kHalf, cols, r);
             }
             if (lost && lane == 0)     // pieces that may still be landing
                 for (int i = fetched - 1; i >= 0 && i >= fetched - C::kJoinSlots; i -= 4)
@@ -1441,7 +1443,7 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
 // while all SMs together read all tiles' parts in about 2.  One CTA per (tile, kSpreadCols columns),
 // thread = row of the tile; the parts are added in share order, eight in flight.
 constexpr int kSpreadCols = 4;
-template <int BN, bool kFp4>
+template <int BN>
 __global__ void __launch_bounds__(256) stream_reduce_kernel(const __grid_constant__ StreamParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -1500,12 +1502,11 @@ __global__ void __launch_bounds__(256) stream_reduce_kernel(const __grid_constan
     if (__builtin_expect(bad != 0.0f, 0)) {
         const uint16_t* list = reinterpret_cast<const uint16_t*>(spread + kSpreadWords);
         const int nlist = __ldcg(spread + kSpreadListed);
-        mend_outputs<kDown, BN, kFp4>(p, list, nlist, 0, c0, cols, r);
+        mend_outputs<kDown, BN>(p, list, nlist, 0, c0, cols, r);
     }
 }
 
-template <bool kFp4>
-cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
+inline cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.row_tiles), static_cast<unsigned>((p.tokens + kSpreadCols - 1) / kSpreadCols));
     cfg.blockDim = dim3(256);
@@ -1517,8 +1518,8 @@ cudaError_t launch_reduce(int bn, const StreamParams& p, cudaStream_t stream) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return bn == 64 ? cudaLaunchKernelEx(&cfg, stream_reduce_kernel<64, kFp4>, p)
-                    : cudaLaunchKernelEx(&cfg, stream_reduce_kernel<128, kFp4>, p);
+    return bn == 64 ? cudaLaunchKernelEx(&cfg, stream_reduce_kernel<64>, p)
+                    : cudaLaunchKernelEx(&cfg, stream_reduce_kernel<128>, p);
 }
 
 template <int kMode, int BN, bool kFp4>
