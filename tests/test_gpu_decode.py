@@ -506,3 +506,26 @@ def test_lora_non_finite_adapters_stay_with_their_tokens(fg, m, n, k, l, r, sms)
     finally:
         fg.set_num_sms(0)
 
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t,sms", [(5, 3), (40, 3), (100, 4), (40, 2)])
+def test_moe_more_down_tiles_than_sms(fg, t, sms, fp4):
+    """The down projection's tiles do not fit the SMs: no clusters, no third launch."""
+    c = D.moe_case(61 + t, t, 1152, 128, 3, 2, fp4=fp4)
+    ref = moe_ref(c)
+    try:
+        fg.set_num_sms(sms)
+        for out in ("bf16", "f32"):
+            check(run_moe(fg, c, out), ref, out)
+    finally:
+        fg.set_num_sms(0)
+
+
+@pytest.mark.parametrize("m,sms", [(1, 3), (8, 5), (40, 3), (100, 2)])
+def test_lora_more_tiles_than_sms(fg, m, sms):
+    c = D.lora_case(71 + m, m, 1600, 256, 5, 16)
+    try:
+        fg.set_num_sms(sms)
+        check(run_lora(fg, c), lora_ref(c))
+    finally:
+        fg.set_num_sms(0)
