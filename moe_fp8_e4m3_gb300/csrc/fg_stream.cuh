@@ -260,7 +260,11 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 }
 
 __device__ __forceinline__ void deal_shares(StreamPlan& pl, int tiles, int grid) {
-    pl.shares = max(1, pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units));
+    if (pl.units == 0) {      // no token uses an expert of this shard: no share, so nothing is read or counted
+        pl.pieces = pl.shares = pl.q = pl.r = 0;
+        return;
+    }
+    pl.shares = pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units);
     const int n = pl.pieces < 0 ? tiles : pl.units;
     pl.q = n / pl.shares;
     pl.r = n - pl.q * pl.shares;
@@ -1456,14 +1460,14 @@ __global__ void __launch_bounds__(256) stream_reduce_kernel(const __grid_constan
     pl.shares = __ldcg(spread + kSpreadShares);
     pl.nk = __ldcg(spread + kSpreadNk);
     pl.pieces = __ldcg(spread + kSpreadPieces);
-    pl.q = pl.units / pl.shares;
-    pl.r = pl.units - pl.q * pl.shares;
     pl.fp8 = pl.nk;
     const int tile = blockIdx.x, c0 = blockIdx.y * kSpreadCols;
     const int row = threadIdx.x & 127, blk = threadIdx.x >> 7;
     const int cols = min(kSpreadCols, tokens - c0);
     float v[kSpreadCols] = {};
-    if (pl.units > 0) {
+    if (pl.units > 0) {                           // (none: no shares either, and D is zero)
+        pl.q = pl.units / pl.shares;
+        pl.r = pl.units - pl.q * pl.shares;
         int first, last;
         const int first_unit = tile * pl.nk;
         shares_of(pl, first_unit, pl.nk, first, last);
