@@ -439,12 +439,14 @@ def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weight
         _check_all(a, "a", "q", sfa, "sfa", "i", w13, "w13", letter, sf13, "sf13", "i", w2, "w2", letter, sf2, "sf2", "i",
                    topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f", d, "d", "o")
     t, h = a.shape
-    e, i2, _ = w13.shape
+    e, i2, k13 = w13.shape
     i = i2 // 2
     ids = topk_ids.shape
-    e2, h2, _ = w2.shape
-    if e2 != e or h2 != h or len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape:
-        raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I], topk_ids and topk_weights [T,topk]")
+    e2, h2, k2 = w2.shape
+    fp4 = letter == "p"                     # two codes a byte, a scale word per 128 K of each row
+    if (e2 != e or h2 != h or i2 != 2 * i or k13 != (h // 2 if fp4 else h) or k2 != (i // 2 if fp4 else i) or
+            len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape):
+        raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I] (FP4: H/2, I/2), topk_ids and topk_weights [T,topk]")
     if not workspace.is_cuda or workspace.nbytes < _moe_mlp_bytes(t, h, i, e):
         raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
     st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
