@@ -421,6 +421,10 @@ def _workspace(nbytes, device, where):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def _align4(x):
+    return (x + 3) // 4 * 4
+
+
 def moe_mlp_workspace(t, h, i, e, device="cuda"):
     """Zeroed workspace of fp8_moe_mlp / fp8_fp4_moe_mlp for t tokens; reusable, one per concurrent call."""
     return _workspace(lib.fg_moe_mlp_workspace(t, h, i, e), device, "moe_mlp_workspace")
@@ -447,6 +451,13 @@ def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weight
     if (e2 != e or h2 != h or i2 != 2 * i or k13 != (h // 2 if fp4 else h) or k2 != (i // 2 if fp4 else i) or
             len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape):
         raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I] (FP4: H/2, I/2), topk_ids and topk_weights [T,topk]")
+    if fp4:
+        words13, words2 = h // 128 * _align4(i2), i // 128 * _align4(h)
+    else:
+        words13, words2 = (h + 511) // 512 * _align4(i2 // 128), (i + 511) // 512 * _align4(h // 128)
+    if sfa.numel() < (h + 511) // 512 * _align4(t) or sf13.numel() < e * words13 or sf2.numel() < e * words2:
+        raise ValueError("scales: sfa [ceil(H/512), align4(T)]; sf13 [E, ceil(H/512), align4(2I/128)], sf2 [E, ceil(I/512), "
+                         "align4(H/128)] (FP4: [E, H/128, align4(2I)], [E, I/128, align4(H)])")
     if not workspace.is_cuda or workspace.nbytes < _moe_mlp_bytes(t, h, i, e):
         raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
     st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
@@ -501,6 +512,8 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
     if (kb != k or x.shape != a.shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
             ids.numel() != m or d.shape != (m, n)):
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
+    if sfa.numel() < (k + 511) // 512 * _align4(m) or sfb.numel() < (k + 511) // 512 * _align4((n + 127) // 128):
+        raise ValueError("scales: sfa [ceil(K/512), align4(M)], sfb [ceil(K/512), align4(ceil(N/128))]")
     if not workspace.is_cuda or workspace.nbytes < _lora_bytes(m, n, k, r):
         raise ValueError("workspace is smaller than lora_workspace(m, n, k, r)")
     st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
