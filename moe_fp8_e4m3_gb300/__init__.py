@@ -421,6 +421,11 @@ def _workspace(nbytes, device, where):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def _check_workspace(workspace, nbytes, what):
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < nbytes:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {what} bytes")
+
+
 def _align4(x):
     return (x + 3) // 4 * 4
 
@@ -458,8 +463,7 @@ def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weight
     if sfa.numel() < (h + 511) // 512 * _align4(t) or sf13.numel() < e * words13 or sf2.numel() < e * words2:
         raise ValueError("scales: sfa [ceil(H/512), align4(T)]; sf13 [E, ceil(H/512), align4(2I/128)], sf2 [E, ceil(I/512), "
                          "align4(H/128)] (FP4: [E, H/128, align4(2I)], [E, I/128, align4(H)])")
-    if not workspace.is_cuda or workspace.nbytes < _moe_mlp_bytes(t, h, i, e):
-        raise ValueError("workspace is smaller than moe_mlp_workspace(t, h, i, e)")
+    _check_workspace(workspace, _moe_mlp_bytes(t, h, i, e), "moe_mlp_workspace(t, h, i, e)")
     st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
             sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), d.data_ptr(),
             FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
@@ -514,8 +518,7 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
     if sfa.numel() < (k + 511) // 512 * _align4(m) or sfb.numel() < (k + 511) // 512 * _align4((n + 127) // 128):
         raise ValueError("scales: sfa [ceil(K/512), align4(M)], sfb [ceil(K/512), align4(ceil(N/128))]")
-    if not workspace.is_cuda or workspace.nbytes < _lora_bytes(m, n, k, r):
-        raise ValueError("workspace is smaller than lora_workspace(m, n, k, r)")
+    _check_workspace(workspace, _lora_bytes(m, n, k, r), "lora_workspace(m, n, k, r)")
     st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
                                  lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), ids.data_ptr(), d.data_ptr(),
                                  FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))

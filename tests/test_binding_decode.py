@@ -81,7 +81,7 @@ def test_moe_refuses_weights_of_the_other_kind(fg, fp4):
 
 
 @pytest.mark.parametrize("fp4", [False, True])
-@pytest.mark.parametrize("name", ["w13 K", "w2 K", "w13 rows", "sfa", "sf13", "sf2"])
+@pytest.mark.parametrize("name", ["w13 K", "w2 K", "w13 rows", "sfa", "sf13", "sf2", "workspace bytes", "workspace strided"])
 def test_moe_refuses_arrays_that_are_too_small(fg, fp4, name):
     args = moe_args(fg, fp4)
     half = 2 if fp4 else 1
@@ -92,6 +92,8 @@ def test_moe_refuses_arrays_that_are_too_small(fg, fp4, name):
         "sfa": lambda: {"sfa": i32(1, 8)},
         "sf13": lambda: {"sf13": i32(2, *args["sf13"].shape[1:])},
         "sf2": lambda: {"sf2": i32(3, 1, 4)},
+        "workspace bytes": lambda: {"workspace": Fake(args["workspace"].nbytes - 1)},
+        "workspace strided": lambda: {"workspace": Fake(args["workspace"].nbytes, contiguous=False)},
     }[name]())
     if name == "sf2" and not fp4:
         args["sf2"] = i32(3, 1, 7)
@@ -116,10 +118,10 @@ def test_lora_takes_the_documented_shapes(fg):
 
 
 @pytest.mark.parametrize("name,small", [
-    ("sfa", (1, 8)), ("sfb", (2, 3)), ("lora_b", (3, 272, 8)), ("lora_a", (3, 16, 512)), ("b", (272, 512))])
+    ("sfa", (1, 8)), ("sfb", (2, 3)), ("workspace", None), ("lora_b", (3, 272, 8)), ("lora_a", (3, 16, 512)), ("b", (272, 512))])
 def test_lora_refuses_arrays_that_are_too_small(fg, name, small):
     args = lora_args(fg)
-    args[name] = Fake(*small, dtype=args[name].dtype)
+    args[name] = (Fake(args[name].nbytes, contiguous=False) if small is None else Fake(*small, dtype=args[name].dtype))
     with pytest.raises(ValueError):
         fg.fp8_gemm_nt_lora(**args, stream=0)
     assert fg.calls == 0
