@@ -130,25 +130,30 @@ def moe_mlp(a, sfa, w13, sf13, w2, sf2, ids, weights, expert_base=0, fp4=False):
 # ------------------------------------------------------------------------- LoRA
 def lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, out="bf16"):
     """(D float64 [M, N], bound float64 [M, N] before D's rounding): see ``fg_fp8_gemm_nt_lora``; x, lora_a, lora_b
-    hold BF16 values."""
+    hold BF16 values.
+
+    Steps that add exact zeros (another token's adapter, padded ranks) leave an accumulator as it is, so
+    a row counts its own only: K / 32 of FP8 products, whose partial sums stay below ``mag``, then
+    one for each BF16 part and 16 ranks of its own adapter, and a join for every K-group and every
+    adapter step that a cut may separate."""
     m, k = a.shape
     n = b.shape[0]
     wa, wb = dequant_k_major(a, row_scales(sfa, m, k)), dequant_k_major(b, block_scales(sfb, n, k))
     d = wa @ wb.T
     mag = np.abs(wa) @ np.abs(wb).T
-    err = np.zeros_like(d)
+    err = (k // 32) * U * mag
     r = lora_a.shape[1]
     for i in range(m):
         j = int(ids[i])
-        if j < 0 or j >= lora_a.shape[0]:
-            continue
-        s = float(scaling[j])
-        v = s * (lora_a[j] @ x[i])
-        dv = (k // 16 + 8) * U * abs(s) * (np.abs(lora_a[j]) @ np.abs(x[i]))
-        dv += (2.0 ** -16 if out == "bf16" else 2.0 ** -23) * (np.abs(v) + dv)       # the BF16 parts
-        d[i] += lora_b[j] @ v
-        err[i] += np.abs(lora_b[j]) @ dv
-        mag[i] += np.abs(lora_b[j]) @ np.abs(v)
-    # every unit of another token's adapter is one more step of the accumulator
-    err += (k // 32 + 3 * min(m, 128) * ((r + 15) // 16) + 8) * U * mag
+        steps = 0
+        if 0 <= j < lora_a.shape[0]:
+            s = float(scaling[j])
+            v = s * (lora_a[j] @ x[i])
+            dv = (k // 16 + 8) * U * abs(s) * (np.abs(lora_a[j]) @ np.abs(x[i]))
+            dv += (2.0 ** -16 if out == "bf16" else 2.0 ** -23) * (np.abs(v) + dv)       # the BF16 parts
+            d[i] += lora_b[j] @ v
+            err[i] += np.abs(lora_b[j]) @ dv
+            mag[i] += np.abs(lora_b[j]) @ np.abs(v)
+            steps = (2 if out == "bf16" else 3) * ((r + 15) // 16)
+        err[i] += (k // 128 + 2 * steps) * U * mag[i]
     return d, err

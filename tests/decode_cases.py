@@ -49,3 +49,30 @@ def lora_case(seed, m, n, k, l, r, none=0.2):
     ids = np.where(g.random(m) < none, -1, g.integers(0, l, m)).astype(np.int32)
     return {"a": a, "sfa": F.pack_ue8m0(sa), "b": b, "sfb": F.pack_ue8m0(sb), "x_bits": xb, "x": x, "la_bits": la_bits,
             "la": la, "lb_bits": lb_bits, "lb": lb, "scaling": (g.random(l) * 2 - 0.5).astype(np.float32), "ids": ids}
+
+
+def lora_args(c):
+    return [c[k] for k in ("a", "sfa", "b", "sfb", "x", "la", "lb", "scaling", "ids")]
+
+
+def parts_case(seed, m, n, k, l, r):
+    """A case whose result is x @ lora_a^T alone, value by value: FP8 rows of zeros, one element in each
+    row of x, and rows of lora_b that pick one rank (even rows) or the difference of two ranks whose
+    values are neighbours in BF16 (odd rows).  Every token has an adapter."""
+    c = lora_case(seed, m, n, k, l, r, none=0.0)
+    g = rng(seed + 1)
+    c["a"] = np.zeros_like(c["a"])
+    x = np.zeros((m, k))
+    x[np.arange(m), g.integers(0, k, m)] = g.standard_normal(m)
+    lb = np.zeros((l, n, r))
+    for j in range(l):
+        lb[j, np.arange(n), g.integers(0, r, n)] = g.choice([-1.0, 0.5, 1.0], n)
+        lb[j, 1::2] = 0.0
+        pair = 2 * g.integers(0, r // 2, n // 2)
+        lb[j, np.arange(1, n, 2), pair] = 1.0
+        lb[j, np.arange(1, n, 2), pair + 1] = -1.0
+    c["la_bits"][:, 1::2] = c["la_bits"][:, 0::2] + 1
+    c["la"] = F.bf16_to_f64(c["la_bits"])
+    c["x_bits"], c["x"] = bf16(x)
+    c["lb_bits"], c["lb"] = bf16(lb)
+    return c
