@@ -12,6 +12,7 @@
 // 1.3 us).
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "fg.h"
@@ -169,6 +170,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p)
         // the key is the logit; the first chosen one is the largest
         const float l = value_of(my_key), top = value_of(__shfl_sync(kAll, my_key, 0));
         if (my_id >= 0) my_w = p.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
+    }
+    // Chosen scores below FP32's normal range (a sigmoid of -88, a softmax that the bias chose far below the
+    // row's largest) have lost bits or are 0, their ratios have not: the scores again, over the largest
+    // chosen one's e^min(l, 0) or e^l.
+    if (p.renormalize && (kScores || p.sigmoid) && __any_sync(kAll, my_id >= 0 && my_w < FLT_MIN)) {
+        const float l = my_id >= 0 ? __ldcg(p.logits + (long long)t * p.E + my_id) : kNegInf;
+        const float top = value_of(__reduce_max_sync(kAll, ordered(l)));
+        if (my_id >= 0) my_w = p.sigmoid ? expf(fminf(l, 0.0f) - fminf(top, 0.0f)) / (1.0f + expf(-fabsf(l))) : expf(l - top);
     }
     if (p.renormalize) {
         float sum = my_w;
