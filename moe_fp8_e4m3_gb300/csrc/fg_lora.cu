@@ -99,12 +99,14 @@ __device__ __forceinline__ void mma_bf16_16x8x16(float (&c)[4], uint32_t a0, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// x as a sum of BF16 parts: each holds what the parts before it leave.
+// x as a sum of BF16 parts: each holds what the parts before it leave.  A finite x that would round
+// to infinity (above 3.396e38) is cut instead; the next part takes the rest.
 __device__ __forceinline__ void store_parts(uint16_t* dst, long long stride, int parts, float x) {
     for (int o = 0; o < parts; ++o) {
-        const __nv_bfloat16 h = __float2bfloat16(x);
-        dst[o * stride] = __bfloat16_as_ushort(h);
-        x -= __bfloat162float(h);
+        uint32_t h = __bfloat16_as_ushort(__float2bfloat16(x));
+        if ((h & 0x7fffu) == 0x7f80u && x - x == 0.0f) --h;      // the largest BF16
+        dst[o * stride] = static_cast<uint16_t>(h);
+        x -= __uint_as_float(h << 16);
         if (!(x == x)) x = 0.0f;       // an infinite or NaN part leaves nothing
     }
 }

@@ -4,7 +4,7 @@ import pytest
 
 import decode_cases as D
 from oracle import decode as O
-from test_gpu_decode import ROUTE_RTOL, fg, run_route  # noqa: F401  (fg: the fixture)
+from test_gpu_decode import ROUTE_RTOL, check, fg, lora_ref, run_lora, run_route  # noqa: F401  (fg: the fixture)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -37,3 +37,22 @@ def test_route_weights_of_scores_below_fp32(fg, score, biased, groups, keep, lev
     assert np.array_equal(ids, rid)
     np.testing.assert_allclose(w, rw, rtol=FAR_RTOL, atol=2.0 ** -149)
     np.testing.assert_allclose(w.sum(axis=1), 1.0, rtol=1e-5)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [3, 20, 200])
+def test_adapter_products_between_bf16_and_fp32_range(fg, m, out):  # noqa: F811
+    """scaling * x @ lora_a^T above the largest BF16 value: its parts are finite, and so is the result."""
+    c = D.lora_case(81 + m, m, 32, 128, 2, 8, none=0.0)
+    x = np.zeros((m, 128))
+    x[:, 0] = 1.0
+    x[1::2, 0] = -1.0
+    c["x_bits"], c["x"] = D.bf16(x)
+    c["la_bits"], c["la"] = D.bf16(np.ones_like(c["la"]))
+    lb = np.zeros_like(c["lb"])
+    lb[:, :, 3] = 2.0 ** -20
+    c["lb_bits"], c["lb"] = D.bf16(lb)
+    c["scaling"][:] = [3.4e38, 3.397e38]
+    got = run_lora(fg, c, out)
+    assert np.isfinite(got).all()
+    check(got, lora_ref(c, out), out)
