@@ -80,9 +80,29 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
-# bytes a workspace needs, by sizes: a call through ctypes (0.6 us) once per size, not once per step
-_moe_mlp_bytes = functools.lru_cache(1024)(lib.fg_moe_mlp_workspace)
-_lora_bytes = functools.lru_cache(1024)(lib.fg_lora_workspace)
+
+
+def _align4(x):
+    return (x + 3) // 4 * 4
+
+
+# Bytes that a call's workspace and scale arrays need, by its sizes: worked out once per size, not once
+# per step (the ctypes call alone takes 0.6 us).
+@functools.lru_cache(1024)
+def _moe_mlp_bytes(t, h, i, e, fp4):
+    """(workspace, sfa, sf13, sf2)"""
+    if fp4:                                 # a word per 128 K of each row
+        sf13, sf2 = h // 128 * _align4(2 * i), i // 128 * _align4(h)
+    else:
+        sf13, sf2 = (h + 511) // 512 * _align4(2 * i // 128), (i + 511) // 512 * _align4(h // 128)
+    return lib.fg_moe_mlp_workspace(t, h, i, e), 4 * ((h + 511) // 512) * _align4(t), 4 * e * sf13, 4 * e * sf2
+
+
+@functools.lru_cache(1024)
+def _lora_bytes(m, n, k, r):
+    """(workspace, sfa, sfb)"""
+    words = (k + 511) // 512
+    return lib.fg_lora_workspace(m, n, k, r), 4 * words * _align4(m), 4 * words * _align4((n + 127) // 128)
 
 
 class FgError(RuntimeError):
@@ -421,15 +441,6 @@ def _workspace(nbytes, device, where):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-def _check_workspace(workspace, nbytes, what):
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < nbytes:
-        raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {what} bytes")
-
-
-def _align4(x):
-    return (x + 3) // 4 * 4
-
-
 def moe_mlp_workspace(t, h, i, e, device="cuda"):
     """Zeroed workspace of fp8_moe_mlp / fp8_fp4_moe_mlp for t tokens; reusable, one per concurrent call."""
     return _workspace(lib.fg_moe_mlp_workspace(t, h, i, e), device, "moe_mlp_workspace")
@@ -447,23 +458,22 @@ def _moe_mlp(fn, name, letter, a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weight
             d.is_contiguous()):
         _check_all(a, "a", "q", sfa, "sfa", "i", w13, "w13", letter, sf13, "sf13", "i", w2, "w2", letter, sf2, "sf2", "i",
                    topk_ids, "topk_ids", "i", topk_weights, "topk_weights", "f", d, "d", "o")
-    t, h = a.shape
+    shape = a.shape
+    t, h = shape
     e, i2, k13 = w13.shape
     i = i2 // 2
     ids = topk_ids.shape
     e2, h2, k2 = w2.shape
-    fp4 = letter == "p"                     # two codes a byte, a scale word per 128 K of each row
+    fp4 = letter == "p"                     # two codes a byte
     if (e2 != e or h2 != h or i2 != 2 * i or k13 != (h // 2 if fp4 else h) or k2 != (i // 2 if fp4 else i) or
-            len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != a.shape):
+            len(ids) != 2 or ids[0] != t or topk_weights.shape != ids or d.shape != shape):
         raise ValueError("shapes: a and d [T,H], w13 [E,2I,H], w2 [E,H,I] (FP4: H/2, I/2), topk_ids and topk_weights [T,topk]")
-    if fp4:
-        words13, words2 = h // 128 * _align4(i2), i // 128 * _align4(h)
-    else:
-        words13, words2 = (h + 511) // 512 * _align4(i2 // 128), (i + 511) // 512 * _align4(h // 128)
-    if sfa.numel() < (h + 511) // 512 * _align4(t) or sf13.numel() < e * words13 or sf2.numel() < e * words2:
+    need, need_a, need13, need2 = _moe_mlp_bytes(t, h, i, e, fp4)
+    if sfa.nbytes < need_a or sf13.nbytes < need13 or sf2.nbytes < need2:
         raise ValueError("scales: sfa [ceil(H/512), align4(T)]; sf13 [E, ceil(H/512), align4(2I/128)], sf2 [E, ceil(I/512), "
                          "align4(H/128)] (FP4: [E, H/128, align4(2I)], [E, I/128, align4(H)])")
-    _check_workspace(workspace, _moe_mlp_bytes(t, h, i, e), "moe_mlp_workspace(t, h, i, e)")
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < need:
+        raise ValueError("workspace must be a contiguous CUDA tensor of at least moe_mlp_workspace(t, h, i, e) bytes")
     st = fn(t, h, i, e, ids[1], expert_base, a.data_ptr(), sfa.data_ptr(), w13.data_ptr(), sf13.data_ptr(), w2.data_ptr(),
             sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), d.data_ptr(),
             FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
@@ -509,16 +519,19 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
             ids.is_contiguous() and d.is_contiguous()):
         _check_all(a, "a", "q", sfa, "sfa", "i", b, "b", "q", sfb, "sfb", "i", x, "x", "b", lora_a, "lora_a", "b",
                    lora_b, "lora_b", "b", scaling, "scaling", "f", ids, "ids", "i", d, "d", "o")
-    m, k = a.shape
+    shape = a.shape
+    m, k = shape
     n, kb = b.shape
     l, r, ka = lora_a.shape
     lb, nb, rb = lora_b.shape
-    if (kb != k or x.shape != a.shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
+    if (kb != k or x.shape != shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
             ids.numel() != m or d.shape != (m, n)):
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
-    if sfa.numel() < (k + 511) // 512 * _align4(m) or sfb.numel() < (k + 511) // 512 * _align4((n + 127) // 128):
+    need, need_a, need_b = _lora_bytes(m, n, k, r)
+    if sfa.nbytes < need_a or sfb.nbytes < need_b:
         raise ValueError("scales: sfa [ceil(K/512), align4(M)], sfb [ceil(K/512), align4(ceil(N/128))]")
-    _check_workspace(workspace, _lora_bytes(m, n, k, r), "lora_workspace(m, n, k, r)")
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < need:
+        raise ValueError("workspace must be a contiguous CUDA tensor of at least lora_workspace(m, n, k, r) bytes")
     st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
                                  lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), ids.data_ptr(), d.data_ptr(),
                                  FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
