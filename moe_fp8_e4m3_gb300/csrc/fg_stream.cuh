@@ -260,10 +260,6 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 }
 
 __device__ __forceinline__ void deal_shares(StreamPlan& pl, int tiles, int grid) {
-    if (pl.units == 0) {      // no token uses an expert of this shard: no share, so nothing is read or counted
-        pl.pieces = pl.shares = pl.q = pl.r = 0;
-        return;
-    }
     pl.shares = pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units);
     const int n = pl.pieces < 0 ? tiles : pl.units;
     pl.q = n / pl.shares;
@@ -733,6 +729,8 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
             pl.q = pl.r = 0;
         } else if (kMode == kProj && !own_tile) {
             plan_prompt(pl, p.token_tiles * p.row_tiles, static_cast<int>(gridDim.x), most / p.row_tiles);
+        } else if (kMoe && nlist == 0) {
+            pl.pieces = pl.shares = pl.q = pl.r = 0;       // no expert of this shard: nothing is read or counted
         } else {
             const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
             plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
