@@ -404,10 +404,13 @@ int fg_fp8_fp4_moe_mlp(int T, int H, int I, int E, int topk, int expert_base, co
  * that are not finite are worked out anew, as above).
  *   x [M][K] BF16;  lora_a [L][R][K], lora_b [L][N][R] BF16 (smaller ranks zero-padded to R);
  *   scaling [L] FP32;  ids [M] int32;  d [M][N] BF16 or FP32
- *   workspace: fg_lora_workspace bytes, under the same rules as fg_moe_mlp_workspace
+ *   workspace: fg_lora_workspace_for bytes, under the same rules as fg_moe_mlp_workspace;
+ *   fg_lora_workspace bytes serve any number of adapters and both types of D (M = 8192, R = 64: 448 MB,
+ *   of which 8 adapters and a BF16 D need 80)
  * M >= 0, N % 16 == 0, K % 128 == 0, R % 8 == 0, 8 <= R <= 128, M <= 65536.  Supported: L <= 1024.
  */
-long long fg_lora_workspace(int M, int N, int K, int R);
+long long fg_lora_workspace(int M, int N, int K, int R);   /* bytes, or -1 */
+long long fg_lora_workspace_for(int M, int N, int K, int L, int R, int d_dtype);
 int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, const int32_t* sfa, const uint8_t* b,
                         const int32_t* sfb, const void* x, const void* lora_a, const void* lora_b,
                         const float* scaling, const int32_t* ids, void* d, int d_dtype, void* workspace,

@@ -54,6 +54,7 @@ _SIGNATURES = {
     "fg_fp8_moe_mlp": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
     "fg_fp8_fp4_moe_mlp": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
     "fg_lora_workspace": (ctypes.c_longlong, [_I, _I, _I, _I]),
+    "fg_lora_workspace_for": (ctypes.c_longlong, [_I, _I, _I, _I, _I, _I]),
     "fg_fp8_gemm_nt_lora": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_get_tma_aligned_size": (_I, [_I, _I]),
@@ -99,10 +100,10 @@ def _moe_mlp_bytes(t, h, i, e, fp4):
 
 
 @functools.lru_cache(1024)
-def _lora_bytes(m, n, k, r):
+def _lora_bytes(m, n, k, l, r, dtype):
     """(workspace, sfa, sfb)"""
     words = (k + 511) // 512
-    return lib.fg_lora_workspace(m, n, k, r), 4 * words * _align4(m), 4 * words * _align4((n + 127) // 128)
+    return lib.fg_lora_workspace_for(m, n, k, l, r, dtype), 4 * words * _align4(m), 4 * words * _align4((n + 127) // 128)
 
 
 class FgError(RuntimeError):
@@ -498,9 +499,16 @@ def fp8_fp4_moe_mlp(a, sfa, w13, sf13, w2, sf2, topk_ids, topk_weights, d, works
              workspace, expert_base, stream)
 
 
-def lora_workspace(m, n, k, r, device="cuda"):
-    """Zeroed workspace of fp8_gemm_nt_lora; reusable, one per concurrent call."""
-    return _workspace(lib.fg_lora_workspace(m, n, k, r), device, "lora_workspace")
+def lora_workspace(m, n, k, r, device="cuda", adapters=None, dtype=None):
+    """Zeroed workspace of fp8_gemm_nt_lora; reusable, one per concurrent call.  With the number of
+    adapters and D's dtype it holds no more than calls with at most so many and that dtype need."""
+    import torch
+    if adapters is None and dtype is None:
+        nbytes = lib.fg_lora_workspace(m, n, k, r)
+    else:
+        nbytes = lib.fg_lora_workspace_for(m, n, k, 1024 if adapters is None else adapters, r,
+                                           FG_BF16 if dtype == torch.bfloat16 else FG_F32)
+    return _workspace(nbytes, device, "lora_workspace")
 
 
 def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspace, stream=None) -> None:
@@ -527,14 +535,16 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
     if (kb != k or x.shape != shape or ka != k or lb != l or nb != n or rb != r or scaling.numel() != l or
             ids.numel() != m or d.shape != (m, n)):
         raise ValueError("shapes: a and x [M,K], b [N,K], lora_a [L,R,K], lora_b [L,N,R], scaling [L], ids [M], d [M,N]")
-    need, need_a, need_b = _lora_bytes(m, n, k, r)
+    code = FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16
+    need, need_a, need_b = _lora_bytes(m, n, k, l, r, code)
     if sfa.nbytes < need_a or sfb.nbytes < need_b:
         raise ValueError("scales: sfa [ceil(K/512), align4(M)], sfb [ceil(K/512), align4(ceil(N/128))]")
     if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < need:
-        raise ValueError("workspace must be a contiguous CUDA tensor of at least lora_workspace(m, n, k, r) bytes")
+        raise ValueError("workspace must be a contiguous CUDA tensor of at least lora_workspace(m, n, k, r, adapters=L, "
+                         "dtype=d.dtype) bytes")
     st = lib.fg_fp8_gemm_nt_lora(m, n, k, l, r, a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), x.data_ptr(),
                                  lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), ids.data_ptr(), d.data_ptr(),
-                                 FG_F32 if d.dtype in _DTYPES["f"] else FG_BF16, workspace.data_ptr(), _stream(stream))
+                                 code, workspace.data_ptr(), _stream(stream))
     if st != FG_OK:
         _check(st, "fp8_gemm_nt_lora")
 

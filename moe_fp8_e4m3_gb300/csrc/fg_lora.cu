@@ -27,24 +27,28 @@ int padded_rank(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 1
 
 struct Layout {
     int bn, rp, tiles;                    // token columns, padded rank, token tiles
+    int slots, parts;                     // adapters that a tile may use; BF16 parts of x @ A^T
     long long ids, count, v, part, bytes; // behind the counters (fg_stream.cuh)
 };
-Layout layout(int M, int R) {
+// Parts of x @ lora_a^T: 16 mantissa bits under a BF16 result, 24 under an FP32 one.
+Layout layout(int M, int R, int L, int d_dtype) {
     Layout l;
     l.bn = fg::stream_bn(M);
     l.rp = padded_rank(R);
     l.tiles = ceil_div(M, l.bn);
+    l.slots = L < l.bn ? L : l.bn;
+    l.parts = d_dtype == FG_F32 ? 3 : 2;
     l.ids = fg::kCounterBytes;
     l.count = l.ids + up256((long long)l.tiles * l.bn * 4);
     l.v = l.count + up256((long long)l.tiles * 4);
-    l.part = l.v + up256((long long)l.tiles * l.bn * 3 * l.bn * l.rp * 2);
+    l.part = l.v + up256((long long)l.tiles * l.slots * l.parts * l.bn * l.rp * 2);
     l.bytes = l.part + (long long)fg::kMaxStreamCtas * 2 * 2 * l.bn * 128 * 4;
     return l;
 }
 
 bool shapes_ok(int M, int N, int K, int R) {
     if (M < 0 || N < 16 || N % 16 != 0 || K < 128 || K % 128 != 0 || R < 8 || R % 8 != 0 || R > 128) return false;
-    const Layout l = layout(M > 0 ? M : 1, R);
+    const Layout l = layout(M > 0 ? M : 1, R, fg::kMaxListed, FG_F32);
     return l.tiles <= fg::kMaxTokenTiles &&
            (long long)l.tiles * ceil_div(N, 256) * (K / 128 + 8 * l.bn) < (1LL << 31) &&
            (long long)l.tiles * l.bn * 3 * l.bn < (1LL << 31);
@@ -489,8 +493,12 @@ cudaError_t launch_shrink(const ShrinkParams& p, const ShrinkMaps& maps, int til
 extern "C" {
 
 long long fg_lora_workspace(int M, int N, int K, int R) {
-    if (!shapes_ok(M, N, K, R)) return -1;
-    return layout(M > 0 ? M : 1, R).bytes;
+    return fg_lora_workspace_for(M, N, K, fg::kMaxListed, R, FG_F32);
+}
+
+long long fg_lora_workspace_for(int M, int N, int K, int L, int R, int d_dtype) {
+    if (!shapes_ok(M, N, K, R) || L < 1 || L > fg::kMaxListed || (d_dtype != FG_BF16 && d_dtype != FG_F32)) return -1;
+    return layout(M > 0 ? M : 1, R, L, d_dtype).bytes;
 }
 
 int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, const int32_t* sfa, const uint8_t* b,
@@ -506,18 +514,17 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         return FG_ERR_INVALID_ARG;
     fg::HostState st;
     if (const int rc = fg::host_state(&st)) return rc;
-    const Layout l = layout(M, R);
+    const Layout l = layout(M, R, L, d_dtype);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int grid = st.sms < fg::kMaxStreamCtas ? st.sms : fg::kMaxStreamCtas;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-    // parts of x @ lora_a^T: 16 mantissa bits under a BF16 result, 24 under an FP32 one; an adapter
-    // unit's parts x columns fit the stage's token area
-    const int parts = d_dtype == FG_F32 ? 3 : 2, unit_cols = d_dtype == FG_F32 ? 16 : 32;
+    // an adapter unit's parts x columns fit the stage's token area
+    const int parts = l.parts, unit_cols = parts == 3 ? 16 : 32;
     if (fg::print_configs_enabled())
         std::fprintf(stderr, "[fg] fp8_gemm_nt_lora M=%d N=%d K=%d L=%d R=%d BN=%d rank=%d grid=%d\n", M, N, K, L, R, l.bn,
                      l.rp, grid);
-    const ShrinkParams sp{M, l.bn, K, R, l.rp, L, l.bn, parts, ids, static_cast<const uint16_t*>(x),
+    const ShrinkParams sp{M, l.bn, K, R, l.rp, L, l.slots, parts, ids, static_cast<const uint16_t*>(x),
                           static_cast<const uint16_t*>(lora_a), scaling, reinterpret_cast<uint16_t*>(ws + l.v),
                           reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<int*>(ws + l.count), st.status, st.timeout_ns};
     ShrinkMaps sm;
@@ -549,7 +556,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
     p.ids = ids;
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.lora_rp = l.rp; p.lora_count = L;
-    p.max_slots = l.bn; p.token_tiles = l.tiles;
+    p.max_slots = l.slots; p.token_tiles = l.tiles;
     p.parts = parts; p.unit_cols = unit_cols;
     p.slot_ids = sp.slot_ids;
     p.slot_count = sp.slot_count;
@@ -566,7 +573,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
                                                  : (cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
         const uint64_t ld[3] = {(uint64_t)R, (uint64_t)N, (uint64_t)L}, lp[2] = {(uint64_t)R * 2, (uint64_t)R * 2 * N};
         const uint32_t lb[3] = {cols, 256, 1};
-        const uint64_t vd[2] = {(uint64_t)l.rp, (uint64_t)l.tiles * l.bn * p.parts * l.bn}, vp[1] = {(uint64_t)l.rp * 2};
+        const uint64_t vd[2] = {(uint64_t)l.rp, (uint64_t)l.tiles * l.slots * parts * l.bn}, vp[1] = {(uint64_t)l.rp * 2};
         const int v_rows = (unit_cols / l.rp > 1 ? unit_cols / l.rp : 1) * parts * l.bn;   // of a unit
         const uint32_t vb[2] = {cols, (uint32_t)(v_rows <= 256 ? v_rows : v_rows / 2)};
         if (!fg::encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, b, wd, wp, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
