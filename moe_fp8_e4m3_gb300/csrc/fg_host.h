@@ -25,4 +25,9 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
 
 bool print_configs_enabled();
 
+// p is a multiple of n, a power of two.
+inline bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int align4(int x) { return (x + 3) / 4 * 4; }
+inline long long up256(long long x) { return (x + 255) / 256 * 256; }
+
 }  // namespace fg

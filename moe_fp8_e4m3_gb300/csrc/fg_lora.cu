@@ -17,10 +17,10 @@
 
 namespace {
 
-bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-int align4(int x) { return (x + 3) / 4 * 4; }
+using fg::al;
+using fg::align4;
+using fg::up256;
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
-long long up256(long long x) { return (x + 255) / 256 * 256; }
 
 // Rank columns as the tensor core takes them: 16 per step, whole or half adapters per unit.
 int padded_rank(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
@@ -569,8 +569,7 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
         const uint64_t xd[2] = {(uint64_t)K, (uint64_t)M}, xp[1] = {(uint64_t)K};
         const uint32_t xb[2] = {128, (uint32_t)l.bn};
         const uint32_t cols = l.rp < p.unit_cols ? l.rp : p.unit_cols;
-        const CUtensorMapSwizzle sw = cols == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                                 : (cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+        const CUtensorMapSwizzle sw = cols == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
         const uint64_t ld[3] = {(uint64_t)R, (uint64_t)N, (uint64_t)L}, lp[2] = {(uint64_t)R * 2, (uint64_t)R * 2 * N};
         const uint32_t lb[3] = {cols, 256, 1};
         const uint64_t vd[2] = {(uint64_t)l.rp, (uint64_t)l.tiles * l.slots * parts * l.bn}, vp[1] = {(uint64_t)l.rp * 2};

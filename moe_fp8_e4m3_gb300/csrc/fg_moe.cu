@@ -14,9 +14,9 @@ namespace {
 
 constexpr int kMaxTokens = 128, kMaxTopk = 32;
 
-bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-int align4(int x) { return (x + 3) / 4 * 4; }
-long long up256(long long x) { return (x + 255) / 256 * 256; }
+using fg::al;
+using fg::align4;
+using fg::up256;
 
 // Workspace: the counters (zero between calls; at the same place for every size, so that a
 // workspace can serve calls of several), then what the first launch leaves for the second (codes

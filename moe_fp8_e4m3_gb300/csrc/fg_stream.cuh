@@ -887,7 +887,7 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
             const uint64_t w0 = make_sdesc(sbase + C::kOffSf + 512 * blk, 0, 128, kLayoutNone);
             const uint64_t t0w = make_sdesc(sbase + C::kOffSf + 1024, 0, 128, kLayoutNone);
             // adapter units: an adapter's rows are rb bytes long, swizzled over as many
-            const uint32_t layout = rb == 128 ? 2u : (rb == 64 ? 4u : 6u);
+            const uint32_t layout = rb == 64 ? 4u : 6u;
             const uint64_t la0 = make_sdesc(sbase + blk * 128 * rb, 0, 8 * rb, layout);
             const uint64_t lb0 = make_sdesc(sbase + C::kOffB, 0, 8 * rb, layout);
             int s = 0, acc = 0;
@@ -933,7 +933,7 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
                                 for (int o = 0; o < 3; ++o) {
                                     if (o >= p.parts) break;
 #pragma unroll
-                                    for (int c = 0; c < 4; ++c) {
+                                    for (int c = 0; c < 2; ++c) {
                                         if (c >= rb / 32) break;
                                         tc_mma_bf16(dt, aj + 2 * c, bj + 2 * c, kIdescBf16, keep);
                                         keep = 1;
