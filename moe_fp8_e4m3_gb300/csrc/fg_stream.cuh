@@ -260,7 +260,7 @@ __device__ __forceinline__ void shares_of(const StreamPlan& pl, int u0, int nk, 
 }
 
 __device__ __forceinline__ void deal_shares(StreamPlan& pl, int tiles, int grid) {
-    pl.shares = pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units);
+    pl.shares = max(1, pl.pieces > 0 ? pl.pieces * tiles : min(grid, pl.pieces < 0 ? tiles : pl.units));
     const int n = pl.pieces < 0 ? tiles : pl.units;
     pl.q = n / pl.shares;
     pl.r = n - pl.q * pl.shares;
@@ -729,12 +729,12 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
             pl.q = pl.r = 0;
         } else if (kMode == kProj && !own_tile) {
             plan_prompt(pl, p.token_tiles * p.row_tiles, static_cast<int>(gridDim.x), most / p.row_tiles);
-        } else if (kMoe && nlist == 0) {
-            pl.pieces = pl.shares = pl.q = pl.r = 0;       // no expert of this shard: nothing is read or counted
         } else {
             const int tiles = kMode == kGateUp ? nlist * p.row_tiles : p.row_tiles;
             plan_shares(pl, tiles, static_cast<int>(gridDim.x), kFp4, C::kChunks, kMode == kDown ? C::kStages : 0,
                         p.spread != nullptr);
+            // no token uses an expert of this shard: no tile, so no share that would read or count one
+            if (kMode == kGateUp && nlist == 0) pl.shares = 0;
         }
         __syncwarp();
         if (lane == 0) {
@@ -1458,14 +1458,14 @@ __global__ void __launch_bounds__(256) stream_reduce_kernel(const __grid_constan
     pl.shares = __ldcg(spread + kSpreadShares);
     pl.nk = __ldcg(spread + kSpreadNk);
     pl.pieces = __ldcg(spread + kSpreadPieces);
+    pl.q = pl.units / pl.shares;
+    pl.r = pl.units - pl.q * pl.shares;
     pl.fp8 = pl.nk;
     const int tile = blockIdx.x, c0 = blockIdx.y * kSpreadCols;
     const int row = threadIdx.x & 127, blk = threadIdx.x >> 7;
     const int cols = min(kSpreadCols, tokens - c0);
     float v[kSpreadCols] = {};
-    if (pl.units > 0) {                           // (none: no shares either, and D is zero)
-        pl.q = pl.units / pl.shares;
-        pl.r = pl.units - pl.q * pl.shares;
+    if (pl.units > 0) {
         int first, last;
         const int first_unit = tile * pl.nk;
         shares_of(pl, first_unit, pl.nk, first, last);
