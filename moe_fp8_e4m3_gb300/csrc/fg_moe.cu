@@ -3,6 +3,7 @@
 // third one adds up its parts).  Two, because every down product needs the scale of 128 gate-up
 // outputs and the sum of all experts: between them lies a wait for the whole grid, which the second
 // launch's CTAs spend with their first weight tiles on the way.
+#include <climits>
 #include <cstdio>
 #include <cstring>
 
@@ -45,7 +46,7 @@ template <bool kFp4>
 int moe_mlp(int T, int H, int I, int E, int topk, int expert_base, const uint8_t* a, const int32_t* sfa,
             const uint8_t* w13, const int32_t* sf13, const uint8_t* w2, const int32_t* sf2, const int32_t* ids,
             const float* weights, void* d, int d_dtype, void* workspace, fg_stream_t stream) {
-    if (!shapes_ok(T, H, I, E) || topk < 1 || expert_base < 0 || (d_dtype != FG_BF16 && d_dtype != FG_F32))
+    if (!shapes_ok(T, H, I, E) || topk < 1 || expert_base < 0 || expert_base > INT_MAX - E || (d_dtype != FG_BF16 && d_dtype != FG_F32))
         return FG_ERR_INVALID_ARG;
     if (T > kMaxTokens || E > fg::kMaxListed || topk > kMaxTopk) return FG_ERR_UNSUPPORTED;
     if (T == 0) return FG_OK;

@@ -78,3 +78,11 @@ def test_no_device_fails_loudly(fg):
     assert route(fg) == fg.FG_ERR_CUDA
     assert moe(fg, False) == fg.FG_ERR_CUDA and moe(fg, True) == fg.FG_ERR_CUDA
     assert lora(fg) == fg.FG_ERR_CUDA
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_moe_experts_end_within_the_ids_type(fg, fp4):
+    """Past it, ids from -2^31 on would count as experts of the shard."""
+    for base in (2 ** 31 - 1, 2 ** 31 - 8):
+        assert moe(fg, fp4, e=8, base=base) == fg.FG_ERR_INVALID_ARG
+    assert moe(fg, fp4, t=0, e=8, base=2 ** 31 - 9) == fg.FG_OK
