@@ -350,6 +350,7 @@ typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_score;
  *     topk_group best groups can be chosen
  *   the topk experts with the largest keys, in falling order; ties go to the lowest index
  *   weight = s (without the bias), divided by the sum of the chosen ones if renormalize, * scale
+ *   (the ratios hold also where the chosen s are below FP32's range)
  * A logit of -inf or NaN (or a NaN bias) takes its expert out; a slot without an expert gets id
  * -1 and weight 0 (fg_*_moe_mlp skips it).
  *   logits [T][E] FP32;  bias [E] FP32 or NULL;  topk_ids [T][topk] int32;  topk_weights FP32
@@ -370,7 +371,7 @@ int fg_moe_route(int T, int E, int topk, int n_group, int topk_group, int score,
  * expert_base + E) belong to other shards (or are -1) and are skipped; a token without an
  * expert here gets zeros whatever its row holds.  Non-finite activations or weights of an expert
  * reach the rows of the tokens that use it, and no others (an output that is not finite is worked
- * out anew from its own token's experts, which takes milliseconds where there are many).
+ * out anew from its own token's experts, which takes tens of milliseconds where there are many).
  *   a    [T][H] E4M3, sfa as for fg_fp8_gemm_nt      w13 [E][2I][H], sf13 [E][ceil(H/512)][align4(2I/128)]
  *   w2   [E][H][I], sf2 [E][ceil(I/512)][align4(H/128)]
  *   topk_ids [T][topk] int32, topk_weights [T][topk] FP32;  d [T][H] BF16 or FP32
@@ -380,7 +381,7 @@ int fg_moe_route(int T, int E, int topk, int n_group, int topk_group, int score,
  * (every completed call leaves its counters zero again; zero it anew after a time-out).  One
  * that is large enough serves calls of any sizes, of both MoE MLPs and of the projection below,
  * one after another; calls that may run at the same time need one each.
- * H % 128 == 0, I % 128 == 0, T >= 0.  Supported: T <= 128, E <= 1024, topk <= 32; more tokens
+ * H % 128 == 0, I % 128 == 0, T >= 0, 0 <= expert_base <= INT32_MAX - E.  Supported: T <= 128, E <= 1024, topk <= 32; more tokens
  * take the grouped GEMMs.
  */
 long long fg_moe_mlp_workspace(int T, int H, int I, int E);   /* bytes, or -1 */

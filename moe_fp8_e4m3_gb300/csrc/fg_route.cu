@@ -6,10 +6,10 @@
 // tie, and the winning lane looks for its next best.  Scores of all experts are worked out only
 // where something needs them (a bias, or softmax weights that are not renormalised): else the
 // chosen logits, one per lane, are enough, since a common factor cancels.
-// Bound: latency for few tokens, instruction issue for many (a warp's topk rounds are one chain of
-// reductions, and its 4 E bytes are read once).  Measured on GB300: 1 token x 256 experts, 8 groups,
-// top 8 5.0 us, of which an empty launch takes 3; 8192 x 256, top 8 7.7 us (1.1 TB/s; the bytes alone
-// 1.3 us).
+// Bound: latency, for few tokens and for many: a warp's topk rounds are one chain of reductions behind
+// the load of its 4 E bytes.  Measured on GB300: 1 token x 256 experts, 8 groups, top 8 5.1 us, of which an
+// empty launch takes 3; 8192 x 256, top 6 7.8 us (1.1 TB/s; the bytes alone 1.3 us), where a scheduler
+// issues in 47 % of the cycles with 7 warps on it, a third of whose waits are for the logits.
 #include <cuda_runtime.h>
 
 #include <cfloat>

@@ -510,9 +510,11 @@ struct StreamSetup {
 // Every weight tile is multiplied with every token of its tile, so a NaN weight or scale, or a
 // non-finite element of an adapter's B, makes a NaN of 0 * NaN for tokens that do not use it.  An
 // output that is not finite is therefore worked out again, from what its token uses alone: one
-// thread an output, the same products in FP32, in K order.  Slow, and only ever there; where all is
-// finite it costs an FMA an output, whose zero becomes a NaN behind an infinity or a NaN (at most 0.2
-// us a call: 1 x 4096 34.4 -> 34.6, 64 x 7168 with adapters 21.55 -> 21.75).  One function for both
+// thread an output, the same products in FP32, in K order.  Slow, and only ever there (a NaN in every
+// row of one expert's w2: 16 x 4096 0.4 ms, 128 x 7168 26 ms; in all of one adapter's B: 64 x 7168 5 ms,
+// 2048 x 4096 86 ms, far inside the 4 s of a bounded wait).  Where all is finite it costs an FMA an
+// output, whose zero becomes a NaN behind an infinity or a NaN (1 x 4096 34.4 -> 34.6 us, 64 x 7168 with
+// adapters 21.55 -> 21.75, 2048 x 4096 with adapters 60.1 -> 60.8).  One function for both
 // weight types: with one each, the reduce kernel beside the FP4 one gets 48 registers instead of 61 and
 // keeps fewer loads in flight (37 x 4096 FP4 93.9 us instead of 92.9).
 __device__ __forceinline__ float ue8m0(uint32_t b) {
@@ -1348,7 +1350,11 @@ fg_stream_kernel(const __grid_constant__ StreamParams p, const __grid_constant__
                 if constexpr (kMode == kGateUp) {
                     // y = w * SiLU(gate) * up, then one scale for each token's 128 values (the rows of
                     // this block): maximum of |y| over the warp's lanes, then over the four warps.
-                    // Lane i of every warp works out column i's scale for the others.
+                    // Lane i of every warp works out column i's scale for the others.  The exponential and the
+                    // division are the fast ones: with expf and a rounded division 128 x 7168 takes 257.7
+                    // us instead of 253.8, 1 x 4096 37.2 instead of 35.5, and the same 26 of 1.6 million
+                    // codes fall to the other side of a rounding than in FP64 (the sums over K decide; 6
+                    // with an FP32 matrix product).
                     uint32_t* rd = red + red_at;
                     red_at ^= 64;
                     uint32_t m[kChunk];
