@@ -417,6 +417,102 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
                         const float* scaling, const int32_t* ids, void* d, int d_dtype, void* workspace,
                         fg_stream_t stream);
 
+/*
+ * The attention side of a serving step: block tables of a paged key/value cache, norms and position
+ * rotation of queries and keys, the cache itself in 4 bits, and attention over it.  The conventions
+ * above hold (caller-owned device arrays, asynchronous on `stream`, contract violations recorded).
+ *
+ * The cache.  Keys and values are two pairs of arrays, in pages of page_size tokens:
+ *   codes  [num_pages][heads][page_size][D / 2]   E2M1, two per byte (nibble 2i: bits 0-3 of byte i)
+ *   scales [num_pages][heads][page_size][D / 32]  UE8M0, one per 32 elements of a token's row
+ * A slot is page * page_size + offset.  Codes stand in the order that the attention reads them in.  With
+ * B = D / 32: element 32 b + 8 c + j of a key row is nibble (c B + b) 8 + j (b < B, c < 4, j < 8); element
+ * 32 b + 4 g + j of a value row is nibble (g B + b) 4 + j (b < B, g < 8, j < 4).  Scale and code of a block
+ * are those of fg_quantize_mxfp4, with the scale kept within [2^-64, 2^63] (bytes 63 to 190).
+ * Supported: D of 64, 128 and 256, page_size a multiple of 16.  page_size * num_pages and page_size *
+ * max_pages are below 2^31 - 4096.  All cache arrays are 16-byte aligned.
+ */
+
+/*
+ * Block tables, slots and positions of a step from the requests' lengths.  Request r holds
+ * context_lens[r] tokens in the cache and brings new_lens[r] more (0: it waits); new_lens[r] == -1: it is
+ * finished, gives its pages back and holds none afterwards.  In the order of the requests,
+ *   the pages of finished requests (ceil(context / page_size) entries of their block_table rows) go on top
+ *   of the free_count[0] free pages, then each request takes the pages that its tokens need from the top,
+ *   into its row behind those it holds;
+ *   query_start[r] = new tokens of the requests before r, query_start[S] = of all;
+ *   seq_lens[r] = context + new tokens (0 if finished); free_count_out[0] = pages left free;
+ *   slots[t], positions[t] = where token t goes, and its place in its request; -1 for t >= query_start[S].
+ *   context_lens, new_lens [S], block_table [S][max_pages], free_pages [free_len], query_start [S + 1],
+ *   seq_lens [S], slots, positions [T]: int32 on the device
+ * seq_lens may be context_lens, free_count_out may be free_count; other arrays do not overlap.  A call
+ * repeated on the same inputs gives the same results.  Lengths below 0 (-1 in new_lens) or past max_pages
+ * pages, more than T tokens or than the free pages, a free_count outside [0, free_len - pages given back]:
+ * 0x107 is recorded and the step is empty (query_start 0, slots and positions -1, lengths and free pages as
+ * they were).  A page id outside [0, num_pages): 0x107, and slot -1 for its tokens.
+ * Supported: S <= 4000, T <= 2^18, max_pages <= 2^18.
+ */
+int fg_build_block_tables(int S, int T, int page_size, int num_pages, int max_pages, int free_len,
+                          const int32_t* context_lens, const int32_t* new_lens, int32_t* free_pages,
+                          const int32_t* free_count, int32_t* block_table, int32_t* query_start,
+                          int32_t* seq_lens, int32_t* slots, int32_t* positions, int32_t* free_count_out,
+                          fg_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head, and the position rotation, in one pass.  Per token t and head,
+ *   y = x * w / sqrt(mean(x^2) + eps)     (w: q_weight or k_weight, BF16 [D]; NULL: y = x)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   over the pairs of the first `rot` elements: elements i and
+ *   i + rot / 2, or 2i and 2i + 1 (interleaved != 0); pair i takes cos_sin[positions[t]][i] and [rot / 2 + i]
+ * in FP32, rounded once to BF16.
+ *   q [T][Hq][D], k [T][Hkv][D] BF16 and their outputs: tokens q_stride, k_stride, ... elements apart (multiples
+ *   of 8, at least Hq * D or Hkv * D); an output may be its input
+ *   positions [T] int32; cos_sin [max_pos][rot] FP32
+ * A negative position leaves its token's outputs as they were; one >= max_pos does too, and 0x109 is
+ * recorded.  D % 8 == 0, rot % 16 == 0, 0 <= rot <= D, Hkv >= 0.  Supported: D <= 256.
+ */
+int fg_qk_norm_rope(int T, int Hq, int Hkv, int D, int rot, int max_pos, const void* q, long long q_stride,
+                    const void* k, long long k_stride, const void* q_weight, const void* k_weight, float eps,
+                    const int32_t* positions, const float* cos_sin, int interleaved, void* q_out,
+                    long long q_out_stride, void* k_out, long long k_out_stride, fg_stream_t stream);
+
+/*
+ * Keys and values of T tokens into the 4-bit cache, and back out of it as BF16 (exactly the values that the
+ * codes stand for).  k and v [T][heads][D] BF16, tokens k_stride and v_stride elements apart (multiples of 8,
+ * at least heads * D).  slots [T] int32: a negative slot is skipped (nothing is stored; the output row stays as
+ * it was), one >= page_size * num_pages too, and 0x108 is recorded.  Slots of one append differ from each
+ * other; what two tokens leave in the same slot is undefined (other slots are not touched).
+ * Infinities are stored as the largest value of their block's scale, NaN as 6 times it.
+ */
+int fg_kv_append_mxfp4(int T, int heads, int D, int page_size, int num_pages, const void* k, long long k_stride,
+                       const void* v, long long v_stride, const int32_t* slots, uint8_t* k_cache, uint8_t* k_sf,
+                       uint8_t* v_cache, uint8_t* v_sf, fg_stream_t stream);
+int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, const int32_t* slots, const uint8_t* k_cache,
+                       const uint8_t* k_sf, const uint8_t* v_cache, const uint8_t* v_sf, void* k, long long k_stride,
+                       void* v, long long v_stride, fg_stream_t stream);
+
+/*
+ * Attention of each request's new tokens over its cached ones.  Request r owns rows [query_start[r],
+ * query_start[r+1]) of q and out, its last tokens: with n such rows, row i stands at position
+ * p = seq_lens[r] - n + i and looks at the cached positions j <= p, and with window > 0 at j > p - window only:
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k_j) v_j      (kv head h / (Hq / Hkv))
+ * with cached position j at offset j mod page_size of page block_table[r][j / page_size].  FP32 scores,
+ * statistics and sums; a weight is rounded once, to FP16.  A row that looks at nothing (p < 0) becomes 0.
+ * Rows >= query_start[S] stay as they were; what the cache holds behind a request's length is never used.
+ *   q, out [T][Hq][D] BF16;  block_table [S][max_pages], query_start [S + 1], seq_lens [S] int32
+ * query_start that falls or leaves [0, T], a seq_lens outside [0, max_pages * page_size]: 0x10A is recorded and
+ * the request's rows stay as they were.  A page outside [0, num_pages): 0x10A, and its tokens count as absent.
+ *   workspace: fg_paged_attention_workspace bytes (11 MB whatever the sizes), under the same rules as
+ *   fg_moe_mlp_workspace
+ * Any number of new tokens is right; the kernel is made for few (a decode step, drafts being verified, pieces of
+ * a prompt).  Hq % Hkv == 0.  Supported: S <= 4096, T <= 2^18, Hq / Hkv <= 256.
+ */
+long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D);   /* bytes, or -1 */
+int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                             const void* q, const uint8_t* k_cache, const uint8_t* k_sf, const uint8_t* v_cache,
+                             const uint8_t* v_sf, const int32_t* block_table, const int32_t* query_start,
+                             const int32_t* seq_lens, float scale, int window, void* out, void* workspace,
+                             fg_stream_t stream);
+
 /* Row alignment of each group segment in the contiguous layout: 128, the M block
  * (docsearch section 9 item 2 and section 10). */
 int fg_get_mk_alignment_for_contiguous_layout(void);
@@ -452,6 +548,10 @@ int fg_get_pdl(void);
  *   0x104  K-grouped ks entries negative, not multiples of 128, or not summing to K_total
  *   0x105  internal: a split-K launch without one tile per cluster
  *   0x106  an adapter id >= L
+ *   0x107  block tables: lengths, free pages or a page id out of range
+ *   0x108  a slot past the cache
+ *   0x109  a position past the rotation table
+ *   0x10A  attention: query_start, seq_lens or a page id out of range
  *   0x2xx  a bounded wait inside a kernel ran out (xx says which role waited)
  * The word is one per device and shared by every stream: a kernel of another stream that
  * records an event concurrently is reported by this call or by the next one (the read

@@ -1,0 +1,795 @@
+// fg_attn.cu - attention of each request's new tokens over its 4-bit key/value cache.
+//
+// Mathematics.  For the R = group x new-token rows that share a kv head, with keys k_j = sum over blocks b of
+// s_jb * (codes), per 16 tokens:
+//   S^T = K Q^T      16 tokens x 8 rows per mma (m16n8k16, FP16 codes, FP16 q scaled to [2^8, 2^9) by a
+//                    power of two per row, exact); one FP32 accumulator per block of 32, then times s_jb
+//   w_jb = 2^(S_j - M) * t_jb      t_jb: the value's block scale; M a running maximum of S_j + max_b log2 t_jb,
+//                    so that w <= 2^14 in FP16 however far the scales of different tokens lie apart
+//   O^T += V^T W^T   32 elements of block b x 16 tokens x 8 rows, FP16 codes, FP32 accumulators
+//   l   += 2^(S_j - M),   o = O / l
+// M moves only when some w would pass 2^14 (a vote a tile); then O and l are scaled.  A weight is rounded
+// once, to FP16 (2^-11 relative, down to 2^-22 of a row's largest weight times scale, 2^-33 of it absolute).
+//
+// Work.  An item is (request, chunk of kRows rows, kv head); its keys are cut into blocks of 128 tokens, of which
+// each of a CTA's eight warps takes 16, with accumulators of its own, joined at the end through shared
+// memory.  The blocks of all items stand in one line that is cut into equal shares, one per CTA, from
+// lengths that only the device knows; an item that crosses a cut leaves partial results in the workspace,
+// and the CTA that arrives last joins them in the items' order (so results do not depend on arrival).
+//
+// Codes and scales come through a ring of kStages tiles of 16 tokens that each warp has to itself (asynchronous
+// 16-byte copies, no barrier of the CTA); the cache's order puts what a lane needs of a row into one load,
+// and sixteen tokens never cross a page.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdio>
+
+#include "fg.h"
+#include "fg_host.h"
+#include "fg_kv.cuh"
+
+namespace {
+
+using fg::al;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlock = 16 * kWarps;           // tokens of a block
+constexpr int kMaxCtas = 640;                 // shares of a launch, at most
+constexpr int kMaxRequests = 4096;
+constexpr float kEmpty = -1e30f;              // M of a row without a key
+constexpr float kBias = 8.0f, kSlack = 6.0f;  // w <= 2^(kBias + kSlack)
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct AttnParams {
+    const uint16_t* q;
+    const uint8_t *kc, *ks, *vc, *vs;
+    const int32_t *table, *start, *lens;
+    uint16_t* out;
+    int T, S, heads, group, page, pages, max_pages, window;
+    float scale_log2;                          // scale * log2(e)
+    unsigned* ctr;                             // [kMaxCtas]
+    float* part;                               // [2 * kMaxCtas][kRows][D + 2]: M, l, O
+    int* status;
+};
+
+template <int B, int NT>
+struct Cfg {
+    static constexpr int D = 32 * B, kRows = 8 * NT;
+    static constexpr int kPad = D + 4;         // floats of a row in shared memory: conflict-free 16-byte stores
+    static constexpr int kJoin = kWarps * kRows * kPad * 4;
+    // a warp's ring: per tile 16 key rows, 16 value rows, their scales
+    static constexpr int kStages = 4;
+    static constexpr int kTileV = 16 * 16 * B, kTileKs = 2 * kTileV, kTileVs = kTileKs + 16 * B, kTile = kTileVs + 16 * B;
+    static constexpr int kRing = kWarps * kStages * kTile;
+    static constexpr int kMain = kJoin > kRing ? kJoin : kRing;          // the join comes when the ring is empty
+    static constexpr bool kQShared = NT > 1;                             // q in shared memory: registers hold O
+    static constexpr int kQ = kQShared ? NT * B * 32 * 16 : 0;
+    static constexpr int kSmem = kMain + kQ;                             // then [S + 1] int
+    static constexpr int kSlot = kRows * (D + 2);
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes an 8 x 8 matrix of 16-bit values (row i / 4, columns 2 (i mod 4) and + 1 in lane i).
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A tile's token that stands in row g (and, plus 8, in row g + 8) of the products, and the swizzle of a row's
+// 16-byte chunks: chosen so that the lanes which a shared-memory phase serves together, those of two (D = 64:
+// four) neighbouring g of a key row and those of four c of a value row, find their words in different banks.
+template <int B>
+__device__ __forceinline__ int token_of(int g) {
+    if (B == 2) return (g & 1) ? 4 + (((g >> 1) + 2) & 3) : g >> 1;
+    if (B == 4) return g ^ (g >> 2 & 1);
+    return g;
+}
+template <int B>
+__device__ __forceinline__ int swizzle(int t) {
+    return B == 2 ? 0 : B == 4 ? (t & 2) : (t & 7);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], uint32_t addr) {
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+    } else {
+        static_assert(N == 4, "one load");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    }
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Key words (column group c of the row at `row`): B of them.
+template <int B>
+__device__ __forceinline__ void load_key(uint32_t (&r)[B], uint32_t row, int sw, int c) {
+    if constexpr (B == 8) {
+        uint32_t lo[4], hi[4];
+        load_words(lo, row + 16 * ((2 * c) ^ sw));
+        load_words(hi, row + 16 * ((2 * c + 1) ^ sw));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { r[i] = lo[i]; r[4 + i] = hi[i]; }
+    } else {
+        load_words(r, B == 4 ? row + 16 * (c ^ sw) : row + 8 * c);
+    }
+}
+// Value words (row group g of the row at `row`): B / 2 of them.
+template <int B>
+__device__ __forceinline__ void load_value(uint32_t (&r)[B / 2], uint32_t row, int sw, int g) {
+    load_words(r, row + (B == 8 ? 16 * (g ^ sw) : B == 4 ? 16 * ((g >> 1) ^ sw) + 8 * (g & 1) : 4 * g));
+}
+template <int B>
+__device__ __forceinline__ void load_scales(uint32_t (&r)[(B + 3) / 4], uint32_t addr) {
+    if constexpr (B == 2) {
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr) : "memory");
+        r[0] = h;
+    } else {
+        load_words(r, addr);
+    }
+}
+
+// Scale of block b as a float.
+template <int B>
+__device__ __forceinline__ float scale_of(const uint32_t (&s)[(B + 3) / 4], int b) {
+    const uint32_t w = s[b / 4];
+    const int sh = 8 * (b % 4);
+    return __uint_as_float((sh <= 23 ? w << (23 - sh) : w >> (sh - 23)) & 0x7F800000u);
+}
+// Largest scale of a token, as an exponent (at least the smallest that the cache holds).
+template <int B>
+__device__ __forceinline__ float top_exponent(const uint32_t (&s)[(B + 3) / 4]) {
+    float m = scale_of<B>(s, 0);
+#pragma unroll
+    for (int b = 1; b < B; ++b) m = fmaxf(m, scale_of<B>(s, b));
+    const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+    return static_cast<float>(max(e, fg::kKvMinExp));
+}
+
+// One request as the kernel sees it (n == 0: nothing to do, or its lengths are wrong).
+struct Req {
+    int n, len, t0;
+};
+__device__ __forceinline__ Req request(const AttnParams& p, int r) {
+    const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
+    const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
+    return ok ? Req{t1 - t0, len, t0} : Req{0, 0, 0};
+}
+// Keys [lo, hi) that some row of a chunk looks at; hi <= lo: none.
+struct Keys {
+    int lo, hi;
+};
+template <int kRows>
+__device__ __forceinline__ Keys keys_of(const AttnParams& p, const Req& q, int chunk) {
+    const int i0 = chunk * kRows / p.group, i1 = min(q.n - 1, (chunk * kRows + kRows - 1) / p.group);
+    const int hi = q.len - q.n + i1 + 1;
+    const int lo = p.window > 0 ? max(0, q.len - q.n + i0 + 1 - p.window) : 0;
+    return Keys{lo, hi};
+}
+__device__ __forceinline__ int blocks_of(const Keys& k) { return k.hi > k.lo ? (k.hi + kBlock - 1) / kBlock - k.lo / kBlock : 1; }
+
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp, unsigned long long& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned long long incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    unsigned long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    return before + incl - v;                  // exclusive
+}
+
+template <int B, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kernel(const AttnParams p) {
+    using C = Cfg<B, NT>;
+    constexpr int D = C::D, kRows = C::kRows, kPad = C::kPad;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* s_join = reinterpret_cast<float*>(smem);                       // [kWarps][kRows][kPad]
+    uint4* s_q = reinterpret_cast<uint4*>(smem + C::kMain);               // [NT][B][32]
+    int* s_pre = reinterpret_cast<int*>(smem + C::kSmem);                 // [S + 1] chunks before a request
+    __shared__ float s_qs[kRows];
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ unsigned long long s_warp[kWarps], s_strip[kThreads + 1];
+    __shared__ volatile unsigned long long s_line[4];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t smem_base = fg::smem_u32(smem);
+    fg::grid_dependency_wait();
+    if (tid == 0) fg::grid_launch_dependents();
+
+    // ---------------------------------------------------------------- shares
+    // Chunks per request, then blocks per chunk, each scanned in strips of consecutive entries.
+    const int per_r = (p.S + kThreads - 1) / kThreads;
+    {
+        unsigned long long sum = 0, total;
+        for (int i = 0; i < per_r; ++i) {
+            const int r = tid * per_r + i;
+            if (r >= p.S) break;
+            const Req q = request(p, r);
+            if (blockIdx.x == 0 && q.n == 0) {
+                const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
+                if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page) fg::kv_record(p.status, fg::kKvErrAttention);
+            }
+            sum += ((long long)q.n * p.group + kRows - 1) / kRows;
+        }
+        unsigned long long at = block_scan(sum, s_warp, total);
+        for (int i = 0; i < per_r; ++i) {
+            const int r = tid * per_r + i;
+            if (r >= p.S) break;
+            s_pre[r] = static_cast<int>(at);
+            at += ((long long)request(p, r).n * p.group + kRows - 1) / kRows;
+        }
+        if (tid == 0) s_pre[p.S] = static_cast<int>(total);
+    }
+    __syncthreads();
+    const int chunks = s_pre[p.S];
+    const int per_c = (chunks + kThreads - 1) / kThreads;
+    unsigned long long total_blocks;
+    {
+        unsigned long long sum = 0;
+        int r = 0;
+        if (tid * per_c < chunks) {                      // last request with s_pre[r] <= the strip's first chunk
+            int hi = p.S;
+            while (hi - r > 1) {
+                const int mid = (r + hi) >> 1;
+                if (s_pre[mid] <= tid * per_c) r = mid;
+                else hi = mid;
+            }
+        }
+        for (int i = 0; i < per_c; ++i) {
+            const int ch = tid * per_c + i;
+            if (ch >= chunks) break;
+            while (s_pre[r + 1] <= ch) ++r;
+            sum += blocks_of(keys_of<kRows>(p, request(p, r), ch - s_pre[r]));
+        }
+        const unsigned long long at = block_scan(sum, s_warp, total_blocks);
+        s_strip[tid] = at;
+        if (tid == 0) s_strip[kThreads] = total_blocks;
+    }
+    __syncthreads();
+    const unsigned long long all = total_blocks * p.heads;
+    // at least two blocks a share
+    const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + 1) / 2);
+    const unsigned long long me = blockIdx.x;
+    if (me >= shares) return;
+    unsigned long long u = all * me / shares;
+    const unsigned long long u_end = all * (me + 1) / shares;
+    auto cta_of = [&](unsigned long long x) {
+        return static_cast<int>(((x + 1) * s_line[0] - 1) / s_line[1]);
+    };
+    if (tid == 0) { s_line[0] = shares; s_line[1] = all; s_line[2] = u_end; }   // wanted between items only
+    __syncthreads();
+
+    // the chunk that holds u
+    int r = 0, ch;
+    unsigned long long item0;                            // first block of the current (chunk, head 0)
+    {
+        int lo = 0, hi = kThreads;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_strip[mid] * p.heads <= u) lo = mid;
+            else hi = mid;
+        }
+        ch = lo * per_c;
+        item0 = s_strip[lo] * p.heads;
+        int hr = p.S;
+        while (hr - r > 1) {
+            const int mid = (r + hr) >> 1;
+            if (s_pre[mid] <= ch) r = mid;
+            else hr = mid;
+        }
+    }
+    while (s_pre[r + 1] <= ch) ++r;
+    Req rq = request(p, r);
+    Keys keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
+    int cost = blocks_of(keys);
+    while (item0 + (unsigned long long)cost * p.heads <= u) {
+        item0 += (unsigned long long)cost * p.heads;
+        ++ch;
+        while (s_pre[r + 1] <= ch) ++r;
+        rq = request(p, r);
+        keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
+        cost = blocks_of(keys);
+    }
+    int h = static_cast<int>((u - item0) / cost);
+
+    // ---------------------------------------------------------------- pieces of items
+    while (true) {
+        const unsigned long long iu0 = item0 + (unsigned long long)h * cost;   // the item's first block
+        const int off0 = static_cast<int>(u - iu0);
+        if (tid == 0) s_line[3] = iu0;
+        const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), s_line[2] - iu0));
+        const int chunk = ch - s_pre[r];
+        const int row0 = chunk * kRows, rows = min(kRows, rq.n * p.group - row0);
+        const int first = rq.len - rq.n;                                       // position of new token 0
+        const int* table = p.table + (long long)r * p.max_pages;
+
+        // q of row tile nt: rows nt * 8 + g, elements 32 b + 8 c .. + 7, as FP16 times 2^x; returns 2^-x * scale
+        auto load_q = [&](int nt, uint32_t (&f)[B][4]) {
+            const int j = row0 + nt * 8 + g;
+            uint4 raw[B];
+            float amax = 0.0f;
+#pragma unroll
+            for (int b = 0; b < B; ++b) raw[b] = make_uint4(0, 0, 0, 0);
+            if (nt * 8 + g < rows) {
+                const int i = j / p.group, hq = h * p.group + j % p.group;
+                const uint16_t* src = p.q + ((long long)(rq.t0 + i) * p.heads * p.group + hq) * D + 8 * c;
+#pragma unroll
+                for (int b = 0; b < B; ++b) raw[b] = __ldcg(reinterpret_cast<const uint4*>(src + 32 * b));
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+            const int x = min(126, 8 + 127 - static_cast<int>(__float_as_uint(amax) >> 23));
+            const float up = __uint_as_float(static_cast<uint32_t>(x + 127) << 23);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[b][i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+            }
+            return __uint_as_float(static_cast<uint32_t>(127 - x) << 23) * p.scale_log2;
+        };
+        uint32_t qf[C::kQShared ? 1 : B][4];
+        float qs1[C::kQShared ? 1 : NT][2];
+        auto qs = [&](int nt, int k) { return C::kQShared ? s_qs[nt * 8 + 2 * c + k] : qs1[C::kQShared ? 0 : nt][k]; };
+        if constexpr (C::kQShared) {
+            for (int nt = warp; nt < NT; nt += kWarps) {
+                uint32_t f[B][4];
+                const float down = load_q(nt, f);
+#pragma unroll
+                for (int b = 0; b < B; ++b) s_q[(nt * B + b) * 32 + lane] = make_uint4(f[b][0], f[b][1], f[b][2], f[b][3]);
+                if (c == 0) s_qs[nt * 8 + g] = down;
+            }
+            __syncthreads();
+        } else {
+            const float down = load_q(0, qf);
+            qs1[0][0] = __shfl_sync(kAll, down, 8 * c);
+            qs1[0][1] = __shfl_sync(kAll, down, 8 * c + 4);
+        }
+
+        float o[NT][2 * B][4], l[NT][2], m[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2 * B; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
+            l[nt][0] = l[nt][1] = 0.0f;
+            m[nt][0] = m[nt][1] = kEmpty;
+        }
+
+        // keys that every row of the chunk looks at: tiles inside need no mask
+        const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
+        const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
+        const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
+        // this warp's tiles: tokens 16 * (8 * block + warp)
+        int base = (block0 + off0) * kBlock + 16 * warp;
+        const int base_end = keys.hi > keys.lo ? min((block0 + off1) * kBlock, keys.hi) : 0;
+        if (base + 16 <= keys.lo) base += kBlock;
+        // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
+        int look = base, look_page = base / p.page, look_off = base % p.page;
+        const int step_page = kBlock / p.page, step_off = kBlock % p.page;
+        auto next_page = [&]() {
+            const int id = look < base_end ? __ldg(table + look_page) : 0;
+            look += kBlock;
+            look_page += step_page;
+            look_off += step_off;
+            if (look_off >= p.page) { look_off -= p.page; ++look_page; }
+            return id;
+        };
+        // copies of a tile into a stage; a page outside the cache is not read and counts as masked
+        auto page_ok = [&](int page) { return page >= 0 && page < p.pages; };
+        const uint32_t ring = smem_base + warp * (C::kStages * C::kTile);
+        auto issue = [&](int tok, int page, int off, int stage) {
+            if (tok < base_end) {
+                if (page_ok(page)) {
+                    const long long row = ((long long)page * p.heads + h) * p.page + off;
+                    const uint32_t dst = ring + stage * C::kTile;
+#pragma unroll
+                    for (int i = 0; i < B / 2; ++i) {
+                        const int x = lane + 32 * i, t = x / B, at = t * (16 * B) + 16 * ((x % B) ^ swizzle<B>(t));
+                        cp_async_16(dst + at, p.kc + row * (16 * B) + 16 * x);
+                        cp_async_16(dst + C::kTileV + at, p.vc + row * (16 * B) + 16 * x);
+                    }
+                    if (lane < 2 * B)
+                        cp_async_16(dst + C::kTileKs + 16 * lane, (lane < B ? p.ks + 16 * lane : p.vs + 16 * (lane - B)) + row * B);
+                } else if (lane == 0) {
+                    fg::kv_record(p.status, fg::kKvErrAttention);
+                }
+            }
+            cp_async_commit();
+        };
+
+        auto compute = [&](uint32_t at, int tok0, bool ok) {
+            const int tau = token_of<B>(g);
+            uint32_t ks0[(B + 3) / 4], ks1[(B + 3) / 4], vs0[(B + 3) / 4], vs1[(B + 3) / 4];
+            load_scales<B>(ks0, at + C::kTileKs + tau * B);
+            load_scales<B>(ks1, at + C::kTileKs + (tau + 8) * B);
+            load_scales<B>(vs0, at + C::kTileVs + tau * B);
+            load_scales<B>(vs1, at + C::kTileVs + (tau + 8) * B);
+            uint32_t k0[B], k1[B];
+            load_key<B>(k0, at + tau * (16 * B), swizzle<B>(tau), c);
+            load_key<B>(k1, at + (tau + 8) * (16 * B), swizzle<B>(tau + 8), c);
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                uint32_t a[4], e[4];
+                fg::e2m1x8_f16(k0[b], a);
+                fg::e2m1x8_f16(k1[b], e);
+                const float s0 = scale_of<B>(ks0, b), s1 = scale_of<B>(ks1, b);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint4 f;
+                    if constexpr (C::kQShared) f = s_q[(nt * B + b) * 32 + lane];
+                    else f = make_uint4(qf[b][0], qf[b][1], qf[b][2], qf[b][3]);
+                    mma_f16(x, a[0], e[0], a[1], e[1], f.x, f.y);
+                    mma_f16(x, a[2], e[2], a[3], e[3], f.z, f.w);
+                    s[nt][0] = fmaf(x[0], s0, s[nt][0]);
+                    s[nt][1] = fmaf(x[1], s0, s[nt][1]);
+                    s[nt][2] = fmaf(x[2], s1, s[nt][2]);
+                    s[nt][3] = fmaf(x[3], s1, s[nt][3]);
+                }
+            }
+            if (!ok || tok0 < all_lo || tok0 + 16 > all_hi) {                  // a border: mask
+                const int t0 = tok0 + tau, t1 = t0 + 8;
+                const bool in0 = ok && t0 >= keys.lo && t0 < keys.hi, in1 = ok && t1 >= keys.lo && t1 < keys.hi;
+#pragma unroll
+                for (int i = 0; i < (B + 3) / 4; ++i) {                        // scales behind the keys may be anything
+                    if (!in0) vs0[i] = 0;
+                    if (!in1) vs1[i] = 0;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int i = (row0 + nt * 8 + 2 * c + k) / p.group;
+                        const int hi = first + i + 1, lo = p.window > 0 ? hi - p.window : 0;
+                        if (!(in0 && t0 >= lo && t0 < hi)) s[nt][k] = -INFINITY;
+                        if (!(in1 && t1 >= lo && t1 < hi)) s[nt][2 + k] = -INFINITY;
+                    }
+            }
+            const float e0 = top_exponent<B>(vs0), e1 = top_exponent<B>(vs1);
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    over |= fmaf(s[nt][k], qs(nt, k), e0 - m[nt][k]) > kSlack;
+                    over |= fmaf(s[nt][2 + k], qs(nt, k), e1 - m[nt][k]) > kSlack;
+                }
+            if (__any_sync(kAll, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = fmaxf(fmaf(s[nt][k], qs(nt, k), e0), fmaf(s[nt][2 + k], qs(nt, k), e1));
+#pragma unroll
+                        for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
+                        top = fmaxf(top, m[nt][k]);
+                        const float f = ex2(m[nt][k] - top);
+                        m[nt][k] = top;
+                        l[nt][k] *= f;
+#pragma unroll
+                        for (int i = 0; i < 2 * B; ++i) {
+                            o[nt][i][k] *= f;
+                            o[nt][i][2 + k] *= f;
+                        }
+                    }
+            }
+            float w[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    w[nt][k] = ex2(fmaf(s[nt][k], qs(nt, k), kBias - m[nt][k]));
+                    w[nt][2 + k] = ex2(fmaf(s[nt][2 + k], qs(nt, k), kBias - m[nt][k]));
+                    l[nt][k] += w[nt][k] + w[nt][2 + k];
+                }
+            uint32_t v[4][B / 2];                              // row group g of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = token_of<B>(2 * c + (i & 1)) + 8 * (i >> 1);
+                load_value<B>(v[i], at + C::kTileV + tok * (16 * B), swizzle<B>(tok), g);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float f0 = scale_of<B>(vs0, b), f1 = scale_of<B>(vs1, b);
+                uint32_t wb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    wb[nt][0] = movmatrix(pack_f16(w[nt][0] * f0, w[nt][1] * f0));
+                    wb[nt][1] = movmatrix(pack_f16(w[nt][2] * f1, w[nt][3] * f1));
+                }
+                // half word b of the four tokens: pairs of tokens side by side, then codes to FP16
+                const int word = b / 2, sel = (b & 1) ? 0x7632 : 0x5410;
+                uint32_t x[4], y[4];
+                fg::e2m1x8_f16(__byte_perm(v[0][word], v[1][word], sel), x);   // x[0], x[1]: token 2c; x[2], x[3]: 2c + 1
+                fg::e2m1x8_f16(__byte_perm(v[2][word], v[3][word], sel), y);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t a0 = __byte_perm(x[i], x[2 + i], 0x5410), a1 = __byte_perm(x[i], x[2 + i], 0x7632);
+                    const uint32_t a2 = __byte_perm(y[i], y[2 + i], 0x5410), a3 = __byte_perm(y[i], y[2 + i], 0x7632);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * b + i], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
+                }
+            }
+        };
+
+        if (base < base_end) {
+            uint32_t ok = 0;                                // bit i: the page of the tile i ahead is in the cache
+#pragma unroll
+            for (int i = 0; i < C::kStages - 1; ++i) {
+                const int off = look_off, page = next_page();
+                ok |= static_cast<uint32_t>(page_ok(page)) << i;
+                issue(base + i * kBlock, page, off, i);
+            }
+            int off = look_off, page = next_page();
+            int stage = 0;
+            while (true) {
+                issue(base + (C::kStages - 1) * kBlock, page, off, stage == 0 ? C::kStages - 1 : stage - 1);
+                ok |= static_cast<uint32_t>(page_ok(page)) << (C::kStages - 1);
+                off = look_off;
+                page = next_page();
+                cp_async_wait<C::kStages - 1>();
+                __syncwarp();
+                compute(ring + stage * C::kTile, base, ok & 1u);
+                __syncwarp();                               // every lane has read the stage that is filled next
+                ok >>= 1;
+                base += kBlock;
+                if (base >= base_end) break;
+                if (++stage == C::kStages) stage = 0;
+            }
+            cp_async_wait<0>();
+        }
+        __syncthreads();                                    // the rings are empty: their place takes the join
+
+        // ---------------------------------------------------------- join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int i = 4; i < 32; i <<= 1) l[nt][k] += __shfl_xor_sync(kAll, l[nt][k], i);
+                if (g == 0) {
+                    s_m[warp][nt * 8 + 2 * c + k] = m[nt][k];
+                    s_l[warp][nt * 8 + 2 * c + k] = l[nt][k];
+                }
+                float* dst = s_join + (warp * kRows + nt * 8 + 2 * c + k) * kPad + 4 * g;
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    *reinterpret_cast<float4*>(dst + 32 * b) =
+                        make_float4(o[nt][2 * b][k], o[nt][2 * b][2 + k], o[nt][2 * b + 1][k], o[nt][2 * b + 1][2 + k]);
+            }
+        __syncthreads();
+        const unsigned long long iu1 = s_line[3];
+        const int a = cta_of(iu1), z = cta_of(iu1 + cost - 1);
+        const bool whole = a == z;
+        float* slot = p.part + (long long)(2 * me + (static_cast<int>(me) == a ? 1 : 0)) * C::kSlot;
+        auto store_row = [&](int j, int d4, float4 v) {
+            const int i = (row0 + j) / p.group, hq = h * p.group + (row0 + j) % p.group;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>(p.out + ((long long)(rq.t0 + i) * p.heads * p.group + hq) * D + 4 * d4) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        };
+        for (int it = tid; it < rows * (D / 4); it += kThreads) {
+            const int j = it / (D / 4), d4 = it % (D / 4);
+            float top = s_m[0][j];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][j]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(s_m[w][j] - top);
+                const float4 v = *reinterpret_cast<const float4*>(s_join + (w * kRows + j) * kPad + 4 * d4);
+                sum = fmaf(s_l[w][j], f, sum);
+                acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+            }
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                store_row(j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+            } else {
+                if (d4 == 0) {
+                    slot[j] = top;
+                    slot[kRows + j] = sum;
+                }
+                *reinterpret_cast<float4*>(slot + 2 * kRows + j * D + 4 * d4) = acc;
+            }
+        }
+        if (!whole) {
+            // the last CTA to arrive joins the pieces, in the order of the CTAs
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const unsigned before = atomicAdd(p.ctr + a, 1u);
+                s_last = before == static_cast<unsigned>(z - a);
+                if (s_last) p.ctr[a] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                for (int it = tid; it < rows * (D / 4); it += kThreads) {
+                    const int j = it / (D / 4), d4 = it % (D / 4);
+                    float top = kEmpty, sum = 0.0f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = a; k <= z; ++k) {
+                        const float* s = p.part + (long long)(2 * k + (k == a ? 1 : 0)) * C::kSlot;
+                        const float mk = __ldcg(s + j), lk = __ldcg(s + kRows + j);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
+                        const float t = fmaxf(top, mk);
+                        const float f = ex2(top - t), e = ex2(mk - t);
+                        top = t;
+                        sum = sum * f + lk * e;
+                        acc.x = acc.x * f + v.x * e; acc.y = acc.y * f + v.y * e;
+                        acc.z = acc.z * f + v.z * e; acc.w = acc.w * f + v.w * e;
+                    }
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    store_row(j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                }
+            }
+        }
+
+        u = iu1 + off1;
+        if (u >= s_line[2]) break;
+        __syncthreads();                                    // s_join is written again
+        if (++h == p.heads) {
+            h = 0;
+            item0 += (unsigned long long)cost * p.heads;
+            ++ch;
+            while (s_pre[r + 1] <= ch) ++r;
+            rq = request(p, r);
+            keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
+            cost = blocks_of(keys);
+        }
+    }
+}
+
+template <int B, int NT>
+int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
+    using C = Cfg<B, NT>;
+    constexpr int kPerSm = NT == 1 && B <= 4 ? 2 : 1;
+    const int smem = C::kSmem + (p.S + 1) * 4;
+    static bool configured[256] = {};        // set once per device; setting it again is harmless
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) {
+        cudaGetLastError();
+        return FG_ERR_CUDA;
+    }
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(attn_kernel<B, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem + (kMaxRequests + 1) * 4) != cudaSuccess) {
+            cudaGetLastError();
+            return FG_ERR_CUDA;
+        }
+        configured[dev] = true;
+    }
+    const int ctas = sms * kPerSm < kMaxCtas ? sms * kPerSm : kMaxCtas;
+    if (fg::print_configs_enabled())
+        std::fprintf(stderr, "[fg] paged_attention_mxfp4 T=%d S=%d heads=%d x %d D=%d rows=%d grid=%d\n", p.T, p.S, p.heads,
+                     p.group, C::D, C::kRows, ctas);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, attn_kernel<B, NT>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FG_ERR_CUDA;
+    }
+    return FG_OK;
+}
+
+// Row tiles of eight: as many as an average request's rows fill, and as many as registers hold the
+// accumulators of.
+int row_tiles(int T, int S, int group, int D) {
+    const long long rows = ((long long)T + S - 1) / S * group;
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    const int most = D == 64 ? 4 : D == 128 ? 2 : 1;
+    return nt < most ? nt : most;
+}
+
+bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
+    return T >= 0 && S >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536 && D >= 1;
+}
+
+// Floats of the largest variant's partial result: one size serves every call.
+constexpr int kMaxSlot = Cfg<2, 4>::kSlot;
+static_assert(Cfg<4, 2>::kSlot <= kMaxSlot && Cfg<8, 1>::kSlot <= kMaxSlot, "largest partial result");
+constexpr long long kCtrBytes = (kMaxCtas * 4 + 255) / 256 * 256;
+
+}  // namespace
+
+extern "C" {
+
+long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D) {
+    if (!shapes_ok(T, S, Hq, Hkv, D) || (D != 64 && D != 128 && D != 256)) return -1;
+    return kCtrBytes + 2LL * kMaxCtas * kMaxSlot * 4;
+}
+
+int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                             const void* q, const uint8_t* k_cache, const uint8_t* k_sf, const uint8_t* v_cache,
+                             const uint8_t* v_sf, const int32_t* block_table, const int32_t* query_start,
+                             const int32_t* seq_lens, float scale, int window, void* out, void* workspace,
+                             fg_stream_t stream) {
+    if (!shapes_ok(T, S, Hq, Hkv, D) || page_size < 1 || num_pages < 1 || max_pages < 1 || window < 0 ||
+        (long long)page_size * num_pages > 0x7fffffffLL || (long long)page_size * max_pages > 0x7fffffffLL - 4096 ||
+        !(scale > 0.0f) || !(scale <= 3.402823466e38f))
+        return FG_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || S > kMaxRequests || T > 1 << 18 || Hq / Hkv > 256)
+        return FG_ERR_UNSUPPORTED;
+    if (T == 0 || S == 0) return FG_OK;
+    if (!q || !k_cache || !k_sf || !v_cache || !v_sf || !block_table || !query_start || !seq_lens || !out || !workspace ||
+        !al(q, 16) || !al(k_cache, 16) || !al(k_sf, 16) || !al(v_cache, 16) || !al(v_sf, 16) || !al(block_table, 4) ||
+        !al(query_start, 4) || !al(seq_lens, 4) || !al(out, 16) || !al(workspace, 256))
+        return FG_ERR_INVALID_ARG;
+    fg::HostState st;
+    if (const int rc = fg::host_state(&st)) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const AttnParams p{static_cast<const uint16_t*>(q), k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens,
+                       static_cast<uint16_t*>(out), T, S, Hkv, Hq / Hkv, page_size, num_pages, max_pages, window,
+                       scale * 1.4426950408889634f, reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCtrBytes),
+                       st.status};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int nt = row_tiles(T, S, Hq / Hkv, D);
+    switch (D) {
+        case 64: return nt == 1 ? launch<2, 1>(p, st.sms, st.pdl, s) : nt == 2 ? launch<2, 2>(p, st.sms, st.pdl, s) : launch<2, 4>(p, st.sms, st.pdl, s);
+        case 128: return nt == 1 ? launch<4, 1>(p, st.sms, st.pdl, s) : launch<4, 2>(p, st.sms, st.pdl, s);
+        default: return launch<8, 1>(p, st.sms, st.pdl, s);
+    }
+}
+
+}  // extern "C"
