@@ -8,7 +8,7 @@
 //                    so that w <= 2^14 in FP16 however far the scales of different tokens lie apart
 //   O^T += V^T W^T   32 elements of block b x 16 tokens x 8 rows, FP16 codes, FP32 accumulators
 //   l   += 2^(S_j - M),   o = O / l
-// M moves only when some w would pass 2^14 (a vote a tile); then O and l are scaled.  A weight is rounded
+// M moves only when some w might pass 2^15 (a vote a tile); then O and l are scaled.  A weight is rounded
 // once, to FP16 (2^-11 relative, down to 2^-22 of a row's largest weight times scale, 2^-33 of it absolute).
 //
 // Work.  An item is (request, chunk of kRows rows, kv head); its keys are cut into blocks of 128 tokens, of which
@@ -36,10 +36,11 @@ using fg::al;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 16 * kWarps;           // tokens of a block
+constexpr int kStart = 3;                     // an item's start, in blocks
 constexpr int kMaxCtas = 640;                 // shares of a launch, at most
 constexpr int kMaxRequests = 4096;
 constexpr float kEmpty = -1e30f;              // M of a row without a key
-constexpr float kBias = 8.0f, kSlack = 6.0f;  // w <= 2^(kBias + kSlack)
+constexpr float kBias = 8.0f, kMostW = 32768.0f;   // w: 2^8 where M has just moved, at most 2^15
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct AttnParams {
@@ -75,6 +76,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Byte i (two codes) of w as an FP16 pair.
+__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t w, int i) {
+    uint32_t r;
+    if (i == 0) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    else if (i == 1) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+    else if (i == 2) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+    else asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
 // Transposes an 8 x 8 matrix of 16-bit values (row i / 4, columns 2 (i mod 4) and + 1 in lane i).
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -154,19 +164,27 @@ __device__ __forceinline__ void load_scales(uint32_t (&r)[(B + 3) / 4], uint32_t
     }
 }
 
-// Scale of block b as a float.
+// The B scales of a token as floats.  A byte's exponent as BF16 is byte << 7, so a mask and a product give two
+// at once (products and sums run beside the ALU pipe, which the conversions fill).
 template <int B>
-__device__ __forceinline__ float scale_of(const uint32_t (&s)[(B + 3) / 4], int b) {
-    const uint32_t w = s[b / 4];
-    const int sh = 8 * (b % 4);
-    return __uint_as_float((sh <= 23 ? w << (23 - sh) : w >> (sh - 23)) & 0x7F800000u);
-}
-// Largest scale of a token, as an exponent (at least the smallest that the cache holds).
-template <int B>
-__device__ __forceinline__ float top_exponent(const uint32_t (&s)[(B + 3) / 4]) {
-    float m = scale_of<B>(s, 0);
+__device__ __forceinline__ void scales_of(float (&f)[B], const uint32_t (&s)[(B + 3) / 4]) {
 #pragma unroll
-    for (int b = 1; b < B; ++b) m = fmaxf(m, scale_of<B>(s, b));
+    for (int i = 0; i < B; i += 4) {
+        const uint32_t w = s[i / 4], even = (w & 0x00FF00FFu) * 128u, odd = (w >> 1) & 0x7F807F80u;
+        f[i] = __uint_as_float(even * 65536u);
+        f[i + 1] = __uint_as_float(odd * 65536u);
+        if (B > 2) {
+            f[i + 2] = __uint_as_float(even & 0xFFFF0000u);
+            f[i + 3] = __uint_as_float(odd & 0xFFFF0000u);
+        }
+    }
+}
+// Exponent of a token's largest scale (at least the smallest that the cache holds).
+template <int B>
+__device__ __forceinline__ float top_exponent(const float (&f)[B]) {
+    float m = f[0];
+#pragma unroll
+    for (int b = 1; b < B; ++b) m = fmaxf(m, f[b]);
     const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
     return static_cast<float>(max(e, fg::kKvMinExp));
 }
@@ -191,7 +209,9 @@ __device__ __forceinline__ Keys keys_of(const AttnParams& p, const Req& q, int c
     const int lo = p.window > 0 ? max(0, q.len - q.n + i0 + 1 - p.window) : 0;
     return Keys{lo, hi};
 }
-__device__ __forceinline__ int blocks_of(const Keys& k) { return k.hi > k.lo ? (k.hi + kBlock - 1) / kBlock - k.lo / kBlock : 1; }
+// Cost of an item in blocks: kStart for what every item takes (its q, filling the pipeline, the join), then its
+// keys' blocks.
+__device__ __forceinline__ int cost_of(const Keys& k) { return kStart + (k.hi > k.lo ? (k.hi + kBlock - 1) / kBlock - k.lo / kBlock : 1); }
 
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp, unsigned long long& total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             const int ch = tid * per_c + i;
             if (ch >= chunks) break;
             while (s_pre[r + 1] <= ch) ++r;
-            sum += blocks_of(keys_of<kRows>(p, request(p, r), ch - s_pre[r]));
+            sum += cost_of(keys_of<kRows>(p, request(p, r), ch - s_pre[r]));
         }
         const unsigned long long at = block_scan(sum, s_warp, total_blocks);
         s_strip[tid] = at;
@@ -283,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     }
     __syncthreads();
     const unsigned long long all = total_blocks * p.heads;
-    // at least two blocks a share
-    const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + 1) / 2);
+    // a share is worth an item's start
+    const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kStart) / (kStart + 1));
     const unsigned long long me = blockIdx.x;
     if (me >= shares) return;
     unsigned long long u = all * me / shares;
@@ -317,14 +337,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     while (s_pre[r + 1] <= ch) ++r;
     Req rq = request(p, r);
     Keys keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-    int cost = blocks_of(keys);
+    int cost = cost_of(keys);
     while (item0 + (unsigned long long)cost * p.heads <= u) {
         item0 += (unsigned long long)cost * p.heads;
         ++ch;
         while (s_pre[r + 1] <= ch) ++r;
         rq = request(p, r);
         keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-        cost = blocks_of(keys);
+        cost = cost_of(keys);
     }
     int h = static_cast<int>((u - item0) / cost);
 
@@ -332,8 +352,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     while (true) {
         const unsigned long long iu0 = item0 + (unsigned long long)h * cost;   // the item's first block
         const int off0 = static_cast<int>(u - iu0);
-        if (tid == 0) s_line[3] = iu0;
         const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), s_line[2] - iu0));
+        if (off1 <= kStart) break;                           // none of its blocks in this share, which ends here
+        if (tid == 0) s_line[3] = iu0;
         const int chunk = ch - s_pre[r];
         const int row0 = chunk * kRows, rows = min(kRows, rq.n * p.group - row0);
         const int first = rq.len - rq.n;                                       // position of new token 0
@@ -406,11 +427,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
         const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
         // this warp's tiles: tokens 16 * (8 * block + warp)
-        int base = (block0 + off0) * kBlock + 16 * warp;
-        const int base_end = keys.hi > keys.lo ? min((block0 + off1) * kBlock, keys.hi) : 0;
+        int base = (block0 + max(off0 - kStart, 0)) * kBlock + 16 * warp;
+        const int base_end = keys.hi > keys.lo ? min((block0 + off1 - kStart) * kBlock, keys.hi) : 0;
         if (base + 16 <= keys.lo) base += kBlock;
         // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
         int look = base, look_page = base / p.page, look_off = base % p.page;
+        const uint32_t page_rows = static_cast<uint32_t>(p.heads) * p.page, head_row = static_cast<uint32_t>(h) * p.page;
         const int step_page = kBlock / p.page, step_off = kBlock % p.page;
         auto next_page = [&]() {
             const int id = look < base_end ? __ldg(table + look_page) : 0;
@@ -426,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         auto issue = [&](int tok, int page, int off, int stage) {
             if (tok < base_end) {
                 if (page_ok(page)) {
-                    const long long row = ((long long)page * p.heads + h) * p.page + off;
+                    // row of the tile's first token: (page * heads + h) * page_size + off
+                    const unsigned long long row = (unsigned long long)static_cast<uint32_t>(page) * page_rows + (head_row + off);
                     const uint32_t dst = ring + stage * C::kTile;
 #pragma unroll
                     for (int i = 0; i < B / 2; ++i) {
@@ -456,12 +479,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             float s[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+            float f0[B], f1[B];
+            scales_of<B>(f0, ks0);
+            scales_of<B>(f1, ks1);
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 uint32_t a[4], e[4];
                 fg::e2m1x8_f16(k0[b], a);
                 fg::e2m1x8_f16(k1[b], e);
-                const float s0 = scale_of<B>(ks0, b), s1 = scale_of<B>(ks1, b);
+                const float s0 = f0[b], s1 = f1[b];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -494,16 +520,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                         if (!(in1 && t1 >= lo && t1 < hi)) s[nt][2 + k] = -INFINITY;
                     }
             }
-            const float e0 = top_exponent<B>(vs0), e1 = top_exponent<B>(vs1);
+            scales_of<B>(f0, vs0);
+            scales_of<B>(f1, vs1);
+            float w[NT][4];
+            auto weights = [&]() {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        w[nt][k] = ex2(fmaf(s[nt][k], qs(nt, k), kBias - m[nt][k]));
+                        w[nt][2 + k] = ex2(fmaf(s[nt][2 + k], qs(nt, k), kBias - m[nt][k]));
+                    }
+            };
+            weights();
+            // no weight times scale is above the sum of all
+            float sum0 = f0[0], sum1 = f1[0];
+#pragma unroll
+            for (int b = 1; b < B; ++b) { sum0 += f0[b]; sum1 += f1[b]; }
             bool over = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    over |= fmaf(s[nt][k], qs(nt, k), e0 - m[nt][k]) > kSlack;
-                    over |= fmaf(s[nt][2 + k], qs(nt, k), e1 - m[nt][k]) > kSlack;
-                }
+                over |= !(fmaf(w[nt][0], sum0, fmaf(w[nt][1], sum0, fmaf(w[nt][2], sum1, w[nt][3] * sum1))) <= kMostW);
             if (__any_sync(kAll, over)) {
+                const float e0 = top_exponent<B>(f0), e1 = top_exponent<B>(f1);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -521,40 +560,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                             o[nt][i][2 + k] *= f;
                         }
                     }
+                weights();
             }
-            float w[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt][0] += w[nt][0] + w[nt][2];
+                l[nt][1] += w[nt][1] + w[nt][3];
+            }
+            uint32_t even[2][B / 2], odd[2][B / 2];            // row group g of tokens 2c and 2c + 1, 2c + 8 and 2c + 9
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    w[nt][k] = ex2(fmaf(s[nt][k], qs(nt, k), kBias - m[nt][k]));
-                    w[nt][2 + k] = ex2(fmaf(s[nt][2 + k], qs(nt, k), kBias - m[nt][k]));
-                    l[nt][k] += w[nt][k] + w[nt][2 + k];
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v0[B / 2], v1[B / 2];
+                const int t0 = token_of<B>(2 * c) + 8 * i, t1 = token_of<B>(2 * c + 1) + 8 * i;
+                load_value<B>(v0, at + C::kTileV + t0 * (16 * B), swizzle<B>(t0), g);
+                load_value<B>(v1, at + C::kTileV + t1 * (16 * B), swizzle<B>(t1), g);
+#pragma unroll
+                for (int j = 0; j < B / 2; ++j) {
+                    even[i][j] = (v0[j] & 0x0F0F0F0Fu) | (v1[j] * 16u & 0xF0F0F0F0u);
+                    odd[i][j] = (v0[j] >> 4 & 0x0F0F0F0Fu) | (v1[j] & 0xF0F0F0F0u);
                 }
-            uint32_t v[4][B / 2];                              // row group g of tokens 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = token_of<B>(2 * c + (i & 1)) + 8 * (i >> 1);
-                load_value<B>(v[i], at + C::kTileV + tok * (16 * B), swizzle<B>(tok), g);
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const float f0 = scale_of<B>(vs0, b), f1 = scale_of<B>(vs1, b);
                 uint32_t wb[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    wb[nt][0] = movmatrix(pack_f16(w[nt][0] * f0, w[nt][1] * f0));
-                    wb[nt][1] = movmatrix(pack_f16(w[nt][2] * f1, w[nt][3] * f1));
+                    wb[nt][0] = movmatrix(pack_f16(w[nt][0] * f0[b], w[nt][1] * f0[b]));
+                    wb[nt][1] = movmatrix(pack_f16(w[nt][2] * f1[b], w[nt][3] * f1[b]));
                 }
-                // half word b of the four tokens: pairs of tokens side by side, then codes to FP16
-                const int word = b / 2, sel = (b & 1) ? 0x7632 : 0x5410;
-                uint32_t x[4], y[4];
-                fg::e2m1x8_f16(__byte_perm(v[0][word], v[1][word], sel), x);   // x[0], x[1]: token 2c; x[2], x[3]: 2c + 1
-                fg::e2m1x8_f16(__byte_perm(v[2][word], v[3][word], sel), y);
+                // half word b of the four tokens, zipped: byte 2 (b mod 2) + i holds code 2 i (even) or 2 i + 1
+                // (odd) of a pair of tokens, which one conversion makes an operand's pair
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t a0 = __byte_perm(x[i], x[2 + i], 0x5410), a1 = __byte_perm(x[i], x[2 + i], 0x7632);
-                    const uint32_t a2 = __byte_perm(y[i], y[2 + i], 0x5410), a3 = __byte_perm(y[i], y[2 + i], 0x7632);
+                    const int at = 2 * (b & 1) + i;
+                    const uint32_t a0 = e2m1x2_f16(even[0][b / 2], at), a1 = e2m1x2_f16(odd[0][b / 2], at);
+                    const uint32_t a2 = e2m1x2_f16(even[1][b / 2], at), a3 = e2m1x2_f16(odd[1][b / 2], at);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * b + i], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
                 }
@@ -608,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
         __syncthreads();
         const unsigned long long iu1 = s_line[3];
-        const int a = cta_of(iu1), z = cta_of(iu1 + cost - 1);
+        const int a = cta_of(iu1 + kStart), z = cta_of(iu1 + cost - 1);
         const bool whole = a == z;
         float* slot = p.part + (long long)(2 * me + (static_cast<int>(me) == a ? 1 : 0)) * C::kSlot;
         auto store_row = [&](int j, int d4, float4 v) {
@@ -686,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             while (s_pre[r + 1] <= ch) ++r;
             rq = request(p, r);
             keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-            cost = blocks_of(keys);
+            cost = cost_of(keys);
         }
     }
 }
@@ -769,7 +809,8 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
         (long long)page_size * num_pages > 0x7fffffffLL || (long long)page_size * max_pages > 0x7fffffffLL - 4096 ||
         !(scale > 0.0f) || !(scale <= 3.402823466e38f))
         return FG_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || S > kMaxRequests || T > 1 << 18 || Hq / Hkv > 256)
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || S > kMaxRequests || T > 1 << 18 || Hq / Hkv > 256 ||
+        (long long)Hkv * page_size > 0x7fffffffLL)
         return FG_ERR_UNSUPPORTED;
     if (T == 0 || S == 0) return FG_OK;
     if (!q || !k_cache || !k_sf || !v_cache || !v_sf || !block_table || !query_start || !seq_lens || !out || !workspace ||
