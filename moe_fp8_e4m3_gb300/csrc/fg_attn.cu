@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     __shared__ unsigned long long s_warp[kWarps], s_strip[kThreads + 1];
     __shared__ volatile unsigned long long s_line[4];
     __shared__ int s_last;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t smem_base = fg::smem_u32(smem);
     fg::grid_dependency_wait();
     if (tid == 0) fg::grid_launch_dependents();
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kStart) / (kStart + 1));
     const unsigned long long me = blockIdx.x;
     if (me >= shares) return;
-    unsigned long long u = all * me / shares;
+    const unsigned long long u = all * me / shares;
     const unsigned long long u_end = all * (me + 1) / shares;
     auto cta_of = [&](unsigned long long x) {
         return static_cast<int>(((x + 1) * s_line[0] - 1) / s_line[1]);
@@ -347,11 +347,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         cost = cost_of(keys);
     }
     int h = static_cast<int>((u - item0) / cost);
+    unsigned long long iu0 = item0 + (unsigned long long)h * cost;   // where the item begins
+    int off0 = static_cast<int>(u - iu0);                            // and the share within it
+
+    // what a lane copies of a tile (16-byte chunk `lane`, and every 32nd on) and where it finds its operands in one
+    const uint32_t page_rows = static_cast<uint32_t>(p.heads) * p.page;
+    const int step_page = kBlock / p.page, step_off = kBlock % p.page;
+    const uint32_t ring = smem_base + warp * (C::kStages * C::kTile);
+    const uint32_t cp_dst = ring + (lane / B) * (16 * B) + 16 * ((lane % B) ^ swizzle<B>(lane / B));
+    const uint32_t cp_dst_odd = ring + (lane / B) * (16 * B) + 16 * ((lane % B) ^ swizzle<B>(lane / B) ^ 4);
+    const uint32_t cp_sf = ring + C::kTileKs + 16 * lane;
+    const uint8_t* sf_lane = lane < B ? p.ks + 16 * lane : p.vs + 16 * (lane - B);
+    const int tau = token_of<B>(g), tau0 = token_of<B>(2 * c), tau1 = token_of<B>(2 * c + 1);
+    const uint32_t at_sf = ring + C::kTileKs + tau * B;
+    const uint32_t at_k = ring + tau * (16 * B), at_v0 = ring + C::kTileV + tau0 * (16 * B), at_v1 = ring + C::kTileV + tau1 * (16 * B);
 
     // ---------------------------------------------------------------- pieces of items
     while (true) {
-        const unsigned long long iu0 = item0 + (unsigned long long)h * cost;   // the item's first block
-        const int off0 = static_cast<int>(u - iu0);
         const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), s_line[2] - iu0));
         if (off1 <= kStart) break;                           // none of its blocks in this share, which ends here
         if (tid == 0) s_line[3] = iu0;
@@ -359,6 +371,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         const int row0 = chunk * kRows, rows = min(kRows, rq.n * p.group - row0);
         const int first = rq.len - rq.n;                                       // position of new token 0
         const int* table = p.table + (long long)r * p.max_pages;
+        const uint32_t head_row = static_cast<uint32_t>(h) * p.page;
+
+        // keys that every row of the chunk looks at: tiles inside need no mask
+        const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
+        const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
+        const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
+        // this warp's tiles: tokens 16 * (8 * block + warp)
+        int base = (block0 + max(off0 - kStart, 0)) * kBlock + 16 * warp;
+        const int base_end = keys.hi > keys.lo ? min((block0 + off1 - kStart) * kBlock, keys.hi) : 0;
+        if (base + 16 <= keys.lo) base += kBlock;
+        // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
+        int look_page = base / p.page, look_off = base % p.page;
+        auto next_page = [&](int tok, uint32_t& page, uint32_t& off) {
+            page = tok < base_end ? static_cast<uint32_t>(__ldg(table + look_page)) : ~0u;
+            off = head_row + look_off;
+            look_page += step_page;
+            look_off += step_off;
+            if (look_off >= p.page) { look_off -= p.page; ++look_page; }
+        };
+        // copies of a tile into a stage; a page outside the cache is not read and counts as masked
+        auto issue = [&](uint32_t page, uint32_t off, int stage, bool wanted) {
+            const bool ok = page < static_cast<uint32_t>(p.pages);
+            if (ok) {
+                // row of the tile's first token: (page * heads + h) * page_size + offset
+                const unsigned long long row = (unsigned long long)page * page_rows + off;
+                const unsigned long long at = row * (16 * B) + 16 * lane;
+                const uint8_t *k = p.kc + at, *v = p.vc + at;
+#pragma unroll
+                for (int i = 0; i < B / 2; ++i) {
+                    // 32 chunks on, 32 / B tokens: B = 8 swizzles four tokens on with another bit
+                    const uint32_t dst = (B == 8 && (i & 1) ? cp_dst_odd : cp_dst) + stage * C::kTile + 512 * i;
+                    cp_async_16(dst, k + 512 * i);
+                    cp_async_16(dst + C::kTileV, v + 512 * i);
+                }
+                if (lane < 2 * B) cp_async_16(cp_sf + stage * C::kTile, sf_lane + row * B);
+            } else if (wanted && lane == 0) {
+                fg::kv_record(p.status, fg::kKvErrAttention);
+            }
+            cp_async_commit();
+            return ok;
+        };
+        // the first copies go ahead of q
+        uint32_t absent = 0;                                // bit: the stage's tile has no page
+        uint32_t page, off;
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            next_page(base + i * kBlock, page, off);
+            if (!issue(page, off, i, base + i * kBlock < base_end)) absent |= 1u << i;
+        }
+        next_page(base + (C::kStages - 1) * kBlock, page, off);
 
         // q of row tile nt: rows nt * 8 + g, elements 32 b + 8 c .. + 7, as FP16 times 2^x; returns 2^-x * scale
         auto load_q = [&](int nt, uint32_t (&f)[B][4]) {
@@ -422,60 +484,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             m[nt][0] = m[nt][1] = kEmpty;
         }
 
-        // keys that every row of the chunk looks at: tiles inside need no mask
-        const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
-        const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
-        const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
-        // this warp's tiles: tokens 16 * (8 * block + warp)
-        int base = (block0 + max(off0 - kStart, 0)) * kBlock + 16 * warp;
-        const int base_end = keys.hi > keys.lo ? min((block0 + off1 - kStart) * kBlock, keys.hi) : 0;
-        if (base + 16 <= keys.lo) base += kBlock;
-        // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
-        int look = base, look_page = base / p.page, look_off = base % p.page;
-        const uint32_t page_rows = static_cast<uint32_t>(p.heads) * p.page, head_row = static_cast<uint32_t>(h) * p.page;
-        const int step_page = kBlock / p.page, step_off = kBlock % p.page;
-        auto next_page = [&]() {
-            const int id = look < base_end ? __ldg(table + look_page) : 0;
-            look += kBlock;
-            look_page += step_page;
-            look_off += step_off;
-            if (look_off >= p.page) { look_off -= p.page; ++look_page; }
-            return id;
-        };
-        // copies of a tile into a stage; a page outside the cache is not read and counts as masked
-        auto page_ok = [&](int page) { return page >= 0 && page < p.pages; };
-        const uint32_t ring = smem_base + warp * (C::kStages * C::kTile);
-        auto issue = [&](int tok, int page, int off, int stage) {
-            if (tok < base_end) {
-                if (page_ok(page)) {
-                    // row of the tile's first token: (page * heads + h) * page_size + off
-                    const unsigned long long row = (unsigned long long)static_cast<uint32_t>(page) * page_rows + (head_row + off);
-                    const uint32_t dst = ring + stage * C::kTile;
-#pragma unroll
-                    for (int i = 0; i < B / 2; ++i) {
-                        const int x = lane + 32 * i, t = x / B, at = t * (16 * B) + 16 * ((x % B) ^ swizzle<B>(t));
-                        cp_async_16(dst + at, p.kc + row * (16 * B) + 16 * x);
-                        cp_async_16(dst + C::kTileV + at, p.vc + row * (16 * B) + 16 * x);
-                    }
-                    if (lane < 2 * B)
-                        cp_async_16(dst + C::kTileKs + 16 * lane, (lane < B ? p.ks + 16 * lane : p.vs + 16 * (lane - B)) + row * B);
-                } else if (lane == 0) {
-                    fg::kv_record(p.status, fg::kKvErrAttention);
-                }
-            }
-            cp_async_commit();
-        };
-
-        auto compute = [&](uint32_t at, int tok0, bool ok) {
-            const int tau = token_of<B>(g);
+        auto compute = [&](int stage, int tok0, bool ok) {
+            const uint32_t at = stage * C::kTile;
             uint32_t ks0[(B + 3) / 4], ks1[(B + 3) / 4], vs0[(B + 3) / 4], vs1[(B + 3) / 4];
-            load_scales<B>(ks0, at + C::kTileKs + tau * B);
-            load_scales<B>(ks1, at + C::kTileKs + (tau + 8) * B);
-            load_scales<B>(vs0, at + C::kTileVs + tau * B);
-            load_scales<B>(vs1, at + C::kTileVs + (tau + 8) * B);
+            load_scales<B>(ks0, at_sf + at);
+            load_scales<B>(ks1, at_sf + at + 8 * B);
+            load_scales<B>(vs0, at_sf + at + 16 * B);
+            load_scales<B>(vs1, at_sf + at + 24 * B);
             uint32_t k0[B], k1[B];
-            load_key<B>(k0, at + tau * (16 * B), swizzle<B>(tau), c);
-            load_key<B>(k1, at + (tau + 8) * (16 * B), swizzle<B>(tau + 8), c);
+            load_key<B>(k0, at_k + at, swizzle<B>(tau), c);
+            load_key<B>(k1, at_k + at + 128 * B, swizzle<B>(tau), c);
             float s[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
@@ -571,9 +589,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t v0[B / 2], v1[B / 2];
-                const int t0 = token_of<B>(2 * c) + 8 * i, t1 = token_of<B>(2 * c + 1) + 8 * i;
-                load_value<B>(v0, at + C::kTileV + t0 * (16 * B), swizzle<B>(t0), g);
-                load_value<B>(v1, at + C::kTileV + t1 * (16 * B), swizzle<B>(t1), g);
+                load_value<B>(v0, at_v0 + at + 128 * B * i, swizzle<B>(tau0), g);
+                load_value<B>(v1, at_v1 + at + 128 * B * i, swizzle<B>(tau1), g);
 #pragma unroll
                 for (int j = 0; j < B / 2; ++j) {
                     even[i][j] = (v0[j] & 0x0F0F0F0Fu) | (v1[j] * 16u & 0xF0F0F0F0u);
@@ -601,32 +618,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
         };
 
-        if (base < base_end) {
-            uint32_t ok = 0;                                // bit i: the page of the tile i ahead is in the cache
+        while (base < base_end) {
 #pragma unroll
-            for (int i = 0; i < C::kStages - 1; ++i) {
-                const int off = look_off, page = next_page();
-                ok |= static_cast<uint32_t>(page_ok(page)) << i;
-                issue(base + i * kBlock, page, off, i);
-            }
-            int off = look_off, page = next_page();
-            int stage = 0;
-            while (true) {
-                issue(base + (C::kStages - 1) * kBlock, page, off, stage == 0 ? C::kStages - 1 : stage - 1);
-                ok |= static_cast<uint32_t>(page_ok(page)) << (C::kStages - 1);
-                off = look_off;
-                page = next_page();
-                cp_async_wait<C::kStages - 1>();
+            for (int i = 0; i < C::kStages; ++i) {          // stages at fixed places
+                constexpr int kAhead = C::kStages - 1;
+                constexpr uint32_t kBits = (1u << C::kStages) - 1;
+                const int next = (i + kAhead) % C::kStages;
+                const bool ok = issue(page, off, next, base + kAhead * kBlock < base_end);
+                absent = (absent & (kBits ^ 1u << next)) | (ok ? 0u : 1u << next);
+                next_page(base + C::kStages * kBlock, page, off);
+                cp_async_wait<kAhead>();
                 __syncwarp();
-                compute(ring + stage * C::kTile, base, ok & 1u);
+                compute(i, base, !(absent >> i & 1u));
                 __syncwarp();                               // every lane has read the stage that is filled next
-                ok >>= 1;
                 base += kBlock;
                 if (base >= base_end) break;
-                if (++stage == C::kStages) stage = 0;
             }
-            cp_async_wait<0>();
         }
+        cp_async_wait<0>();
         __syncthreads();                                    // the rings are empty: their place takes the join
 
         // ---------------------------------------------------------- join the warps
@@ -699,16 +708,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                     const int j = it / (D / 4), d4 = it % (D / 4);
                     float top = kEmpty, sum = 0.0f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = a; k <= z; ++k) {
-                        const float* s = p.part + (long long)(2 * k + (k == a ? 1 : 0)) * C::kSlot;
-                        const float mk = __ldcg(s + j), lk = __ldcg(s + kRows + j);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
-                        const float t = fmaxf(top, mk);
-                        const float f = ex2(top - t), e = ex2(mk - t);
+                    constexpr int kFlight = 8;              // pieces in flight together
+                    for (int k0 = a; k0 <= z; k0 += kFlight) {
+                        float mk[kFlight], lk[kFlight], t = top;
+                        float4 v[kFlight];
+#pragma unroll
+                        for (int i = 0; i < kFlight; ++i) {
+                            const int k = min(k0 + i, z);
+                            const float* s = p.part + (long long)(2 * k + (k == a ? 1 : 0)) * C::kSlot;
+                            mk[i] = __ldcg(s + j);
+                            lk[i] = __ldcg(s + kRows + j);
+                            v[i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kFlight; ++i) t = fmaxf(t, mk[i]);
+                        const float f = ex2(top - t);
                         top = t;
-                        sum = sum * f + lk * e;
-                        acc.x = acc.x * f + v.x * e; acc.y = acc.y * f + v.y * e;
-                        acc.z = acc.z * f + v.z * e; acc.w = acc.w * f + v.w * e;
+                        sum *= f;
+                        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+                        for (int i = 0; i < kFlight; ++i) {
+                            const float e = k0 + i <= z ? ex2(mk[i] - t) : 0.0f;
+                            sum = fmaf(lk[i], e, sum);
+                            acc.x = fmaf(v[i].x, e, acc.x); acc.y = fmaf(v[i].y, e, acc.y);
+                            acc.z = fmaf(v[i].z, e, acc.z); acc.w = fmaf(v[i].w, e, acc.w);
+                        }
                     }
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     store_row(j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
@@ -716,12 +740,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
         }
 
-        u = iu1 + off1;
-        if (u >= s_line[2]) break;
+        iu0 = iu1 + cost;
+        if (iu1 + off1 >= s_line[2]) break;
+        off0 = 0;
         __syncthreads();                                    // s_join is written again
         if (++h == p.heads) {
             h = 0;
-            item0 += (unsigned long long)cost * p.heads;
             ++ch;
             while (s_pre[r + 1] <= ch) ++r;
             rq = request(p, r);
