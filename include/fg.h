@@ -513,6 +513,17 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
                              const int32_t* seq_lens, float scale, int window, void* out, void* workspace,
                              fg_stream_t stream);
 
+/*
+ * The calls of a serving step with their arguments in one record, for bindings that pay by the argument: word i of
+ * `words` (64 bits, host memory, read before the call returns) is argument i of the named entry point; integers
+ * sign-extended, pointers and streams as they are, float arguments as the bits of a double.
+ */
+typedef enum {
+    FG_CALL_BUILD_BLOCK_TABLES = 0, FG_CALL_QK_NORM_ROPE = 1, FG_CALL_KV_APPEND_MXFP4 = 2, FG_CALL_KV_GATHER_MXFP4 = 3,
+    FG_CALL_PAGED_ATTENTION_MXFP4 = 4
+} fg_call_id;
+int fg_call(int id, const void* words);
+
 /* Row alignment of each group segment in the contiguous layout: 128, the M block
  * (docsearch section 9 item 2 and section 10). */
 int fg_get_mk_alignment_for_contiguous_layout(void);

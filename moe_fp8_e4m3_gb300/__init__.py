@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfg.so")
@@ -63,6 +64,7 @@ _SIGNATURES = {
     "fg_kv_gather_mxfp4": (_I, [_I] * 5 + [_P] * 5 + [_P, _L, _P, _L, _P]),
     "fg_paged_attention_workspace": (_L, [_I] * 5),
     "fg_paged_attention_mxfp4": (_I, [_I] * 8 + [_P] * 8 + [ctypes.c_float, _I, _P, _P, _P]),
+    "fg_call": (_I, [_I, ctypes.c_char_p]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_get_tma_aligned_size": (_I, [_I, _I]),
     "fg_set_num_sms": (None, [_I]),
@@ -128,11 +130,17 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_RAW_STREAM = None
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
+        global _RAW_STREAM, _DEVICE
+        if _RAW_STREAM is None:
+            import torch
+            _RAW_STREAM, _DEVICE = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         # the handle of torch.cuda.current_stream(), without making a Stream object (2.8 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _RAW_STREAM(_DEVICE())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -396,6 +404,7 @@ def quantize_1x128_cols(x, q, sf, stream=None) -> None:
 
 _SCORES = {"softmax": FG_SCORE_SOFTMAX, "sigmoid": FG_SCORE_SIGMOID}
 _DTYPES = {}
+_U8 = _BF = _I32 = _F32 = None
 
 
 def _dtypes():
@@ -403,7 +412,15 @@ def _dtypes():
     import torch
     _DTYPES.update(u={torch.uint8}, q={torch.uint8, torch.float8_e4m3fn}, i={torch.int32}, f={torch.float32}, b={torch.bfloat16},
                    p={torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)}, o={torch.bfloat16, torch.float32})
+    global _U8, _BF, _I32, _F32
+    _U8, _BF, _I32, _F32 = torch.uint8, torch.bfloat16, torch.int32, torch.float32
     return _DTYPES
+
+
+def _int32():
+    """torch.int32; looks the dtypes up at a program's first call."""
+    _dtypes()
+    return _I32
 
 
 _NAMES = {"u": "uint8", "q": "uint8/float8_e4m3fn", "i": "int32", "f": "float32", "b": "bfloat16", "p": "uint8/float4_e2m1fn_x2 (packed E2M1)",
@@ -556,6 +573,16 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
         _check(st, "fp8_gemm_nt_lora")
 
 
+# The calls of a serving step are short on the GPU, so their arguments go in one record: ctypes takes 0.09 us an
+# argument, of which there are about twenty (measured on a GB300's host: 1.73 us against 0.65 us packed).
+_TABLES_ARGS = struct.Struct("=17q")
+_ROPE_ARGS = struct.Struct("=12qd8q")
+_APPEND_ARGS = struct.Struct("=15q")
+_ATTENTION_ARGS = struct.Struct("=16qd4q")
+_CALL_TABLES, _CALL_ROPE, _CALL_APPEND, _CALL_GATHER, _CALL_ATTENTION = range(5)
+_call = lib.fg_call
+
+
 def build_block_tables(context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots, positions,
                        free_count_out, page_size, num_pages, stream=None) -> None:
     """Block tables, slots and positions of a step from the requests' lengths (all int32).
@@ -563,27 +590,37 @@ def build_block_tables(context_lens, new_lens, free_pages, free_count, block_tab
     free_count [1] of them free; block_table [S, max_pages] (extended in place); out: query_start
     [S + 1], seq_lens [S] (may be context_lens), slots and positions [T], free_count_out [1] (may be
     free_count)."""
-    _check_all(context_lens, "context_lens", "i", new_lens, "new_lens", "i", free_pages, "free_pages", "i", free_count,
-               "free_count", "i", block_table, "block_table", "i", query_start, "query_start", "i", seq_lens, "seq_lens", "i",
-               slots, "slots", "i", positions, "positions", "i", free_count_out, "free_count_out", "i")
+    i32 = _I32 or _int32()
+    for x in (context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots, positions, free_count_out):
+        if x.dtype is not i32 or not x.is_cuda or not x.is_contiguous():
+            _check_all(context_lens, "context_lens", "i", new_lens, "new_lens", "i", free_pages, "free_pages", "i", free_count,
+                       "free_count", "i", block_table, "block_table", "i", query_start, "query_start", "i", seq_lens, "seq_lens",
+                       "i", slots, "slots", "i", positions, "positions", "i", free_count_out, "free_count_out", "i")
     s, width = block_table.shape
     t = slots.numel()
     if (context_lens.numel() != s or new_lens.numel() != s or seq_lens.numel() != s or query_start.numel() != s + 1 or
             positions.numel() != t or free_count.numel() != 1 or free_count_out.numel() != 1):
         raise ValueError("shapes: context_lens, new_lens, seq_lens [S], block_table [S, max_pages], query_start [S + 1], "
                          "slots and positions [T], free_count and free_count_out [1]")
-    _check(lib.fg_build_block_tables(s, t, page_size, num_pages, width, free_pages.numel(), context_lens.data_ptr(),
-                                     new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(),
-                                     query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-                                     free_count_out.data_ptr(), _stream(stream)), "build_block_tables")
+    st = _call(_CALL_TABLES, _TABLES_ARGS.pack(
+        s, t, page_size, num_pages, width, free_pages.numel(), context_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+        free_count.data_ptr(), block_table.data_ptr(), query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), free_count_out.data_ptr(), _stream(stream)))
+    if st != FG_OK:
+        _check(st, "build_block_tables")
 
 
-def _rows(t, name):
-    """Elements between tokens of a BF16 [T, heads, D] tensor whose heads are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype not in _DTYPES["b"] or not t.is_cuda or len(shape) != 3 or stride[2] != 1 or stride[1] != shape[2]:
-        raise TypeError(f"{name} must be a CUDA bfloat16 tensor [T, heads, D] with contiguous heads")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+def _rows(x, name):
+    """(shape, elements between tokens) of a BF16 [T, heads, D] tensor whose heads are contiguous."""
+    shape = x.shape
+    if x.dtype is _BF and x.is_cuda and len(shape) == 3:
+        t, h, d = shape
+        if x.is_contiguous():
+            return shape, h * d
+        first, second, third = x.stride()
+        if (third == 1 or d == 1) and (second == d or h == 1):
+            return shape, first if t > 1 else h * d
+    raise TypeError(f"{name} must be a CUDA bfloat16 tensor [T, heads, D] with contiguous heads")
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -592,22 +629,37 @@ def qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight
     pass.  q, q_out [T,Hq,D], k, k_out [T,Hkv,D] BF16 (tokens may be any multiple of 8 elements apart;
     outputs may be the inputs); positions int32 [T]; cos_sin float32 [max_pos, rot]: rot / 2 cosines,
     then rot / 2 sines; weights BF16 [D]; interleaved: pairs are neighbours, else halves."""
-    _DTYPES or _dtypes()
-    strides = [_rows(x, n) for x, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
-    _check_all(positions, "positions", "i", cos_sin, "cos_sin", "f")
-    t, hq, d = q.shape
-    hkv = k.shape[1]
+    i32 = _I32 or _int32()
+    q_shape, qs = _rows(q, "q")
+    k_shape, ks = _rows(k, "k")
+    qo_shape, qos = (q_shape, qs) if q_out is q else _rows(q_out, "q_out")
+    ko_shape, kos = (k_shape, ks) if k_out is k else _rows(k_out, "k_out")
+    if (positions.dtype is not i32 or not positions.is_cuda or not positions.is_contiguous() or cos_sin.dtype is not _F32 or
+            not cos_sin.is_cuda or not cos_sin.is_contiguous()):
+        _check_all(positions, "positions", "i", cos_sin, "cos_sin", "f")
+    t, hq, d = q_shape
+    tk, hkv, dk = k_shape
     max_pos, rot = cos_sin.shape
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _check_all(w, name, "b")
-            if w.numel() != d:
-                raise ValueError(f"{name} must be [D]")
-    if k.shape != (t, hkv, d) or q_out.shape != q.shape or k_out.shape != k.shape or positions.numel() != t:
+    qw = kw = 0
+    if q_weight is not None:
+        if q_weight.dtype is not _BF or not q_weight.is_cuda or not q_weight.is_contiguous():
+            _check_all(q_weight, "q_weight", "b")
+        if q_weight.numel() != d:
+            raise ValueError("q_weight must be [D]")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not _BF or not k_weight.is_cuda or not k_weight.is_contiguous():
+            _check_all(k_weight, "k_weight", "b")
+        if k_weight.numel() != d:
+            raise ValueError("k_weight must be [D]")
+        kw = k_weight.data_ptr()
+    if tk != t or dk != d or qo_shape != q_shape or ko_shape != k_shape or positions.numel() != t:
         raise ValueError("shapes: q and q_out [T,Hq,D], k and k_out [T,Hkv,D], positions [T], cos_sin [max_pos, rot]")
-    _check(lib.fg_qk_norm_rope(t, hq, hkv, d, rot, max_pos, q.data_ptr(), strides[0], k.data_ptr(), strides[1], _ptr(q_weight),
-                               _ptr(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), 1 if interleaved else 0,
-                               q_out.data_ptr(), strides[2], k_out.data_ptr(), strides[3], _stream(stream)), "qk_norm_rope")
+    st = _call(_CALL_ROPE, _ROPE_ARGS.pack(
+        t, hq, hkv, d, rot, max_pos, q.data_ptr(), qs, k.data_ptr(), ks, qw, kw, eps, positions.data_ptr(), cos_sin.data_ptr(),
+        1 if interleaved else 0, q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream)))
+    if st != FG_OK:
+        _check(st, "qk_norm_rope")
 
 
 def kv_cache_mxfp4(num_pages, heads, page_size, d, device="cuda"):
@@ -619,53 +671,57 @@ def kv_cache_mxfp4(num_pages, heads, page_size, d, device="cuda"):
 
 def _cache(k_cache, k_sf, v_cache, v_sf):
     """(num_pages, heads, page_size, D) of a cache."""
-    u8 = _DTYPES["u"]
-    if not (k_cache.dtype in u8 and k_sf.dtype in u8 and v_cache.dtype in u8 and v_sf.dtype in u8 and k_cache.is_cuda and
+    u8 = _U8
+    if not (k_cache.dtype is u8 and k_sf.dtype is u8 and v_cache.dtype is u8 and v_sf.dtype is u8 and k_cache.is_cuda and
             k_sf.is_cuda and v_cache.is_cuda and v_sf.is_cuda and k_cache.is_contiguous() and k_sf.is_contiguous() and
             v_cache.is_contiguous() and v_sf.is_contiguous()):
         _check_all(k_cache, "k_cache", "u", k_sf, "k_sf", "u", v_cache, "v_cache", "u", v_sf, "v_sf", "u")
-    pages, heads, size, half = k_cache.shape
-    sf = (pages, heads, size, half // 16)
-    if half % 16 or v_cache.shape != k_cache.shape or k_sf.shape != sf or v_sf.shape != sf:
+    shape, sf = k_cache.shape, k_sf.shape
+    pages, heads, size, half = shape
+    if half % 16 or v_cache.shape != shape or v_sf.shape != sf or sf != (pages, heads, size, half // 16):
         raise ValueError("cache: codes [num_pages, heads, page_size, D/2], scales [num_pages, heads, page_size, D/32]")
     return pages, heads, size, 2 * half
-
-
-def _kv_args(k, v, slots, cache, name):
-    _DTYPES or _dtypes()
-    pages, heads, size, d = _cache(*cache)
-    strides = _rows(k, "k"), _rows(v, "v")
-    _check_all(slots, "slots", "i")
-    t = slots.numel()
-    if k.shape != (t, heads, d) or v.shape != k.shape:
-        raise ValueError(f"{name}: k and v must be [T, heads, D] and slots [T]")
-    return (t, heads, d, size, pages), strides
 
 
 def kv_append_mxfp4(k, v, slots, k_cache, k_sf, v_cache, v_sf, stream=None) -> None:
     """Keys and values [T, heads, D] BF16 into the 4-bit cache, at slots int32 [T] (negative: skipped).
     Tokens of k and v may be any multiple of 8 elements apart."""
-    sizes, (ks, vs) = _kv_args(k, v, slots, (k_cache, k_sf, v_cache, v_sf), "kv_append_mxfp4")
-    _check(lib.fg_kv_append_mxfp4(*sizes, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), k_cache.data_ptr(),
-                                  k_sf.data_ptr(), v_cache.data_ptr(), v_sf.data_ptr(), _stream(stream)), "kv_append_mxfp4")
+    _move(_CALL_APPEND, "kv_append_mxfp4", k, v, slots, k_cache, k_sf, v_cache, v_sf, stream)
 
 
 def kv_gather_mxfp4(slots, k_cache, k_sf, v_cache, v_sf, k, v, stream=None) -> None:
     """Keys and values at slots int32 [T] out of the 4-bit cache, as BF16 [T, heads, D] (a negative
     slot leaves its row as it was)."""
-    sizes, (ks, vs) = _kv_args(k, v, slots, (k_cache, k_sf, v_cache, v_sf), "kv_gather_mxfp4")
-    _check(lib.fg_kv_gather_mxfp4(*sizes, slots.data_ptr(), k_cache.data_ptr(), k_sf.data_ptr(), v_cache.data_ptr(),
-                                  v_sf.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "kv_gather_mxfp4")
+    _move(_CALL_GATHER, "kv_gather_mxfp4", k, v, slots, k_cache, k_sf, v_cache, v_sf, stream)
 
 
-@functools.lru_cache(1024)
-def _attention_bytes(t, s, hq, hkv, d):
-    return lib.fg_paged_attention_workspace(t, s, hq, hkv, d)
+def _move(call, name, k, v, slots, k_cache, k_sf, v_cache, v_sf, stream):
+    i32 = _I32 or _int32()
+    pages, heads, size, d = _cache(k_cache, k_sf, v_cache, v_sf)
+    shape, ks = _rows(k, "k")
+    v_shape, vs = _rows(v, "v")
+    if slots.dtype is not i32 or not slots.is_cuda or not slots.is_contiguous():
+        _check_all(slots, "slots", "i")
+    t = slots.numel()
+    if shape != (t, heads, d) or v_shape != shape:
+        raise ValueError(f"{name}: k and v must be [T, heads, D] and slots [T]")
+    if call == _CALL_APPEND:
+        args = _APPEND_ARGS.pack(t, heads, d, size, pages, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), k_cache.data_ptr(),
+                                 k_sf.data_ptr(), v_cache.data_ptr(), v_sf.data_ptr(), _stream(stream))
+    else:
+        args = _APPEND_ARGS.pack(t, heads, d, size, pages, slots.data_ptr(), k_cache.data_ptr(), k_sf.data_ptr(), v_cache.data_ptr(),
+                                 v_sf.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream))
+    st = _call(call, args)
+    if st != FG_OK:
+        _check(st, name)
 
 
 def paged_attention_workspace(t, s, hq, hkv, d, device="cuda"):
-    """Zeroed workspace of paged_attention_mxfp4 for t tokens of s requests; reusable, one per concurrent call."""
-    return _workspace(_attention_bytes(t, s, hq, hkv, d), device, "paged_attention_workspace")
+    """Zeroed workspace of paged_attention_mxfp4 (of one size for all of them); reusable, one per concurrent call."""
+    return _workspace(lib.fg_paged_attention_workspace(t, s, hq, hkv, d), device, "paged_attention_workspace")
+
+
+_ATTENTION_BYTES = lib.fg_paged_attention_workspace(1, 1, 1, 1, 128)
 
 
 def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens, out, workspace, scale=None,
@@ -674,11 +730,11 @@ def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_st
     block_table int32 [S, max_pages]; query_start int32 [S + 1]: first row of each request; seq_lens
     int32 [S]: cached tokens of each, the new ones included; scale: D^-0.5 if not given; window > 0: only
     the last `window` tokens up to each row's own.  workspace from paged_attention_workspace."""
-    kinds = _DTYPES or _dtypes()
+    i32 = _I32 or _int32()
+    bf = _BF
     pages, hkv, size, d = _cache(k_cache, k_sf, v_cache, v_sf)
-    bf, i32 = kinds["b"], kinds["i"]
-    if not (q.dtype in bf and out.dtype in bf and block_table.dtype in i32 and query_start.dtype in i32 and
-            seq_lens.dtype in i32 and q.is_cuda and out.is_cuda and block_table.is_cuda and query_start.is_cuda and
+    if not (q.dtype is bf and out.dtype is bf and block_table.dtype is i32 and query_start.dtype is i32 and
+            seq_lens.dtype is i32 and q.is_cuda and out.is_cuda and block_table.is_cuda and query_start.is_cuda and
             seq_lens.is_cuda and q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous() and
             query_start.is_contiguous() and seq_lens.is_contiguous()):
         _check_all(q, "q", "b", out, "out", "b", block_table, "block_table", "i", query_start, "query_start", "i", seq_lens,
@@ -688,13 +744,12 @@ def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_st
     s, width = block_table.shape
     if dq != d or out.shape != shape or query_start.numel() != s + 1 or seq_lens.numel() != s:
         raise ValueError("shapes: q and out [T,Hq,D], block_table [S, max_pages], query_start [S + 1], seq_lens [S]")
-    need = _attention_bytes(t, s, hq, hkv, d)
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < need:
+    if workspace.nbytes < _ATTENTION_BYTES or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor of at least paged_attention_workspace(t, s, hq, hkv, d) bytes")
-    st = lib.fg_paged_attention_mxfp4(t, s, hq, hkv, d, size, pages, width, q.data_ptr(), k_cache.data_ptr(), k_sf.data_ptr(),
-                                      v_cache.data_ptr(), v_sf.data_ptr(), block_table.data_ptr(), query_start.data_ptr(),
-                                      seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                                      workspace.data_ptr(), _stream(stream))
+    st = _call(_CALL_ATTENTION, _ATTENTION_ARGS.pack(
+        t, s, hq, hkv, d, size, pages, width, q.data_ptr(), k_cache.data_ptr(), k_sf.data_ptr(), v_cache.data_ptr(), v_sf.data_ptr(),
+        block_table.data_ptr(), query_start.data_ptr(), seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), workspace.data_ptr(), _stream(stream)))
     if st != FG_OK:
         _check(st, "paged_attention_mxfp4")
 

@@ -77,6 +77,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same without a sum before it.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Byte i (two codes) of w as an FP16 pair.
 __device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t w, int i) {
     uint32_t r;
@@ -495,8 +502,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             load_key<B>(k0, at_k + at, swizzle<B>(tau), c);
             load_key<B>(k1, at_k + at + 128 * B, swizzle<B>(tau), c);
             float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
             float f0[B], f1[B];
             scales_of<B>(f0, ks0);
             scales_of<B>(f1, ks1);
@@ -508,16 +513,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                 const float s0 = f0[b], s1 = f1[b];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float x[4];
                     uint4 f;
                     if constexpr (C::kQShared) f = s_q[(nt * B + b) * 32 + lane];
                     else f = make_uint4(qf[b][0], qf[b][1], qf[b][2], qf[b][3]);
-                    mma_f16(x, a[0], e[0], a[1], e[1], f.x, f.y);
+                    mma_f16_new(x, a[0], e[0], a[1], e[1], f.x, f.y);
                     mma_f16(x, a[2], e[2], a[3], e[3], f.z, f.w);
-                    s[nt][0] = fmaf(x[0], s0, s[nt][0]);
-                    s[nt][1] = fmaf(x[1], s0, s[nt][1]);
-                    s[nt][2] = fmaf(x[2], s1, s[nt][2]);
-                    s[nt][3] = fmaf(x[3], s1, s[nt][3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[nt][i] = b == 0 ? x[i] * (i < 2 ? s0 : s1) : fmaf(x[i], i < 2 ? s0 : s1, s[nt][i]);
                 }
             }
             if (!ok || tok0 < all_lo || tok0 + 16 > all_hi) {                  // a border: mask

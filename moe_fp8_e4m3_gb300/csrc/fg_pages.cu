@@ -57,7 +57,7 @@ template <bool kClustered>
 __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
     extern __shared__ int sm[];
     int* s_start = sm;                        // [S] tokens before a request
-    int* s_more = sm + p.S;                   // [S] pages taken before it
+    int* s_more = sm + p.S;                   // [S] pages given back before it, then pages taken before it
     int* s_context = sm + 2 * p.S;            // [S]
     __shared__ Sums s_warp[32];
     __shared__ int s_bad;
@@ -117,6 +117,23 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
           total.more > count + total.back;
     Sums at = warp ? s_warp[warp - 1] + incl : incl;        // inclusive
     at = Sums{at.tokens - mine.tokens, at.back - mine.back, at.more - mine.more};
+    const Sums before = at;
+    const int step = ctas * kThreads, first = rank * kThreads + tid;
+    if (!bad && total.back > 0) {                           // the same for all: finished requests' pages, dealt by the page
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = tid * kPer + i;
+            if (r < p.S) s_more[r] = at.back;
+            at = at + each[i];
+        }
+        __syncthreads();
+        for (int i = first; i < total.back; i += step) {
+            const int r = find(s_more, p.S, i);
+            p.free[count + i] = p.table[(long long)r * p.max_pages + i - s_more[r]];
+        }
+        __syncthreads();
+        at = before;
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int r = tid * kPer + i;
@@ -124,15 +141,6 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
             s_start[r] = at.tokens;
             s_more[r] = at.more;
             s_context[r] = context[i];
-        }
-        // pages of the warp's finished requests, one after another, on top of the free ones
-        uint32_t todo = __ballot_sync(0xffffffffu, !bad && each[i].back > 0 && r % ctas == rank);
-        while (todo) {
-            const int from = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int n = __shfl_sync(0xffffffffu, each[i].back, from), to = count + __shfl_sync(0xffffffffu, at.back, from);
-            const int32_t* row = p.table + (long long)__shfl_sync(0xffffffffu, r, from) * p.max_pages;
-            for (int j = lane; j < n; j += 32) p.free[to + j] = row[j];
         }
         at = at + each[i];
     }
@@ -158,7 +166,6 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
             if (bad) fg::kv_record(p.status, fg::kKvErrPages);
         }
     }
-    const int step = ctas * kThreads, first = rank * kThreads + tid;
     if (!bad) {
         for (int i = first; i < total.more; i += step) {    // new pages into the table
             const int r = find(s_more, p.S, i);

@@ -79,6 +79,30 @@ def test_attention_argument_errors(fg, kw, want):
     assert attention(fg, **kw) == want
 
 
+def test_calls_with_their_arguments_in_one_record(fg):
+    """A record reaches the entry point that it names, word by word: each bad argument is the one that is found."""
+    call, n = fg.lib.fg_call, FAKE
+    assert call(-1, b"") == -1 and call(5, bytes(200)) == -1 and call(0, None) == -1
+    tables_ok = [4, 8, 16, 10, 5, 10] + [n] * 10 + [0]
+    rope_ok = [4, 4, 2, 128, 64, 100, n, 512, n, 256, n, n, 1e-6, n, n, 0, n, 512, n, 256, 0]
+    append_ok = [4, 2, 128, 16, 10, n, 256, n, 256] + [n] * 5 + [0]
+    gather_ok = [4, 2, 128, 16, 10] + [n] * 6 + [256, n, 256, 0]
+    attention_ok = [4, 2, 8, 2, 128, 16, 10, 5] + [n] * 8 + [0.1, 0, n, n, 0]
+    bad = {"int": -1, "ptr": n + 2, "stride": 17, "float": NAN}
+    for i, (args, form, kinds) in enumerate([
+            (tables_ok, fg._TABLES_ARGS, "iiiiii" + "p" * 10), (rope_ok, fg._ROPE_ARGS, "iiiiiipspsppfpp.psps"),
+            (append_ok, fg._APPEND_ARGS, "iiiiipspsppppp"), (gather_ok, fg._APPEND_ARGS, "iiiiippppppsps"),
+            (attention_ok, fg._ATTENTION_ARGS, "iiiiiiii" + "p" * 8 + "fipp")]):
+        assert call(i, form.pack(*args)) in (fg.FG_OK, fg.FG_ERR_CUDA) if not torch.cuda.is_available() else True
+        for j, kind in enumerate(kinds):
+            if kind == ".":
+                continue
+            wrong = bad[{"i": "int", "p": "ptr", "s": "stride", "f": "float"}[kind]]
+            assert call(i, form.pack(*args[:j], wrong, *args[j + 1:])) == -1, (i, j)
+    # sizes past 32 bits are refused, not cut
+    assert call(4, fg._ATTENTION_ARGS.pack(*([2 ** 32 + 4] + attention_ok[1:]))) == -1
+
+
 def test_workspace_sizes(fg):
     size = fg.lib.fg_paged_attention_workspace
     assert size(4, 2, 7, 2, 128) == -1 and size(-1, 2, 8, 2, 128) == -1 and size(4, 2, 8, 2, 96) == -1
@@ -119,8 +143,7 @@ def stub(fg, monkeypatch):
         fg.calls += 1
         return fg.FG_OK
 
-    for name in ("fg_build_block_tables", "fg_qk_norm_rope", "fg_kv_append_mxfp4", "fg_kv_gather_mxfp4", "fg_paged_attention_mxfp4"):
-        monkeypatch.setattr(fg.lib, name, call)
+    monkeypatch.setattr(fg, "_call", call)
     return fg
 
 
