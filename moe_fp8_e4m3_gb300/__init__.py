@@ -716,12 +716,14 @@ def _move(call, name, k, v, slots, k_cache, k_sf, v_cache, v_sf, stream):
         _check(st, name)
 
 
+@functools.lru_cache(1024)
+def _attention_bytes(t, s, hq, hkv, d):
+    return lib.fg_paged_attention_workspace(t, s, hq, hkv, d)
+
+
 def paged_attention_workspace(t, s, hq, hkv, d, device="cuda"):
-    """Zeroed workspace of paged_attention_mxfp4 (of one size for all of them); reusable, one per concurrent call."""
-    return _workspace(lib.fg_paged_attention_workspace(t, s, hq, hkv, d), device, "paged_attention_workspace")
-
-
-_ATTENTION_BYTES = lib.fg_paged_attention_workspace(1, 1, 1, 1, 128)
+    """Zeroed workspace of paged_attention_mxfp4 for t tokens of s requests; reusable, one per concurrent call."""
+    return _workspace(_attention_bytes(t, s, hq, hkv, d), device, "paged_attention_workspace")
 
 
 def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens, out, workspace, scale=None,
@@ -744,7 +746,7 @@ def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_st
     s, width = block_table.shape
     if dq != d or out.shape != shape or query_start.numel() != s + 1 or seq_lens.numel() != s:
         raise ValueError("shapes: q and out [T,Hq,D], block_table [S, max_pages], query_start [S + 1], seq_lens [S]")
-    if workspace.nbytes < _ATTENTION_BYTES or not workspace.is_cuda or not workspace.is_contiguous():
+    if workspace.nbytes < _attention_bytes(t, s, hq, hkv, d) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor of at least paged_attention_workspace(t, s, hq, hkv, d) bytes")
     st = _call(_CALL_ATTENTION, _ATTENTION_ARGS.pack(
         t, s, hq, hkv, d, size, pages, width, q.data_ptr(), k_cache.data_ptr(), k_sf.data_ptr(), v_cache.data_ptr(), v_sf.data_ptr(),

@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libfg.so")
 SOURCES = ["fg_api.cu", "fg_gemm_nt.cu", "fg_gemm_split.cu", "fg_gemm_tn.cu", "fg_gemm_layouts.cu",
            "fg_gemm_sepc.cu", "fg_gemm_dense.cu", "fg_gemm_swiglu.cu", "fg_gemm_fp4.cu", "fg_gemm_fp4_grouped.cu",
            "fg_mqa.cu", "fg_quant.cu", "fg_moe.cu", "fg_lora.cu", "fg_route.cu",
-           "fg_pages.cu", "fg_rope.cu", "fg_kv.cu", "fg_attn.cu", "fg_call.cu"]
+           "fg_pages.cu", "fg_rope.cu", "fg_kv.cu", "fg_attn.cu", "fg_attn_prompt.cu", "fg_call.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -20,40 +20,26 @@
 // Codes and scales come through a ring of kStages tiles of 16 tokens that each warp has to itself (asynchronous
 // 16-byte copies, no barrier of the CTA); the cache's order puts what a lane needs of a row into one load,
 // and sixteen tokens never cross a page.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdio>
 
 #include "fg.h"
 #include "fg_host.h"
-#include "fg_kv.cuh"
+#include "fg_attn.cuh"
 
 namespace {
 
 using fg::al;
+using fg::AttnParams;
+using fg::ex2;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 16 * kWarps;           // tokens of a block
-constexpr int kStart = 3;                     // an item's start, in blocks
-constexpr int kMaxCtas = 640;                 // shares of a launch, at most
-constexpr int kMaxRequests = 4096;
-constexpr float kEmpty = -1e30f;              // M of a row without a key
+constexpr float kEmpty = fg::kAttnEmpty;
 constexpr float kBias = 8.0f, kMostW = 32768.0f;   // w: 2^8 where M has just moved, at most 2^15
-constexpr uint32_t kAll = 0xffffffffu;
-
-struct AttnParams {
-    const uint16_t* q;
-    const uint8_t *kc, *ks, *vc, *vs;
-    const int32_t *table, *start, *lens;
-    uint16_t* out;
-    int T, S, heads, group, page, pages, max_pages, window;
-    float scale_log2;                          // scale * log2(e)
-    unsigned* ctr;                             // [kMaxCtas]
-    float* part;                               // [2 * kMaxCtas][kRows][D + 2]: M, l, O
-    int* status;
-};
+constexpr uint32_t kAll = fg::kAllLanes;
 
 template <int B, int NT>
 struct Cfg {
@@ -68,7 +54,7 @@ struct Cfg {
     static constexpr bool kQShared = NT > 1;                             // q in shared memory: registers hold O
     static constexpr int kQ = kQShared ? NT * B * 32 * 16 : 0;
     static constexpr int kSmem = kMain + kQ;                             // then [S + 1] int
-    static constexpr int kSlot = kRows * (D + 2);
+    static constexpr int kSlot = fg::attn_slot<kRows, D>();
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -104,12 +90,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A tile's token that stands in row g (and, plus 8, in row g + 8) of the products, and the swizzle of a row's
 // 16-byte chunks: chosen so that the lanes which a shared-memory phase serves together, those of two (D = 64:
 // four) neighbouring g of a key row and those of four c of a value row, find their words in different banks.
@@ -196,51 +176,6 @@ __device__ __forceinline__ float top_exponent(const float (&f)[B]) {
     return static_cast<float>(max(e, fg::kKvMinExp));
 }
 
-// One request as the kernel sees it (n == 0: nothing to do, or its lengths are wrong).
-struct Req {
-    int n, len, t0;
-};
-__device__ __forceinline__ Req request(const AttnParams& p, int r) {
-    const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
-    const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
-    return ok ? Req{t1 - t0, len, t0} : Req{0, 0, 0};
-}
-// Keys [lo, hi) that some row of a chunk looks at; hi <= lo: none.
-struct Keys {
-    int lo, hi;
-};
-template <int kRows>
-__device__ __forceinline__ Keys keys_of(const AttnParams& p, const Req& q, int chunk) {
-    const int i0 = chunk * kRows / p.group, i1 = min(q.n - 1, (chunk * kRows + kRows - 1) / p.group);
-    const int hi = q.len - q.n + i1 + 1;
-    const int lo = p.window > 0 ? max(0, q.len - q.n + i0 + 1 - p.window) : 0;
-    return Keys{lo, hi};
-}
-// Cost of an item in blocks: kStart for what every item takes (its q, filling the pipeline, the join), then its
-// keys' blocks.
-__device__ __forceinline__ int cost_of(const Keys& k) { return kStart + (k.hi > k.lo ? (k.hi + kBlock - 1) / kBlock - k.lo / kBlock : 1); }
-
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp, unsigned long long& total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned long long incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    unsigned long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s_warp[w];
-        total += s_warp[w];
-    }
-    return before + incl - v;                  // exclusive
-}
-
 template <int B, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kernel(const AttnParams p) {
     using C = Cfg<B, NT>;
@@ -251,111 +186,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     int* s_pre = reinterpret_cast<int*>(smem + C::kSmem);                 // [S + 1] chunks before a request
     __shared__ float s_qs[kRows];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    __shared__ unsigned long long s_warp[kWarps], s_strip[kThreads + 1];
-    __shared__ volatile unsigned long long s_line[4];
-    __shared__ int s_last;
+    __shared__ fg::AttnPlanSmem<kThreads> s_plan;
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t smem_base = fg::smem_u32(smem);
     fg::grid_dependency_wait();
     if (tid == 0) fg::grid_launch_dependents();
 
-    // ---------------------------------------------------------------- shares
-    // Chunks per request, then blocks per chunk, each scanned in strips of consecutive entries.
-    const int per_r = (p.S + kThreads - 1) / kThreads;
-    {
-        unsigned long long sum = 0, total;
-        for (int i = 0; i < per_r; ++i) {
-            const int r = tid * per_r + i;
-            if (r >= p.S) break;
-            const Req q = request(p, r);
-            if (blockIdx.x == 0 && q.n == 0) {
-                const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
-                if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page) fg::kv_record(p.status, fg::kKvErrAttention);
-            }
-            sum += ((long long)q.n * p.group + kRows - 1) / kRows;
-        }
-        unsigned long long at = block_scan(sum, s_warp, total);
-        for (int i = 0; i < per_r; ++i) {
-            const int r = tid * per_r + i;
-            if (r >= p.S) break;
-            s_pre[r] = static_cast<int>(at);
-            at += ((long long)request(p, r).n * p.group + kRows - 1) / kRows;
-        }
-        if (tid == 0) s_pre[p.S] = static_cast<int>(total);
-    }
-    __syncthreads();
-    const int chunks = s_pre[p.S];
-    const int per_c = (chunks + kThreads - 1) / kThreads;
-    unsigned long long total_blocks;
-    {
-        unsigned long long sum = 0;
-        int r = 0;
-        if (tid * per_c < chunks) {                      // last request with s_pre[r] <= the strip's first chunk
-            int hi = p.S;
-            while (hi - r > 1) {
-                const int mid = (r + hi) >> 1;
-                if (s_pre[mid] <= tid * per_c) r = mid;
-                else hi = mid;
-            }
-        }
-        for (int i = 0; i < per_c; ++i) {
-            const int ch = tid * per_c + i;
-            if (ch >= chunks) break;
-            while (s_pre[r + 1] <= ch) ++r;
-            sum += cost_of(keys_of<kRows>(p, request(p, r), ch - s_pre[r]));
-        }
-        const unsigned long long at = block_scan(sum, s_warp, total_blocks);
-        s_strip[tid] = at;
-        if (tid == 0) s_strip[kThreads] = total_blocks;
-    }
-    __syncthreads();
-    const unsigned long long all = total_blocks * p.heads;
-    // a share is worth an item's start
-    const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kStart) / (kStart + 1));
-    const unsigned long long me = blockIdx.x;
-    if (me >= shares) return;
-    const unsigned long long u = all * me / shares;
-    const unsigned long long u_end = all * (me + 1) / shares;
-    auto cta_of = [&](unsigned long long x) {
-        return static_cast<int>(((x + 1) * s_line[0] - 1) / s_line[1]);
-    };
-    if (tid == 0) { s_line[0] = shares; s_line[1] = all; s_line[2] = u_end; }   // wanted between items only
-    __syncthreads();
-
-    // the chunk that holds u
-    int r = 0, ch;
-    unsigned long long item0;                            // first block of the current (chunk, head 0)
-    {
-        int lo = 0, hi = kThreads;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_strip[mid] * p.heads <= u) lo = mid;
-            else hi = mid;
-        }
-        ch = lo * per_c;
-        item0 = s_strip[lo] * p.heads;
-        int hr = p.S;
-        while (hr - r > 1) {
-            const int mid = (r + hr) >> 1;
-            if (s_pre[mid] <= ch) r = mid;
-            else hr = mid;
-        }
-    }
-    while (s_pre[r + 1] <= ch) ++r;
-    Req rq = request(p, r);
-    Keys keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-    int cost = cost_of(keys);
-    while (item0 + (unsigned long long)cost * p.heads <= u) {
-        item0 += (unsigned long long)cost * p.heads;
-        ++ch;
-        while (s_pre[r + 1] <= ch) ++r;
-        rq = request(p, r);
-        keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-        cost = cost_of(keys);
-    }
-    int h = static_cast<int>((u - item0) / cost);
-    unsigned long long iu0 = item0 + (unsigned long long)h * cost;   // where the item begins
-    int off0 = static_cast<int>(u - iu0);                            // and the share within it
+    fg::AttnCursor<kRows, kBlock, kThreads> cur;
+    if (!cur.open(p, s_plan, s_pre)) return;
 
     // what a lane copies of a tile (16-byte chunk `lane`, and every 32nd on) and where it finds its operands in one
     const uint32_t page_rows = static_cast<uint32_t>(p.heads) * p.page;
@@ -371,23 +209,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
 
     // ---------------------------------------------------------------- pieces of items
     while (true) {
-        const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), s_line[2] - iu0));
-        if (off1 <= kStart) break;                           // none of its blocks in this share, which ends here
-        if (tid == 0) s_line[3] = iu0;
-        const int chunk = ch - s_pre[r];
-        const int row0 = chunk * kRows, rows = min(kRows, rq.n * p.group - row0);
-        const int first = rq.len - rq.n;                                       // position of new token 0
-        const int* table = p.table + (long long)r * p.max_pages;
+        int b0, b1;
+        if (!cur.piece(s_plan, b0, b1)) break;
+        const int h = cur.h;
+        const int row0 = (cur.ch - s_pre[cur.r]) * kRows, rows = min(kRows, cur.rq.n * p.group - row0);
+        const int first = cur.rq.len - cur.rq.n;                               // position of new token 0
+        const int* table = p.table + (long long)cur.r * p.max_pages;
         const uint32_t head_row = static_cast<uint32_t>(h) * p.page;
 
         // keys that every row of the chunk looks at: tiles inside need no mask
         const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
         const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
-        const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
         // this warp's tiles: tokens 16 * (8 * block + warp)
-        int base = (block0 + max(off0 - kStart, 0)) * kBlock + 16 * warp;
-        const int base_end = keys.hi > keys.lo ? min((block0 + off1 - kStart) * kBlock, keys.hi) : 0;
-        if (base + 16 <= keys.lo) base += kBlock;
+        int base = b0 * kBlock + 16 * warp;
+        const int base_end = cur.keys.hi > cur.keys.lo ? min(b1 * kBlock, cur.keys.hi) : 0;
+        if (base + 16 <= cur.keys.lo) base += kBlock;
         // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
         int look_page = base / p.page, look_off = base % p.page;
         auto next_page = [&](int tok, uint32_t& page, uint32_t& off) {
@@ -438,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             for (int b = 0; b < B; ++b) raw[b] = make_uint4(0, 0, 0, 0);
             if (nt * 8 + g < rows) {
                 const int i = j / p.group, hq = h * p.group + j % p.group;
-                const uint16_t* src = p.q + ((long long)(rq.t0 + i) * p.heads * p.group + hq) * D + 8 * c;
+                const uint16_t* src = p.q + ((long long)(cur.rq.t0 + i) * p.heads * p.group + hq) * D + 8 * c;
 #pragma unroll
                 for (int b = 0; b < B; ++b) raw[b] = __ldcg(reinterpret_cast<const uint4*>(src + 32 * b));
             }
@@ -525,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
             if (!ok || tok0 < all_lo || tok0 + 16 > all_hi) {                  // a border: mask
                 const int t0 = tok0 + tau, t1 = t0 + 8;
-                const bool in0 = ok && t0 >= keys.lo && t0 < keys.hi, in1 = ok && t1 >= keys.lo && t1 < keys.hi;
+                const bool in0 = ok && t0 >= cur.keys.lo && t0 < cur.keys.hi, in1 = ok && t1 >= cur.keys.lo && t1 < cur.keys.hi;
 #pragma unroll
                 for (int i = 0; i < (B + 3) / 4; ++i) {                        // scales behind the keys may be anything
                     if (!in0) vs0[i] = 0;
@@ -659,16 +495,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                         make_float4(o[nt][2 * b][k], o[nt][2 * b][2 + k], o[nt][2 * b + 1][k], o[nt][2 * b + 1][2 + k]);
             }
         __syncthreads();
-        const unsigned long long iu1 = s_line[3];
-        const int a = cta_of(iu1 + kStart), z = cta_of(iu1 + cost - 1);
+        int a, z;
+        cur.holders(s_plan, a, z);
         const bool whole = a == z;
-        float* slot = p.part + (long long)(2 * me + (static_cast<int>(me) == a ? 1 : 0)) * C::kSlot;
-        auto store_row = [&](int j, int d4, float4 v) {
-            const int i = (row0 + j) / p.group, hq = h * p.group + (row0 + j) % p.group;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2*>(p.out + ((long long)(rq.t0 + i) * p.heads * p.group + hq) * D + 4 * d4) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        };
+        float* slot = fg::attn_piece<kRows, D>(p, blockIdx.x, a);
         for (int it = tid; it < rows * (D / 4); it += kThreads) {
             const int j = it / (D / 4), d4 = it % (D / 4);
             float top = s_m[0][j];
@@ -686,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                store_row(j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                fg::attn_store<D>(p, cur.rq.t0, h, row0 + j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
             } else {
                 if (d4 == 0) {
                     slot[j] = top;
@@ -695,66 +525,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                 *reinterpret_cast<float4*>(slot + 2 * kRows + j * D + 4 * d4) = acc;
             }
         }
-        if (!whole) {
-            // the last CTA to arrive joins the pieces, in the order of the CTAs
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const unsigned before = atomicAdd(p.ctr + a, 1u);
-                s_last = before == static_cast<unsigned>(z - a);
-                if (s_last) p.ctr[a] = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int it = tid; it < rows * (D / 4); it += kThreads) {
-                    const int j = it / (D / 4), d4 = it % (D / 4);
-                    float top = kEmpty, sum = 0.0f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    constexpr int kFlight = 8;              // pieces in flight together
-                    for (int k0 = a; k0 <= z; k0 += kFlight) {
-                        float mk[kFlight], lk[kFlight], t = top;
-                        float4 v[kFlight];
-#pragma unroll
-                        for (int i = 0; i < kFlight; ++i) {
-                            const int k = min(k0 + i, z);
-                            const float* s = p.part + (long long)(2 * k + (k == a ? 1 : 0)) * C::kSlot;
-                            mk[i] = __ldcg(s + j);
-                            lk[i] = __ldcg(s + kRows + j);
-                            v[i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
-                        }
-#pragma unroll
-                        for (int i = 0; i < kFlight; ++i) t = fmaxf(t, mk[i]);
-                        const float f = ex2(top - t);
-                        top = t;
-                        sum *= f;
-                        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-#pragma unroll
-                        for (int i = 0; i < kFlight; ++i) {
-                            const float e = k0 + i <= z ? ex2(mk[i] - t) : 0.0f;
-                            sum = fmaf(lk[i], e, sum);
-                            acc.x = fmaf(v[i].x, e, acc.x); acc.y = fmaf(v[i].y, e, acc.y);
-                            acc.z = fmaf(v[i].z, e, acc.z); acc.w = fmaf(v[i].w, e, acc.w);
-                        }
-                    }
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    store_row(j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-                }
-            }
-        }
-
-        iu0 = iu1 + cost;
-        if (iu1 + off1 >= s_line[2]) break;
-        off0 = 0;
+        if (!whole) fg::attn_join<kRows, D, kThreads>(p, s_plan, a, z, cur.rq.t0, h, row0, rows);
+        if (!cur.next(p, s_plan, s_pre)) break;
         __syncthreads();                                    // s_join is written again
-        if (++h == p.heads) {
-            h = 0;
-            ++ch;
-            while (s_pre[r + 1] <= ch) ++r;
-            rq = request(p, r);
-            keys = keys_of<kRows>(p, rq, ch - s_pre[r]);
-            cost = cost_of(keys);
-        }
     }
 }
 
@@ -771,13 +544,13 @@ int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
     }
     if (!configured[dev]) {
         if (cudaFuncSetAttribute(attn_kernel<B, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::kSmem + (kMaxRequests + 1) * 4) != cudaSuccess) {
+                                 C::kSmem + (fg::kAttnMaxRequests + 1) * 4) != cudaSuccess) {
             cudaGetLastError();
             return FG_ERR_CUDA;
         }
         configured[dev] = true;
     }
-    const int ctas = sms * kPerSm < kMaxCtas ? sms * kPerSm : kMaxCtas;
+    const int ctas = sms * kPerSm < fg::kAttnMaxCtas ? sms * kPerSm : fg::kAttnMaxCtas;
     if (fg::print_configs_enabled())
         std::fprintf(stderr, "[fg] paged_attention_mxfp4 T=%d S=%d heads=%d x %d D=%d rows=%d grid=%d\n", p.T, p.S, p.heads,
                      p.group, C::D, C::kRows, ctas);
@@ -800,23 +573,26 @@ int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
     return FG_OK;
 }
 
-// Row tiles of eight: as many as an average request's rows fill, and as many as registers hold the
-// accumulators of.
+// Rows of an average request's kv head.
+long long rows_of(int T, int S, int group) { return ((long long)T + S - 1) / S * group; }
+// Row tiles of eight: as many as those rows fill, and as many as registers hold the accumulators of.
 int row_tiles(int T, int S, int group, int D) {
-    const long long rows = ((long long)T + S - 1) / S * group;
+    const long long rows = rows_of(T, S, group);
     const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const int most = D == 64 ? 4 : D == 128 ? 2 : 1;
     return nt < most ? nt : most;
 }
+// Whether a call takes the kernel for many rows a request.
+bool many_rows(int T, int S, int group) { return S <= fg::kAttnPromptRequests && rows_of(T, S, group) >= 64; }
 
 bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
     return T >= 0 && S >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536 && D >= 1;
 }
 
-// Floats of the largest variant's partial result: one size serves every call.
+// Floats of the largest partial result of this file's variants.
 constexpr int kMaxSlot = Cfg<2, 4>::kSlot;
 static_assert(Cfg<4, 2>::kSlot <= kMaxSlot && Cfg<8, 1>::kSlot <= kMaxSlot, "largest partial result");
-constexpr long long kCtrBytes = (kMaxCtas * 4 + 255) / 256 * 256;
+constexpr long long kCtrBytes = (fg::kAttnMaxCtas * 4 + 255) / 256 * 256;
 
 }  // namespace
 
@@ -824,7 +600,11 @@ extern "C" {
 
 long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D) {
     if (!shapes_ok(T, S, Hq, Hkv, D) || (D != 64 && D != 128 && D != 256)) return -1;
-    return kCtrBytes + 2LL * kMaxCtas * kMaxSlot * 4;
+    const bool many = many_rows(T, S > 0 ? S : 1, Hq / Hkv);
+    const long long slot = D == 64 ? fg::attn_slot<fg::kPromptRows, 64>() : D == 128 ? fg::attn_slot<fg::kPromptRows, 128>()
+                                                                                    : fg::attn_slot<fg::kPromptRows, 256>();
+    const long long few = 2LL * fg::kAttnMaxCtas * kMaxSlot * 4, most = 2LL * fg::kAttnPromptCtas * slot * 4;
+    return kCtrBytes + (many && most > few ? most : few);
 }
 
 int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
@@ -836,7 +616,7 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
         (long long)page_size * num_pages > 0x7fffffffLL || (long long)page_size * max_pages > 0x7fffffffLL - 4096 ||
         !(scale > 0.0f) || !(scale <= 3.402823466e38f))
         return FG_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || S > kMaxRequests || T > 1 << 18 || Hq / Hkv > 256 ||
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || S > fg::kAttnMaxRequests || T > 1 << 18 || Hq / Hkv > 256 ||
         (long long)Hkv * page_size > 0x7fffffffLL)
         return FG_ERR_UNSUPPORTED;
     if (T == 0 || S == 0) return FG_OK;
@@ -850,8 +630,9 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
     const AttnParams p{static_cast<const uint16_t*>(q), k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens,
                        static_cast<uint16_t*>(out), T, S, Hkv, Hq / Hkv, page_size, num_pages, max_pages, window,
                        scale * 1.4426950408889634f, reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCtrBytes),
-                       st.status};
+                       st.status, st.timeout_ns};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (many_rows(T, S, Hq / Hkv)) return fg::launch_attn_prompt(p, D, st.sms, st.pdl, s);
     const int nt = row_tiles(T, S, Hq / Hkv, D);
     switch (D) {
         case 64: return nt == 1 ? launch<2, 1>(p, st.sms, st.pdl, s) : nt == 2 ? launch<2, 2>(p, st.sms, st.pdl, s) : launch<2, 4>(p, st.sms, st.pdl, s);

@@ -1,0 +1,299 @@
+// fg_attn.cuh - what the attention kernels over the 4-bit cache share: a launch's parameters, the cut of all
+// items into equal shares, and the join of an item's pieces.
+//
+// An item is (request, chunk of kRows rows, kv head); its keys are cut into blocks of kBlock tokens.  The blocks of all
+// items stand in one line that is cut into equal shares, one per CTA, from lengths that only the device knows; an
+// item that crosses a cut leaves partial results (a row's maximum, sum and unscaled output) in the workspace, and
+// the CTA that arrives last joins them in the items' order, so results do not depend on the order of arrival.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "fg_kv.cuh"
+
+namespace fg {
+
+constexpr int kAttnStart = 3;                 // what every item takes besides its keys (its q, filling the pipeline,
+                                              // the join), in blocks
+constexpr int kAttnMaxCtas = 640;             // shares of a launch, at most
+constexpr int kAttnMaxRequests = 4096;
+constexpr float kAttnEmpty = -1e30f;          // maximum of a row without a key
+constexpr uint32_t kAllLanes = 0xffffffffu;
+
+struct AttnParams {
+    const uint16_t* q;
+    const uint8_t *kc, *ks, *vc, *vs;
+    const int32_t *table, *start, *lens;
+    uint16_t* out;
+    int T, S, heads, group, page, pages, max_pages, window;
+    float scale_log2;                          // scale * log2(e)
+    unsigned* ctr;                             // [kAttnMaxCtas]
+    float* part;                               // [2 * kAttnMaxCtas][kRows][D + 2]: M, l, O
+    int* status;
+    unsigned long long timeout_ns;
+};
+
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One request as the kernels see it (n == 0: nothing to do, or its lengths are wrong).
+struct AttnRequest {
+    int n, len, t0;
+};
+__device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int r) {
+    const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
+    const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
+    return ok ? AttnRequest{t1 - t0, len, t0} : AttnRequest{0, 0, 0};
+}
+// Keys [lo, hi) that some row of a chunk looks at; hi <= lo: none.
+struct AttnKeys {
+    int lo, hi;
+};
+
+// Shared memory of a plan.
+template <int kThreads>
+struct AttnPlanSmem {
+    unsigned long long warp[kThreads / 32], strip[kThreads + 1];
+    volatile unsigned long long line[4];       // shares, blocks of all items, this share's end, where the current item begins
+    int last;
+};
+
+// Where a CTA stands in the line.
+template <int kRows, int kBlock, int kThreads>
+struct AttnCursor {
+    AttnRequest rq;
+    AttnKeys keys;
+    int r, ch, h, cost, off0;                  // request, chunk (of all), head, the item's cost, the share's begin within it
+    unsigned long long begin;                  // where the item begins; the next one's while next() runs
+
+    __device__ __forceinline__ void look(const AttnParams& p, const int* s_pre) {
+        rq = attn_request(p, r);
+        const int chunk = ch - s_pre[r];
+        const int i0 = chunk * kRows / p.group, i1 = min(rq.n - 1, (chunk * kRows + kRows - 1) / p.group);
+        keys.hi = rq.len - rq.n + i1 + 1;
+        keys.lo = p.window > 0 ? max(0, rq.len - rq.n + i0 + 1 - p.window) : 0;
+        cost = kAttnStart + (keys.hi > keys.lo ? (keys.hi + kBlock - 1) / kBlock - keys.lo / kBlock : 1);
+    }
+
+    // Sum of v over the threads before this one, and of all.
+    static __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long* s_warp, unsigned long long& total) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        unsigned long long incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(kAllLanes, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        unsigned long long before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            total += s_warp[w];
+        }
+        return before + incl - v;
+    }
+
+    // Last entry of a with a[i] <= x, a[0] == 0, over n entries.
+    static __device__ __forceinline__ int find(const int* a, int n, int x) {
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+
+    // Works out this CTA's share and its first item; false: there is none.  All threads call it.  Chunks per request,
+    // then blocks per chunk, are scanned in strips of consecutive entries.
+    __device__ __forceinline__ bool open(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int* s_pre) {
+        const int tid = threadIdx.x;
+        const int per_r = (p.S + kThreads - 1) / kThreads;
+        {
+            unsigned long long sum = 0, total;
+            for (int i = 0; i < per_r; ++i) {
+                const int q = tid * per_r + i;
+                if (q >= p.S) break;
+                const AttnRequest x = attn_request(p, q);
+                if (blockIdx.x == 0 && x.n == 0) {
+                    const int t0 = __ldg(p.start + q), t1 = __ldg(p.start + q + 1), len = __ldg(p.lens + q);
+                    if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page)
+                        kv_record(p.status, kKvErrAttention);
+                }
+                sum += ((long long)x.n * p.group + kRows - 1) / kRows;
+            }
+            unsigned long long at = scan(sum, sm.warp, total);
+            for (int i = 0; i < per_r; ++i) {
+                const int q = tid * per_r + i;
+                if (q >= p.S) break;
+                s_pre[q] = static_cast<int>(at);
+                at += ((long long)attn_request(p, q).n * p.group + kRows - 1) / kRows;
+            }
+            if (tid == 0) s_pre[p.S] = static_cast<int>(total);
+        }
+        __syncthreads();
+        const int chunks = s_pre[p.S];
+        const int per_c = (chunks + kThreads - 1) / kThreads;
+        unsigned long long total_blocks;
+        {
+            unsigned long long sum = 0;
+            ch = tid * per_c;
+            if (ch < chunks) {
+                r = find(s_pre, p.S, ch);
+                for (int i = 0; i < per_c && ch < chunks; ++i, ++ch) {
+                    while (s_pre[r + 1] <= ch) ++r;
+                    look(p, s_pre);
+                    sum += cost;
+                }
+            }
+            const unsigned long long at = scan(sum, sm.warp, total_blocks);
+            sm.strip[tid] = at;
+            if (tid == 0) sm.strip[kThreads] = total_blocks;
+        }
+        __syncthreads();
+        const unsigned long long all = total_blocks * p.heads;
+        // a share is worth an item's start
+        const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kAttnStart) / (kAttnStart + 1));
+        if (blockIdx.x >= shares) return false;
+        const unsigned long long u = all * blockIdx.x / shares;
+        if (tid == 0) { sm.line[0] = shares; sm.line[1] = all; sm.line[2] = all * (blockIdx.x + 1) / shares; }
+        __syncthreads();
+        // the chunk that holds u: its strip, then the strip's chunks one by one
+        int lo = 0, hi = kThreads;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.strip[mid] * p.heads <= u) lo = mid;
+            else hi = mid;
+        }
+        ch = lo * per_c;
+        begin = sm.strip[lo] * p.heads;
+        r = find(s_pre, p.S, ch);
+        while (s_pre[r + 1] <= ch) ++r;
+        look(p, s_pre);
+        while (begin + (unsigned long long)cost * p.heads <= u) {
+            begin += (unsigned long long)cost * p.heads;
+            ++ch;
+            while (s_pre[r + 1] <= ch) ++r;
+            look(p, s_pre);
+        }
+        h = static_cast<int>((u - begin) / cost);
+        begin += (unsigned long long)h * cost;
+        off0 = static_cast<int>(u - begin);
+        return true;
+    }
+
+    // Blocks [b0, b1) of the current item that are this share's; false: none of them, and the share ends here.
+    __device__ __forceinline__ bool piece(AttnPlanSmem<kThreads>& sm, int& b0, int& b1) const {
+        const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), sm.line[2] - begin));
+        if (off1 <= kAttnStart) return false;
+        if (threadIdx.x == 0) sm.line[3] = begin;            // read again behind the piece's first barrier
+        const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
+        b0 = block0 + max(off0 - kAttnStart, 0);
+        b1 = block0 + off1 - kAttnStart;
+        return true;
+    }
+
+    // The CTAs that hold pieces of the current item, first and last.
+    __device__ __forceinline__ void holders(AttnPlanSmem<kThreads>& sm, int& a, int& z) const {
+        const unsigned long long at = sm.line[3], shares = sm.line[0], all = sm.line[1];
+        a = static_cast<int>(((at + kAttnStart + 1) * shares - 1) / all);
+        z = static_cast<int>(((at + cost) * shares - 1) / all);
+    }
+
+    // On to the next item; false: the share ends with this one.  Every thread calls it, and a barrier stands between it
+    // and the next piece().
+    __device__ __forceinline__ bool next(const AttnParams& p, AttnPlanSmem<kThreads>& sm, const int* s_pre) {
+        begin = sm.line[3] + cost;
+        if (begin >= sm.line[2]) return false;
+        off0 = 0;
+        if (++h == p.heads) {
+            h = 0;
+            ++ch;
+            while (s_pre[r + 1] <= ch) ++r;
+            look(p, s_pre);
+        }
+        return true;
+    }
+};
+
+// Floats of a partial result: kRows maxima, kRows sums, kRows x D outputs.
+template <int kRows, int D>
+__host__ __device__ constexpr int attn_slot() { return kRows * (D + 2); }
+
+// Where CTA k keeps its piece of the item that begins at CTA a.
+template <int kRows, int D>
+__device__ __forceinline__ float* attn_piece(const AttnParams& p, int k, int a) {
+    return p.part + (long long)(2 * k + (k == a ? 1 : 0)) * attn_slot<kRows, D>();
+}
+
+template <int D>
+__device__ __forceinline__ void attn_store(const AttnParams& p, int t0, int h, int row, int d4, float4 v) {
+    const int i = row / p.group, hq = h * p.group + row % p.group;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p.out + ((long long)(t0 + i) * p.heads * p.group + hq) * D + 4 * d4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Called by all threads once this CTA's piece is written: the CTA that arrives last joins the pieces of CTAs a to z, in
+// their order, and stores rows [row0, row0 + rows).
+template <int kRows, int D, int kThreads>
+__device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int a, int z, int t0, int h, int row0, int rows) {
+    const int tid = threadIdx.x;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const unsigned before = atomicAdd(p.ctr + a, 1u);
+        sm.last = before == static_cast<unsigned>(z - a);
+        if (sm.last) p.ctr[a] = 0;
+    }
+    __syncthreads();
+    if (!sm.last) return;
+    __threadfence();
+    for (int it = tid; it < rows * (D / 4); it += kThreads) {
+        const int j = it / (D / 4), d4 = it % (D / 4);
+        float top = kAttnEmpty, sum = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kFlight = 8;                            // pieces in flight together
+        for (int k0 = a; k0 <= z; k0 += kFlight) {
+            float mk[kFlight], lk[kFlight], t = top;
+            float4 v[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const float* s = attn_piece<kRows, D>(p, min(k0 + i, z), a);
+                mk[i] = __ldcg(s + j);
+                lk[i] = __ldcg(s + kRows + j);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) t = fmaxf(t, mk[i]);
+            const float f = ex2(top - t);
+            top = t;
+            sum *= f;
+            acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const float e = k0 + i <= z ? ex2(mk[i] - t) : 0.0f;
+                sum = fmaf(lk[i], e, sum);
+                acc.x = fmaf(v[i].x, e, acc.x); acc.y = fmaf(v[i].y, e, acc.y);
+                acc.z = fmaf(v[i].z, e, acc.z); acc.w = fmaf(v[i].w, e, acc.w);
+            }
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        attn_store<D>(p, t0, h, row0 + j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+}
+
+// Launches the kernel for many rows a request (fg_attn_prompt.cu).
+int launch_attn_prompt(const AttnParams& p, int D, int sms, int pdl, cudaStream_t stream);
+constexpr int kPromptRows = 128, kAttnPromptCtas = 152, kAttnPromptRequests = 1024;
+
+}  // namespace fg

@@ -117,7 +117,7 @@ def cached(table_row, n, codes, sf, kind, head):
 
 
 # -------------------------------------------------------------------------- attention
-def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0):
+def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0, weight=2.0 ** -11):
     """q [T, Hq, D] FP64 values.  (out, bound, used): rows of requests are True in `used`.
 
     Bound, row by row: a score of D products, whose absolute values add up to S, is off by D + 8 units of S in
@@ -156,7 +156,7 @@ def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0):
                 ds = np.expm1(np.minimum(ds, 1.0))
                 o = p @ v
                 largest = np.max(p[:, :, None] * vscale[None], axis=(1, 2))[:, None]
-                num = (p * (ds + 2.0 ** -11)) @ np.abs(v) + (p @ np.abs(v)) * (length + 16) * 2 * U
+                num = (p * (ds + weight)) @ np.abs(v) + (p @ np.abs(v)) * (length + 16) * 2 * U
                 num += 2.0 ** -33 * largest * 6 * seen.sum(1, keepdims=True)
                 den = (p * ds).sum(1, keepdims=True) + (length + 16) * 2 * U
                 out[t0:t0 + n, hh] = o

@@ -41,9 +41,15 @@ def cache_case(seed, lens, new, hq, hkv, d, page, spread=2, extra_rows=2, q_scal
             "pages": pages}
 
 
+def weight_step(c):
+    """Half a step of the weights' type: BF16 where an average request brings 64 rows or more of a kv head, else FP16."""
+    rows = -(-len(c["q"]) // len(c["lens"])) * (c["hq"] // c["hkv"])
+    return 2.0 ** -8 if rows >= 64 else 2.0 ** -11
+
+
 def reference(c, scale=None, window=0):
     return O.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["table"], c["start"], c["lens"],
-                       c["d"] ** -0.5 if scale is None else scale, window)
+                       c["d"] ** -0.5 if scale is None else scale, window, weight_step(c))
 
 
 def tables_case(seed, s, page, longest, width, mode):

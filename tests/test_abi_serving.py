@@ -106,7 +106,7 @@ def test_calls_with_their_arguments_in_one_record(fg):
 def test_workspace_sizes(fg):
     size = fg.lib.fg_paged_attention_workspace
     assert size(4, 2, 7, 2, 128) == -1 and size(-1, 2, 8, 2, 128) == -1 and size(4, 2, 8, 2, 96) == -1
-    assert size(1, 1, 8, 1, 128) == size(8192, 4000, 64, 1, 64) == size(1, 0, 1, 1, 256) > 0
+    assert 0 < size(1, 1, 8, 1, 128) == size(8192, 4000, 64, 1, 64) == size(1, 0, 1, 1, 256) < size(64, 1, 1, 1, 128) < size(64, 1, 1, 1, 256)
 
 
 def test_no_device_fails_loudly(fg):

@@ -76,6 +76,75 @@ def test_several_new_tokens(fg, d, hq, hkv, window):
     check(c, out, window)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,new", [(2, 2, [70, 64, 65]), (8, 1, [30, 0, 17]), (6, 2, [1, 100, 9]), (16, 1, [8, 8, 3])])
+@pytest.mark.parametrize("window", [0, 33])
+@pytest.mark.parametrize("page", [16, 80])
+def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
+    """Chunks of 128 rows on the tensor cores: ends inside a token's heads, requests of few rows among them, tiles that
+    end behind the keys, windows that begin inside a tile."""
+    lens = [n + extra for n, extra in zip(new, (0, 200, 131))]
+    c = C.cache_case(d + hq + sum(new) + window + page, lens, new, hq, hkv, d, page, extra_rows=3 * -(-64 * hkv // hq))
+    assert C.weight_step(c) == 2.0 ** -8
+    out, ws = attend(fg, c, window)
+    expect(fg)
+    check(c, out, window)
+    assert not ws[:2560].any(), "counters are left as they were"
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_over_long_contexts_are_split_and_joined(fg, d):
+    c = C.cache_case(d, [2500, 1800], [40, 1], 8, 1, d, 32)
+    out, ws = attend(fg, c)
+    expect(fg)
+    check(c, out)
+    for _ in range(3):
+        again, _ = attend(fg, c, ws=ws)
+        assert torch.equal(again, out)
+
+
+def test_many_rows_scores_that_keep_rising(fg):
+    """Keys whose scores rise by far more than a step of the running maximum, tile by tile, and fall again."""
+    c = C.cache_case(12, [1000], [20], 8, 1, 64, 16)
+    c["q"][:] = np.abs(c["q"])
+    c["q_bits"], c["q"] = O.bf16(c["q"])
+    n = np.arange(1000)
+    x = np.zeros((1000, 1, 64))
+    x[:] = (np.where(n < 700, n, 1400 - n) / 50.0)[:, None, None]
+    codes, sf = O.encode(x)
+    p, o = c["table"][0, n // 16], n % 16
+    c["kc"][p, :, o], c["ks"][p, :, o] = O.rows(codes, "k"), sf
+    out, _ = attend(fg, c)
+    expect(fg)
+    check(c, out)
+
+
+def test_many_rows_contract_violations_and_non_finite_queries(fg):
+    c = C.cache_case(13, [300, 90], [40, 30], 4, 2, 128, 16)
+    c = dict(c, q_bits=np.concatenate([c["q_bits"]] * 1), table=c["table"].copy())
+    ref = O.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["table"], c["start"], c["lens"], 128 ** -0.5, 0, 2.0 ** -8)
+    c["q_bits"][5, 1, 7] = 0x7FC0
+    c["q_bits"][6, 3, 0] = 0x7F80
+    c["table"][1, 2] = -1
+    out, _ = attend(fg, c)
+    expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
+    got = f64(out)
+    assert np.isnan(got[5, 1]).all() and np.isnan(got[6, 3]).any()
+    ok = np.ones((40, 4), bool)
+    ok[5, 1] = ok[6, 3] = False
+    assert within(got[:40][ok], (ref[0][:40][ok], ref[1][:40][ok]), "bf16").all()
+    # request 1 without the tokens of its third page: the others move up, positions and all
+    keep = np.r_[0:32, 48:90]
+    small = {k: c[k].copy() for k in ("kc", "ks", "vc", "vs")}
+    page, off = c["table"][1, keep // 16], keep % 16
+    at = np.arange(len(keep))
+    for k in small:
+        small[k][c["table"][0, at // 16], :, at % 16] = c[k][page, :, off]
+    one = O.attention(c["q"][40:70], *[small[k] for k in ("kc", "ks", "vc", "vs")], c["table"][:1], [0, 30], [74], 128 ** -0.5, 0, 2.0 ** -8)
+    assert within(got[40:70], one[:2], "bf16").all()
+    assert (got[70:] == -77).all()
+
+
 def test_rows_before_the_first_key(fg):
     """More rows than cached tokens: the rows before position 0 look at nothing and become zero."""
     c = C.cache_case(3, [3, 0, 20], [3, 0, 2], 4, 2, 128, 16, extra_rows=9)
@@ -99,9 +168,10 @@ def test_one_long_request_is_split_and_joined(fg, hkv, length):
 
 
 def test_a_workspace_serves_calls_of_other_sizes(fg):
-    ws = fg.paged_attention_workspace(64, 8, 32, 1, 256)
+    ws = fg.paged_attention_workspace(64, 1, 32, 1, 256)
     for seed, (lens, new, hq, hkv, d) in enumerate([([700, 3], [2, 1], 8, 2, 128), ([5000], [1], 4, 1, 256),
-                                                    ([90] * 5, [4] * 5, 16, 4, 64), ([5000, 17], [1, 1], 3, 3, 128)]):
+                                                    ([90] * 5, [4] * 5, 16, 4, 64), ([700], [33], 8, 2, 256),
+                                                    ([5000, 17], [1, 1], 3, 3, 128), ([60, 300], [60, 9], 4, 1, 64)]):
         c = C.cache_case(seed, lens, new, hq, hkv, d, 32)
         out, _ = attend(fg, c, ws=ws)
         expect(fg)
