@@ -4,15 +4,17 @@
 // An item is 128 rows (new tokens x the query heads that share a kv head) of one request; per tile of kTok keys
 //   S = Q K^T       tcgen05.mma, BF16, FP32 in tensor memory (two tiles of it, so the next product runs while a
 //                   tile's exponentials are taken)
-//   P = 2^(S - m)   one thread a row; m a running maximum that moves only when a score passes it by 2^8, because
+//   P = 2^(S - m)   two threads a row, half of the keys each, in registers; m a running maximum that moves only when a score passes it by 2^8, because
 //                   moving it scales O, which lives in tensor memory; P rounded once, to BF16
 //   O += P V        tcgen05.mma, BF16, FP32 in tensor memory
 // Keys and values become BF16 tiles in shared memory once per item tile, exactly (a code has two significant bits,
 // its scale is a power of two): 256 threads decode what 128 rows use.  Keys, values and Q stand as rows of 64
 // elements in 128-byte swizzled atoms; a value tile is the product's MN-major operand as it is.
 //
-// Warps: 0-3 softmax and output (a row a thread), 4 the MMA issuer, 5-12 the decoders.  They meet at mbarriers
-// (every wait is bounded, as in the GEMMs); pieces of items follow one another with a CTA barrier between.
+// Warps: 0-7 softmax and output (warps w and w + 4 share 32 rows), 8 the MMA issuer, 9-16 the decoders.  They meet at
+// mbarriers (every wait is bounded, as in the GEMMs); a row's two threads meet at a barrier of their two warps,
+// which both reach on every tile, also after a wait that ran out; pieces of items follow one another with a CTA
+// barrier between.
 #include <cuda_runtime.h>
 
 #include <cstdio>
@@ -28,7 +30,7 @@ using fg::AttnParams;
 using fg::ex2;
 
 constexpr int kRows = fg::kPromptRows;
-constexpr int kMmaWarp = 4, kDecodeWarp0 = 5, kDecodeWarps = 8;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kDecodeWarp0 = 9, kDecodeWarps = 8;
 constexpr int kThreads = 32 * (kDecodeWarp0 + kDecodeWarps);
 constexpr int kWaitPrompt = 12;                // status code of a wait that ran out
 constexpr float kSlack = 8.0f;                 // scores above m by at most this (log2): P <= 2^8
@@ -78,6 +80,18 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Barrier of the 64 threads of two warps; returns whether the predicate holds for any of them.
+__device__ __forceinline__ bool pair_any(int id, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"(pred ? 1u : 0u) : "memory");
+    return r != 0;
+}
+
 // What a decoder thread holds of a tile: its column groups of one token's key and value rows, and their scales.
 template <int B>
 struct Raw {
@@ -116,6 +130,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = fg::smem_u32(smem);
     __shared__ fg::AttnPlanSmem<kThreads> s_plan;
+    __shared__ float s_top[2][kRows], s_l[2][kRows];           // of a row's two halves
+    __shared__ int s_dead[kSoftWarps];
+    __shared__ fg::AttnCursor<kRows, C::kTok, kThreads> s_cur;  // while the roles run, out of their registers
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
     const uint32_t bar = sbase + C::kOffBar;
     const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48, s_full = bar + 64, s_empty = bar + 80,
@@ -132,9 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
             fg::mbar_init(v_full + 8 * i, kDecodeWarps);
             fg::mbar_init(v_empty + 8 * i, 1);
             fg::mbar_init(s_full + 8 * i, 1);
-            fg::mbar_init(s_empty + 8 * i, 4);
+            fg::mbar_init(s_empty + 8 * i, kSoftWarps);
         }
-        fg::mbar_init(p_full, 4);
+        fg::mbar_init(p_full, kSoftWarps);
         fg::mbar_init(p_empty, 1);
         fg::mbar_init(fg::smem_u32(drain), 1);
         *abort_flag = 0;
@@ -164,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
         const int first = cur.rq.len - cur.rq.n;               // position of new token 0
         const int* table = p.table + (long long)cur.r * p.max_pages;
         const bool empty = cur.keys.hi <= cur.keys.lo;
+        const int t0 = cur.rq.t0, keys_lo = cur.keys.lo;
+        if (tid == 0) s_cur = cur;
         const int tok0 = b0 * kTok, tok1 = empty ? tok0 : min(b1 * kTok, cur.keys.hi);
         const int tiles = (tok1 - tok0 + kTok - 1) / kTok;     // 0 where no row of the item has a key
 
@@ -171,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
         if (warp >= kDecodeWarp0) {
             const int t = tid - 32 * kDecodeWarp0, j = t % kRows;
             const int i = (row0 + j) / p.group, hq = h * p.group + (row0 + j) % p.group;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(cur.rq.t0 + i) * p.heads * p.group + hq) * D);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(t0 + i) * p.heads * p.group + hq) * D);
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
                 const int ch = (t / kRows) * (D / 16) + x;      // chunk of eight elements
@@ -182,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
         }
         __syncthreads();
 
-        float m = fg::kAttnEmpty, l = 0.0f;                    // of this thread's row (softmax warps)
+        float m = fg::kAttnEmpty, l = 0.0f;                    // of this thread's row, and of its half (softmax warps)
         if (warp >= kDecodeWarp0) {
             // ------------------------------------------------------------- decoders
             const int t = tid - 32 * kDecodeWarp0, my = t % kTok, c0 = t / kTok * C::kC;
@@ -190,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
             const int step_page = kTok / p.page, step_off = kTok % p.page;
             auto next_page = [&](int tok) {                     // the page of token tok (its row's offset in `off`); -1: none
                 const int group = tok & ~15;
-                const bool wanted = tok < tok1 && group + 16 > cur.keys.lo;
+                const bool wanted = tok < tok1 && group + 16 > keys_lo;
                 const int id = wanted ? __ldg(table + page_i) : -1;
                 return id >= 0 && id < p.pages ? id : -1;
             };
@@ -263,13 +282,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                 return true;
             };
             Raw<B> x, ahead;                                    // a tile, and the next one on its way
-            int tok = tok0 + my;
-            load(x, next_page(tok), page_off);
-#pragma unroll 1
-            for (int i = 0; i < tiles; ++i) {
+            int tok = tok0 + my, off = page_off, page = next_page(tok);
+            load(x, page, off);
+            auto look = [&]() {                                 // the page of the tile after the last one looked up
                 advance();
                 tok += kTok;
-                load(ahead, next_page(tok), page_off);
+                off = page_off;
+                page = next_page(tok);
+            };
+            look();
+#pragma unroll 1
+            for (int i = 0; i < tiles; ++i) {
+                load(ahead, page, off);
+                look();
                 if (!fill(x, n0 + i)) break;
                 x = ahead;
             }
@@ -309,12 +334,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
             }
             __syncwarp();
         } else {
-            // --------------------------------------------------- softmax, a row a thread
-            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-            const int row = row0 + tid, hi = first + row / p.group + 1, lo = p.window > 0 ? hi - p.window : 0;
+            // ------------------------------------------- softmax, half a row's keys a thread
+            constexpr int kHalf = kTok / 2;
+            const int half = warp >> 2, my = (warp & 3) * 32 + lane, col0 = half * kHalf;
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const int hi = first + (row0 + my) / p.group + 1, lo = p.window > 0 ? hi - p.window : 0;
             // keys that every row of the chunk looks at
             const int all_hi = first + row0 / p.group + 1;
             const int all_lo = p.window > 0 ? max(0, first + (row0 + rows - 1) / p.group + 1 - p.window) : 0;
+            const uint32_t p_row = sbase + C::kOffP + (col0 / 64) * (kRows * 128) + my * 128;
             for (int i = 0; i < tiles; ++i) {
                 const uint32_t n = n0 + i, st = n & 1, ph = (n >> 1) & 1;
                 const int base = tok0 + i * kTok;
@@ -323,90 +351,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                 {
                     const int at = base + 16 * lane;
                     bool bad = false;
-                    if (lane < kTok / 16 && at < tok1 && at + 16 > cur.keys.lo) {
+                    if (lane < kTok / 16 && at < tok1 && at + 16 > keys_lo) {
                         const int id = __ldg(table + at / p.page);
                         bad = id < 0 || id >= p.pages;
                     }
                     absent = __ballot_sync(kAll, bad);
                     if (absent && lane == 0) fg::kv_record(p.status, fg::kKvErrAttention);
                 }
-                const bool border = absent != 0 || base < all_lo || base + kTok > all_hi;
-                bool ok = wait(s_full + 8 * st, ph);
-                if (!__all_sync(kAll, ok)) break;
+                bool dead = !__all_sync(kAll, wait(s_full + 8 * st, ph));
                 fg::tc_fence_after();
-                const uint32_t sc = tmem + lanes + st * 128;
-                auto masked = [&](float x, int col) {
-                    const int tok = base + col;
-                    return tok >= lo && tok < hi && !(absent >> (col >> 4) & 1u) ? x : -INFINITY;
-                };
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kTok; c += 32) {
-                    uint32_t r[32];
-                    fg::tmem_ld_32x32b_x32(sc + c, r);
+                const uint32_t at_s = tmem + lanes + st * 128 + col0;
+                const bool border = absent != 0 || base < all_lo || base + kTok > all_hi;
+                auto scores = [&](int c, uint32_t (&r)[32]) {   // columns col0 + c .. + 31, masked at a border
+                    fg::tmem_ld_32x32b_x32(at_s + c, r);
                     fg::tmem_wait_ld();
                     if (border) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) top = fmaxf(top, masked(__uint_as_float(r[x]), c + x));
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(r[x]));
+                        for (int x = 0; x < 32; ++x) {
+                            const int tok = base + col0 + c + x;
+                            if (tok < lo || tok >= hi || (absent >> ((col0 + c + x) >> 4) & 1u)) r[x] = 0xFF800000u;
+                        }
                     }
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32) {
+                    uint32_t r[32];
+                    scores(c, r);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(r[x]));
                 }
                 top *= p.scale_log2;
                 // the last tile's P has been read, and O is whole, once its product is done
-                if (n > 0) {
-                    ok = wait(p_empty, (n - 1) & 1);
-                    if (!__all_sync(kAll, ok)) break;
-                }
-                if (__any_sync(kAll, top > m + kSlack)) {
-                    const float now = fmaxf(m, top), f = ex2(m - now);
+                if (n > 0) dead = dead || !__all_sync(kAll, wait(p_empty, (n - 1) & 1));
+                if (pair_any(1 + (warp & 3), dead || top > m + kSlack)) {
+                    s_top[half][my] = top;
+                    if (lane == 0) s_dead[warp] = dead;
+                    pair_any(1 + (warp & 3), false);
+                    const float both = fmaxf(top, s_top[half ^ 1][my]);
+                    if (dead || s_dead[warp ^ 4]) break;
+                    const float now = both > m + kSlack ? both : m, f = ex2(m - now);
                     m = now;
                     l *= f;
                     if (i > 0) {
                         fg::tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t r[32];
-                            fg::tmem_ld_32x32b_x32(tmem + lanes + C::kCols + c, r);
+                        for (int c = 0; c < D / 2; c += 32) {
+                            uint32_t x[32];
+                            const uint32_t at = tmem + lanes + C::kCols + half * (D / 2) + c;
+                            fg::tmem_ld_32x32b_x32(at, x);
                             fg::tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
-                            tmem_st_32x32b_x32(tmem + lanes + C::kCols + c, r);
+                            for (int y = 0; y < 32; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * f);
+                            tmem_st_32x32b_x32(at, x);
                         }
                         tmem_wait_st();
+                        fg::tc_fence_before();
                     }
+                    pair_any(1 + (warp & 3), false);            // both have read before either writes again
                 }
                 const float shift = -m;
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int c = 0; c < kTok; c += 32) {
+                for (int c = 0; c < kHalf; c += 32) {
                     uint32_t r[32];
-                    fg::tmem_ld_32x32b_x32(sc + c, r);
-                    fg::tmem_wait_ld();
-                    if (border) {
+                    scores(c, r);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(masked(__uint_as_float(r[x]), c + x));
-                    }
-                    float part = 0.0f;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float w = ex2(fmaf(__uint_as_float(r[x]), p.scale_log2, shift));
-                        part += w;
-                        r[x] = __float_as_uint(w);
-                    }
-                    l += part;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 32; x += 8) {
                         uint32_t o[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const __nv_bfloat162 w = __floats2bfloat162_rn(__uint_as_float(r[8 * x + 2 * y]), __uint_as_float(r[8 * x + 2 * y + 1]));
+                            const float w0 = ex2(fmaf(__uint_as_float(r[x + 2 * y]), p.scale_log2, shift));
+                            const float w1 = ex2(fmaf(__uint_as_float(r[x + 2 * y + 1]), p.scale_log2, shift));
+                            part[y] += w0 + w1;
+                            const __nv_bfloat162 w = __floats2bfloat162_rn(w0, w1);
                             o[y] = *reinterpret_cast<const uint32_t*>(&w);
                         }
-                        const int ch = (c % 64) / 8 + x;
-                        st_shared_16(sbase + C::kOffP + (c / 64) * (kRows * 128) + tid * 128 + ((ch ^ (tid & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                        st_shared_16(p_row + (((((col0 + c) % 64 + x) / 8) ^ (my & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
+                l += (part[0] + part[1]) + (part[2] + part[3]);
                 fg::tc_fence_before();
                 fg::fence_proxy_async_smem();
                 __syncwarp();
@@ -421,25 +445,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                 __syncwarp();
                 fg::tc_fence_after();
             }
+            s_l[half][my] = l;
         }
         __syncthreads();
         if (*abort_flag) break;
         n0 += tiles;
+        cur = s_cur;
 
         // ------------------------------------------------------------------ output
         int a, z;
         cur.holders(s_plan, a, z);
         const bool whole = a == z;
-        if (warp < kMmaWarp) {
-            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (warp < kSoftWarps) {
+            const int half = warp >> 2, my = (warp & 3) * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const float sum = s_l[0][my] + s_l[1][my];
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             float* slot = fg::attn_piece<kRows, D>(p, blockIdx.x, a);
-            if (!whole && tid < rows) {
-                slot[tid] = m;
-                slot[kRows + tid] = l;
+            if (!whole && half == 0 && my < rows) {
+                slot[my] = m;
+                slot[kRows + my] = sum;
             }
+            const int i = (row0 + my) / p.group, hq = h * p.group + (row0 + my) % p.group;
+            uint16_t* out = p.out + ((long long)(cur.rq.t0 + i) * p.heads * p.group + hq) * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 uint32_t r[32];
                 if (tiles > 0) {
                     fg::tmem_ld_32x32b_x32(tmem + lanes + C::kCols + c, r);
@@ -448,14 +478,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
 #pragma unroll
                     for (int x = 0; x < 32; ++x) r[x] = 0;
                 }
-                if (tid < rows) {
+                if (my < rows && whole) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float4 v = make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 2]),
-                                                     __uint_as_float(r[4 * x + 3]));
-                        if (whole) fg::attn_store<D>(p, cur.rq.t0, h, row0 + tid, c / 4 + x, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                        else *reinterpret_cast<float4*>(slot + 2 * kRows + tid * D + c + 4 * x) = v;
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const __nv_bfloat162 w = __floats2bfloat162_rn(__uint_as_float(r[8 * x + 2 * y]) * inv, __uint_as_float(r[8 * x + 2 * y + 1]) * inv);
+                            o[y] = *reinterpret_cast<const uint32_t*>(&w);
+                        }
+                        *reinterpret_cast<uint4*>(out + c + 8 * x) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
+                } else if (my < rows) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<float4*>(slot + 2 * kRows + my * D + c + 4 * x) =
+                            make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]));
                 }
             }
             fg::tc_fence_before();
