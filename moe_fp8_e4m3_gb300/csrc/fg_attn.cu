@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                 *reinterpret_cast<float4*>(slot + 2 * kRows + j * D + 4 * d4) = acc;
             }
         }
-        if (!whole) fg::attn_join<kRows, D, kThreads>(p, s_plan, a, z, cur.rq.t0, h, row0, rows);
+        if (!whole) fg::attn_join<kRows, D, kThreads, false>(p, s_plan, a, z, cur.rq.t0, h, row0, rows);
         if (!cur.next(p, s_plan, s_pre)) break;
         __syncthreads();                                    // s_join is written again
     }
@@ -584,6 +584,8 @@ int row_tiles(int T, int S, int group, int D) {
 }
 // Whether a call takes the kernel for many rows a request.
 bool many_rows(int T, int S, int group) { return S <= fg::kAttnPromptRequests && rows_of(T, S, group) >= 64; }
+// Rows of its items.
+int prompt_rows(int T, int S, int group, int D) { return D <= 128 && rows_of(T, S, group) >= 256 ? 256 : 128; }
 
 bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
     return T >= 0 && S >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536 && D >= 1;
@@ -601,8 +603,7 @@ extern "C" {
 long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D) {
     if (!shapes_ok(T, S, Hq, Hkv, D) || (D != 64 && D != 128 && D != 256)) return -1;
     const bool many = many_rows(T, S > 0 ? S : 1, Hq / Hkv);
-    const long long slot = D == 64 ? fg::attn_slot<fg::kPromptRows, 64>() : D == 128 ? fg::attn_slot<fg::kPromptRows, 128>()
-                                                                                    : fg::attn_slot<fg::kPromptRows, 256>();
+    const long long slot = (long long)prompt_rows(T, S > 0 ? S : 1, Hq / Hkv, D) * (D + 2);
     const long long few = 2LL * fg::kAttnMaxCtas * kMaxSlot * 4, most = 2LL * fg::kAttnPromptCtas * slot * 4;
     return kCtrBytes + (many && most > few ? most : few);
 }
@@ -632,7 +633,7 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
                        scale * 1.4426950408889634f, reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCtrBytes),
                        st.status, st.timeout_ns};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (many_rows(T, S, Hq / Hkv)) return fg::launch_attn_prompt(p, D, st.sms, st.pdl, s);
+    if (many_rows(T, S, Hq / Hkv)) return fg::launch_attn_prompt(p, D, prompt_rows(T, S, Hq / Hkv, D), st.sms, st.pdl, s);
     const int nt = row_tiles(T, S, Hq / Hkv, D);
     switch (D) {
         case 64: return nt == 1 ? launch<2, 1>(p, st.sms, st.pdl, s) : nt == 2 ? launch<2, 2>(p, st.sms, st.pdl, s) : launch<2, 4>(p, st.sms, st.pdl, s);

@@ -225,7 +225,8 @@ struct AttnCursor {
     }
 };
 
-// Floats of a partial result: kRows maxima, kRows sums, kRows x D outputs.
+// Floats of a partial result: kRows maxima, kRows sums, kRows x D outputs (rows outermost, or kByColumn: groups of four
+// columns outermost, for writers that hold a row a thread).
 template <int kRows, int D>
 __host__ __device__ constexpr int attn_slot() { return kRows * (D + 2); }
 
@@ -243,9 +244,67 @@ __device__ __forceinline__ void attn_store(const AttnParams& p, int t0, int h, i
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// Joins the pieces of CTAs a to z, kFlight of them and kSame quarters of rows a thread in flight together.
+template <int kRows, int D, int kThreads, bool kByColumn, int kFlight, int kSame>
+__device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int z, int t0, int h, int row0, int rows) {
+    const int end = (kByColumn ? kRows : rows) * (D / 4);
+    for (int it0 = threadIdx.x; it0 < end; it0 += kThreads * kSame) {
+        float top[kSame], sum[kSame];
+        float4 acc[kSame];
+#pragma unroll
+        for (int q = 0; q < kSame; ++q) {
+            top[q] = kAttnEmpty;
+            sum[q] = 0.0f;
+            acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int k0 = a; k0 <= z; k0 += kFlight) {
+            float mk[kSame][kFlight], lk[kSame][kFlight];
+            float4 v[kSame][kFlight];
+#pragma unroll
+            for (int q = 0; q < kSame; ++q) {
+                const int it = min(it0 + q * kThreads, end - 1);
+                const int j = kByColumn ? it % kRows : it / (D / 4), d4 = kByColumn ? it / kRows : it % (D / 4);
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const float* s = attn_piece<kRows, D>(p, min(k0 + i, z), a);
+                    mk[q][i] = __ldcg(s + j);
+                    lk[q][i] = __ldcg(s + kRows + j);
+                    v[q][i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows) + (kByColumn ? it : j * (D / 4) + d4));
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kSame; ++q) {
+                float t = top[q];
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) t = fmaxf(t, mk[q][i]);
+                const float f = ex2(top[q] - t);
+                top[q] = t;
+                sum[q] *= f;
+                acc[q].x *= f; acc[q].y *= f; acc[q].z *= f; acc[q].w *= f;
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const float e = k0 + i <= z ? ex2(mk[q][i] - t) : 0.0f;
+                    sum[q] = fmaf(lk[q][i], e, sum[q]);
+                    acc[q].x = fmaf(v[q][i].x, e, acc[q].x); acc[q].y = fmaf(v[q][i].y, e, acc[q].y);
+                    acc[q].z = fmaf(v[q][i].z, e, acc[q].z); acc[q].w = fmaf(v[q][i].w, e, acc[q].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kSame; ++q) {
+            const int it = it0 + q * kThreads;
+            const float inv = sum[q] == 0.0f ? 0.0f : 1.0f / sum[q];
+            const int j = kByColumn ? it % kRows : it / (D / 4), d4 = kByColumn ? it / kRows : it % (D / 4);
+            if (it < end && j < rows)
+                attn_store<D>(p, t0, h, row0 + j, d4,
+                              make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv));
+        }
+    }
+}
+
 // Called by all threads once this CTA's piece is written: the CTA that arrives last joins the pieces of CTAs a to z, in
 // their order, and stores rows [row0, row0 + rows).
-template <int kRows, int D, int kThreads>
+template <int kRows, int D, int kThreads, bool kByColumn>
 __device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int a, int z, int t0, int h, int row0, int rows) {
     const int tid = threadIdx.x;
     __threadfence();
@@ -258,42 +317,14 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThr
     __syncthreads();
     if (!sm.last) return;
     __threadfence();
-    for (int it = tid; it < rows * (D / 4); it += kThreads) {
-        const int j = it / (D / 4), d4 = it % (D / 4);
-        float top = kAttnEmpty, sum = 0.0f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kFlight = 8;                            // pieces in flight together
-        for (int k0 = a; k0 <= z; k0 += kFlight) {
-            float mk[kFlight], lk[kFlight], t = top;
-            float4 v[kFlight];
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const float* s = attn_piece<kRows, D>(p, min(k0 + i, z), a);
-                mk[i] = __ldcg(s + j);
-                lk[i] = __ldcg(s + kRows + j);
-                v[i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows + j * D) + d4);
-            }
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i) t = fmaxf(t, mk[i]);
-            const float f = ex2(top - t);
-            top = t;
-            sum *= f;
-            acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const float e = k0 + i <= z ? ex2(mk[i] - t) : 0.0f;
-                sum = fmaf(lk[i], e, sum);
-                acc.x = fmaf(v[i].x, e, acc.x); acc.y = fmaf(v[i].y, e, acc.y);
-                acc.z = fmaf(v[i].z, e, acc.z); acc.w = fmaf(v[i].w, e, acc.w);
-            }
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        attn_store<D>(p, t0, h, row0 + j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    }
+    // pieces in flight together, times rows where there are many: most items are cut once, long ones many times
+    if (z - a < 2) attn_join_rows<kRows, D, kThreads, kByColumn, 2, (kRows * D / 4) / kThreads >= 4 ? 3 : 1>(p, a, z, t0, h, row0, rows);
+    else attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, z, t0, h, row0, rows);
 }
 
 // Launches the kernel for many rows a request (fg_attn_prompt.cu).
-int launch_attn_prompt(const AttnParams& p, int D, int sms, int pdl, cudaStream_t stream);
-constexpr int kPromptRows = 128, kAttnPromptCtas = 152, kAttnPromptRequests = 1024;
+// rows: of an item, 128 or (D <= 128) 256.
+int launch_attn_prompt(const AttnParams& p, int D, int rows, int sms, int pdl, cudaStream_t stream);
+constexpr int kAttnPromptCtas = 152, kAttnPromptRequests = 1024;
 
 }  // namespace fg

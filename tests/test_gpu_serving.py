@@ -77,7 +77,8 @@ def test_several_new_tokens(fg, d, hq, hkv, window):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("hq,hkv,new", [(2, 2, [70, 64, 65]), (8, 1, [30, 0, 17]), (6, 2, [1, 100, 9]), (16, 1, [8, 8, 3])])
+@pytest.mark.parametrize("hq,hkv,new", [(2, 2, [70, 64, 65]), (8, 1, [30, 0, 17]), (6, 2, [1, 100, 9]), (16, 1, [8, 8, 3]),
+                                        (16, 1, [40, 5, 61]), (4, 2, [300, 1, 150])])
 @pytest.mark.parametrize("window", [0, 33])
 @pytest.mark.parametrize("page", [16, 80])
 def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
@@ -93,8 +94,9 @@ def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_many_rows_over_long_contexts_are_split_and_joined(fg, d):
-    c = C.cache_case(d, [2500, 1800], [40, 1], 8, 1, d, 32)
+@pytest.mark.parametrize("new", [[40, 1], [70, 60]])
+def test_many_rows_over_long_contexts_are_split_and_joined(fg, d, new):
+    c = C.cache_case(d, [2500, 1800], new, 8, 1, d, 32)
     out, ws = attend(fg, c)
     expect(fg)
     check(c, out)
@@ -103,9 +105,10 @@ def test_many_rows_over_long_contexts_are_split_and_joined(fg, d):
         assert torch.equal(again, out)
 
 
-def test_many_rows_scores_that_keep_rising(fg):
+@pytest.mark.parametrize("new", [20, 50])
+def test_many_rows_scores_that_keep_rising(fg, new):
     """Keys whose scores rise by far more than a step of the running maximum, tile by tile, and fall again."""
-    c = C.cache_case(12, [1000], [20], 8, 1, 64, 16)
+    c = C.cache_case(12, [1000], [new], 8, 1, 64, 16)
     c["q"][:] = np.abs(c["q"])
     c["q_bits"], c["q"] = O.bf16(c["q"])
     n = np.arange(1000)
@@ -119,8 +122,9 @@ def test_many_rows_scores_that_keep_rising(fg):
     check(c, out)
 
 
-def test_many_rows_contract_violations_and_non_finite_queries(fg):
-    c = C.cache_case(13, [300, 90], [40, 30], 4, 2, 128, 16)
+@pytest.mark.parametrize("hq", [4, 16])
+def test_many_rows_contract_violations_and_non_finite_queries(fg, hq):
+    c = C.cache_case(13, [300, 90], [40, 30], hq, 2, 128, 16)
     c = dict(c, q_bits=np.concatenate([c["q_bits"]] * 1), table=c["table"].copy())
     ref = O.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["table"], c["start"], c["lens"], 128 ** -0.5, 0, 2.0 ** -8)
     c["q_bits"][5, 1, 7] = 0x7FC0
@@ -130,7 +134,7 @@ def test_many_rows_contract_violations_and_non_finite_queries(fg):
     expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
     got = f64(out)
     assert np.isnan(got[5, 1]).all() and np.isnan(got[6, 3]).any()
-    ok = np.ones((40, 4), bool)
+    ok = np.ones((40, hq), bool)
     ok[5, 1] = ok[6, 3] = False
     assert within(got[:40][ok], (ref[0][:40][ok], ref[1][:40][ok]), "bf16").all()
     # request 1 without the tokens of its third page: the others move up, positions and all
