@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     fg::grid_dependency_wait();
     if (tid == 0) fg::grid_launch_dependents();
 
-    fg::AttnCursor<kRows, kBlock, kThreads> cur;
+    fg::AttnCursor<kRows, kBlock, kThreads, true> cur;
     if (!cur.open(p, s_plan, s_pre)) return;
 
     // what a lane copies of a tile (16-byte chunk `lane`, and every 32nd on) and where it finds its operands in one
@@ -255,21 +255,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             cp_async_commit();
             return ok;
         };
-        // the first copies go ahead of q
-        uint32_t absent = 0;                                // bit: the stage's tile has no page
-        uint32_t page, off;
-#pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) {
-            next_page(base + i * kBlock, page, off);
-            if (!issue(page, off, i, base + i * kBlock < base_end)) absent |= 1u << i;
-        }
-        next_page(base + (C::kStages - 1) * kBlock, page, off);
-
-        // q of row tile nt: rows nt * 8 + g, elements 32 b + 8 c .. + 7, as FP16 times 2^x; returns 2^-x * scale
-        auto load_q = [&](int nt, uint32_t (&f)[B][4]) {
+        // q of row tile nt: rows nt * 8 + g, elements 32 b + 8 c .. + 7; then as FP16 times 2^x, with 2^-x * scale
+        auto load_q = [&](int nt, uint4 (&raw)[B]) {
             const int j = row0 + nt * 8 + g;
-            uint4 raw[B];
-            float amax = 0.0f;
 #pragma unroll
             for (int b = 0; b < B; ++b) raw[b] = make_uint4(0, 0, 0, 0);
             if (nt * 8 + g < rows) {
@@ -278,6 +266,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
 #pragma unroll
                 for (int b = 0; b < B; ++b) raw[b] = __ldcg(reinterpret_cast<const uint4*>(src + 32 * b));
             }
+        };
+        auto convert_q = [&](const uint4 (&raw)[B], uint32_t (&f)[B][4]) {
+            float amax = 0.0f;
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
@@ -298,20 +289,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
             return __uint_as_float(static_cast<uint32_t>(127 - x) << 23) * p.scale_log2;
         };
+        // One after another in flight: q, the pages of the first tiles, those tiles.
+        uint4 raw[B];
+        if (!C::kQShared || warp < NT) load_q(C::kQShared ? warp : 0, raw);
+        uint32_t absent = 0;                                // bit: the stage's tile has no page
+        uint32_t page, off;
+        {
+            uint32_t pages[C::kStages - 1], offs[C::kStages - 1];
+#pragma unroll
+            for (int i = 0; i < C::kStages - 1; ++i) next_page(base + i * kBlock, pages[i], offs[i]);
+            next_page(base + (C::kStages - 1) * kBlock, page, off);
+#pragma unroll
+            for (int i = 0; i < C::kStages - 1; ++i)
+                if (!issue(pages[i], offs[i], i, base + i * kBlock < base_end)) absent |= 1u << i;
+        }
         uint32_t qf[C::kQShared ? 1 : B][4];
         float qs1[C::kQShared ? 1 : NT][2];
         auto qs = [&](int nt, int k) { return C::kQShared ? s_qs[nt * 8 + 2 * c + k] : qs1[C::kQShared ? 0 : nt][k]; };
         if constexpr (C::kQShared) {
-            for (int nt = warp; nt < NT; nt += kWarps) {
+            static_assert(NT <= kWarps, "a row tile a warp");
+            if (warp < NT) {
                 uint32_t f[B][4];
-                const float down = load_q(nt, f);
+                const float down = convert_q(raw, f);
 #pragma unroll
-                for (int b = 0; b < B; ++b) s_q[(nt * B + b) * 32 + lane] = make_uint4(f[b][0], f[b][1], f[b][2], f[b][3]);
-                if (c == 0) s_qs[nt * 8 + g] = down;
+                for (int b = 0; b < B; ++b) s_q[(warp * B + b) * 32 + lane] = make_uint4(f[b][0], f[b][1], f[b][2], f[b][3]);
+                if (c == 0) s_qs[warp * 8 + g] = down;
             }
             __syncthreads();
         } else {
-            const float down = load_q(0, qf);
+            const float down = convert_q(raw, qf);
             qs1[0][0] = __shfl_sync(kAll, down, 8 * c);
             qs1[0][1] = __shfl_sync(kAll, down, 8 * c + 4);
         }

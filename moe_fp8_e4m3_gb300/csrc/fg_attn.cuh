@@ -64,16 +64,25 @@ struct AttnPlanSmem {
 };
 
 // Where a CTA stands in the line.
-template <int kRows, int kBlock, int kThreads>
+// kByRequest: requests bring few chunks.
+template <int kRows, int kBlock, int kThreads, bool kByRequest>
 struct AttnCursor {
     AttnRequest rq;
     AttnKeys keys;
     int r, ch, h, cost, off0;                  // request, chunk (of all), head, the item's cost, the share's begin within it
     unsigned long long begin;                  // where the item begins; the next one's while next() runs
 
+    static constexpr unsigned long long kCostMask = (1ull << 40) - 1;
+
+    static __device__ __forceinline__ void complain(const AttnParams& p, int q) {   // of a request without rows: are its lengths right?
+        const int t0 = __ldg(p.start + q), t1 = __ldg(p.start + q + 1), len = __ldg(p.lens + q);
+        if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page) kv_record(p.status, kKvErrAttention);
+    }
     __device__ __forceinline__ void look(const AttnParams& p, const int* s_pre) {
         rq = attn_request(p, r);
-        const int chunk = ch - s_pre[r];
+        look_at(p, ch - s_pre[r]);
+    }
+    __device__ __forceinline__ void look_at(const AttnParams& p, int chunk) {
         const int i0 = chunk * kRows / p.group, i1 = min(rq.n - 1, (chunk * kRows + kRows - 1) / p.group);
         keys.hi = rq.len - rq.n + i1 + 1;
         keys.lo = p.window > 0 ? max(0, rq.len - rq.n + i0 + 1 - p.window) : 0;
@@ -117,6 +126,30 @@ struct AttnCursor {
     // then blocks per chunk, are scanned in strips of consecutive entries.
     __device__ __forceinline__ bool open(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int* s_pre) {
         const int tid = threadIdx.x;
+        unsigned long long total_blocks;
+        if (kByRequest && p.S <= kThreads) {
+            // few chunks a request, a request a thread: chunks and costs in one scan
+            unsigned long long sum = 0, total;
+            ch = 0;
+            r = 0;
+            if (tid < p.S) {
+                rq = attn_request(p, tid);
+                if (blockIdx.x == 0 && rq.n == 0) complain(p, tid);
+                const int n = static_cast<int>(((long long)rq.n * p.group + kRows - 1) / kRows);
+                for (int i = 0; i < n; ++i) {
+                    look_at(p, i);
+                    sum += cost;
+                }
+                sum |= static_cast<unsigned long long>(n) << 40;   // costs stay below 2^36: 2^12 chunks of at most 2^24 blocks
+            }
+            const unsigned long long at = scan(sum, sm.warp, total);
+            sm.strip[tid] = at & kCostMask;
+            if (tid <= p.S) s_pre[tid] = static_cast<int>(at >> 40);
+            if (tid == 0 && p.S == kThreads) s_pre[kThreads] = static_cast<int>(total >> 40);
+            total_blocks = total & kCostMask;
+            __syncthreads();
+            return settle(p, sm, s_pre, total_blocks, true);
+        }
         const int per_r = (p.S + kThreads - 1) / kThreads;
         {
             unsigned long long sum = 0, total;
@@ -124,11 +157,7 @@ struct AttnCursor {
                 const int q = tid * per_r + i;
                 if (q >= p.S) break;
                 const AttnRequest x = attn_request(p, q);
-                if (blockIdx.x == 0 && x.n == 0) {
-                    const int t0 = __ldg(p.start + q), t1 = __ldg(p.start + q + 1), len = __ldg(p.lens + q);
-                    if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page)
-                        kv_record(p.status, kKvErrAttention);
-                }
+                if (blockIdx.x == 0 && x.n == 0) complain(p, q);
                 sum += ((long long)x.n * p.group + kRows - 1) / kRows;
             }
             unsigned long long at = scan(sum, sm.warp, total);
@@ -143,7 +172,6 @@ struct AttnCursor {
         __syncthreads();
         const int chunks = s_pre[p.S];
         const int per_c = (chunks + kThreads - 1) / kThreads;
-        unsigned long long total_blocks;
         {
             unsigned long long sum = 0;
             ch = tid * per_c;
@@ -160,23 +188,34 @@ struct AttnCursor {
             if (tid == 0) sm.strip[kThreads] = total_blocks;
         }
         __syncthreads();
+        return settle(p, sm, s_pre, total_blocks, false);
+    }
+
+    // Finds this CTA's share and its first item.  by_request: the strips are requests, else per_c chunks each.
+    __device__ __forceinline__ bool settle(const AttnParams& p, AttnPlanSmem<kThreads>& sm, const int* s_pre, unsigned long long total_blocks,
+                                           bool by_request) {
         const unsigned long long all = total_blocks * p.heads;
         // a share is worth an item's start
         const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kAttnStart) / (kAttnStart + 1));
         if (blockIdx.x >= shares) return false;
         const unsigned long long u = all * blockIdx.x / shares;
-        if (tid == 0) { sm.line[0] = shares; sm.line[1] = all; sm.line[2] = all * (blockIdx.x + 1) / shares; }
+        if (threadIdx.x == 0) { sm.line[0] = shares; sm.line[1] = all; sm.line[2] = all * (blockIdx.x + 1) / shares; }
         __syncthreads();
         // the chunk that holds u: its strip, then the strip's chunks one by one
-        int lo = 0, hi = kThreads;
+        int lo = 0, hi = by_request ? p.S : kThreads;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (sm.strip[mid] * p.heads <= u) lo = mid;
             else hi = mid;
         }
-        ch = lo * per_c;
         begin = sm.strip[lo] * p.heads;
-        r = find(s_pre, p.S, ch);
+        if (by_request) {
+            r = lo;
+            ch = s_pre[lo];
+        } else {
+            ch = lo * ((s_pre[p.S] + kThreads - 1) / kThreads);
+            r = find(s_pre, p.S, ch);
+        }
         while (s_pre[r + 1] <= ch) ++r;
         look(p, s_pre);
         while (begin + (unsigned long long)cost * p.heads <= u) {
@@ -318,7 +357,8 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThr
     if (!sm.last) return;
     __threadfence();
     // pieces in flight together, times rows where there are many: most items are cut once, long ones many times
-    if (z - a < 2) attn_join_rows<kRows, D, kThreads, kByColumn, 2, (kRows * D / 4) / kThreads >= 4 ? 3 : 1>(p, a, z, t0, h, row0, rows);
+    if (z - a >= 8 && kRows * D <= 4 * kThreads) attn_join_rows<kRows, D, kThreads, kByColumn, 16, 1>(p, a, z, t0, h, row0, rows);
+    else if (z - a < 2) attn_join_rows<kRows, D, kThreads, kByColumn, 2, (kRows * D / 4) / kThreads >= 4 ? 3 : 1>(p, a, z, t0, h, row0, rows);
     else attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, z, t0, h, row0, rows);
 }
 

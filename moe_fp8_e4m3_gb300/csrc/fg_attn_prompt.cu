@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
     __shared__ float s_top[2][128], s_l[2][128];               // of a row's two halves, or of two row tiles
     __shared__ int s_dead[kSoftWarps];
     __shared__ uint32_t s_absent[4][kDecodeWarps];             // of tile n in [n & 3], a decoder warp's tokens that have no page
-    __shared__ fg::AttnCursor<kRows, C::kTok, kThreads> s_cur;  // while the roles run, out of their registers
+    __shared__ fg::AttnCursor<kRows, C::kTok, kThreads, false> s_cur;  // while the roles run, out of their registers
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
     const uint32_t bar = sbase + C::kOffBar;
     const uint32_t k_full = bar, k_empty = bar + 8, v_full = bar + 16, v_empty = bar + 32, s_full = bar + 48, s_empty = bar + 64,
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
     const fg::WaitCtl wctl{abort_flag, p.status, p.timeout_ns};
     auto wait = [&](uint32_t b, uint32_t parity) { return fg::wait_bar<false, false>(b, parity, wctl, kWaitPrompt); };
 
-    fg::AttnCursor<kRows, kTok, kThreads> cur;
+    fg::AttnCursor<kRows, kTok, kThreads, false> cur;
     const bool any = cur.open(p, s_plan, s_pre);
     uint32_t n0 = 0;                                           // tiles of the pieces before this one
     while (any) {
