@@ -676,9 +676,9 @@ def _cache(k_cache, k_sf, v_cache, v_sf):
             k_sf.is_cuda and v_cache.is_cuda and v_sf.is_cuda and k_cache.is_contiguous() and k_sf.is_contiguous() and
             v_cache.is_contiguous() and v_sf.is_contiguous()):
         _check_all(k_cache, "k_cache", "u", k_sf, "k_sf", "u", v_cache, "v_cache", "u", v_sf, "v_sf", "u")
-    shape, sf = k_cache.shape, k_sf.shape
-    pages, heads, size, half = shape
-    if half % 16 or v_cache.shape != shape or v_sf.shape != sf or sf != (pages, heads, size, half // 16):
+    pages, heads, size, half = k_cache.shape
+    n = k_cache.nbytes                                      # a byte an element: sizes say what a kernel may read
+    if half % 16 or v_cache.nbytes != n or k_sf.nbytes * 16 != n or v_sf.nbytes * 16 != n:
         raise ValueError("cache: codes [num_pages, heads, page_size, D/2], scales [num_pages, heads, page_size, D/32]")
     return pages, heads, size, 2 * half
 

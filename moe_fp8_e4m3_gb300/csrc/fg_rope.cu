@@ -1,13 +1,13 @@
 // fg_rope.cu - norms of queries and keys for each head with the position rotation, in one pass.
 //
-// A head of D elements is held by L lanes of eight consecutive elements each (L: D / 8 rounded up to a
-// power of two), in registers from its one read to its one write: sum of squares over the lanes, then
+// A head of D elements is held by L lanes (L: D / 8 rounded up to a power of two), eight elements each, in
+// registers from its one read to its one write: sum of squares over the lanes, then
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin)
-// in FP32, rounded once.  Pairs are neighbours, which a lane holds itself, or halves of the rotated part,
-// where a lane takes its partner's four words by shuffles (and the partner's weights from memory).
-// Bound: HBM bytes for many tokens (each element read and written once), launch latency for few.  The
-// rotation's FP32 cosines and sines take four times the bytes of a lane's elements, so a lane keeps them
-// for kHeads heads of its token, whose loads are all in flight together.
+// in FP32, rounded once.  A lane holds both elements of its four pairs (two runs of four elements, from the two halves
+// of the rotated part or side by side), so that it needs four cosines and sines and nothing of its neighbours; lanes
+// behind the rotated part hold eight elements that stay.
+// Bound: HBM bytes for many tokens (each element read and written once), launch latency for few.  A lane keeps its
+// cosines, sines and weights for kHeads heads of its token, whose loads are all in flight together.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,19 +32,21 @@ struct RopeParams {
     int* status;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+__device__ __forceinline__ void unpack4(const uint2& x, float (&f)[4]) {
+    f[0] = __uint_as_float(x.x << 16);
+    f[1] = __uint_as_float(x.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(x.y << 16);
+    f[3] = __uint_as_float(x.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // One (token, chunk of kHeads query or key heads) per group of L lanes; all lanes of the warp stay for
 // the shuffles.
 template <int L, int kHeads, bool kPairs>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 7) rope_kernel(const RopeParams p) {
     constexpr uint32_t kAll = 0xffffffffu;
     fg::grid_dependency_wait();
     if (threadIdx.x == 0) fg::grid_launch_dependents();
@@ -56,87 +58,72 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     const bool is_q = chunk < p.q_chunks;
     const int h0 = (is_q ? chunk : chunk - p.q_chunks) * kHeads;
     const int heads = is_q ? p.Hq : p.Hkv;
-    const int e0 = 8 * l;                                     // first element of this lane
     const int pos = live ? __ldg(p.positions + t) : -1;
     if (pos >= p.max_pos && l == 0) fg::kv_record(p.status, fg::kKvErrPosition);
-    live = live && pos >= 0 && pos < p.max_pos && e0 < p.D;
+    const bool turned = 8 * l < p.rot;
+    const int ea = kPairs ? 8 * l : turned ? 4 * l : p.rot + 8 * (l - p.rot / 8);      // this lane's two runs of four
+    const int eb = !kPairs && turned ? p.rot / 2 + 4 * l : ea + 4;
+    live = live && pos >= 0 && pos < p.max_pos && 8 * l < p.D;
 
-    const uint16_t* src = (is_q ? p.q + t * p.q_ld : p.k + t * p.k_ld) + (long long)h0 * p.D + e0;
-    uint16_t* dst = (is_q ? p.qo + t * p.qo_ld : p.ko + t * p.ko_ld) + (long long)h0 * p.D + e0;
-    uint4 x[kHeads];
+    const uint16_t* src = (is_q ? p.q + t * p.q_ld : p.k + t * p.k_ld) + (long long)h0 * p.D;
+    uint16_t* dst = (is_q ? p.qo + t * p.qo_ld : p.ko + t * p.ko_ld) + (long long)h0 * p.D;
+    uint2 xa[kHeads], xb[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (live && h0 + i < heads) x[i] = *reinterpret_cast<const uint4*>(src + (long long)i * p.D);
-    }
-    const int half = p.rot / 2;
-    const bool turned = live && e0 < p.rot;
-    const bool second = !kPairs && e0 >= half;                // this lane's elements are the pairs' b
-    const int partner = (threadIdx.x & 31) - l + (turned && !kPairs ? (second ? l - half / 8 : l + half / 8) : l);
-    float cs[8], sn[8];                                       // pairs: four of each
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { cs[i] = 1.0f; sn[i] = 0.0f; }
-    if (turned) {
-        const float* row = p.cos_sin + (long long)pos * p.rot + (kPairs ? e0 / 2 : (second ? e0 - half : e0));
-#pragma unroll
-        for (int i = 0; i < (kPairs ? 4 : 8); i += 4) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(row + i));
-            const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i));
-            cs[i] = c.x; cs[i + 1] = c.y; cs[i + 2] = c.z; cs[i + 3] = c.w;
-            sn[i] = s.x; sn[i + 1] = s.y; sn[i + 2] = s.z; sn[i + 3] = s.w;
+        xa[i] = xb[i] = make_uint2(0, 0);
+        if (live && h0 + i < heads) {
+            xa[i] = *reinterpret_cast<const uint2*>(src + i * p.D + ea);
+            xb[i] = *reinterpret_cast<const uint2*>(src + i * p.D + eb);
         }
     }
+    float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (live && turned) {
+        const float* row = p.cos_sin + (long long)pos * p.rot + 4 * l;
+        cs = __ldg(reinterpret_cast<const float4*>(row));
+        sn = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2));
+    }
     const uint16_t* w = is_q ? p.qw : p.kw;
-    float wt[8], wp[8];                                       // this lane's weights, its partner's
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wt[i] = wp[i] = 1.0f;
+    uint2 wa = make_uint2(0, 0), wb = wa;                     // as they are stored: registers hold more heads
     if (w && live) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + e0)), wt);
-        if (!kPairs && turned) unpack8(__ldg(reinterpret_cast<const uint4*>(w + (second ? e0 - half : e0 + half))), wp);
+        wa = __ldg(reinterpret_cast<const uint2*>(w + ea));
+        wb = __ldg(reinterpret_cast<const uint2*>(w + eb));
     }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        float f[8], g[8];
-        unpack8(x[i], f);
-        float r = 1.0f;
+        float a[4], b[4];
+        unpack4(xa[i], a);
+        unpack4(xb[i], b);
         if (p.qw || p.kw) {                                   // the same for the whole grid
             float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+            for (int j = 0; j < 4; ++j) sum = fmaf(a[j], a[j], fmaf(b[j], b[j], sum));
 #pragma unroll
             for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (w) r = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-        }
-        if constexpr (!kPairs) {
-            uint4 y;
-            y.x = __shfl_sync(kAll, x[i].x, partner);
-            y.y = __shfl_sync(kAll, x[i].y, partner);
-            y.z = __shfl_sync(kAll, x[i].z, partner);
-            y.w = __shfl_sync(kAll, x[i].w, partner);
-            unpack8(y, g);
+            if (w) {
+                const float r = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+                float fa[4], fb[4];
+                unpack4(wa, fa);
+                unpack4(wb, fb);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = g[j] * r * wp[j];
-        }
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * wt[j];
-        if constexpr (kPairs) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[2 * j] = f[2 * j] * cs[j] - f[2 * j + 1] * sn[j];
-                o[2 * j + 1] = f[2 * j + 1] * cs[j] + f[2 * j] * sn[j];
+                for (int j = 0; j < 4; ++j) {
+                    a[j] = a[j] * r * fa[j];
+                    b[j] = b[j] * r * fb[j];
+                }
             }
+        }
+        uint2 ya, yb;
+        if constexpr (kPairs) {
+            ya = pack4(a[0] * cs.x - a[1] * sn.x, a[1] * cs.x + a[0] * sn.x, a[2] * cs.y - a[3] * sn.y, a[3] * cs.y + a[2] * sn.y);
+            yb = pack4(b[0] * cs.z - b[1] * sn.z, b[1] * cs.z + b[0] * sn.z, b[2] * cs.w - b[3] * sn.w, b[3] * cs.w + b[2] * sn.w);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = second ? f[j] * cs[j] + g[j] * sn[j] : f[j] * cs[j] - g[j] * sn[j];
+            ya = pack4(a[0] * cs.x - b[0] * sn.x, a[1] * cs.y - b[1] * sn.y, a[2] * cs.z - b[2] * sn.z, a[3] * cs.w - b[3] * sn.w);
+            yb = pack4(b[0] * cs.x + a[0] * sn.x, b[1] * cs.y + a[1] * sn.y, b[2] * cs.z + a[2] * sn.z, b[3] * cs.w + a[3] * sn.w);
         }
-        uint32_t out[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 v = turned ? __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]) : __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-            out[j] = *reinterpret_cast<const uint32_t*>(&v);
+        if (live && h0 + i < heads) {
+            // an element that is not turned keeps its value, also where its partner in the lane is not finite
+            *reinterpret_cast<uint2*>(dst + i * p.D + ea) = turned ? ya : pack4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint2*>(dst + i * p.D + eb) = turned ? yb : pack4(b[0], b[1], b[2], b[3]);
         }
-        if (live && h0 + i < heads) *reinterpret_cast<uint4*>(dst + (long long)i * p.D) = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }
 
@@ -170,7 +157,7 @@ int launch(RopeParams p, bool pairs, int pdl, cudaStream_t stream) {
 template <int L>
 int launch_heads(const RopeParams& p, bool pairs, int sms, int pdl, cudaStream_t stream) {
     const long long warps = (long long)p.T * (p.Hq + p.Hkv) * L / 32;
-    return warps >= (long long)sms * 64 ? launch<L, 4>(p, pairs, pdl, stream) : launch<L, 1>(p, pairs, pdl, stream);
+    return warps >= (long long)sms * 64 ? launch<L, 8>(p, pairs, pdl, stream) : launch<L, 1>(p, pairs, pdl, stream);
 }
 
 }  // namespace
