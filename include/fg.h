@@ -497,12 +497,14 @@ int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k_j) v_j      (kv head h / (Hq / Hkv))
  * with cached position j at offset j mod page_size of page block_table[r][j / page_size].  FP32 scores,
  * statistics and sums; a weight is rounded once, to FP16, or to BF16 where an average request (ceil(T / S) rows)
- * brings at least 64 rows of a kv head (S <= 1024), which go to the tensor cores 128 at a time.  A row that looks at nothing (p < 0) becomes 0.
+ * brings at least 64 rows of a kv head (S <= 1024), which go to the tensor cores 128 or 256 at a time.  A row that
+ * looks at nothing (p < 0) becomes 0.
  * Rows >= query_start[S] stay as they were; what the cache holds behind a request's length is never used.
  *   q, out [T][Hq][D] BF16;  block_table [S][max_pages], query_start [S + 1], seq_lens [S] int32
  * query_start that falls or leaves [0, T], a seq_lens outside [0, max_pages * page_size]: 0x10A is recorded and
  * the request's rows stay as they were.  A page outside [0, num_pages): 0x10A, and its tokens count as absent.
- *   workspace: fg_paged_attention_workspace bytes (11 to 40 MB), under the same rules as fg_moe_mlp_workspace
+ *   workspace: fg_paged_attention_workspace bytes (11 to 40 MB; enough for any call of as many rows or fewer), under the same
+ *   rules as fg_moe_mlp_workspace
  * Hq % Hkv == 0.  Supported: S <= 4096, T <= 2^18, Hq / Hkv <= 256.
  */
 long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D);   /* bytes, or -1 */

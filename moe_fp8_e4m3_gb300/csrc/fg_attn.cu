@@ -47,7 +47,7 @@ struct Cfg {
     static constexpr int kPad = D + 4;         // floats of a row in shared memory: conflict-free 16-byte stores
     static constexpr int kJoin = kWarps * kRows * kPad * 4;
     // a warp's ring: per tile 16 key rows, 16 value rows, their scales
-    static constexpr int kStages = 4;
+    static constexpr int kStages = 3;
     static constexpr int kTileV = 16 * 16 * B, kTileKs = 2 * kTileV, kTileVs = kTileKs + 16 * B, kTile = kTileVs + 16 * B;
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kMain = kJoin > kRing ? kJoin : kRing;          // the join comes when the ring is empty
@@ -600,7 +600,7 @@ bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
 // Floats of the largest partial result of this file's variants.
 constexpr int kMaxSlot = Cfg<2, 4>::kSlot;
 static_assert(Cfg<4, 2>::kSlot <= kMaxSlot && Cfg<8, 1>::kSlot <= kMaxSlot, "largest partial result");
-constexpr long long kCtrBytes = (fg::kAttnMaxCtas * 4 + 255) / 256 * 256;
+constexpr long long kCtrBytes = (3 * fg::kAttnMaxCtas * 4 + 255) / 256 * 256;
 
 }  // namespace
 
@@ -608,8 +608,9 @@ extern "C" {
 
 long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D) {
     if (!shapes_ok(T, S, Hq, Hkv, D) || (D != 64 && D != 128 && D != 256)) return -1;
-    const bool many = many_rows(T, S > 0 ? S : 1, Hq / Hkv);
-    const long long slot = (long long)prompt_rows(T, S > 0 ? S : 1, Hq / Hkv, D) * (D + 2);
+    // enough for any fewer rows and requests too
+    const bool many = many_rows(T, 1, Hq / Hkv);
+    const long long slot = (long long)prompt_rows(T, 1, Hq / Hkv, D) * (D + 2);
     const long long few = 2LL * fg::kAttnMaxCtas * kMaxSlot * 4, most = 2LL * fg::kAttnPromptCtas * slot * 4;
     return kCtrBytes + (many && most > few ? most : few);
 }

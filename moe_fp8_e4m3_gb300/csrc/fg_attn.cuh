@@ -14,8 +14,6 @@
 
 namespace fg {
 
-constexpr int kAttnStart = 3;                 // what every item takes besides its keys (its q, filling the pipeline,
-                                              // the join), in blocks
 constexpr int kAttnMaxCtas = 640;             // shares of a launch, at most
 constexpr int kAttnMaxRequests = 4096;
 constexpr float kAttnEmpty = -1e30f;          // maximum of a row without a key
@@ -28,7 +26,7 @@ struct AttnParams {
     uint16_t* out;
     int T, S, heads, group, page, pages, max_pages, window;
     float scale_log2;                          // scale * log2(e)
-    unsigned* ctr;                             // [kAttnMaxCtas]
+    unsigned* ctr;                             // [3 * kAttnMaxCtas]: per item, then per eight pieces
     float* part;                               // [2 * kAttnMaxCtas][kRows][D + 2]: M, l, O
     int* status;
     unsigned long long timeout_ns;
@@ -64,7 +62,7 @@ struct AttnPlanSmem {
 };
 
 // Where a CTA stands in the line.
-// kByRequest: requests bring few chunks.
+// kByRequest: requests bring few chunks (and a CTA's blocks are short).
 template <int kRows, int kBlock, int kThreads, bool kByRequest>
 struct AttnCursor {
     AttnRequest rq;
@@ -72,6 +70,8 @@ struct AttnCursor {
     int r, ch, h, cost, off0;                  // request, chunk (of all), head, the item's cost, the share's begin within it
     unsigned long long begin;                  // where the item begins; the next one's while next() runs
 
+    // What every item takes besides its keys (its q, filling the pipeline, the join), in blocks.
+    static constexpr int kStart = kByRequest ? 5 : 3;
     static constexpr unsigned long long kCostMask = (1ull << 40) - 1;
 
     static __device__ __forceinline__ void complain(const AttnParams& p, int q) {   // of a request without rows: are its lengths right?
@@ -86,7 +86,7 @@ struct AttnCursor {
         const int i0 = chunk * kRows / p.group, i1 = min(rq.n - 1, (chunk * kRows + kRows - 1) / p.group);
         keys.hi = rq.len - rq.n + i1 + 1;
         keys.lo = p.window > 0 ? max(0, rq.len - rq.n + i0 + 1 - p.window) : 0;
-        cost = kAttnStart + (keys.hi > keys.lo ? (keys.hi + kBlock - 1) / kBlock - keys.lo / kBlock : 1);
+        cost = kStart + (keys.hi > keys.lo ? (keys.hi + kBlock - 1) / kBlock - keys.lo / kBlock : 1);
     }
 
     // Sum of v over the threads before this one, and of all.
@@ -196,7 +196,7 @@ struct AttnCursor {
                                            bool by_request) {
         const unsigned long long all = total_blocks * p.heads;
         // a share is worth an item's start
-        const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kAttnStart) / (kAttnStart + 1));
+        const unsigned long long shares = min(static_cast<unsigned long long>(gridDim.x), (all + kStart) / (kStart + 1));
         if (blockIdx.x >= shares) return false;
         const unsigned long long u = all * blockIdx.x / shares;
         if (threadIdx.x == 0) { sm.line[0] = shares; sm.line[1] = all; sm.line[2] = all * (blockIdx.x + 1) / shares; }
@@ -233,18 +233,18 @@ struct AttnCursor {
     // Blocks [b0, b1) of the current item that are this share's; false: none of them, and the share ends here.
     __device__ __forceinline__ bool piece(AttnPlanSmem<kThreads>& sm, int& b0, int& b1) const {
         const int off1 = static_cast<int>(min(static_cast<unsigned long long>(cost), sm.line[2] - begin));
-        if (off1 <= kAttnStart) return false;
+        if (off1 <= kStart) return false;
         if (threadIdx.x == 0) sm.line[3] = begin;            // read again behind the piece's first barrier
         const int block0 = keys.hi > keys.lo ? keys.lo / kBlock : 0;
-        b0 = block0 + max(off0 - kAttnStart, 0);
-        b1 = block0 + off1 - kAttnStart;
+        b0 = block0 + max(off0 - kStart, 0);
+        b1 = block0 + off1 - kStart;
         return true;
     }
 
     // The CTAs that hold pieces of the current item, first and last.
     __device__ __forceinline__ void holders(AttnPlanSmem<kThreads>& sm, int& a, int& z) const {
         const unsigned long long at = sm.line[3], shares = sm.line[0], all = sm.line[1];
-        a = static_cast<int>(((at + kAttnStart + 1) * shares - 1) / all);
+        a = static_cast<int>(((at + kStart + 1) * shares - 1) / all);
         z = static_cast<int>(((at + cost) * shares - 1) / all);
     }
 
@@ -283,9 +283,10 @@ __device__ __forceinline__ void attn_store(const AttnParams& p, int t0, int h, i
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// Joins the pieces of CTAs a to z, kFlight of them and kSame quarters of rows a thread in flight together.
-template <int kRows, int D, int kThreads, bool kByColumn, int kFlight, int kSame>
-__device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int z, int t0, int h, int row0, int rows) {
+// Joins `count` pieces of the item that begins at CTA a, those of CTAs k0, k0 + stride, ...; kFlight of them and kSame
+// quarters of rows a thread in flight together.  done(it, maximum, sum, four outputs) takes each quarter row.
+template <int kRows, int D, int kThreads, bool kByColumn, int kFlight, int kSame, class F>
+__device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int k0, int count, int stride, int rows, const F& done) {
     const int end = (kByColumn ? kRows : rows) * (D / 4);
     for (int it0 = threadIdx.x; it0 < end; it0 += kThreads * kSame) {
         float top[kSame], sum[kSame];
@@ -296,19 +297,19 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int z
             sum[q] = 0.0f;
             acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int k0 = a; k0 <= z; k0 += kFlight) {
+        for (int x = 0; x < count; x += kFlight) {
             float mk[kSame][kFlight], lk[kSame][kFlight];
             float4 v[kSame][kFlight];
 #pragma unroll
             for (int q = 0; q < kSame; ++q) {
                 const int it = min(it0 + q * kThreads, end - 1);
-                const int j = kByColumn ? it % kRows : it / (D / 4), d4 = kByColumn ? it / kRows : it % (D / 4);
+                const int j = kByColumn ? it % kRows : it / (D / 4);
 #pragma unroll
                 for (int i = 0; i < kFlight; ++i) {
-                    const float* s = attn_piece<kRows, D>(p, min(k0 + i, z), a);
+                    const float* s = attn_piece<kRows, D>(p, k0 + min(x + i, count - 1) * stride, a);
                     mk[q][i] = __ldcg(s + j);
                     lk[q][i] = __ldcg(s + kRows + j);
-                    v[q][i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows) + (kByColumn ? it : j * (D / 4) + d4));
+                    v[q][i] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows) + it);
                 }
             }
 #pragma unroll
@@ -322,7 +323,7 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int z
                 acc[q].x *= f; acc[q].y *= f; acc[q].z *= f; acc[q].w *= f;
 #pragma unroll
                 for (int i = 0; i < kFlight; ++i) {
-                    const float e = k0 + i <= z ? ex2(mk[q][i] - t) : 0.0f;
+                    const float e = x + i < count ? ex2(mk[q][i] - t) : 0.0f;
                     sum[q] = fmaf(lk[q][i], e, sum[q]);
                     acc[q].x = fmaf(v[q][i].x, e, acc[q].x); acc[q].y = fmaf(v[q][i].y, e, acc[q].y);
                     acc[q].z = fmaf(v[q][i].z, e, acc[q].z); acc[q].w = fmaf(v[q][i].w, e, acc[q].w);
@@ -330,36 +331,64 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, int a, int z
             }
         }
 #pragma unroll
-        for (int q = 0; q < kSame; ++q) {
-            const int it = it0 + q * kThreads;
-            const float inv = sum[q] == 0.0f ? 0.0f : 1.0f / sum[q];
-            const int j = kByColumn ? it % kRows : it / (D / 4), d4 = kByColumn ? it / kRows : it % (D / 4);
-            if (it < end && j < rows)
-                attn_store<D>(p, t0, h, row0 + j, d4,
-                              make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv));
-        }
+        for (int q = 0; q < kSame; ++q)
+            if (it0 + q * kThreads < end) done(it0 + q * kThreads, top[q], sum[q], acc[q]);
     }
 }
 
-// Called by all threads once this CTA's piece is written: the CTA that arrives last joins the pieces of CTAs a to z, in
-// their order, and stores rows [row0, row0 + rows).
-template <int kRows, int D, int kThreads, bool kByColumn>
-__device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int a, int z, int t0, int h, int row0, int rows) {
-    const int tid = threadIdx.x;
+// Whether this CTA is the last of `count` to arrive at a counter, which is left at zero.  All threads call it, behind
+// what they have written for the others.
+template <int kThreads>
+__device__ __forceinline__ bool attn_last(AttnPlanSmem<kThreads>& sm, unsigned* ctr, int count) {
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        const unsigned before = atomicAdd(p.ctr + a, 1u);
-        sm.last = before == static_cast<unsigned>(z - a);
-        if (sm.last) p.ctr[a] = 0;
+    if (threadIdx.x == 0) {
+        sm.last = atomicAdd(ctr, 1u) == static_cast<unsigned>(count - 1);
+        if (sm.last) *ctr = 0;
     }
     __syncthreads();
-    if (!sm.last) return;
+    if (!sm.last) return false;
     __threadfence();
+    return true;
+}
+
+// Called by all threads once this CTA's piece is written: the CTA that arrives last joins the pieces of CTAs a to z, in
+// their order, and stores rows [row0, row0 + rows).  Many pieces of few rows are joined eight at a time first, each
+// eight by its own last CTA.
+template <int kRows, int D, int kThreads, bool kByColumn>
+__device__ __forceinline__ void attn_join(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int a, int z, int t0, int h, int row0, int rows) {
+    auto store = [&](int it, float, float sum, const float4& v) {
+        const int j = kByColumn ? it % kRows : it / (D / 4), d4 = kByColumn ? it / kRows : it % (D / 4);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (j < rows) attn_store<D>(p, t0, h, row0 + j, d4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    };
+    const int n = z - a + 1;
+    if (!kByColumn && n > 12) {
+        const int k0 = a + (static_cast<int>(blockIdx.x) - a) / 8 * 8, eight = min(8, z - k0 + 1);
+        if (!attn_last<kThreads>(sm, p.ctr + kAttnMaxCtas + 2 * k0 + (k0 == a), eight)) return;
+        float* slot = attn_piece<kRows, D>(p, k0, a);
+        float* tops = reinterpret_cast<float*>(sm.strip);    // the plan is done with it: the joined maxima and sums
+        static_assert(sizeof(sm.strip) >= 2 * kRows * sizeof(float) || kByColumn, "room for them");
+        attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, k0, eight, 1, rows, [&](int it, float top, float sum, const float4& v) {
+            reinterpret_cast<float4*>(slot + 2 * kRows)[it] = v;
+            if (it % (D / 4) == 0) {
+                tops[it / (D / 4)] = top;
+                tops[kRows + it / (D / 4)] = sum;
+            }
+        });
+        __syncthreads();                                     // every thread has read the pieces' own
+        for (int j = threadIdx.x; j < rows; j += kThreads) {
+            slot[j] = tops[j];
+            slot[kRows + j] = tops[kRows + j];
+        }
+        if (!attn_last<kThreads>(sm, p.ctr + a, (n + 7) / 8)) return;
+        attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, a, (n + 7) / 8, 8, rows, store);
+        return;
+    }
+    if (!attn_last<kThreads>(sm, p.ctr + a, n)) return;
     // pieces in flight together, times rows where there are many: most items are cut once, long ones many times
-    if (z - a >= 8 && kRows * D <= 4 * kThreads) attn_join_rows<kRows, D, kThreads, kByColumn, 16, 1>(p, a, z, t0, h, row0, rows);
-    else if (z - a < 2) attn_join_rows<kRows, D, kThreads, kByColumn, 2, (kRows * D / 4) / kThreads >= 4 ? 3 : 1>(p, a, z, t0, h, row0, rows);
-    else attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, z, t0, h, row0, rows);
+    if (n <= 2) attn_join_rows<kRows, D, kThreads, kByColumn, 2, (kRows * D / 4) / kThreads >= 4 ? 3 : 1>(p, a, a, n, 1, rows, store);
+    else attn_join_rows<kRows, D, kThreads, kByColumn, 8, 1>(p, a, a, n, 1, rows, store);
 }
 
 // Launches the kernel for many rows a request (fg_attn_prompt.cu).

@@ -106,7 +106,11 @@ def test_calls_with_their_arguments_in_one_record(fg):
 def test_workspace_sizes(fg):
     size = fg.lib.fg_paged_attention_workspace
     assert size(4, 2, 7, 2, 128) == -1 and size(-1, 2, 8, 2, 128) == -1 and size(4, 2, 8, 2, 96) == -1
-    assert 0 < size(1, 1, 8, 1, 128) == size(8192, 4000, 64, 1, 64) == size(1, 0, 1, 1, 256) < size(64, 1, 1, 1, 128) < size(64, 1, 1, 1, 256)
+    assert 0 < size(1, 1, 8, 1, 128) == size(63, 7, 1, 1, 64) == size(1, 0, 1, 1, 256) < size(64, 1, 1, 1, 128) < size(64, 1, 1, 1, 256)
+    for hq in (1, 8, 64):                   # what serves many rows serves fewer, of any number of requests
+        for d in (64, 128, 256):
+            sizes = [size(t, s, hq, 1, d) for t in (1, 4, 7, 8, 31, 32, 63, 64, 255, 256, 8192) for s in (1, 4096)]
+            assert sizes == sorted(sizes)
 
 
 def test_no_device_fails_loudly(fg):

@@ -62,7 +62,7 @@ def test_decode_over_ragged_lengths(fg, d, hq, hkv, page):
     out, ws = attend(fg, c)
     expect(fg)
     check(c, out)
-    assert not ws[:2560].any(), "counters are left as they were"
+    assert not ws[:7680].any(), "counters are left as they were"
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -90,7 +90,7 @@ def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
     out, ws = attend(fg, c, window)
     expect(fg)
     check(c, out, window)
-    assert not ws[:2560].any(), "counters are left as they were"
+    assert not ws[:7680].any(), "counters are left as they were"
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
