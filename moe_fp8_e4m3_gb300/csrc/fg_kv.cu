@@ -4,7 +4,10 @@
 // neighbouring lanes, and the eight elements of lane 4 b + c are the word (b, c) of a key row.  A value
 // row wants half words (b, 2c) and (b, 2c + 1) instead, the first of block b beside the first of block
 // b + 1: lanes of neighbouring blocks trade one half word each, so every lane stores one whole word.
-// Bound: HBM bytes for many tokens, launch latency for few.
+// A thread has its part of one or two heads of a token in flight, keys and values both.
+// Bound: HBM bytes and, near them, instructions for many tokens (8192 tokens of 8 heads of 128 in and out
+// again, 85 MB: 15.2 us, 5.6 TB/s; an append runs some 200 instructions per 16 lanes' row), launch latency for few
+// (37 tokens: 3.5 us for both calls).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,15 +46,15 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+__device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
 // Codes of a lane's eight elements (code i at bits 4i) and its block's scale exponent.
 __device__ __forceinline__ uint32_t encode8(const uint4& x, int& e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float amax = 0.0f;
+    __nv_bfloat162 most = __habs2(pair(w[0]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = bf2(w[i]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
+    for (int i = 1; i < 4; ++i) most = __hmax2(most, __habs2(pair(w[i])));
+    float amax = fmaxf(__low2float(most), __high2float(most));       // NaN is passed over
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     e = kv_exponent(amax);
@@ -66,57 +69,64 @@ __device__ __forceinline__ uint32_t encode8(const uint4& x, int& e) {
     return codes;
 }
 
+// What a thread works on: its part of up to kRows heads of one token.
 struct Item {
-    int t, h, l;                  // token, head, lane within the row
-    bool live;
-    long long row;                // row of the cache, -1: none
+    int t, h, n;                  // token, first head, heads; n < 0: the slot is outside the cache
+    long long row;                // the first head's row of the cache, the next one's p.page rows on
 };
 
-// L = D / 8 lanes per (token, head); every lane of the warp stays for the shuffles.
-template <int L>
+// L = D / 8 lanes per token and kRows heads; every lane of the warp stays for the shuffles.  A thread without work gets
+// a place that it may read.
+template <int L, int kRows>
 __device__ __forceinline__ Item item_of(const KvParams& p) {
-    Item it;
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) / L;
-    it.l = threadIdx.x % L;
-    it.live = i < (long long)p.T * p.heads;
-    it.t = it.live ? static_cast<int>(i / p.heads) : 0;
-    it.h = it.live ? static_cast<int>(i % p.heads) : 0;
-    it.row = -1;
-    if (it.live) {
-        const int slot = __ldg(p.slots + it.t);
-        if (slot >= p.slots_total) {
-            if (it.l == 0) fg::kv_record(p.status, fg::kKvErrSlot);
-        } else if (slot >= 0) {
-            it.row = ((long long)(slot / p.page) * p.heads + it.h) * p.page + slot % p.page;
-        }
-    }
-    return it;
+    const unsigned x = blockIdx.x * static_cast<unsigned>(kThreads / L) + threadIdx.x / L;
+    const unsigned groups = (static_cast<unsigned>(p.heads) + kRows - 1) / kRows, t = x / groups;
+    if (t >= static_cast<unsigned>(p.T)) return Item{0, 0, 0, 0};
+    const int slot = __ldg(p.slots + t), h = static_cast<int>(x - t * groups) * kRows;
+    if (slot < 0 || slot >= p.slots_total) return Item{static_cast<int>(t), h, slot < 0 ? 0 : -1, 0};
+    const unsigned page = static_cast<unsigned>(slot) / static_cast<unsigned>(p.page);
+    return Item{static_cast<int>(t), h, min(kRows, p.heads - h),
+                ((long long)page * p.heads + h) * p.page + (slot - page * static_cast<unsigned>(p.page))};
+}
+template <int L>
+__device__ __forceinline__ void complain(const KvParams& p, const Item& it) {
+    if (it.n < 0 && it.h == 0 && threadIdx.x % L == 0) fg::kv_record(p.status, fg::kKvErrSlot);
 }
 
-template <int L>
+template <int L, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvParams p) {
     constexpr int B = L / 4;
     fg::grid_dependency_wait();
     if (threadIdx.x == 0) fg::grid_launch_dependents();
-    const Item it = item_of<L>(p);
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    if (it.row >= 0) {
-        k = __ldg(reinterpret_cast<const uint4*>(p.k_in + it.t * p.k_ld + it.h * (8 * L)) + it.l);
-        v = __ldg(reinterpret_cast<const uint4*>(p.v_in + it.t * p.v_ld + it.h * (8 * L)) + it.l);
+    const Item it = item_of<L, kRows>(p);
+    const int l = threadIdx.x % L, b = l / 4, c = l % 4;
+    const uint4* kin = reinterpret_cast<const uint4*>(p.k_in + it.t * p.k_ld + it.h * (8 * L)) + l;
+    const uint4* vin = reinterpret_cast<const uint4*>(p.v_in + it.t * p.v_ld + it.h * (8 * L)) + l;
+    uint4 k[kRows], v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int j = max(min(i, it.n - 1), 0);               // a head that is there, so that no branch parts the loads
+        k[i] = __ldg(kin + j * L);
+        v[i] = __ldg(vin + j * L);
     }
-    int ek, ev;
-    const uint32_t ck = encode8(k, ek), cv = encode8(v, ev);
-    const int b = it.l / 4, c = it.l % 4;
-    // an even block's lane gives its second half word and takes the odd block's first one
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? cv & 0xFFFFu : cv >> 16, 4);
-    const uint32_t wv = (b & 1) ? other | (cv & 0xFFFF0000u) : (cv & 0xFFFFu) | other << 16;
-    if (it.row < 0) return;
-    reinterpret_cast<uint32_t*>(p.kc + it.row * (4 * L))[c * B + b] = ck;
-    reinterpret_cast<uint32_t*>(p.vc + it.row * (4 * L))[((2 * c + (b & 1)) * B + (b & ~1)) / 2] = wv;
-    if (c == 0) {
-        p.ks[it.row * B + b] = static_cast<uint8_t>(ek + 127);
-        p.vs[it.row * B + b] = static_cast<uint8_t>(ev + 127);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        int ek, ev;
+        const uint32_t ck = encode8(k[i], ek), cv = encode8(v[i], ev);
+        // an even block's lane gives its second half word and takes the odd block's first one
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? cv & 0xFFFFu : cv >> 16, 4);
+        const uint32_t wv = (b & 1) ? other | (cv & 0xFFFF0000u) : (cv & 0xFFFFu) | other << 16;
+        if (i < it.n) {
+            const long long row = it.row + (long long)i * p.page;
+            reinterpret_cast<uint32_t*>(p.kc)[row * L + c * B + b] = ck;
+            reinterpret_cast<uint32_t*>(p.vc)[row * L + ((2 * c + (b & 1)) * B + (b & ~1)) / 2] = wv;
+            if (c == 0) {
+                p.ks[row * B + b] = static_cast<uint8_t>(ek + 127);
+                p.vs[row * B + b] = static_cast<uint8_t>(ev + 127);
+            }
+        }
     }
+    complain<L>(p, it);
 }
 
 // Values of eight codes as BF16 (E2M1 times a power of two within the cache's range: exact).
@@ -134,31 +144,39 @@ __device__ __forceinline__ uint4 decode8(uint32_t codes, uint32_t u) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int L>
+template <int L, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const KvParams p) {
     constexpr int B = L / 4;
     fg::grid_dependency_wait();
     if (threadIdx.x == 0) fg::grid_launch_dependents();
-    const Item it = item_of<L>(p);
-    const int b = it.l / 4, c = it.l % 4;
-    uint32_t ck = 0, wv = 0, uk = 0, uv = 0;
-    if (it.row >= 0) {
-        ck = __ldcg(reinterpret_cast<const uint32_t*>(p.kc + it.row * (4 * L)) + c * B + b);
-        wv = __ldcg(reinterpret_cast<const uint32_t*>(p.vc + it.row * (4 * L)) + ((2 * c + (b & 1)) * B + (b & ~1)) / 2);
-        uk = __ldcg(p.ks + it.row * B + b);
-        uv = __ldcg(p.vs + it.row * B + b);
+    const Item it = item_of<L, kRows>(p);
+    const int l = threadIdx.x % L, b = l / 4, c = l % 4;
+    uint32_t ck[kRows], wv[kRows], uk[kRows], uv[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const long long row = it.row + (long long)max(min(i, it.n - 1), 0) * p.page;
+        ck[i] = __ldcg(reinterpret_cast<const uint32_t*>(p.kc) + row * L + c * B + b);
+        wv[i] = __ldcg(reinterpret_cast<const uint32_t*>(p.vc) + row * L + ((2 * c + (b & 1)) * B + (b & ~1)) / 2);
+        uk[i] = __ldcg(p.ks + row * B + b);
+        uv[i] = __ldcg(p.vs + row * B + b);
     }
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? wv & 0xFFFFu : wv >> 16, 4);
-    const uint32_t cv = (b & 1) ? other | (wv & 0xFFFF0000u) : (wv & 0xFFFFu) | other << 16;
-    if (it.row < 0) return;
-    reinterpret_cast<uint4*>(p.k_out + it.t * p.k_ld + it.h * (8 * L))[it.l] = decode8(ck, uk);
-    reinterpret_cast<uint4*>(p.v_out + it.t * p.v_ld + it.h * (8 * L))[it.l] = decode8(cv, uv);
+    uint4* ko = reinterpret_cast<uint4*>(p.k_out + it.t * p.k_ld + it.h * (8 * L)) + l;
+    uint4* vo = reinterpret_cast<uint4*>(p.v_out + it.t * p.v_ld + it.h * (8 * L)) + l;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? wv[i] & 0xFFFFu : wv[i] >> 16, 4);
+        const uint32_t cv = (b & 1) ? other | (wv[i] & 0xFFFF0000u) : (wv[i] & 0xFFFFu) | other << 16;
+        if (i < it.n) {
+            ko[i * L] = decode8(ck[i], uk[i]);
+            vo[i * L] = decode8(cv, uv[i]);
+        }
+    }
+    complain<L>(p, it);
 }
 
 template <class F>
-int launch(F kernel, int L, const KvParams& p, int pdl, cudaStream_t stream) {
-    const long long blocks = ((long long)p.T * p.heads * L + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffLL) return FG_ERR_INVALID_ARG;
+int launch(F kernel, int rows, int per_block, const KvParams& p, int pdl, cudaStream_t stream) {
+    const long long blocks = ((long long)p.T * ((p.heads + rows - 1) / rows) + per_block - 1) / per_block;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -176,6 +194,20 @@ int launch(F kernel, int L, const KvParams& p, int pdl, cudaStream_t stream) {
     }
     return FG_OK;
 }
+// One head a thread where the device holds all their threads at once (37 tokens of 8 heads of 128 in and out again: 3.5
+// us, with two 4.1; 1024: 4.9 either way), two where it does not (2048: 6.3 us, with one 7.4; 8192: 15.2 and 18.6; with
+// four 18.8).
+template <int L>
+int launch(bool append, const KvParams& p, const fg::HostState& st, cudaStream_t stream) {
+    constexpr int kGroups = kThreads / L;
+    const bool two = (long long)p.T * p.heads * L > st.sms * 1024LL;
+    if (append)
+        return two ? launch(kv_append_kernel<L, 2>, 2, kGroups, p, st.pdl, stream) : launch(kv_append_kernel<L, 1>, 1, kGroups, p, st.pdl, stream);
+    return two ? launch(kv_gather_kernel<L, 2>, 2, kGroups, p, st.pdl, stream) : launch(kv_gather_kernel<L, 1>, 1, kGroups, p, st.pdl, stream);
+}
+int launch(bool append, int D, const KvParams& p, const fg::HostState& st, cudaStream_t stream) {
+    return D == 64 ? launch<8>(append, p, st, stream) : D == 128 ? launch<16>(append, p, st, stream) : launch<32>(append, p, st, stream);
+}
 
 // The arguments that append and gather share; rows = k and v.
 int check(int T, int heads, int D, int page_size, int num_pages, const void* k, long long k_stride, const void* v,
@@ -183,7 +215,7 @@ int check(int T, int heads, int D, int page_size, int num_pages, const void* k, 
     if (T < 0 || heads < 1 || D < 1 || page_size < 1 || num_pages < 1 || (long long)page_size * num_pages > 0x7fffffffLL ||
         heads > 65536 || k_stride < (long long)heads * D || v_stride < (long long)heads * D || k_stride % 8 || v_stride % 8)
         return FG_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128 && D != 256) || page_size % 16) return FG_ERR_UNSUPPORTED;
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 || (long long)T * heads > 0x7fffffffLL) return FG_ERR_UNSUPPORTED;
     if (T == 0) return FG_OK;
     if (!k || !v || !slots || !kc || !ks || !vc || !vs || !al(k, 16) || !al(v, 16) || !al(slots, 4) || !al(kc, 16) ||
         !al(ks, 16) || !al(vc, 16) || !al(vs, 16))
@@ -205,9 +237,7 @@ int fg_kv_append_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
     if (const int rc = fg::host_state(&st)) return rc;
     const KvParams p{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), nullptr, nullptr, k_stride, v_stride,
                      slots, k_cache, k_sf, v_cache, v_sf, T, heads, page_size, page_size * num_pages, st.status};
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return D == 64 ? launch(kv_append_kernel<8>, 8, p, st.pdl, s)
-         : D == 128 ? launch(kv_append_kernel<16>, 16, p, st.pdl, s) : launch(kv_append_kernel<32>, 32, p, st.pdl, s);
+    return launch(true, D, p, st, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, const int32_t* slots, const uint8_t* k_cache,
@@ -221,9 +251,7 @@ int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
     const KvParams p{nullptr, nullptr, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), k_stride, v_stride, slots,
                      const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(k_sf), const_cast<uint8_t*>(v_cache),
                      const_cast<uint8_t*>(v_sf), T, heads, page_size, page_size * num_pages, st.status};
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return D == 64 ? launch(kv_gather_kernel<8>, 8, p, st.pdl, s)
-         : D == 128 ? launch(kv_gather_kernel<16>, 16, p, st.pdl, s) : launch(kv_gather_kernel<32>, 32, p, st.pdl, s);
+    return launch(false, D, p, st, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
