@@ -496,8 +496,9 @@ int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
  * p = seq_lens[r] - n + i and looks at the cached positions j <= p, and with window > 0 at j > p - window only:
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k_j) v_j      (kv head h / (Hq / Hkv))
  * with cached position j at offset j mod page_size of page block_table[r][j / page_size].  FP32 scores,
- * statistics and sums; a weight is rounded once, to FP16, or to BF16 where an average request (ceil(T / S) rows)
- * brings at least 64 rows of a kv head (S <= 1024), which go to the tensor cores 128 or 256 at a time.  A row that
+ * statistics and sums; a weight is rounded once, to FP16, or to BF16 where the tensor cores take 128 or 256 rows at a
+ * time: where an average request (ceil(T / S) tokens) brings more than 32 rows of a kv head and that is faster, which
+ * depends on T, S, Hkv, D, window and max_pages * page_size, on nothing that only the device knows.  A row that
  * looks at nothing (p < 0) becomes 0.
  * Rows >= query_start[S] stay as they were; what the cache holds behind a request's length is never used.
  *   q, out [T][Hq][D] BF16;  block_table [S][max_pages], query_start [S + 1], seq_lens [S] int32

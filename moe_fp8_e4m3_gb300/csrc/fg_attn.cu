@@ -581,17 +581,34 @@ int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
 
 // Rows of an average request's kv head.
 long long rows_of(int T, int S, int group) { return ((long long)T + S - 1) / S * group; }
-// Row tiles of eight: as many as those rows fill, and as many as registers hold the accumulators of.
+// Row tiles of eight: as many as those rows fill, and as many as registers hold the accumulators of.  16 requests of
+// 8192 tokens, 4 kv heads, us with one, two and four tiles: D = 64, 8 rows 16.7, 21.9, 28.7; 16 rows 25.8, 22.3, 28.7;
+// 32 rows 42.5, 35.8, 30.1; D = 128, 8 rows 23.6, 30.3; 16 rows 37.2, 31.7.
 int row_tiles(int T, int S, int group, int D) {
     const long long rows = rows_of(T, S, group);
     const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const int most = D == 64 ? 4 : D == 128 ? 2 : 1;
     return nt < most ? nt : most;
 }
-// Whether a call takes the kernel for many rows a request.
-bool many_rows(int T, int S, int group) { return S <= fg::kAttnPromptRequests && rows_of(T, S, group) >= 64; }
-// Rows of its items.
-int prompt_rows(int T, int S, int group, int D) { return D <= 128 && rows_of(T, S, group) >= 256 ? 256 : 128; }
+// Whether a call takes the kernel for many rows a request: where its work, in blocks of 128 keys times chunks of rows
+// and each chunk's start, is less by more than it takes to begin and end (some 12 us).  Lengths are known on the device
+// only; max_pages stands for them.  Measured, us here and there, 4 kv heads, 8192 keys: 16 requests, D = 64, 64 rows 50
+// and 54, 128 rows 90 and 56; D = 128, 48 rows 73 and 76, 64 rows 93 and 76, 128 rows 176 and 80; 4 requests, D = 256,
+// 64 rows 65 and 71, 128 rows 119 and 80.  One request of 1024 keys, D = 128: 64 rows 13 and 25, 512 rows 25.2 and 28.3;
+// 64 requests of 512 keys: 64 rows 52 and 37.
+constexpr int kFewestMany = 33;               // no call of fewer rows meets that
+bool many_rows(int T, int S, int heads, int group, int D, long long keys, int window) {
+    const long long rows = rows_of(T, S, group);
+    if (S > fg::kAttnPromptRequests || rows < kFewestMany) return false;
+    if (window > 0 && keys > window + rows / group) keys = window + rows / group;
+    const double blocks = static_cast<double>(keys / kBlock + 1), items = static_cast<double>(S) * heads;
+    const int few = 8 * row_tiles(T, S, group, D);
+    const double a_block = D == 64 ? 2.1 : D == 128 ? 3.2 : 9.0;     // of 128 rows there, in blocks of `few` rows here
+    return items * ((rows + few - 1) / few) * (5 + blocks) > a_block * items * ((rows + 127) / 128) * (3 + blocks) + 2300;
+}
+// Rows of its items (16 requests of 8192 tokens, D = 128, us with 128 and 256: 256 rows 133.5 and 136.3, 320 rows 190 and
+// 217, 512 rows 242 and 220).
+int prompt_rows(int T, int S, int group, int D) { return D <= 128 && rows_of(T, S, group) >= 512 ? 256 : 128; }
 
 bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
     return T >= 0 && S >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536 && D >= 1;
@@ -609,7 +626,7 @@ extern "C" {
 long long fg_paged_attention_workspace(int T, int S, int Hq, int Hkv, int D) {
     if (!shapes_ok(T, S, Hq, Hkv, D) || (D != 64 && D != 128 && D != 256)) return -1;
     // enough for any fewer rows and requests too
-    const bool many = many_rows(T, 1, Hq / Hkv);
+    const bool many = rows_of(T, 1, Hq / Hkv) >= kFewestMany;
     const long long slot = (long long)prompt_rows(T, 1, Hq / Hkv, D) * (D + 2);
     const long long few = 2LL * fg::kAttnMaxCtas * kMaxSlot * 4, most = 2LL * fg::kAttnPromptCtas * slot * 4;
     return kCtrBytes + (many && most > few ? most : few);
@@ -640,7 +657,8 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
                        scale * 1.4426950408889634f, reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCtrBytes),
                        st.status, st.timeout_ns};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (many_rows(T, S, Hq / Hkv)) return fg::launch_attn_prompt(p, D, prompt_rows(T, S, Hq / Hkv, D), st.sms, st.pdl, s);
+    if (many_rows(T, S, Hkv, Hq / Hkv, D, (long long)max_pages * page_size, window))
+        return fg::launch_attn_prompt(p, D, prompt_rows(T, S, Hq / Hkv, D), st.sms, st.pdl, s);
     const int nt = row_tiles(T, S, Hq / Hkv, D);
     switch (D) {
         case 64: return nt == 1 ? launch<2, 1>(p, st.sms, st.pdl, s) : nt == 2 ? launch<2, 2>(p, st.sms, st.pdl, s) : launch<2, 4>(p, st.sms, st.pdl, s);

@@ -41,15 +41,27 @@ def cache_case(seed, lens, new, hq, hkv, d, page, spread=2, extra_rows=2, q_scal
             "pages": pages}
 
 
-def weight_step(c):
-    """Half a step of the weights' type: BF16 where an average request brings 64 rows or more of a kv head, else FP16."""
-    rows = -(-len(c["q"]) // len(c["lens"])) * (c["hq"] // c["hkv"])
-    return 2.0 ** -8 if rows >= 64 else 2.0 ** -11
+def wide(c, tokens=1 << 18):
+    """The same case with room for longer contexts in its block table (what is faster is chosen by that)."""
+    more = max(0, tokens // c["page"] - c["table"].shape[1])
+    return dict(c, table=np.pad(c["table"], ((0, 0), (0, more)), constant_values=-1))
+
+
+def many_rows(c, window=0):
+    """Whether the tensor cores take 128 rows or more at a time."""
+    group, s, d = c["hq"] // c["hkv"], len(c["lens"]), c["d"]
+    new = -(-len(c["q"]) // s)
+    rows, keys = new * group, c["table"].shape[1] * c["page"]
+    if window:
+        keys = min(keys, window + new)
+    blocks, few = keys // 128 + 1, min({64: 32, 128: 16, 256: 8}[d], 8 if rows <= 8 else 16 if rows <= 16 else 32)
+    here, there = s * c["hkv"] * -(-rows // few) * (5 + blocks), s * c["hkv"] * -(-rows // 128) * (3 + blocks)
+    return s <= 1024 and rows > 32 and here > {64: 2.1, 128: 3.2, 256: 9.0}[d] * there + 2300
 
 
 def reference(c, scale=None, window=0):
     return O.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["table"], c["start"], c["lens"],
-                       c["d"] ** -0.5 if scale is None else scale, window, weight_step(c))
+                       c["d"] ** -0.5 if scale is None else scale, window, 2.0 ** (-8 if many_rows(c, window) else -11))
 
 
 def tables_case(seed, s, page, longest, width, mode):

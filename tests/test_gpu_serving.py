@@ -85,8 +85,9 @@ def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
     """Chunks of 128 rows on the tensor cores: ends inside a token's heads, requests of few rows among them, tiles that
     end behind the keys, windows that begin inside a tile."""
     lens = [n + extra for n, extra in zip(new, (0, 200, 131))]
-    c = C.cache_case(d + hq + sum(new) + window + page, lens, new, hq, hkv, d, page, extra_rows=3 * -(-64 * hkv // hq))
-    assert C.weight_step(c) == 2.0 ** -8
+    extra_rows = 3 * 2048 if window else 3 * -(-256 * hkv // hq)
+    c = C.wide(C.cache_case(d + hq + sum(new) + window + page, lens, new, hq, hkv, d, page, extra_rows=extra_rows))
+    assert C.many_rows(c, window)
     out, ws = attend(fg, c, window)
     expect(fg)
     check(c, out, window)
@@ -94,9 +95,34 @@ def test_many_rows_a_request(fg, d, hq, hkv, new, window, page):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 50, 400])
+def test_many_requests_of_many_rows(fg, d, window):
+    """More items than CTAs, windows that begin inside a tile, requests without rows among them."""
+    g = C.rng(d + window)
+    new = g.integers(0, 40, 60)
+    c = C.cache_case(d + window, new + g.integers(0, 200, 60), new, 8, 2, d, 16, extra_rows=2000)
+    assert C.many_rows(c, window)
+    out, ws = attend(fg, c, window)
+    expect(fg)
+    check(c, out, window)
+    assert not ws[:7680].any(), "counters are left as they were"
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [512, 1 << 18])
+@pytest.mark.parametrize("rows", [24, 32, 33, 48, 64, 65, 80, 128, 136])
+def test_row_counts_around_the_choice_of_kernel(fg, d, tokens, rows):
+    c = C.wide(C.cache_case(rows, [rows + 40, 400], [rows, rows], 1, 1, d, 16, extra_rows=0), tokens)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check(c, out)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("new", [[40, 1], [70, 60]])
 def test_many_rows_over_long_contexts_are_split_and_joined(fg, d, new):
-    c = C.cache_case(d, [2500, 1800], new, 8, 1, d, 32)
+    c = C.wide(C.cache_case(d, [2500, 1800], new, 8, 1, d, 32))
+    assert C.many_rows(c)
     out, ws = attend(fg, c)
     expect(fg)
     check(c, out)
@@ -105,10 +131,11 @@ def test_many_rows_over_long_contexts_are_split_and_joined(fg, d, new):
         assert torch.equal(again, out)
 
 
-@pytest.mark.parametrize("new", [20, 50])
+@pytest.mark.parametrize("new", [20, 50, 70])
 def test_many_rows_scores_that_keep_rising(fg, new):
     """Keys whose scores rise by far more than a step of the running maximum, tile by tile, and fall again."""
-    c = C.cache_case(12, [1000], [new], 8, 1, 64, 16)
+    c = C.wide(C.cache_case(12, [1000], [new], 8, 1, 64, 16))
+    assert C.many_rows(c)
     c["q"][:] = np.abs(c["q"])
     c["q_bits"], c["q"] = O.bf16(c["q"])
     n = np.arange(1000)
@@ -122,9 +149,10 @@ def test_many_rows_scores_that_keep_rising(fg, new):
     check(c, out)
 
 
-@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("hq", [4, 16, 32])
 def test_many_rows_contract_violations_and_non_finite_queries(fg, hq):
-    c = C.cache_case(13, [300, 90], [40, 30], hq, 2, 128, 16)
+    c = C.wide(C.cache_case(13, [300, 90], [40, 30], hq, 2, 128, 16))
+    assert C.many_rows(c)
     c = dict(c, q_bits=np.concatenate([c["q_bits"]] * 1), table=c["table"].copy())
     ref = O.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["table"], c["start"], c["lens"], 128 ** -0.5, 0, 2.0 ** -8)
     c["q_bits"][5, 1, 7] = 0x7FC0
@@ -174,9 +202,9 @@ def test_one_long_request_is_split_and_joined(fg, hkv, length):
 def test_a_workspace_serves_calls_of_other_sizes(fg):
     ws = fg.paged_attention_workspace(64, 1, 32, 1, 256)
     for seed, (lens, new, hq, hkv, d) in enumerate([([700, 3], [2, 1], 8, 2, 128), ([5000], [1], 4, 1, 256),
-                                                    ([90] * 5, [4] * 5, 16, 4, 64), ([700], [33], 8, 2, 256),
+                                                    ([90] * 5, [4] * 5, 16, 4, 64), ([700], [40], 8, 2, 256),
                                                     ([5000, 17], [1, 1], 3, 3, 128), ([60, 300], [60, 9], 4, 1, 64)]):
-        c = C.cache_case(seed, lens, new, hq, hkv, d, 32)
+        c = C.wide(C.cache_case(seed, lens, new, hq, hkv, d, 32))
         out, _ = attend(fg, c, ws=ws)
         expect(fg)
         check(c, out)
