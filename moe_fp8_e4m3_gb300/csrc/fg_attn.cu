@@ -54,7 +54,6 @@ struct Cfg {
     static constexpr bool kQShared = NT > 1;                             // q in shared memory: registers hold O
     static constexpr int kQ = kQShared ? NT * B * 32 * 16 : 0;
     static constexpr int kSmem = kMain + kQ;                             // then [S + 1] int
-    static constexpr int kSlot = fg::attn_slot<kRows, D>();
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
         int look_page = base / p.page, look_off = base % p.page;
         auto next_page = [&](int tok, uint32_t& page, uint32_t& off) {
-            page = tok < base_end ? static_cast<uint32_t>(__ldg(table + look_page)) : ~0u;
+            page = tok < base_end ? static_cast<uint32_t>(table[look_page]) : ~0u;
             off = head_row + look_off;
             look_page += step_page;
             look_off += step_off;
@@ -615,8 +614,8 @@ bool shapes_ok(int T, int S, int Hq, int Hkv, int D) {
 }
 
 // Floats of the largest partial result of this file's variants.
-constexpr int kMaxSlot = Cfg<2, 4>::kSlot;
-static_assert(Cfg<4, 2>::kSlot <= kMaxSlot && Cfg<8, 1>::kSlot <= kMaxSlot, "largest partial result");
+constexpr int kMaxSlot = fg::attn_slot<32, 64>();
+static_assert(fg::attn_slot<16, 128>() <= kMaxSlot && fg::attn_slot<8, 256>() <= kMaxSlot, "largest partial result");
 constexpr long long kCtrBytes = (3 * fg::kAttnMaxCtas * 4 + 255) / 256 * 256;
 
 }  // namespace

@@ -44,7 +44,7 @@ struct AttnRequest {
     int n, len, t0;
 };
 __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int r) {
-    const int t0 = __ldg(p.start + r), t1 = __ldg(p.start + r + 1), len = __ldg(p.lens + r);
+    const int t0 = __ldcg(p.start + r), t1 = __ldcg(p.start + r + 1), len = __ldcg(p.lens + r);
     const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
     return ok ? AttnRequest{t1 - t0, len, t0} : AttnRequest{0, 0, 0};
 }
@@ -75,7 +75,7 @@ struct AttnCursor {
     static constexpr unsigned long long kCostMask = (1ull << 40) - 1;
 
     static __device__ __forceinline__ void complain(const AttnParams& p, int q) {   // of a request without rows: are its lengths right?
-        const int t0 = __ldg(p.start + q), t1 = __ldg(p.start + q + 1), len = __ldg(p.lens + q);
+        const int t0 = __ldcg(p.start + q), t1 = __ldcg(p.start + q + 1), len = __ldcg(p.lens + q);
         if (t0 != t1 || t0 < 0 || t0 > p.T || len < 0 || len > (long long)p.max_pages * p.page) kv_record(p.status, kKvErrAttention);
     }
     __device__ __forceinline__ void look(const AttnParams& p, const int* s_pre) {

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
             const int step_page = kTok / p.page, step_off = kTok % p.page;
             // whether token tok's page is wanted, and its id (looked at only a tile later: nothing waits for it here)
             auto wanted = [&](int tok) { return tok < tok1 && (tok & ~15) + 16 > keys_lo; };
-            auto page_at = [&](int tok) { return wanted(tok) ? static_cast<uint32_t>(__ldg(table + page_i)) : ~0u; };
+            auto page_at = [&](int tok) { return wanted(tok) ? static_cast<uint32_t>(table[page_i]) : ~0u; };
             auto load = [&](Raw<B>& x, uint32_t page, int off) {
                 if (page < static_cast<uint32_t>(p.pages)) {
                     const long long row = ((long long)page * p.heads + h) * p.page + off;

@@ -82,7 +82,7 @@ __device__ __forceinline__ Item item_of(const KvParams& p) {
     const unsigned x = blockIdx.x * static_cast<unsigned>(kThreads / L) + threadIdx.x / L;
     const unsigned groups = (static_cast<unsigned>(p.heads) + kRows - 1) / kRows, t = x / groups;
     if (t >= static_cast<unsigned>(p.T)) return Item{0, 0, 0, 0};
-    const int slot = __ldg(p.slots + t), h = static_cast<int>(x - t * groups) * kRows;
+    const int slot = __ldcg(p.slots + t), h = static_cast<int>(x - t * groups) * kRows;
     if (slot < 0 || slot >= p.slots_total) return Item{static_cast<int>(t), h, slot < 0 ? 0 : -1, 0};
     const unsigned page = static_cast<unsigned>(slot) / static_cast<unsigned>(p.page);
     return Item{static_cast<int>(t), h, min(kRows, p.heads - h),
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvParams p) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int j = max(min(i, it.n - 1), 0);               // a head that is there, so that no branch parts the loads
-        k[i] = __ldg(kin + j * L);
-        v[i] = __ldg(vin + j * L);
+        k[i] = __ldcg(kin + j * L);
+        v[i] = __ldcg(vin + j * L);
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 7) rope_kernel(const RopeParams p) {
     const bool is_q = chunk < p.q_chunks;
     const int h0 = (is_q ? chunk : chunk - p.q_chunks) * kHeads;
     const int heads = is_q ? p.Hq : p.Hkv;
-    const int pos = live ? __ldg(p.positions + t) : -1;
+    const int pos = live ? __ldcg(p.positions + t) : -1;
     if (pos >= p.max_pos && l == 0) fg::kv_record(p.status, fg::kKvErrPosition);
     const bool turned = 8 * l < p.rot;
     const int ea = kPairs ? 8 * l : turned ? 4 * l : p.rot + 8 * (l - p.rot / 8);      // this lane's two runs of four
@@ -79,14 +79,14 @@ __global__ void __launch_bounds__(kThreads, 7) rope_kernel(const RopeParams p) {
     float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live && turned) {
         const float* row = p.cos_sin + (long long)pos * p.rot + 4 * l;
-        cs = __ldg(reinterpret_cast<const float4*>(row));
-        sn = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2));
+        cs = __ldcg(reinterpret_cast<const float4*>(row));
+        sn = __ldcg(reinterpret_cast<const float4*>(row + p.rot / 2));
     }
     const uint16_t* w = is_q ? p.qw : p.kw;
     uint2 wa = make_uint2(0, 0), wb = wa;                     // as they are stored: registers hold more heads
     if (w && live) {
-        wa = __ldg(reinterpret_cast<const uint2*>(w + ea));
-        wb = __ldg(reinterpret_cast<const uint2*>(w + eb));
+        wa = __ldcg(reinterpret_cast<const uint2*>(w + ea));
+        wb = __ldcg(reinterpret_cast<const uint2*>(w + eb));
     }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
