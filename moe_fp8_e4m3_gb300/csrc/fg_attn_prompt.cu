@@ -1,20 +1,28 @@
 // fg_attn_prompt.cu - attention of many new tokens a request over its 4-bit key/value cache, on the tensor
 // cores of the fifth generation.
 //
-// An item is 128 rows (new tokens x the query heads that share a kv head) of one request; per tile of kTok keys
+// An item (fg_attn.cuh) is 128 rows (new tokens x the query heads that share a kv head) of one request, or 256 in two row
+// tiles of 128; per row tile and tile of kTok keys
 //   S = Q K^T       tcgen05.mma, BF16, FP32 in tensor memory (two tiles of it, so the next product runs while a
 //                   tile's exponentials are taken)
-//   P = 2^(S - m)   two threads a row, half of the keys each, in registers; m a running maximum that moves only when a score passes it by 2^8, because
-//                   moving it scales O, which lives in tensor memory; P rounded once, to BF16
+//   P = 2^(S - m)   in registers: two threads a row, half of the keys each, or a thread a row where there are two row
+//                   tiles; m a running maximum that moves only when a score passes it by 2^8, because moving it
+//                   scales O, which lives in tensor memory; P rounded once, to BF16 (2^-8 relative; no sum goes through it:
+//                   l adds the unrounded weights)
 //   O += P V        tcgen05.mma, BF16, FP32 in tensor memory
 // Keys and values become BF16 tiles in shared memory once per item tile, exactly (a code has two significant bits,
-// its scale is a power of two): 256 threads decode what 128 rows use.  Keys, values and Q stand as rows of 64
+// its scale is a power of two): 256 threads decode what 128 or 256 rows use.  Keys, values and Q stand as rows of 64
 // elements in 128-byte swizzled atoms; a value tile is the product's MN-major operand as it is.
 //
-// Warps: 0-7 softmax and output (warps w and w + 4 share 32 rows), 8 the MMA issuer, 9-16 the decoders.  They meet at
-// mbarriers (every wait is bounded, as in the GEMMs); a row's two threads meet at a barrier of their two warps,
-// which both reach on every tile, also after a wait that ran out; pieces of items follow one another with a CTA
+// Warps: 0-7 softmax and output (one row tile: warps w and w + 4 share 32 rows), 8 the MMA issuer, 9-16 the decoders.
+// They meet at mbarriers (every wait is bounded, as in the GEMMs); a row's two threads meet at a barrier of their two
+// warps, which both reach on every tile, also after a wait that ran out; pieces of items follow one another with a CTA
 // barrier between.
+//
+// Bound: latency.  4 prompts of up to 512 tokens over 6000, 32 query heads on 4 of 128: 118 us (450 TFLOP/s; items of
+// one row tile 131), 2.9 us a key tile and pair of row tiles, with the tensor pipe at work in 27 % of it: decode, product,
+// exponentials, product are one chain over four hand-offs, and each role's warps issue once in 4 clocks.  Without
+// the decoders' arithmetic, the exponentials or half of the products a call is at most 8 % shorter, without all three 17 %.
 #include <cuda_runtime.h>
 
 #include <cstdio>
