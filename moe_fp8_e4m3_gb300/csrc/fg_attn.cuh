@@ -127,28 +127,39 @@ struct AttnCursor {
     __device__ __forceinline__ bool open(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int* s_pre) {
         const int tid = threadIdx.x;
         unsigned long long total_blocks;
+        // chunks of requests that do not overlap
+        const unsigned long long most = (unsigned long long)p.T * p.group / kRows + p.S;
+        constexpr int kFew = 64;                               // chunks that a thread walks
         if (kByRequest && p.S <= kThreads) {
             // few chunks a request, a request a thread: chunks and costs in one scan
             unsigned long long sum = 0, total;
+            int n = 0;
             ch = 0;
             r = 0;
             if (tid < p.S) {
                 rq = attn_request(p, tid);
-                if (blockIdx.x == 0 && rq.n == 0) complain(p, tid);
-                const int n = static_cast<int>(((long long)rq.n * p.group + kRows - 1) / kRows);
+                n = static_cast<int>(((long long)rq.n * p.group + kRows - 1) / kRows);
+            }
+            if (!__syncthreads_or(n > kFew)) {
+                if (blockIdx.x == 0 && tid < p.S && rq.n == 0) complain(p, tid);
                 for (int i = 0; i < n; ++i) {
                     look_at(p, i);
                     sum += cost;
                 }
-                sum |= static_cast<unsigned long long>(n) << 40;   // costs stay below 2^36: 2^12 chunks of at most 2^24 blocks
+                sum |= static_cast<unsigned long long>(n) << 40;   // costs stay below 2^39: kThreads x kFew chunks of at most 2^24 blocks
+                static_assert(kThreads * kFew <= 1 << 14 || !kByRequest, "room for both");
+                const unsigned long long at = scan(sum, sm.warp, total);
+                if (total >> 40 > most) {
+                    if (blockIdx.x == 0 && tid == 0) kv_record(p.status, kKvErrAttention);
+                    return false;
+                }
+                sm.strip[tid] = at & kCostMask;
+                if (tid <= p.S) s_pre[tid] = static_cast<int>(at >> 40);
+                if (tid == 0 && p.S == kThreads) s_pre[kThreads] = static_cast<int>(total >> 40);
+                total_blocks = total & kCostMask;
+                __syncthreads();
+                return settle(p, sm, s_pre, total_blocks, true);
             }
-            const unsigned long long at = scan(sum, sm.warp, total);
-            sm.strip[tid] = at & kCostMask;
-            if (tid <= p.S) s_pre[tid] = static_cast<int>(at >> 40);
-            if (tid == 0 && p.S == kThreads) s_pre[kThreads] = static_cast<int>(total >> 40);
-            total_blocks = total & kCostMask;
-            __syncthreads();
-            return settle(p, sm, s_pre, total_blocks, true);
         }
         const int per_r = (p.S + kThreads - 1) / kThreads;
         {
@@ -161,6 +172,10 @@ struct AttnCursor {
                 sum += ((long long)x.n * p.group + kRows - 1) / kRows;
             }
             unsigned long long at = scan(sum, sm.warp, total);
+            if (total > most) {                                // requests overlap: their chunks could be more than anything holds
+                if (blockIdx.x == 0 && tid == 0) kv_record(p.status, kKvErrAttention);
+                return false;
+            }
             for (int i = 0; i < per_r; ++i) {
                 const int q = tid * per_r + i;
                 if (q >= p.S) break;

@@ -281,6 +281,31 @@ def test_contract_violations_leave_the_others_right(fg):
     assert within(got[2:4], two[:2], "bf16").all()
 
 
+@pytest.mark.parametrize("s,new", [(8, 4), (300, 1), (6, 100), (700, 3)])
+@pytest.mark.parametrize("tokens", [16, 1 << 18])
+def test_requests_that_claim_the_same_rows(fg, s, new, tokens):
+    """query_start goes up and down over all rows again and again: nothing is written, and the next call is right."""
+    c = C.wide(C.cache_case(s, [new + 3] * s, [new] * s, 4, 2, 64, 16), tokens)
+    out, ws = attend(fg, dict(c, start=np.resize(np.array([0, s * new], np.int32), s + 1)))
+    expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
+    assert (f64(out) == -77).all()
+    out, _ = attend(fg, c, ws=ws)
+    expect(fg)
+    check(c, out)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_prompt_among_many_decodes(fg, d):
+    new = [1] * 40
+    new[17] = 260
+    lens = [30 + 7 * i for i in range(40)]
+    lens[17] = 400
+    c = C.cache_case(d, lens, new, 8, 2, d, 16, extra_rows=0)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check(c, out)
+
+
 def test_streams_and_graph_replays_with_new_lengths(fg):
     """Lengths are read on the device: a captured call serves whatever they are when it is replayed."""
     c = C.cache_case(6, [200, 90, 31], [1, 1, 1], 8, 2, 128, 32)
