@@ -54,6 +54,8 @@ struct Cfg {
     static constexpr int kTileV = 16 * 16 * B, kTileKs = 2 * kTileV, kTileVs = kTileKs + 16 * B, kTile = kTileVs + 16 * B;
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kMain = kJoin > kRing ? kJoin : kRing;          // the join comes when the ring is empty
+    static constexpr int kPerSm = NT * B <= 4 ? 2 : 1;                   // CTAs: 128 registers a thread
+    static constexpr bool kParked = NT > 1 && kPerSm == 2;
     static constexpr bool kQShared = NT > 1;                             // q in shared memory: registers hold O
     static constexpr int kQ = kQShared ? NT * B * 32 * 16 : 0;
     static constexpr int kSmem = kMain + kQ;                             // then [S + 1] int
@@ -179,7 +181,7 @@ __device__ __forceinline__ float top_exponent(const float (&f)[B]) {
 }
 
 template <int B, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(const AttnParams p) {
     using C = Cfg<B, NT>;
     constexpr int D = C::D, kRows = C::kRows, kPad = C::kPad;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
     __shared__ float s_qs[kRows];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     __shared__ fg::AttnPlanSmem<kThreads> s_plan;
+    __shared__ fg::AttnCursor<kRows, kBlock, kThreads, true> s_cur;       // kParked: out of the tiles' registers
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t smem_base = fg::smem_u32(smem);
     fg::grid_dependency_wait();
@@ -218,14 +221,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         const int first = cur.rq.len - cur.rq.n;                               // position of new token 0
         const int* table = p.table + (long long)cur.r * p.max_pages;
         const uint32_t head_row = static_cast<uint32_t>(h) * p.page;
+        const int keys_lo = cur.keys.lo, keys_hi = cur.keys.hi, row_t0 = cur.rq.t0;
+        if (C::kParked && tid == 0) s_cur = cur;
 
         // keys that every row of the chunk looks at: tiles inside need no mask
         const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
         const int all_hi = first + i_first + 1, all_lo = p.window > 0 ? max(0, first + i_last + 1 - p.window) : 0;
         // this warp's tiles: tokens 16 * (8 * block + warp)
         int base = b0 * kBlock + 16 * warp;
-        const int base_end = cur.keys.hi > cur.keys.lo ? min(b1 * kBlock, cur.keys.hi) : 0;
-        if (base + 16 <= cur.keys.lo) base += kBlock;
+        const int base_end = keys_hi > keys_lo ? min(b1 * kBlock, keys_hi) : 0;
+        if (base + 16 <= keys_lo) base += kBlock;
         // page and offset of the next tile to look up: a warp's tiles are kBlock tokens apart
         int look_page = base / p.page, look_off = base % p.page;
         auto next_page = [&](int tok, uint32_t& page, uint32_t& off) {
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             for (int b = 0; b < B; ++b) raw[b] = make_uint4(0, 0, 0, 0);
             if (nt * 8 + g < rows) {
                 const int i = j / p.group, hq = h * p.group + j % p.group;
-                const uint16_t* src = p.q + ((long long)(cur.rq.t0 + i) * p.heads * p.group + hq) * D + 8 * c;
+                const uint16_t* src = p.q + ((long long)(row_t0 + i) * p.heads * p.group + hq) * D + 8 * c;
 #pragma unroll
                 for (int b = 0; b < B; ++b) raw[b] = __ldcg(reinterpret_cast<const uint4*>(src + 32 * b));
             }
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
             if (!ok || tok0 < all_lo || tok0 + 16 > all_hi) {                  // a border: mask
                 const int t0 = tok0 + tau, t1 = t0 + 8;
-                const bool in0 = ok && t0 >= cur.keys.lo && t0 < cur.keys.hi, in1 = ok && t1 >= cur.keys.lo && t1 < cur.keys.hi;
+                const bool in0 = ok && t0 >= keys_lo && t0 < keys_hi, in1 = ok && t1 >= keys_lo && t1 < keys_hi;
 #pragma unroll
                 for (int i = 0; i < (B + 3) / 4; ++i) {                        // scales behind the keys may be anything
                     if (!in0) vs0[i] = 0;
@@ -484,6 +489,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         }
         cp_async_wait<0>();
         __syncthreads();                                    // the rings are empty: their place takes the join
+        if (C::kParked) cur = s_cur;
+        const int row0_ = (cur.ch - s_pre[cur.r]) * kRows, rows_ = min(kRows, cur.rq.n * p.group - row0_);
 
         // ---------------------------------------------------------- join the warps
 #pragma unroll
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
         cur.holders(s_plan, a, z);
         const bool whole = a == z;
         float* slot = fg::attn_piece<kRows, D>(p, blockIdx.x, a);
-        for (int it = tid; it < rows * (D / 4); it += kThreads) {
+        for (int it = tid; it < rows_ * (D / 4); it += kThreads) {
             const int j = it / (D / 4), d4 = it % (D / 4);
             float top = s_m[0][j];
 #pragma unroll
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
             }
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                fg::attn_store<D>(p, cur.rq.t0, h, row0 + j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                fg::attn_store<D>(p, cur.rq.t0, cur.h, row0_ + j, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
             } else {
                 if (d4 == 0) {
                     slot[j] = top;
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
                 *reinterpret_cast<float4*>(slot + 2 * kRows + j * D + 4 * d4) = acc;
             }
         }
-        if (!whole) fg::attn_join<kRows, D, kThreads, false>(p, s_plan, a, z, cur.rq.t0, h, row0, rows);
+        if (!whole) fg::attn_join<kRows, D, kThreads, false>(p, s_plan, a, z, cur.rq.t0, cur.h, row0_, rows_);
         if (!cur.next(p, s_plan, s_pre)) break;
         __syncthreads();                                    // s_join is written again
     }
@@ -542,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && B <= 4 ? 2 : 1) attn_kern
 template <int B, int NT>
 int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
     using C = Cfg<B, NT>;
-    constexpr int kPerSm = NT == 1 && B <= 4 ? 2 : 1;
     const int smem = C::kSmem + (p.S + 1) * 4;
     static bool configured[256] = {};        // set once per device; setting it again is harmless
     int dev = 0;
@@ -558,7 +564,7 @@ int launch(const AttnParams& p, int sms, int pdl, cudaStream_t stream) {
         }
         configured[dev] = true;
     }
-    const int ctas = sms * kPerSm < fg::kAttnMaxCtas ? sms * kPerSm : fg::kAttnMaxCtas;
+    const int ctas = sms * C::kPerSm < fg::kAttnMaxCtas ? sms * C::kPerSm : fg::kAttnMaxCtas;
     if (fg::print_configs_enabled())
         std::fprintf(stderr, "[fg] paged_attention_mxfp4 T=%d S=%d heads=%d x %d D=%d rows=%d grid=%d\n", p.T, p.S, p.heads,
                      p.group, C::D, C::kRows, ctas);
