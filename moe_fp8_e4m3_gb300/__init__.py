@@ -573,14 +573,25 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
         _check(st, "fp8_gemm_nt_lora")
 
 
-# The calls of a serving step are short on the GPU, so their arguments go in one record: ctypes takes 0.09 us an
-# argument, of which there are about twenty (measured on a GB300's host: 1.73 us against 0.65 us packed).
+# The calls of a serving step are short on the GPU, so a module in C++ (fg_bind.cpp) takes their arguments first; what it
+# does not take (a stream of the caller's, arguments that are wrong) is checked here, and goes in one record: ctypes
+# takes 0.09 us an argument, of which there are about twenty (measured on a GB300's host: 1.73 us against 0.65 us packed).
 _TABLES_ARGS = struct.Struct("=17q")
 _ROPE_ARGS = struct.Struct("=12qd8q")
 _APPEND_ARGS = struct.Struct("=15q")
 _ATTENTION_ARGS = struct.Struct("=16qd4q")
 _CALL_TABLES, _CALL_ROPE, _CALL_APPEND, _CALL_GATHER, _CALL_ATTENTION = range(5)
 _call = lib.fg_call
+_bind = None
+
+
+def _native():
+    """The module in C++; torch's libraries are there before it."""
+    global _bind
+    import torch  # noqa: F401
+    from . import fg_bind
+    _bind = fg_bind
+    return fg_bind
 
 
 def build_block_tables(context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots, positions,
@@ -590,6 +601,13 @@ def build_block_tables(context_lens, new_lens, free_pages, free_count, block_tab
     free_count [1] of them free; block_table [S, max_pages] (extended in place); out: query_start
     [S + 1], seq_lens [S] (may be context_lens), slots and positions [T], free_count_out [1] (may be
     free_count)."""
+    if stream is None:
+        st = (_bind or _native()).tables(context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots,
+                                       positions, free_count_out, page_size, num_pages)
+        if st == FG_OK:
+            return
+        if st is not None:
+            _check(st, "build_block_tables")
     i32 = _I32 or _int32()
     for x in (context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots, positions, free_count_out):
         if x.dtype is not i32 or not x.is_cuda or not x.is_contiguous():
@@ -629,6 +647,12 @@ def qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight
     pass.  q, q_out [T,Hq,D], k, k_out [T,Hkv,D] BF16 (tokens may be any multiple of 8 elements apart;
     outputs may be the inputs); positions int32 [T]; cos_sin float32 [max_pos, rot]: rot / 2 cosines,
     then rot / 2 sines; weights BF16 [D]; interleaved: pairs are neighbours, else halves."""
+    if stream is None:
+        st = (_bind or _native()).rope(q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight, eps, interleaved)
+        if st == FG_OK:
+            return
+        if st is not None:
+            _check(st, "qk_norm_rope")
     i32 = _I32 or _int32()
     q_shape, qs = _rows(q, "q")
     k_shape, ks = _rows(k, "k")
@@ -686,12 +710,24 @@ def _cache(k_cache, k_sf, v_cache, v_sf):
 def kv_append_mxfp4(k, v, slots, k_cache, k_sf, v_cache, v_sf, stream=None) -> None:
     """Keys and values [T, heads, D] BF16 into the 4-bit cache, at slots int32 [T] (negative: skipped).
     Tokens of k and v may be any multiple of 8 elements apart."""
+    if stream is None:
+        st = (_bind or _native()).append(k, v, slots, k_cache, k_sf, v_cache, v_sf)
+        if st == FG_OK:
+            return
+        if st is not None:
+            _check(st, "kv_append_mxfp4")
     _move(_CALL_APPEND, "kv_append_mxfp4", k, v, slots, k_cache, k_sf, v_cache, v_sf, stream)
 
 
 def kv_gather_mxfp4(slots, k_cache, k_sf, v_cache, v_sf, k, v, stream=None) -> None:
     """Keys and values at slots int32 [T] out of the 4-bit cache, as BF16 [T, heads, D] (a negative
     slot leaves its row as it was)."""
+    if stream is None:
+        st = (_bind or _native()).gather(k, v, slots, k_cache, k_sf, v_cache, v_sf)
+        if st == FG_OK:
+            return
+        if st is not None:
+            _check(st, "kv_gather_mxfp4")
     _move(_CALL_GATHER, "kv_gather_mxfp4", k, v, slots, k_cache, k_sf, v_cache, v_sf, stream)
 
 
@@ -732,6 +768,13 @@ def paged_attention_mxfp4(q, k_cache, k_sf, v_cache, v_sf, block_table, query_st
     block_table int32 [S, max_pages]; query_start int32 [S + 1]: first row of each request; seq_lens
     int32 [S]: cached tokens of each, the new ones included; scale: D^-0.5 if not given; window > 0: only
     the last `window` tokens up to each row's own.  workspace from paged_attention_workspace."""
+    if stream is None:
+        st = (_bind or _native()).attention(q, k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens, out, workspace,
+                                          scale, window)
+        if st == FG_OK:
+            return
+        if st is not None:
+            _check(st, "paged_attention_mxfp4")
     i32 = _I32 or _int32()
     bf = _BF
     pages, hkv, size, d = _cache(k_cache, k_sf, v_cache, v_sf)

@@ -1,14 +1,17 @@
-"""Builds the CUDA library ``libfg.so`` in-tree for sm_103a with nvcc.
+"""Builds the CUDA library ``libfg.so`` in-tree for sm_103a with nvcc, and beside it ``fg_bind.so``, the Python
+module of the calls whose marshalling has to be short.
 
 The translation units compile in parallel; ``-Xptxas -v`` output goes to
 ``_build/ptxas.log`` and the build fails if any kernel spills registers or uses local
 memory."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,7 @@ SOURCES = ["fg_api.cu", "fg_gemm_nt.cu", "fg_gemm_split.cu", "fg_gemm_tn.cu", "f
            "fg_gemm_sepc.cu", "fg_gemm_dense.cu", "fg_gemm_swiglu.cu", "fg_gemm_fp4.cu", "fg_gemm_fp4_grouped.cu",
            "fg_mqa.cu", "fg_quant.cu", "fg_moe.cu", "fg_lora.cu", "fg_route.cu",
            "fg_pages.cu", "fg_rope.cu", "fg_kv.cu", "fg_attn.cu", "fg_attn_prompt.cu", "fg_call.cu"]
+BIND = os.path.join(HERE, "fg_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,9 +40,9 @@ def _flags() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "fg.h"),
                                                                  os.path.abspath(__file__)]
     return any(os.path.getmtime(f) > t for f in deps)
@@ -51,6 +55,29 @@ def _compile(src: str) -> tuple[str, str]:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
     return obj, r.stderr
+
+
+def _compile_bind() -> str:
+    obj = os.path.join(BUILD, "fg_bind.o")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    include = [sysconfig.get_paths()["include"], os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include")]
+    cmd += [x for path in include for x in ("-isystem", path)] + ["-c", os.path.join(CSRC, "fg_bind.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fg_bind.cpp:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    torch = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", BIND + ".tmp", "-L", HERE, "-l:libfg.so", "-L", torch, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of fg_bind.so failed:\n{r.stderr[-4000:]}")
+    os.replace(BIND + ".tmp", BIND)
 
 
 def check_ptxas(log: str) -> None:
@@ -66,8 +93,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        bind = ex.submit(_compile_bind)
         results = list(ex.map(_compile, SOURCES))
+        bind = bind.result()
     log = "\n".join(r[1] for r in results)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write(log)
@@ -78,6 +107,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    _link_bind(bind)
     if verbose:
         print(log)
     return LIB

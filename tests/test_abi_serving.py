@@ -199,3 +199,19 @@ def test_binding_refuses_other_shapes_and_types(stub, name, wrong):
     with pytest.raises((ValueError, TypeError)):
         getattr(stub, name)(**dict(ARGS[name](stub), **wrong), stream=0)
     assert stub.calls == 0
+
+
+# ------------------------------------------------------------------- the module in C++
+def test_native_calls_leave_what_they_do_not_take_to_the_binding(fg):
+    bind = fg._native()
+    i32, b16, u8, f32 = (lambda *n, t=t: torch.zeros(n, dtype=t) for t in (I32, BF, torch.uint8, F32))
+    tensors = [i32(2), i32(2), i32(9), i32(1), i32(2, 4), i32(3), i32(2), i32(5), i32(5), i32(1)]
+    caches = [u8(4, 2, 16, 64), u8(4, 2, 16, 4)] * 2
+    k = b16(5, 2, 128)
+    calls = [(bind.tables, tensors + [16, 9]), (bind.rope, [k, k, i32(5), f32(9, 128), k, k, None, None, 1e-6, False]),
+             (bind.append, [k, k, i32(5)] + caches), (bind.gather, [k, k, i32(5)] + caches),
+             (bind.attention, [k] + caches + [i32(2, 4), i32(3), i32(2), k, u8(1 << 24), None, 0])]
+    for call, args in calls:
+        assert call(*args) is None                          # tensors of the CPU
+        assert call(*args[:-1]) is None and call(*args, None) is None and call() is None
+        assert call(*([None] * len(args))) is None and call(*([2 ** 70] * len(args))) is None

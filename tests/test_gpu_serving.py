@@ -623,3 +623,81 @@ def test_steps_of_a_layer(fg):
         assert within(got[used], (ref[used], bound[used]), "bf16").all() and (got[~used] == -77.0).all()
         held = sum(-(-int(x) // page) for x in lens.cpu().numpy())
         assert int(count) + held == pages
+
+
+# ------------------------------------------------------------------- the module in C++
+def native_calls(fg):
+    bind = fg._native()
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    bf16 = lambda *n: torch.zeros(n, dtype=BF, device="cuda")  # noqa: E731
+    caches = list(fg.kv_cache_mxfp4(4, 2, 16, 128))
+    free = torch.arange(9, dtype=torch.int32, device="cuda")
+    ws = fg.paged_attention_workspace(5, 2, 8, 2, 128)
+    q, k = bf16(5, 8, 128), bf16(5, 2, 128)
+    w = bf16(128)
+    return {
+        "tables": (bind.tables, [i32(2), i32(2), free, i32(1), i32(2, 4), i32(3), i32(2), i32(5), i32(5), i32(1), 16, 9]),
+        "rope": (bind.rope, [q, k, i32(5), torch.ones(9, 128, device="cuda"), q.clone(), k.clone(), w, w, 1e-6, True]),
+        "append": (bind.append, [k, k, i32(5) - 1] + caches),
+        "gather": (bind.gather, [k.clone(), k.clone(), i32(5)] + caches),
+        "attention": (bind.attention, [q] + caches + [i32(2, 4), i32(3), i32(2), q.clone(), ws, 0.1, 7]),
+    }
+
+
+@pytest.mark.parametrize("name", ["tables", "rope", "append", "gather", "attention"])
+def test_native_calls_take_good_arguments_only(fg, name):
+    call, args = native_calls(fg)[name]
+    assert call(*args) == fg.FG_OK
+    expect(fg)
+    for i, x in enumerate(args):
+        wrong = [object(), "x", 2 ** 40] + ([] if isinstance(x, float) else [0.5])
+        if torch.is_tensor(x):
+            wrong.append(x.cpu())
+            if not (name == "attention" and i == 9):        # a workspace is of any type
+                wrong.append(x.double())
+            if x.numel() > 1:
+                wrong.append(torch.stack([x, x], -1)[..., 0])                  # elements apart
+        for y in wrong:
+            assert call(*args[:i], y, *args[i + 1:]) is None, (i, y)
+    expect(fg)
+
+
+def test_native_calls_refuse_shapes_that_do_not_belong_together(fg):
+    calls = native_calls(fg)
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    bf16 = lambda *n: torch.zeros(n, dtype=BF, device="cuda")  # noqa: E731
+    u8 = lambda *n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    for name, i, y in [("tables", 0, i32(3)), ("tables", 1, i32(1)), ("tables", 3, i32(2)), ("tables", 4, i32(8)), ("tables", 4, i32(3, 4)),
+                       ("tables", 5, i32(2)), ("tables", 6, i32(1)), ("tables", 8, i32(4)), ("tables", 9, i32(2)),
+                       ("rope", 0, bf16(4, 8, 128)), ("rope", 0, bf16(5, 8, 64)), ("rope", 1, bf16(5, 3, 128)), ("rope", 2, i32(4)),
+                       ("rope", 3, torch.ones(128, device="cuda")), ("rope", 4, bf16(5, 4, 128)), ("rope", 5, bf16(5, 8, 128)),
+                       ("rope", 6, bf16(64)), ("rope", 0, bf16(5, 8, 256)[:, :, ::2]), ("rope", 0, bf16(5, 9, 128)[:, ::2]),
+                       ("append", 0, bf16(5, 3, 128)), ("append", 1, bf16(4, 2, 128)), ("append", 2, i32(4)), ("append", 3, u8(4, 2, 16, 32)),
+                       ("append", 4, u8(4, 2, 16, 3)), ("gather", 0, bf16(5, 2, 64)), ("gather", 5, u8(3, 2, 16, 64)),
+                       ("gather", 6, u8(4, 2, 16, 8)), ("gather", 3, u8(4 * 2 * 16, 64)),
+                       ("attention", 0, bf16(5, 8, 64)), ("attention", 0, bf16(4, 8, 128)), ("attention", 0, bf16(40, 128)),
+                       ("attention", 5, i32(3, 4)), ("attention", 5, i32(8)), ("attention", 6, i32(2)), ("attention", 7, i32(3)),
+                       ("attention", 8, bf16(5, 4, 128)), ("attention", 9, u8(1000))]:
+        call, args = calls[name]
+        assert call(*args[:i], y, *args[i + 1:]) is None, (name, i)
+    expect(fg)
+
+
+def test_native_calls_and_the_binding_agree(fg):
+    """A call without a stream goes through the module, one with the current stream through the binding."""
+    c = C.cache_case(77, [50, 300, 0], [3, 1, 0], 8, 2, 128, 16)
+    out, ws = attend(fg, c)
+    other, _ = attend(fg, c, ws=ws, stream=torch.cuda.current_stream())
+    assert torch.equal(out, other)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other, _ = attend(fg, c)
+    side.synchronize()
+    assert torch.equal(out, other)
+    check(c, out)
+    with pytest.raises(fg.FgError):
+        attend(fg, c, scale=-1.0)
+    with pytest.raises(ValueError):
+        attend(fg, c, ws=ws[:1000])
+    expect(fg)
