@@ -199,6 +199,18 @@ def test_one_long_request_is_split_and_joined(fg, hkv, length):
         assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("d,hq,new", [(64, 8, 1), (64, 16, 1), (64, 8, 3), (128, 16, 1), (128, 8, 1), (256, 8, 1), (256, 16, 1)])
+def test_long_requests_beside_short_ones(fg, d, hq, new):
+    """Many pieces an item, joined eight at a time, of one and more row tiles; items that end inside a group of eight."""
+    c = C.cache_case(d + hq, [9000, 3, 17, 6500], [new, 1, 0, new], hq, 1, d, 32)
+    out, ws = attend(fg, c)
+    expect(fg)
+    check(c, out)
+    assert not ws[:7680].any(), "counters are left as they were"
+    again, _ = attend(fg, c, ws=ws)
+    assert torch.equal(again, out)
+
+
 def test_a_workspace_serves_calls_of_other_sizes(fg):
     ws = fg.paged_attention_workspace(64, 1, 32, 1, 256)
     for seed, (lens, new, hq, hkv, d) in enumerate([([700, 3], [2, 1], 8, 2, 128), ([5000], [1], 4, 1, 256),
