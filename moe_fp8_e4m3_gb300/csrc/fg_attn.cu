@@ -663,7 +663,7 @@ int fg_paged_attention_mxfp4(int T, int S, int Hq, int Hkv, int D, int page_size
     const AttnParams p{static_cast<const uint16_t*>(q), k_cache, k_sf, v_cache, v_sf, block_table, query_start, seq_lens,
                        static_cast<uint16_t*>(out), T, S, Hkv, Hq / Hkv, page_size, num_pages, max_pages, window,
                        scale * 1.4426950408889634f, reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCtrBytes),
-                       st.status, st.timeout_ns};
+                       st.status, st.timeout_ns, st.debug_stall};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (many_rows(T, S, Hkv, Hq / Hkv, D, (long long)max_pages * page_size, window))
         return fg::launch_attn_prompt(p, D, prompt_rows(T, S, Hq / Hkv, D), st.sms, st.pdl, s);

@@ -30,6 +30,7 @@ struct AttnParams {
     float* part;                               // [2 * kAttnMaxCtas][kRows][D + 2]: M, l, O
     int* status;
     unsigned long long timeout_ns;
+    int stall;                                 // for tests: a key tile that is never announced
 };
 
 

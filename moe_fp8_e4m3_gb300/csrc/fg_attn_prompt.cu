@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                     for (int b = 0; b < B; ++b) st_shared_16(kt + place(b, c0 + i), decode(x.k[i][b], scale_of<B>(x.ks, b)));
                 fg::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) fg::mbar_arrive(k_full);
+                if (lane == 0 && !(p.stall != 0 && n == 0 && warp == kDecodeWarp0)) fg::mbar_arrive(k_full);   // stalled: the MMA issuer times out
                 ok = wait(v_empty + 8 * st, ph ^ 1);
                 if (!__all_sync(kAll, ok)) return false;
 #pragma unroll

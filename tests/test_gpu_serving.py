@@ -177,6 +177,25 @@ def test_many_rows_contract_violations_and_non_finite_queries(fg, hq):
     assert (got[70:] == -77).all()
 
 
+@pytest.mark.parametrize("hq", [4, 32])
+def test_a_stalled_wait_times_out_and_the_context_survives(fg, hq):
+    """The bounded waits of the tensor-core kernel, of one row tile and two: with its first key tile held back (host-side
+    hook) the call records a time-out and returns, and the same call is right afterwards, on a workspace zeroed anew."""
+    c = C.wide(C.cache_case(21, [300, 190], [70, 80], hq, 1 if hq == 32 else 2, 128, 16))
+    assert C.many_rows(c)
+    fg.debug_inject_stall(True, 200_000)
+    try:
+        out, ws = attend(fg, c)
+        status, detail = fg.get_device_error()
+    finally:
+        fg.debug_inject_stall(False)
+    assert status == fg.FG_ERR_DEVICE_TIMEOUT and detail & 0xF00 == 0x200
+    ws.zero_()
+    out, _ = attend(fg, c, ws=ws)
+    expect(fg)
+    check(c, out)
+
+
 def test_rows_before_the_first_key(fg):
     """More rows than cached tokens: the rows before position 0 look at nothing and become zero."""
     c = C.cache_case(3, [3, 0, 20], [3, 0, 2], 4, 2, 128, 16, extra_rows=9)
