@@ -49,6 +49,11 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int r) 
     const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
     return ok ? AttnRequest{t1 - t0, len, t0} : AttnRequest{0, 0, 0};
 }
+// First key that a row at position hi - 1 looks at.  A row before position 0 has a negative hi, of which a window as large
+// as its type is not taken away: the difference would wrap.
+__device__ __forceinline__ int attn_from(const AttnParams& p, int hi) {
+    return p.window > 0 ? max(0, max(hi, 0) - p.window) : 0;
+}
 // Keys [lo, hi) that some row of a chunk looks at; hi <= lo: none.
 struct AttnKeys {
     int lo, hi;
@@ -86,7 +91,7 @@ struct AttnCursor {
     __device__ __forceinline__ void look_at(const AttnParams& p, int chunk) {
         const int i0 = chunk * kRows / p.group, i1 = min(rq.n - 1, (chunk * kRows + kRows - 1) / p.group);
         keys.hi = rq.len - rq.n + i1 + 1;
-        keys.lo = p.window > 0 ? max(0, rq.len - rq.n + i0 + 1 - p.window) : 0;
+        keys.lo = attn_from(p, rq.len - rq.n + i0 + 1);
         cost = kStart + (keys.hi > keys.lo ? (keys.hi + kBlock - 1) / kBlock - keys.lo / kBlock : 1);
     }
 

@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
             const int group = warp >> 2, my = (warp & 3) * 32 + lane;
             const int rt = RT == 1 ? 0 : group, col0 = RT == 1 ? group * C::kWide : 0;
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const int hi = first + (row0 + rt * 128 + my) / p.group + 1, lo = p.window > 0 ? hi - p.window : 0;
+            const int hi = first + (row0 + rt * 128 + my) / p.group + 1, lo = fg::attn_from(p, hi);
             // keys that every row of the chunk looks at
             const int all_hi = first + row0 / p.group + 1;
-            const int all_lo = p.window > 0 ? max(0, first + (row0 + rows - 1) / p.group + 1 - p.window) : 0;
+            const int all_lo = fg::attn_from(p, first + (row0 + rows - 1) / p.group + 1);
             const uint32_t p_row = sbase + C::kOffP + (col0 / 64) * (128 * 128) + my * 128;
             for (int i = 0; i < tiles; ++i) {
                 const uint32_t n = n0 + i, u = RT * n + rt, st = u & 1, ph = (u >> 1) & 1;

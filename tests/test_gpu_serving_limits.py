@@ -1,0 +1,38 @@
+"""The attention side of a serving step at the limits of its arguments: windows as large as their type."""
+import numpy as np
+import pytest
+
+import serving_cases as C
+from test_gpu_serving import attend, check, expect, f64, fg  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ---------------------------------------------------------------------------- windows
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 3, 40, 2 ** 30, 2 ** 31 - 4, 2 ** 31 - 1])
+def test_windows_over_rows_before_the_first_key(fg, d, window):
+    """Requests of more rows than cached tokens: rows before position 0 look at nothing, the others at what the window
+    holds, however large it is."""
+    c = C.cache_case(d + window % 97, [3, 0, 20, 9], [3, 0, 2, 9], 4, 2, d, 16, extra_rows=9)
+    c["start"] = np.array([0, 9, 12, 14, 23], np.int32)
+    out, _ = attend(fg, c, window)
+    expect(fg)
+    check(c, out, window)
+    got = f64(out)
+    assert not got[:6].any() and not got[9:12].any() and got[6:9].any(axis=(1, 2)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq", [8, 32])
+@pytest.mark.parametrize("window", [20, 2 ** 31 - 4, 2 ** 31 - 1])
+def test_windows_over_many_rows_before_the_first_key(fg, d, hq, window):
+    c = C.wide(C.cache_case(d + hq, [30, 90], [30, 40], hq, 1, d, 16, extra_rows=3 * 2048))
+    c["start"] = np.array([0, 70, 110], np.int32)
+    assert C.many_rows(c, window)
+    out, _ = attend(fg, c, window)
+    expect(fg)
+    check(c, out, window)
+    got = f64(out)
+    assert not got[:40].any() and got[40:70].any(axis=(1, 2)).all()
