@@ -504,8 +504,8 @@ int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
  * Rows >= query_start[S] stay as they were; what the cache holds behind a request's length is never used.
  *   q, out [T][Hq][D] BF16;  block_table [S][max_pages], query_start [S + 1], seq_lens [S] int32
  * query_start that falls or leaves [0, T], a seq_lens outside [0, max_pages * page_size]: 0x10A is recorded and
- * the request's rows stay as they were (all rows, where query_start falls so far that requests claim more than
- * T).  A page outside [0, num_pages): 0x10A, and its tokens count as absent.
+ * the request's rows stay as they were (all rows, where a request's rows begin before those of an earlier request
+ * end, so that two might claim the same ones).  A page outside [0, num_pages): 0x10A, and its tokens count as absent.
  *   workspace: fg_paged_attention_workspace bytes (11 to 40 MB; enough for any call of as many rows or fewer), under the same
  *   rules as fg_moe_mlp_workspace, but not one that those calls use
  * Hq % Hkv == 0.  Supported: S <= 4096, T <= 2^18, Hq / Hkv <= 256.

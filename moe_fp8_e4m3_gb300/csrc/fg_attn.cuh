@@ -40,14 +40,27 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// One request as the kernels see it (n == 0: nothing to do, or its lengths are wrong).
+// One request as the kernels see it (n == 0: nothing to do, or its lengths are wrong; then t0 < 0: query_start falls).
 struct AttnRequest {
     int n, len, t0;
 };
 __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int r) {
     const int t0 = __ldcg(p.start + r), t1 = __ldcg(p.start + r + 1), len = __ldcg(p.lens + r);
     const bool ok = t0 >= 0 && t1 >= t0 && t1 <= p.T && len >= 0 && len <= (long long)p.max_pages * p.page;
-    return ok ? AttnRequest{t1 - t0, len, t0} : AttnRequest{0, 0, 0};
+    return ok ? AttnRequest{t1 - t0, len, t0} : AttnRequest{0, 0, t1 < t0 ? -1 : 0};
+}
+// Whether a request's rows begin before those of an earlier one end, so that two might write the same ones.  Where
+// query_start does not fall there is none.
+__device__ __forceinline__ bool attn_claimed_twice(const AttnParams& p) {
+    int end = 0;
+#pragma unroll 1
+    for (int q = 0; q < p.S; ++q) {
+        const AttnRequest x = attn_request(p, q);
+        if (x.n == 0) continue;
+        if (x.t0 < end) return true;
+        end = x.t0 + x.n;
+    }
+    return false;
 }
 // First key that a row at position hi - 1 looks at.  A row before position 0 has a negative hi, of which a window as large
 // as its type is not taken away: the difference would wrap.
@@ -133,8 +146,6 @@ struct AttnCursor {
     __device__ __forceinline__ bool open(const AttnParams& p, AttnPlanSmem<kThreads>& sm, int* s_pre) {
         const int tid = threadIdx.x;
         unsigned long long total_blocks;
-        // chunks of requests that do not overlap
-        const unsigned long long most = (unsigned long long)p.T * p.group / kRows + p.S;
         constexpr int kFew = 64;                               // chunks that a thread walks
         if (kByRequest && p.S <= kThreads) {
             // few chunks a request, a request a thread: chunks and costs in one scan
@@ -142,11 +153,12 @@ struct AttnCursor {
             int n = 0;
             ch = 0;
             r = 0;
+            rq.t0 = 0;
             if (tid < p.S) {
                 rq = attn_request(p, tid);
                 n = static_cast<int>(((long long)rq.n * p.group + kRows - 1) / kRows);
             }
-            if (!__syncthreads_or(n > kFew)) {
+            if (!__syncthreads_or(n > kFew || rq.t0 < 0)) {
                 if (blockIdx.x == 0 && tid < p.S && rq.n == 0) complain(p, tid);
                 for (int i = 0; i < n; ++i) {
                     look_at(p, i);
@@ -155,10 +167,6 @@ struct AttnCursor {
                 sum |= static_cast<unsigned long long>(n) << 40;   // costs stay below 2^39: kThreads x kFew chunks of at most 2^24 blocks
                 static_assert(kThreads * kFew <= 1 << 14 || !kByRequest, "room for both");
                 const unsigned long long at = scan(sum, sm.warp, total);
-                if (total >> 40 > most) {
-                    if (blockIdx.x == 0 && tid == 0) kv_record(p.status, kKvErrAttention);
-                    return false;
-                }
                 sm.strip[tid] = at & kCostMask;
                 if (tid <= p.S) s_pre[tid] = static_cast<int>(at >> 40);
                 if (tid == 0 && p.S == kThreads) s_pre[kThreads] = static_cast<int>(total >> 40);
@@ -169,26 +177,24 @@ struct AttnCursor {
         }
         const int per_r = (p.S + kThreads - 1) / kThreads;
         {
+            constexpr unsigned long long kFalls = 1ull << 48;      // of query_start, counted above the chunks (below 2^36)
             unsigned long long sum = 0, total;
             for (int i = 0; i < per_r; ++i) {
                 const int q = tid * per_r + i;
                 if (q >= p.S) break;
                 const AttnRequest x = attn_request(p, q);
                 if (blockIdx.x == 0 && x.n == 0) complain(p, q);
-                sum += ((long long)x.n * p.group + kRows - 1) / kRows;
+                sum += ((long long)x.n * p.group + kRows - 1) / kRows + (x.t0 < 0 ? kFalls : 0);
             }
-            unsigned long long at = scan(sum, sm.warp, total);
-            if (total > most) {                                // requests overlap: their chunks could be more than anything holds
-                if (blockIdx.x == 0 && tid == 0) kv_record(p.status, kKvErrAttention);
-                return false;
-            }
+            unsigned long long at = scan(sum, sm.warp, total) % kFalls;
+            if (total >= kFalls && attn_claimed_twice(p)) return false;    // the fall is on record
             for (int i = 0; i < per_r; ++i) {
                 const int q = tid * per_r + i;
                 if (q >= p.S) break;
                 s_pre[q] = static_cast<int>(at);
                 at += ((long long)attn_request(p, q).n * p.group + kRows - 1) / kRows;
             }
-            if (tid == 0) s_pre[p.S] = static_cast<int>(total);
+            if (tid == 0) s_pre[p.S] = static_cast<int>(total % kFalls);
         }
         __syncthreads();
         const int chunks = s_pre[p.S];

@@ -1,4 +1,5 @@
-"""The attention side of a serving step at the limits of its arguments: windows as large as their type."""
+"""The attention side of a serving step at the limits of its arguments: windows as large as their type, requests that
+claim the same rows."""
 import numpy as np
 import pytest
 
@@ -36,3 +37,33 @@ def test_windows_over_many_rows_before_the_first_key(fg, d, hq, window):
     check(c, out, window)
     got = f64(out)
     assert not got[:40].any() and got[40:70].any(axis=(1, 2)).all()
+
+
+# ------------------------------------------------------------- rows claimed more than once
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("s", [3, 300, 1000])
+@pytest.mark.parametrize("tokens", [16, 1 << 18])
+def test_a_few_rows_claimed_twice(fg, d, s, tokens):
+    """query_start falls once and by little: requests 0 and 2 both claim rows 3 and 4, all requests together fewer rows
+    than the call has.  Nothing is written, whatever the order of the two, and the next call is right."""
+    new = [5, 0, 5] + [1] * (s - 3)
+    c = C.wide(C.cache_case(s + d, [n + 3 for n in new], new, 4, 2, d, 16, extra_rows=40 * s if tokens > 16 else 8), tokens)
+    assert C.many_rows(c) == (tokens > 16)
+    start = c["start"].copy()
+    start[2:] -= 2
+    out, ws = attend(fg, dict(c, start=start))
+    expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
+    assert (f64(out) == -77).all()
+    out, _ = attend(fg, c, ws=ws)
+    expect(fg)
+    check(c, out)
+
+
+def test_many_chunks_a_request_and_rows_claimed_twice(fg):
+    """Requests of more chunks than one thread walks take another way through the plan."""
+    c = C.cache_case(31, [600, 20, 600], [600, 0, 600], 4, 1, 64, 16, extra_rows=8)
+    c["start"] = np.array([0, 600, 598, 1198], np.int32)
+    assert not C.many_rows(c)
+    out, _ = attend(fg, c)
+    expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
+    assert (f64(out) == -77).all()
