@@ -42,6 +42,11 @@ __device__ __forceinline__ Sums shfl_up(Sums v, int o) {
                 __shfl_up_sync(0xffffffffu, v.more, o)};
 }
 
+// Pages of n >= 0 tokens.  Unsigned: n + page - 1 may pass 2^31 (a page holds up to 2^31 - 1 tokens), and not 2^32.
+__device__ __forceinline__ int pages_of(int n, int page) {
+    return static_cast<int>((static_cast<unsigned>(n) + static_cast<unsigned>(page) - 1) / static_cast<unsigned>(page));
+}
+
 // Last r with a[r] <= i, a[0] == 0, over n entries.
 __device__ __forceinline__ int find(const int* a, int n, int i) {
     int lo = 0, hi = n;
@@ -84,11 +89,11 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
             bad = true;
             continue;
         }
-        const int held = (context[i] + p.page - 1) / p.page;
+        const int held = pages_of(context[i], p.page);
         if (fresh[i] < 0) each[i].back = held;
         else {
             each[i].tokens = fresh[i];
-            each[i].more = (context[i] + fresh[i] + p.page - 1) / p.page - held;
+            each[i].more = pages_of(context[i] + fresh[i], p.page) - held;
         }
         mine = mine + each[i];
     }
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
     if (!bad) {
         for (int i = first; i < total.more; i += step) {    // new pages into the table
             const int r = find(s_more, p.S, i);
-            const int held = (s_context[r] + p.page - 1) / p.page;
+            const int held = pages_of(s_context[r], p.page);
             p.table[(long long)r * p.max_pages + held + i - s_more[r]] = __ldcg(p.free + top - 1 - i);
         }
     }
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesParams p) {
         if (!bad && i < total.tokens) {
             const int r = find(s_start, p.S, i);
             pos = s_context[r] + i - s_start[r];
-            const int held = (s_context[r] + p.page - 1) / p.page, j = pos / p.page;
+            const int held = pages_of(s_context[r], p.page), j = pos / p.page;
             const int id = j < held ? __ldcg(p.table + (long long)r * p.max_pages + j)
                                     : __ldcg(p.free + top - 1 - (s_more[r] + j - held));
             if (id >= 0 && id < p.num_pages) slot = id * p.page + pos % p.page;

@@ -1,10 +1,10 @@
-"""The attention side of a serving step at the limits of its arguments: windows as large as their type, requests that
-claim the same rows."""
+"""The serving step's operators at the limits of their arguments: windows as large as their type, requests that claim
+the same rows, pages of more than 2^30 tokens."""
 import numpy as np
 import pytest
 
 import serving_cases as C
-from test_gpu_serving import attend, check, expect, f64, fg  # noqa: F401
+from test_gpu_serving import attend, check, expect, f64, fg, tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -67,3 +67,42 @@ def test_many_chunks_a_request_and_rows_claimed_twice(fg):
     out, _ = attend(fg, c)
     expect(fg, fg.FG_ERR_DEVICE_CONTRACT, 0x10A)
     assert (f64(out) == -77).all()
+
+
+# ------------------------------------------------------------------------- block tables
+@pytest.mark.parametrize("page,width,context,new", [
+    (2 ** 31 - 1, 1, [5, 0, 2 ** 31 - 4], [3, 0, 2]), (2 ** 30 + 16, 1, [2 ** 30, 7, 0], [9, -1, 1]),
+    (2 ** 30 - 8, 2, [2 ** 30 - 9, 2 ** 30, 2 ** 31 - 20], [2, 1, -1]), (2 ** 29 + 1, 3, [2 ** 30, 2 ** 29 + 1, 2], [4, 1, 1])])
+def test_block_tables_of_pages_past_2_30_tokens(fg, page, width, context, new):
+    """Rounding up to pages passes 2^31 on the way: the tables are the oracle's all the same."""
+    held = [-(-n // page) for n in context]
+    table, at = np.full((3, width), -5), 0
+    for r, n in enumerate(held):
+        table[r, :n] = np.arange(at, at + n) % ((2 ** 31 - 1) // page)
+        at += n
+    c = {"context": context, "new": new, "free": [0] * 8, "count": 4, "table": table, "pages": (2 ** 31 - 1) // page}
+    a = tables(fg, c, sum(max(n, 0) for n in new) + 2, page)
+    expect(fg)
+    check_block_tables(a, c, page)
+
+
+def check_block_tables(a, c, page):
+    """O.block_tables walks every position; here only the new ones are walked."""
+    stack, table = list(c["free"][:c["count"]]), c["table"].copy()
+    for r, n in enumerate(c["new"]):
+        if n < 0:
+            stack += [int(x) for x in table[r, :-(-c["context"][r] // page)]]
+    free = np.array(stack + list(c["free"][len(stack):]))
+    slots, positions, lens, start = [], [], [], [0]
+    for r, n in enumerate(c["new"]):
+        lens.append(c["context"][r] + n if n >= 0 else 0)
+        for j in range(-(-c["context"][r] // page), -(-lens[r] // page)):
+            table[r, j] = stack.pop()
+        for pos in range(c["context"][r], lens[r]):
+            slots.append(int(table[r, pos // page]) * page + pos % page)
+            positions.append(pos)
+        start.append(len(slots))
+    spare = [-1] * (a["slots"].numel() - len(slots))
+    assert a["slots"].tolist() == slots + spare and a["positions"].tolist() == positions + spare
+    assert a["lens"].tolist() == lens and a["start"].tolist() == start and int(a["count_out"]) == len(stack)
+    assert np.array_equal(a["table"].cpu().numpy(), table) and np.array_equal(a["free"].cpu().numpy(), free)
