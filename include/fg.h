@@ -496,11 +496,14 @@ int fg_kv_gather_mxfp4(int T, int heads, int D, int page_size, int num_pages, co
  * p = seq_lens[r] - n + i and looks at the cached positions j <= p, and with window > 0 at j > p - window only:
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k_j) v_j      (kv head h / (Hq / Hkv))
  * with cached position j at offset j mod page_size of page block_table[r][j / page_size].  FP32 scores,
- * statistics and sums; a weight is rounded once, to FP16, or to BF16 where the tensor cores take 128 or 256 rows at a
- * time: where an average request (ceil(T / S) tokens) brings more than 32 rows of a kv head and that is faster, which
+ * statistics and sums.  A weight is rounded once: times its value's block scale to FP16 (by 2^-11 of itself, or by
+ * 2^-25 of the largest such product of its row and block; not at all from where a token's block scales lie more than 2^8
+ * apart, which is three times as slow), or to BF16 (2^-8) where the tensor cores take 128 or 256 rows at a time.
+ * They do where an average request (ceil(T / S) tokens) brings more than 32 rows of a kv head and that is faster, which
  * depends on T, S, Hkv, D, window and max_pages * page_size, on nothing that only the device knows (so a few prompts
- * among many requests of single tokens are faster in a call of their own).  A row that
- * looks at nothing (p < 0) becomes 0.
+ * among many requests of single tokens are faster in a call of their own).  Elsewhere q becomes FP16 after a scaling of
+ * each row by a power of two: exact down to 2^-22 of the row's largest element, off by up to 2^-33 of it below.
+ * A row that looks at nothing (p < 0) becomes 0.
  * Rows >= query_start[S] stay as they were; what the cache holds behind a request's length is never used.
  *   q, out [T][Hq][D] BF16;  block_table [S][max_pages], query_start [S + 1], seq_lens [S] int32
  * query_start that falls or leaves [0, T], a seq_lens outside [0, max_pages * page_size]: 0x10A is recorded and

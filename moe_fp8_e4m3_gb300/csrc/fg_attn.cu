@@ -4,12 +4,16 @@
 // s_jb * (codes), per 16 tokens:
 //   S^T = K Q^T      16 tokens x 8 rows per mma (m16n8k16, FP16 codes, FP16 q scaled to [2^8, 2^9) by a
 //                    power of two per row, exact); one FP32 accumulator per block of 32, then times s_jb
-//   w_jb = 2^(S_j - M) * t_jb      t_jb: the value's block scale; M a running maximum of S_j + max_b log2 t_jb,
-//                    so that w <= 2^14 in FP16 however far the scales of different tokens lie apart
+//   w_jb = 2^(S_j - M) * t_jb      t_jb: the value's block scale; M follows the maximum of S_j + max_b log2 t_jb,
+//                    so that w <= 2^15 in FP16 however far the scales of different tokens lie apart
 //   O^T += V^T W^T   32 elements of block b x 16 tokens x 8 rows, FP16 codes, FP32 accumulators
 //   l   += 2^(S_j - M),   o = O / l
-// M moves only when some w might pass 2^15 (a vote a tile); then O and l are scaled.  A weight is rounded
-// once, to FP16 (2^-11 relative, down to 2^-22 of a row's largest weight times scale, 2^-33 of it absolute).
+// M moves only when some w might pass 2^15 (a vote a tile), to where the largest is 2^8; then O and l are scaled.
+// A weight is rounded once, to FP16: by 2^-11 of itself, or by 2^-33 of the row's largest w where that is more.  M
+// speaks for all blocks, so that is 2^-25 of a block's own largest w as long as the scales of a token lie within 2^8 of each
+// other.  From the first tile on in which they do not (the same vote), a warp multiplies its piece's weights and values in
+// FP32 on the CUDA cores: called alone, 64 requests of up to 8192 tokens then take 229 us for 69, one of 131072 127 for 45.
+// The check costs 0.6 of 67.7 us; with the FP32 products in the same loop it was 4.3 (registers).
 //
 // Work.  An item (fg_attn.cuh: request, chunk of kRows rows, kv head) is walked in blocks of 128 tokens, of which each of
 // a CTA's eight warps takes 16 with accumulators of its own, joined at the end through shared memory.  Codes and scales
@@ -26,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdio>
+#include <type_traits>
 
 #include "fg.h"
 #include "fg_host.h"
@@ -82,6 +87,9 @@ __device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t w, int i) {
     else if (i == 2) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
     else asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
     return r;
+}
+__device__ __forceinline__ void f16x2_f32(uint32_t h, float& lo, float& hi) {
+    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h));
 }
 // Transposes an 8 x 8 matrix of 16-bit values (row i / 4, columns 2 (i mod 4) and + 1 in lane i).
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -178,6 +186,19 @@ __device__ __forceinline__ float top_exponent(const float (&f)[B]) {
     for (int b = 1; b < B; ++b) m = fmaxf(m, f[b]);
     const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
     return static_cast<float>(max(e, fg::kKvMinExp));
+}
+
+// Whether a token's B scales are more than 2^8 apart, at the latest: B sum e^2 - (sum e)^2, the squared differences of its
+// exponents over all pairs, is at least B / 2 times the largest of them.
+template <int B>
+__device__ __forceinline__ bool scales_apart(const uint32_t (&s)[(B + 3) / 4]) {
+    uint32_t sum = 0, squares = 0;
+#pragma unroll
+    for (int i = 0; i < (B + 3) / 4; ++i) {
+        sum = __dp4a(s[i], 0x01010101u, sum);
+        squares = __dp4a(s[i], s[i], squares);
+    }
+    return B * squares > sum * sum + 32 * B;
 }
 
 template <int B, int NT>
@@ -299,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
         // One after another in flight: q, the pages of the first tiles, those tiles.
         uint4 raw[B];
         if (!C::kQShared || warp < NT) load_q(C::kQShared ? warp : 0, raw);
-        uint32_t absent = 0;                                // bit: the stage's tile has no page
+        uint32_t absent = 0;                                // bit: the stage's tile has no page; a tile left to the FP32 loop: its stage + 1, from bit 8 on
         uint32_t page, off;
         {
             uint32_t pages[C::kStages - 1], offs[C::kStages - 1];
@@ -340,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
             m[nt][0] = m[nt][1] = kEmpty;
         }
 
-        auto compute = [&](int stage, int tok0, bool ok) {
+        // A tile.  False: a token's value scales are far apart, nothing is done yet, and kApart has to do it.
+        auto compute = [&](auto is_apart, int stage, int tok0, bool ok) {
+            constexpr bool kApart = decltype(is_apart)::value;
             const uint32_t at = stage * C::kTile;
             uint32_t ks0[(B + 3) / 4], ks1[(B + 3) / 4], vs0[(B + 3) / 4], vs1[(B + 3) / 4];
             load_scales<B>(ks0, at_sf + at);
@@ -390,6 +413,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
                         if (!(in1 && t1 >= lo && t1 < hi)) s[nt][2 + k] = -INFINITY;
                     }
             }
+            bool far = false;
+            if constexpr (!kApart) {                            // two of the four lanes that have a token's scales look at them
+                uint32_t mine[(B + 3) / 4];
+#pragma unroll
+                for (int i = 0; i < (B + 3) / 4; ++i) mine[i] = (c & 1) ? vs1[i] : vs0[i];
+                far = scales_apart<B>(mine);
+            }
             scales_of<B>(f0, vs0);
             scales_of<B>(f1, vs1);
             float w[NT][4];
@@ -407,11 +437,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
             float sum0 = f0[0], sum1 = f1[0];
 #pragma unroll
             for (int b = 1; b < B; ++b) { sum0 += f0[b]; sum1 += f1[b]; }
-            bool over = false;
+            bool over = far;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 over |= !(fmaf(w[nt][0], sum0, fmaf(w[nt][1], sum0, fmaf(w[nt][2], sum1, w[nt][3] * sum1))) <= kMostW);
             if (__any_sync(kAll, over)) {
+                if (!kApart && __any_sync(kAll, far)) return false;
                 const float e0 = top_exponent<B>(f0), e1 = top_exponent<B>(f1);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -436,6 +467,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
             for (int nt = 0; nt < NT; ++nt) {
                 l[nt][0] += w[nt][0] + w[nt][2];
                 l[nt][1] += w[nt][1] + w[nt][3];
+            }
+            if constexpr (kApart) {
+#pragma unroll 1
+                for (int t = 0; t < 8; ++t) {
+                    const int from = 4 * t + c, row = token_of<B>(t);     // the lane that has this token's weights
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t v[B / 2];
+                        load_value<B>(v, ring + at + C::kTileV + row * (16 * B) + 128 * B * i, swizzle<B>(row), g);
+                        float u[NT][2];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) u[nt][k] = __shfl_sync(kAll, w[nt][2 * i + k], from);
+#pragma unroll
+                        for (int b = 0; b < B; ++b) {
+                            const float f = __shfl_sync(kAll, i ? f1[b] : f0[b], from);
+                            float x[4];
+                            f16x2_f32(e2m1x2_f16(v[b / 2], 2 * (b & 1)), x[0], x[1]);
+                            f16x2_f32(e2m1x2_f16(v[b / 2], 2 * (b & 1) + 1), x[2], x[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const float uf = u[nt][k] * f;
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        o[nt][2 * b + j / 2][2 * (j & 1) + k] = fmaf(uf, x[j], o[nt][2 * b + j / 2][2 * (j & 1) + k]);
+                                }
+                        }
+                    }
+                }
+                return true;
             }
             uint32_t even[2][B / 2], odd[2][B / 2];            // row group g of tokens 2c and 2c + 1, 2c + 8 and 2c + 9
 #pragma unroll
@@ -468,23 +532,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
                     for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * b + i], a0, a1, a2, a3, wb[nt][0], wb[nt][1]);
                 }
             }
+            return true;
+        };
+        // Waits for the tile in `stage` and sends for the one kAhead tiles on.
+        constexpr int kAhead = C::kStages - 1;
+        auto advance = [&](int stage) {
+            constexpr uint32_t kBits = (1u << C::kStages) - 1;
+            const int next = (stage + kAhead) % C::kStages;
+            const bool ok = issue(page, off, next, base + kAhead * kBlock < base_end);
+            absent = (absent & (kBits ^ 1u << next)) | (ok ? 0u : 1u << next);
+            next_page(base + C::kStages * kBlock, page, off);
+            cp_async_wait<kAhead>();
+            __syncwarp();
         };
 
         while (base < base_end) {
 #pragma unroll
             for (int i = 0; i < C::kStages; ++i) {          // stages at fixed places
-                constexpr int kAhead = C::kStages - 1;
-                constexpr uint32_t kBits = (1u << C::kStages) - 1;
-                const int next = (i + kAhead) % C::kStages;
-                const bool ok = issue(page, off, next, base + kAhead * kBlock < base_end);
-                absent = (absent & (kBits ^ 1u << next)) | (ok ? 0u : 1u << next);
-                next_page(base + C::kStages * kBlock, page, off);
-                cp_async_wait<kAhead>();
-                __syncwarp();
-                compute(i, base, !(absent >> i & 1u));
+                advance(i);
+                if (!compute(std::false_type{}, i, base, !(absent >> i & 1u))) {
+                    absent |= (i + 1u) << 8;
+                    break;
+                }
                 __syncwarp();                               // every lane has read the stage that is filled next
                 base += kBlock;
                 if (base >= base_end) break;
+            }
+            if (absent >> 8) break;
+        }
+        if (absent >> 8) {                                  // this tile and all that follow
+            int stage = static_cast<int>(absent >> 8) - 1;
+            while (true) {
+                compute(std::true_type{}, stage, base, !(absent >> stage & 1u));
+                __syncwarp();
+                base += kBlock;
+                if (base >= base_end) break;
+                stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                advance(stage);
             }
         }
         cp_async_wait<0>();

@@ -117,13 +117,13 @@ def cached(table_row, n, codes, sf, kind, head):
 
 
 # -------------------------------------------------------------------------- attention
-def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0, weight=2.0 ** -11):
+def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0, weight=2.0 ** -11, floor=2.0 ** -33):
     """q [T, Hq, D] FP64 values.  (out, bound, used): rows of requests are True in `used`.
 
     Bound, row by row: a score of D products, whose absolute values add up to S, is off by D + 8 units of S in
     FP32 (products and partial sums; q's conversion to FP16 after a power-of-two scaling is exact down to 2^-22 of
     the row's largest, 2^-33 of it absolute); the exponential adds 8 units; a weight times its value's scale is
-    rounded to FP16, 2^-11 of itself or 2^-33 of the row's largest; sums over n keys are off by n + 16 units (n / 16
+    rounded to FP16, 2^-11 of itself (``weight``) or 2^-33 (``floor``) of the row's largest; sums over n keys are off by n + 16 units (n / 16
     accumulations and the joins).  Numerator and denominator errors add up."""
     t, hq, d = q.shape
     hkv = kc.shape[1]
@@ -157,7 +157,7 @@ def attention(q, kc, ks, vc, vs, table, start, lens, scale, window=0, weight=2.0
                 o = p @ v
                 largest = np.max(p[:, :, None] * vscale[None], axis=(1, 2))[:, None]
                 num = (p * (ds + weight)) @ np.abs(v) + (p @ np.abs(v)) * (length + 16) * 2 * U
-                num += 2.0 ** -33 * largest * 6 * seen.sum(1, keepdims=True)
+                num += floor * largest * 6 * seen.sum(1, keepdims=True)
                 den = (p * ds).sum(1, keepdims=True) + (length + 16) * 2 * U
                 out[t0:t0 + n, hh] = o
                 bound[t0:t0 + n, hh] = num + np.abs(o) * den

@@ -1,9 +1,11 @@
 """The serving step's operators at the limits of their arguments: windows as large as their type, requests that claim
-the same rows, pages of more than 2^30 tokens."""
+the same rows, pages of more than 2^30 tokens, value scales far apart within a token."""
 import numpy as np
 import pytest
 
 import serving_cases as C
+from oracle import serving as O
+from oracle.decode import within
 from test_gpu_serving import attend, check, expect, f64, fg, tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +108,94 @@ def check_block_tables(a, c, page):
     assert a["slots"].tolist() == slots + spare and a["positions"].tolist() == positions + spare
     assert a["lens"].tolist() == lens and a["start"].tolist() == start and int(a["count_out"]) == len(stack)
     assert np.array_equal(a["table"].cpu().numpy(), table) and np.array_equal(a["free"].cpu().numpy(), free)
+
+
+# ------------------------------------------------------ value scales far apart in a token
+def values_apart(c, seed, spread, fall, tokens=None):
+    """The case with values whose 32-element blocks differ by up to 2^(2 spread) within a token: anyhow, or (fall) from
+    the first block down to the last one in every token; tokens: only these of every request."""
+    g = C.rng(seed)
+    d, hkv, page = c["d"], c["hkv"], c["page"]
+    for r, n in enumerate(c["lens"]):
+        t = np.arange(n) if tokens is None else np.array([i for i in tokens if i < n], np.int64)
+        e = g.integers(-spread, spread + 1, (len(t), hkv, d // 32, 1))
+        if fall:
+            e[:] = np.linspace(spread, -spread, d // 32).round().astype(np.int64)[:, None]
+        x = g.standard_normal((len(t), hkv, d // 32, 32)) * 2.0 ** e
+        codes, sf = O.encode(x.reshape(len(t), hkv, d))
+        p, o = c["table"][r, t // page], t % page
+        c["vc"][p, :, o], c["vs"][p, :, o] = O.rows(codes, "v"), sf
+    return c
+
+
+def check_by_block(c, out, window=0):
+    """A weight times a block's scale is off by 2^-11 of itself (2^-8 where the tensor cores take many rows) or by 2^-25
+    of the largest such product of the same row and block; the exponent that both are taken of, up to 2^8, is off by 2^-17."""
+    got = f64(out)
+    weight = 2.0 ** (-8 if C.many_rows(c, window) else -11) + 2.0 ** -16
+    for b in range(c["d"] // 32):
+        # with block b's scales in the place of all, the oracle's largest product is block b's
+        vs = np.repeat(c["vs"][..., b:b + 1], c["d"] // 32, -1)
+        ref, bound, used = O.attention(c["q"], c["kc"], c["ks"], c["vc"], vs, c["table"], c["start"], c["lens"], c["d"] ** -0.5,
+                                       window, weight, floor=2.0 ** -25)
+        e = slice(32 * b, 32 * b + 32)
+        bad = ~within(got[used][..., e], (ref[used][..., e], bound[used][..., e]), "bf16")
+        assert not bad.any(), (b, bad.sum(), np.argwhere(bad)[:4], got[used][..., e][bad][:4], ref[used][..., e][bad][:4])
+
+
+@pytest.mark.parametrize("d,hq", [(64, 1), (64, 16), (64, 32), (128, 8), (128, 16), (256, 5)])
+@pytest.mark.parametrize("spread", [3, 12, 31])
+@pytest.mark.parametrize("fall", [False, True])
+@pytest.mark.parametrize("window", [0, 50])
+def test_value_scales_far_apart_within_a_token(fg, d, hq, spread, fall, window):
+    c = values_apart(C.cache_case(d + hq + spread, [150, 17, 1, 0, 64], [2, 1, 1, 0, 3], hq, 1, d, 16), 5, spread, fall)
+    out, _ = attend(fg, c, window)
+    expect(fg)
+    check_by_block(c, out, window)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 8), (128, 16), (256, 8)])
+@pytest.mark.parametrize("tokens", [[3], [130, 131], [299]])
+def test_a_token_with_scales_far_apart_among_others(fg, d, hq, tokens):
+    """One block of one token far above everything else: the other blocks keep the other tokens' digits."""
+    c = values_apart(C.cache_case(d + tokens[0], [300, 300], [1, 1], hq, 1, d, 32), 7, 25, True, tokens)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check_by_block(c, out)
+
+
+def test_value_blocks_of_zeros_beside_small_ones(fg):
+    """A block of zeros has scale 1, however small its neighbours are."""
+    c = C.cache_case(41, [200, 90], [1, 2], 8, 2, 128, 16)
+    g = C.rng(41)
+    for r, n in enumerate(c["lens"]):
+        x = g.standard_normal((n, 2, 128)) * 2.0 ** -45
+        x[:, :, 32:64] = 0.0
+        codes, sf = O.encode(x)
+        p, o = c["table"][r, np.arange(n) // 16], np.arange(n) % 16
+        c["vc"][p, :, o], c["vs"][p, :, o] = O.rows(codes, "v"), sf
+    out, _ = attend(fg, c)
+    expect(fg)
+    check_by_block(c, out)
+    assert not out[:3, :, 32:64].any()
+
+
+@pytest.mark.parametrize("d,hq", [(64, 8), (128, 8), (128, 16), (256, 8)])
+@pytest.mark.parametrize("fall", [False, True])
+def test_value_scales_far_apart_over_a_long_context(fg, d, hq, fall):
+    """Pieces of one item in several CTAs, their maxima far apart."""
+    c = values_apart(C.cache_case(d + hq + 1, [5000], [1], hq, 1, d, 64), 9, 25, fall)
+    out, ws = attend(fg, c)
+    expect(fg)
+    check_by_block(c, out)
+    again, _ = attend(fg, c, ws=ws)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("hq", [8, 32])
+def test_many_rows_and_value_scales_far_apart(fg, hq):
+    c = values_apart(C.wide(C.cache_case(hq, [150, 60], [70, 50], hq, 1, 128, 16)), 11, 31, True)
+    assert C.many_rows(c)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check_by_block(c, out)
