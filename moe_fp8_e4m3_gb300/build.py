@@ -1,5 +1,6 @@
-"""Builds the CUDA library ``libfg.so`` in-tree for sm_103a with nvcc, and beside it ``fg_bind.so``, the Python
-module of the calls whose marshalling has to be short.
+"""Builds the CUDA library ``libfg.so`` in-tree for sm_103a with nvcc, and beside it, where torch is installed,
+``fg_bind.so``, the Python module of the calls whose marshalling has to be short.  The library needs nvcc only; a
+module that does not compile (no Python headers, no g++) is a warning.
 
 The translation units compile in parallel; ``-Xptxas -v`` output goes to
 ``_build/ptxas.log`` and the build fails if any kernel spills registers or uses local
@@ -12,6 +13,7 @@ import re
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,13 +41,19 @@ def _flags() -> list[str]:
                    "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _stale(target: str) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    t = os.path.getmtime(target)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "fg.h"),
                                                                  os.path.abspath(__file__)]
     return any(os.path.getmtime(f) > t for f in deps)
+
+
+def _torch() -> str | None:
+    """The directory of the installed torch."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -59,7 +67,7 @@ def _compile(src: str) -> tuple[str, str]:
 
 def _compile_bind() -> str:
     obj = os.path.join(BUILD, "fg_bind.o")
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch()
     include = [sysconfig.get_paths()["include"], os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include")]
@@ -71,7 +79,7 @@ def _compile_bind() -> str:
 
 
 def _link_bind(obj: str) -> None:
-    torch = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+    torch = os.path.join(_torch(), "lib")
     cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", BIND + ".tmp", "-L", HERE, "-l:libfg.so", "-L", torch, "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -89,27 +97,37 @@ def check_ptxas(log: str) -> None:
         raise RuntimeError("register spills / local memory in kernels: " + "; ".join(bad))
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        bind = ex.submit(_compile_bind)
-        results = list(ex.map(_compile, SOURCES))
-        bind = bind.result()
-    log = "\n".join(r[1] for r in results)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        f.write(log)
-    check_ptxas(log)
+def _link(objs: list[str]) -> None:
     tmp = LIB + ".tmp"
-    cmd = [_nvcc()] + ARCH + ["-shared", "-o", tmp] + [r[0] for r in results]
+    cmd = [_nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
-    _link_bind(bind)
-    if verbose:
-        print(log)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    lib = force or _stale(LIB)
+    bind = _torch() is not None and (force or _stale(BIND))
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        bind_obj = ex.submit(_compile_bind) if bind else None
+        results = list(ex.map(_compile, SOURCES)) if lib else []
+    if lib:
+        log = "\n".join(r[1] for r in results)
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            f.write(log)
+        check_ptxas(log)
+        _link([r[0] for r in results])
+        if verbose:
+            print(log)
+    if bind:
+        try:
+            _link_bind(bind_obj.result())
+        except (RuntimeError, OSError) as e:
+            if os.path.exists(BIND):                        # of other sources
+                os.remove(BIND)
+            warnings.warn(f"fg_bind.so is not built: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 

@@ -1,0 +1,84 @@
+"""The build script on a host without a GPU: what it builds where torch or Python's headers are missing.  The compilers are
+stood in for by a function that writes the files they are asked for."""
+import importlib.util
+import os
+import subprocess
+import types
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture
+def build(tmp_path, monkeypatch):
+    """The build script with its outputs in tmp_path; .commands: what it ran."""
+    spec = importlib.util.spec_from_file_location("fg_build_under_test", os.path.join(ROOT, "moe_fp8_e4m3_gb300", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for name, file in (("BUILD", "_build"), ("LIB", "libfg.so"), ("BIND", "fg_bind.so")):
+        monkeypatch.setattr(mod, name, str(tmp_path / file))
+    mod.commands, mod.fails = [], lambda cmd: False
+
+    def run(cmd, **kw):
+        mod.commands.append(cmd)
+        if mod.fails(cmd):
+            return types.SimpleNamespace(returncode=1, stdout="", stderr="fatal error: Python.h: No such file or directory")
+        out = cmd[cmd.index("-o") + 1]
+        with open(out, "w") as f:
+            f.write(" ".join(cmd))
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(mod, "subprocess", types.SimpleNamespace(run=run, PIPE=subprocess.PIPE))
+    return mod
+
+
+def without_torch(monkeypatch, mod):
+    real = importlib.util.find_spec
+    fake = types.SimpleNamespace(util=types.SimpleNamespace(find_spec=lambda n, *a: None if n == "torch" else real(n, *a)))
+    monkeypatch.setattr(mod, "importlib", fake)
+
+
+def test_the_library_is_built_without_torch(build, monkeypatch):
+    without_torch(monkeypatch, build)
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert not os.path.exists(build.BIND) and not any("fg_bind.cpp" in " ".join(c) for c in build.commands)
+    n = len(build.commands)
+    build.build()
+    assert len(build.commands) == n, "nothing is out of date"
+
+
+def test_the_library_is_built_where_the_module_does_not_compile(build):
+    pytest.importorskip("torch")
+    build.fails = lambda cmd: any("fg_bind" in x for x in cmd)
+    with pytest.warns(RuntimeWarning, match="Python.h"):
+        build.build()
+    assert os.path.exists(build.LIB) and not os.path.exists(build.BIND)
+    with open(build.BIND, "w") as f:                         # one of older sources is not left to be loaded
+        f.write("old")
+    os.utime(build.BIND, (0, 0))
+    with pytest.warns(RuntimeWarning):
+        build.build()
+    assert not os.path.exists(build.BIND)
+    n = len(build.commands)
+    build.fails = lambda cmd: False
+    build.build()
+    assert os.path.exists(build.BIND)
+    assert all("fg_bind" in " ".join(c) for c in build.commands[n:]), "the library was up to date"
+
+
+def test_both_are_built_once(build):
+    pytest.importorskip("torch")
+    build.build()
+    assert os.path.exists(build.LIB) and os.path.exists(build.BIND)
+    n = len(build.commands)
+    build.build()
+    assert len(build.commands) == n
+    build.build(force=True)
+    assert len(build.commands) == 2 * n
+
+
+def test_a_library_that_does_not_link_is_an_error(build):
+    build.fails = lambda cmd: "-shared" in cmd
+    with pytest.raises(RuntimeError):
+        build.build()
