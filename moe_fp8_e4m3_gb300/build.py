@@ -7,6 +7,7 @@ The translation units compile in parallel; ``-Xptxas -v`` output goes to
 memory."""
 from __future__ import annotations
 
+import hashlib
 import importlib.util
 import os
 import re
@@ -56,6 +57,25 @@ def _torch() -> str | None:
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def bind_abi() -> str | None:
+    """What fg_bind.so is built for, as its docstring says: torch's version file and Python's binary interface."""
+    torch = _torch()
+    if torch is None:
+        return None
+    with open(os.path.join(torch, "version.py"), "rb") as f:
+        text = f.read()
+    return "fg_bind for " + hashlib.sha1(text + str(sysconfig.get_config_var("SOABI")).encode()).hexdigest()
+
+
+def bind_fits() -> bool:
+    """Whether the fg_bind.so that is there was built for the torch and the Python that are there now."""
+    abi = bind_abi()
+    if abi is None or not os.path.exists(BIND):
+        return False
+    with open(BIND, "rb") as f:
+        return abi.encode() in f.read()
+
+
 def _compile(src: str) -> tuple[str, str]:
     obj = os.path.join(BUILD, src.replace(".cu", ".o"))
     cmd = [_nvcc()] + _flags() + ["-Xptxas", "-v", "-c", os.path.join(CSRC, src), "-o", obj]
@@ -70,7 +90,8 @@ def _compile_bind() -> str:
     torch = _torch()
     include = [sysconfig.get_paths()["include"], os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"),
+           f'-DFG_BIND_ABI="{bind_abi()}"']
     cmd += [x for path in include for x in ("-isystem", path)] + ["-c", os.path.join(CSRC, "fg_bind.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -108,7 +129,7 @@ def _link(objs: list[str]) -> None:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     lib = force or _stale(LIB)
-    bind = _torch() is not None and (force or _stale(BIND))
+    bind = _torch() is not None and (force or _stale(BIND) or not bind_fits())
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         bind_obj = ex.submit(_compile_bind) if bind else None

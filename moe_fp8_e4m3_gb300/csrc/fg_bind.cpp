@@ -207,7 +207,9 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef g_methods[] = {method<py_tables>("tables"), method<py_rope>("rope"), method<py_append>("append"),
                            method<py_gather>("gather"), method<py_attention>("attention"), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fg_bind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+// The docstring says which torch and which Python the module is built for: it holds their inlined code, so it is not
+// loaded beside others (the build script's bind_fits looks for it in the file).
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fg_bind", FG_BIND_ABI, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

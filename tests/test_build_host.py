@@ -25,8 +25,13 @@ def build(tmp_path, monkeypatch):
         if mod.fails(cmd):
             return types.SimpleNamespace(returncode=1, stdout="", stderr="fatal error: Python.h: No such file or directory")
         out = cmd[cmd.index("-o") + 1]
+        text = " ".join(cmd)
+        for x in cmd:                                       # objects go into what is linked from them
+            if x.endswith(".o") and x != out and os.path.exists(x):
+                with open(x) as f:
+                    text += f.read()
         with open(out, "w") as f:
-            f.write(" ".join(cmd))
+            f.write(text)
         return types.SimpleNamespace(returncode=0, stdout="", stderr="")
 
     monkeypatch.setattr(mod, "subprocess", types.SimpleNamespace(run=run, PIPE=subprocess.PIPE))
@@ -82,3 +87,23 @@ def test_a_library_that_does_not_link_is_an_error(build):
     build.fails = lambda cmd: "-shared" in cmd
     with pytest.raises(RuntimeError):
         build.build()
+
+
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_the_module_is_built_anew_for_another_torch_or_python(build, tmp_path, monkeypatch, what):
+    """File times say nothing about it: the packages may be older than the module."""
+    pytest.importorskip("torch")
+    build.build()
+    assert build.bind_fits()
+    n = len(build.commands)
+    if what == "torch":
+        other = tmp_path / "torch"
+        other.mkdir()
+        (other / "version.py").write_text("__version__ = '0.0'")
+        monkeypatch.setattr(build, "_torch", lambda: str(other))
+    else:
+        monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-300")
+    assert not build.bind_fits()
+    build.build()
+    assert build.bind_fits() and len(build.commands) > n
+    assert all("fg_bind" in " ".join(c) for c in build.commands[n:])
