@@ -573,9 +573,10 @@ def fp8_gemm_nt_lora(a, sfa, b, sfb, x, lora_a, lora_b, scaling, ids, d, workspa
         _check(st, "fp8_gemm_nt_lora")
 
 
-# The calls of a serving step are short on the GPU, so a module in C++ (fg_bind.cpp) takes their arguments first; what it
-# does not take (a stream of the caller's, arguments that are wrong) is checked here, and goes in one record: ctypes
-# takes 0.09 us an argument, of which there are about twenty (measured on a GB300's host: 1.73 us against 0.65 us packed).
+# The calls of a serving step are short on the GPU, so a module in C++ (fg_bind.cpp) takes their arguments first.  What it
+# does not take (a stream of the caller's, arguments that are wrong, all where it cannot be loaded) is checked here, and
+# goes in one record: ctypes takes 0.09 us an argument, of which there are about twenty (measured on a GB300's host: 1.73
+# us against 0.65 us packed).
 _TABLES_ARGS = struct.Struct("=17q")
 _ROPE_ARGS = struct.Struct("=12qd8q")
 _APPEND_ARGS = struct.Struct("=15q")
@@ -585,13 +586,33 @@ _call = lib.fg_call
 _bind = None
 
 
+class _NoModule:
+    """In the place of a module that cannot be loaded: takes no call, so that the binding below does."""
+    @staticmethod
+    def tables(*args):
+        return None
+
+    rope = append = gather = attention = tables
+
+
 def _native():
-    """The module in C++; torch's libraries are there before it."""
+    """The module in C++; torch's libraries are there before it.  One that was built for another torch or Python is not
+    loaded."""
     global _bind
     import torch  # noqa: F401
-    from . import fg_bind
-    _bind = fg_bind
-    return fg_bind
+
+    from . import build
+    try:
+        if not build.bind_fits():
+            raise ImportError("fg_bind.so is missing or was built for another torch or Python")
+        from . import fg_bind
+        _bind = fg_bind
+    except ImportError as e:
+        import warnings
+        warnings.warn(f"a serving step's calls take 4 us longer: {e} (moe_fp8_e4m3_gb300.build.build() builds it)", RuntimeWarning,
+                      stacklevel=3)
+        _bind = _NoModule
+    return _bind
 
 
 def build_block_tables(context_lens, new_lens, free_pages, free_count, block_table, query_start, seq_lens, slots, positions,

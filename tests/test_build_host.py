@@ -107,3 +107,26 @@ def test_the_module_is_built_anew_for_another_torch_or_python(build, tmp_path, m
     build.build()
     assert build.bind_fits() and len(build.commands) > n
     assert all("fg_bind" in " ".join(c) for c in build.commands[n:])
+
+
+@pytest.mark.parametrize("why", ["missing", "other"])
+def test_calls_go_through_the_binding_where_the_module_does_not_fit(why, tmp_path, monkeypatch):
+    torch = pytest.importorskip("torch")
+    import moe_fp8_e4m3_gb300 as fg
+    from moe_fp8_e4m3_gb300 import build as mod
+
+    from test_abi_serving import ARGS
+    if why == "other":
+        (tmp_path / "fg_bind.so").write_text("of another torch")
+    monkeypatch.setattr(mod, "BIND", str(tmp_path / "fg_bind.so"))
+    monkeypatch.setattr(fg, "_bind", None)
+    monkeypatch.setattr(fg, "_stream", lambda stream: 0)
+    calls = []
+    monkeypatch.setattr(fg, "_call", lambda *a: calls.append(a[0]) or fg.FG_OK)
+    with pytest.warns(RuntimeWarning, match="fg_bind.so"):
+        fg.build_block_tables(**ARGS["build_block_tables"](fg))
+    for name in ("qk_norm_rope", "kv_append_mxfp4", "kv_gather_mxfp4", "paged_attention_mxfp4"):
+        getattr(fg, name)(**ARGS[name](fg))
+    assert calls == [0, 1, 2, 3, 4]
+    with pytest.raises(TypeError):
+        fg.build_block_tables(**dict(ARGS["build_block_tables"](fg), slots=torch.zeros(7, dtype=torch.int32)))
