@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
                 for (int i = 0; i < 4; ++i)
                     f[b][i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
             }
-            return __uint_as_float(static_cast<uint32_t>(127 - x) << 23) * p.scale_log2;
+            // never 0, which a masked score's -inf must not meet; below 2^-126 no score (at most 2^82 before) counts
+            return fmaxf(__uint_as_float(static_cast<uint32_t>(127 - x) << 23) * p.scale_log2, 0x1p-126f);
         };
         // One after another in flight: q, the pages of the first tiles, those tiles.
         uint4 raw[B];

@@ -1,5 +1,5 @@
 """The serving step's operators at the limits of their arguments: windows as large as their type, requests that claim
-the same rows, pages of more than 2^30 tokens, value scales far apart within a token."""
+the same rows, pages of more than 2^30 tokens, value scales far apart within a token, scales that leave no score."""
 import numpy as np
 import pytest
 
@@ -199,3 +199,21 @@ def test_many_rows_and_value_scales_far_apart(fg, hq):
     out, _ = attend(fg, c)
     expect(fg)
     check_by_block(c, out)
+
+
+# -------------------------------------------------------------------- scores of any size
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [2.0 ** -23, 2.0 ** -40, 2.0 ** -126, 2.0 ** -149])
+def test_scales_that_leave_no_score(fg, d, scale):
+    """Queries of zeros and small ones, the smallest scales: every key that a row looks at counts the same, and no other."""
+    c = C.cache_case(d, [37, 300, 5], [3, 1, 5], 4, 2, d, 16)
+    c["q"][0] = 0.0
+    c["q"][1] *= 2.0 ** -120
+    c["q_bits"], c["q"] = O.bf16(c["q"])
+    for many in (False, True):
+        if many:
+            c = C.wide(dict(c, q=np.concatenate([c["q"]] + [c["q"][:1]] * 300), q_bits=np.concatenate([c["q_bits"]] + [c["q_bits"][:1]] * 300)))
+            assert C.many_rows(c)
+        out, _ = attend(fg, c, scale=scale)
+        expect(fg)
+        check(c, out, scale=scale)
