@@ -11,8 +11,9 @@
 // M moves only when some w might pass 2^15 (a vote a tile), to where the largest is 2^8; then O and l are scaled.
 // A weight is rounded once, to FP16: by 2^-11 of itself, or by 2^-33 of the row's largest w where that is more.  M
 // speaks for all blocks, so that is 2^-25 of a block's own largest w as long as the scales of a token lie within 2^8 of each
-// other.  From the first tile on in which they do not (the same vote), a warp multiplies its piece's weights and values in
-// FP32 on the CUDA cores: called alone, 64 requests of up to 8192 tokens then take 229 us for 69, one of 131072 127 for 45.
+// other.  From the first tile on in which they do not (the same vote), or in which a score passes 2^20 (whose rounding then
+// is more than FP16's range takes), a warp multiplies its piece's weights and values in FP32 on the CUDA cores, M the largest
+// score: called alone, 64 requests of up to 8192 tokens then take 229 us for 69, one of 131072 127 for 45.
 // The check costs 0.6 of 67.7 us; with the FP32 products in the same loop it was 4.3 (registers).
 //
 // Work.  An item (fg_attn.cuh: request, chunk of kRows rows, kv head) is walked in blocks of 128 tokens, of which each of
@@ -363,6 +364,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
         }
 
         // A tile.  False: a token's value scales are far apart, nothing is done yet, and kApart has to do it.
+        // M up to the largest of the lanes' `top`, where that is more.
+        auto move = [&](int nt, int k, float top) {
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
+            top = fmaxf(top, m[nt][k]);
+            const float f = ex2(m[nt][k] - top);
+            m[nt][k] = top;
+            l[nt][k] *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * B; ++i) {
+                o[nt][i][k] *= f;
+                o[nt][i][2 + k] *= f;
+            }
+        };
         auto compute = [&](auto is_apart, int stage, int tok0, bool ok) {
             constexpr bool kApart = decltype(is_apart)::value;
             const uint32_t at = stage * C::kTile;
@@ -414,55 +429,60 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
                         if (!(in1 && t1 >= lo && t1 < hi)) s[nt][2 + k] = -INFINITY;
                     }
             }
-            bool far = false;
-            if constexpr (!kApart) {                            // two of the four lanes that have a token's scales look at them
-                uint32_t mine[(B + 3) / 4];
+            uint32_t mine[(B + 3) / 4];                         // two of the four lanes that have a token's scales look at them
 #pragma unroll
-                for (int i = 0; i < (B + 3) / 4; ++i) mine[i] = (c & 1) ? vs1[i] : vs0[i];
-                far = scales_apart<B>(mine);
-            }
+            for (int i = 0; i < (B + 3) / 4; ++i) mine[i] = (c & 1) ? vs1[i] : vs0[i];
+            bool far = scales_apart<B>(mine);
             scales_of<B>(f0, vs0);
             scales_of<B>(f1, vs1);
             float w[NT][4];
-            auto weights = [&]() {
+            if constexpr (kApart) {                             // as usual: M is the largest score
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        w[nt][k] = ex2(fmaf(s[nt][k], qs(nt, k), kBias - m[nt][k]));
-                        w[nt][2 + k] = ex2(fmaf(s[nt][2 + k], qs(nt, k), kBias - m[nt][k]));
+                        // rounded before the difference, so that it is 0 for the largest, whatever its size
+                        const float s0 = __fmul_rn(s[nt][k], qs(nt, k)), s1 = __fmul_rn(s[nt][2 + k], qs(nt, k));
+                        move(nt, k, fmaxf(s0, s1));
+                        w[nt][k] = ex2(s0 - m[nt][k] + kBias);
+                        w[nt][2 + k] = ex2(s1 - m[nt][k] + kBias);
                     }
-            };
-            weights();
-            // no weight times scale is above the sum of all
-            float sum0 = f0[0], sum1 = f1[0];
+            } else {
+                auto weights = [&]() {
 #pragma unroll
-            for (int b = 1; b < B; ++b) { sum0 += f0[b]; sum1 += f1[b]; }
-            bool over = far;
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                over |= !(fmaf(w[nt][0], sum0, fmaf(w[nt][1], sum0, fmaf(w[nt][2], sum1, w[nt][3] * sum1))) <= kMostW);
-            if (__any_sync(kAll, over)) {
-                if (!kApart && __any_sync(kAll, far)) return false;
-                const float e0 = top_exponent<B>(f0), e1 = top_exponent<B>(f1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float top = fmaxf(fmaf(s[nt][k], qs(nt, k), e0), fmaf(s[nt][2 + k], qs(nt, k), e1));
-#pragma unroll
-                        for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
-                        top = fmaxf(top, m[nt][k]);
-                        const float f = ex2(m[nt][k] - top);
-                        m[nt][k] = top;
-                        l[nt][k] *= f;
-#pragma unroll
-                        for (int i = 0; i < 2 * B; ++i) {
-                            o[nt][i][k] *= f;
-                            o[nt][i][2 + k] *= f;
+                        for (int k = 0; k < 2; ++k) {
+                            w[nt][k] = ex2(fmaf(s[nt][k], qs(nt, k), kBias - m[nt][k]));
+                            w[nt][2 + k] = ex2(fmaf(s[nt][2 + k], qs(nt, k), kBias - m[nt][k]));
                         }
-                    }
+                };
                 weights();
+                // no weight times scale is above the sum of all
+                float sum0 = f0[0], sum1 = f1[0];
+#pragma unroll
+                for (int b = 1; b < B; ++b) { sum0 += f0[b]; sum1 += f1[b]; }
+                bool over = far;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    over |= !(fmaf(w[nt][0], sum0, fmaf(w[nt][1], sum0, fmaf(w[nt][2], sum1, w[nt][3] * sum1))) <= kMostW);
+                if (__any_sync(kAll, over)) {
+                    // a score past 2^20 leaves no room for the scales in M, nor FP16's range to what M is rounded by
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = s[nt][i] * qs(nt, i & 1);
+                            far |= fabsf(x) > 0x1p20f && x > -INFINITY;
+                        }
+                    if (__any_sync(kAll, far)) return false;
+                    const float e0 = top_exponent<B>(f0), e1 = top_exponent<B>(f1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) move(nt, k, fmaxf(fmaf(s[nt][k], qs(nt, k), e0), fmaf(s[nt][2 + k], qs(nt, k), e1)));
+                    weights();
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {

@@ -16,7 +16,7 @@ namespace fg {
 
 constexpr int kAttnMaxCtas = 640;             // shares of a launch, at most
 constexpr int kAttnMaxRequests = 4096;
-constexpr float kAttnEmpty = -1e30f;          // maximum of a row without a key
+constexpr float kAttnEmpty = -3e38f;          // maximum of a row without a key: below every score, and finite
 constexpr uint32_t kAllLanes = 0xffffffffu;
 
 struct AttnParams {

@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdio>
+#include <type_traits>
 
 #include "fg.h"
 #include "fg_host.h"
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                 // One pass over the scores, 16 columns ahead on their way: weights under the present m, their sum, the
                 // largest score.  Where that one passes m by more than kSlack, m moves and the pass is done again.
                 float top, sum;
-                auto weights = [&](int c, uint32_t (&r)[16]) {
+                auto weights = [&](auto rounded, int c, uint32_t (&r)[16]) {
+                    constexpr bool kRounded = decltype(rounded)::value;
                     if (border) {                               // bit x: column c + x counts
                         const int at = base + col0 + c;
                         const int from = min(max(lo - at, 0), 16), to = min(max(hi - at, 0), 16);
@@ -397,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                             const float s0 = __uint_as_float(r[x + 2 * y]), s1 = __uint_as_float(r[x + 2 * y + 1]);
                             most[0] = fmaxf(most[0], s0);
                             most[1] = fmaxf(most[1], s1);
-                            const float w0 = ex2(fmaf(s0, p.scale_log2, -m)), w1 = ex2(fmaf(s1, p.scale_log2, -m));
+                            const float w0 = ex2(kRounded ? __fmul_rn(s0, p.scale_log2) - m : fmaf(s0, p.scale_log2, -m));
+                            const float w1 = ex2(kRounded ? __fmul_rn(s1, p.scale_log2) - m : fmaf(s1, p.scale_log2, -m));
                             part[0] += w0;
                             part[1] += w1;
                             const __nv_bfloat162 w = __floats2bfloat162_rn(w0, w1);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                     sum += part[0] + part[1];
                     top = fmaxf(top, fmaxf(most[0], most[1]));
                 };
-                auto pass = [&]() {
+                auto pass = [&](auto rounded) {
                     top = -INFINITY;
                     sum = 0.0f;
                     uint32_t ra[16], rb[16];
@@ -417,16 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
 #pragma unroll 1
                     for (int c = 0; c < C::kWide; c += 32) {
                         fg::tmem_ld_32x32b_x16(at_s + c + 16, rb);
-                        weights(c, ra);
+                        weights(rounded, c, ra);
                         fg::tmem_wait_ld();
                         if (c + 32 < C::kWide) fg::tmem_ld_32x32b_x16(at_s + c + 32, ra);
-                        weights(c + 16, rb);
+                        weights(rounded, c + 16, rb);
                         fg::tmem_wait_ld();
                     }
                     top *= p.scale_log2;
                 };
-                pass();
-                const bool rise = dead || top > m + kSlack;
+                pass(std::false_type{});
+                // m is rounded, which a large score minus m would be off by (past 2^30 beyond what a weight holds): then the pass
+                // is done again with rounded scores.  That costs every pass 4 us of 116 where it is always done.
+                const bool large = fabsf(m) > 0x1p20f && m > fg::kAttnEmpty;
+                const bool rise = dead || large || top > m + kSlack;
                 if (RT == 1 ? pair_any(1 + (warp & 3), rise) : __any_sync(kAll, rise)) {
                     float both = top;
                     if constexpr (RT == 1) {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const AttnPara
                         tmem_wait_st();
                     }
                     if (RT == 1) pair_any(1 + (warp & 3), false);   // both have read before either writes again
-                    pass();
+                    pass(std::true_type{});
                 }
                 l += sum;
                 fg::tc_fence_before();

@@ -1,5 +1,6 @@
 """The serving step's operators at the limits of their arguments: windows as large as their type, requests that claim
-the same rows, pages of more than 2^30 tokens, value scales far apart within a token, scales that leave no score."""
+the same rows, pages of more than 2^30 tokens, value scales far apart within a token, scales that
+leave no score, scores of any size."""
 import numpy as np
 import pytest
 
@@ -217,3 +218,60 @@ def test_scales_that_leave_no_score(fg, d, scale):
         out, _ = attend(fg, c, scale=scale)
         expect(fg)
         check(c, out, scale=scale)
+
+
+def peaked(c, sign, power, tie):
+    """Keys 2^-min(|j - middle|, tie) in every element, queries of one value, `sign` times 2^power to 2^(power + 1), in every
+    element of a row: scores differ by at least a factor of two, so that a row's output is the mean of the values whose
+    score is the largest, the middle key's or (sign -1) the farthest ones'.  Returns the outputs' exact values."""
+    d, page = c["d"], c["page"]
+    c["q"][:] = sign * 2.0 ** power * (1 + C.rng(power).integers(0, 128, c["q"].shape[:2] + (1,)) / 128)
+    c["q_bits"], c["q"] = O.bf16(c["q"])
+    out = np.zeros(c["q"].shape)
+    for r, n in enumerate(c["lens"]):
+        j = np.arange(n)
+        level = -np.minimum(np.abs(j - n // 2), tie)
+        codes, sf = O.encode(np.broadcast_to((2.0 ** level)[:, None, None], (n, c["hkv"], d)))
+        p, o = c["table"][r, j // page], j % page
+        c["kc"][p, :, o], c["ks"][p, :, o] = O.rows(codes, "k"), sf
+        t0, new = c["start"][r], c["start"][r + 1] - c["start"][r]
+        for h in range(c["hkv"]):
+            v = O.cached(c["table"][r], n, c["vc"], c["vs"], "v", h)
+            for i in range(new):
+                s = sign * level[:n - new + i + 1]
+                top = np.flatnonzero(s == s.max(initial=-99))
+                group = c["hq"] // c["hkv"]
+                out[t0 + i, h * group:(h + 1) * group] = v[top].mean(0) if len(top) else 0.0
+    return out
+
+
+def check_peaked(c, out, want):
+    """The other weights are 2^-(2^18) of the largest and less.  Each of up to n equal weights and their sum is rounded
+    to FP32, a weight (times a scale) to FP16 or BF16: a term of up to n is off by at most 2^-8 of |v| together."""
+    got, n = f64(out), int(c["start"][-1])
+    size = max(np.abs(want[:n]).max(), 2.0 ** -8)
+    assert np.isfinite(got[:n]).all()
+    assert (np.abs(got[:n] - want[:n]) <= 2.0 ** -8 * np.abs(want[:n]) + 2.0 ** -8 * 24.0 * size).all(), np.abs(got[:n] - want[:n]).max()
+
+
+@pytest.mark.parametrize("d,hq", [(64, 8), (64, 32), (128, 8), (128, 16), (256, 8)])
+@pytest.mark.parametrize("power", [18, 24, 27, 30, 50, 100, 110])
+@pytest.mark.parametrize("sign,tie", [(1, 8), (-1, 8), (1, 0)])
+def test_scores_of_any_size(fg, d, hq, power, sign, tie):
+    c = C.cache_case(d + hq, [1, 37, 300], [1, 2, 1], hq, 1, d, 16, spread=0)
+    want = peaked(c, sign, power, tie)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check_peaked(c, out, want)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 8), (128, 8), (128, 32), (256, 8)])
+@pytest.mark.parametrize("power", [18, 24, 30, 50, 100, 110])
+@pytest.mark.parametrize("sign,tie", [(1, 8), (-1, 8), (1, 0)])
+def test_many_rows_and_scores_of_any_size(fg, d, hq, power, sign, tie):
+    c = C.wide(C.cache_case(d + hq, [70, 300], [70, 60], hq, 1, d, 16, spread=0))
+    assert C.many_rows(c)
+    want = peaked(c, sign, power, tie)
+    out, _ = attend(fg, c)
+    expect(fg)
+    check_peaked(c, out, want)
