@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
 
         // keys that every row of the chunk looks at: tiles inside need no mask
         const int i_first = row0 / p.group, i_last = (row0 + rows - 1) / p.group;
-        const int all_hi = first + i_first + 1, all_lo = fg::attn_from(p, first + i_last + 1);
+        const int all_hi = first + i_first + 1, all_lo = max(0, fg::attn_back(p, first + i_last + 1));
         // this warp's tiles: tokens 16 * (8 * block + warp)
         int base = b0 * kBlock + 16 * warp;
         const int base_end = keys_hi > keys_lo ? min(b1 * kBlock, keys_hi) : 0;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<B, NT>::kPerSm) attn_kernel(cons
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int i = (row0 + nt * 8 + 2 * c + k) / p.group;
-                        const int hi = first + i + 1, lo = fg::attn_from(p, hi);
+                        const int hi = first + i + 1, lo = fg::attn_back(p, hi);
                         if (!(in0 && t0 >= lo && t0 < hi)) s[nt][k] = -INFINITY;
                         if (!(in1 && t1 >= lo && t1 < hi)) s[nt][2 + k] = -INFINITY;
                     }

@@ -67,6 +67,10 @@ __device__ __forceinline__ bool attn_claimed_twice(const AttnParams& p) {
 __device__ __forceinline__ int attn_from(const AttnParams& p, int hi) {
     return p.window > 0 ? max(0, max(hi, 0) - p.window) : 0;
 }
+// The same where nothing depends on it for hi <= 0, and what is below 0 counts as 0: without a comparison, and allowed to wrap.
+__device__ __forceinline__ int attn_back(const AttnParams& p, int hi) {
+    return p.window > 0 ? static_cast<int>(static_cast<unsigned>(hi) - static_cast<unsigned>(p.window)) : 0;
+}
 // Keys [lo, hi) that some row of a chunk looks at; hi <= lo: none.
 struct AttnKeys {
     int lo, hi;
