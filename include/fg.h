@@ -580,9 +580,10 @@ int fg_get_device_error(fg_stream_t stream, int* detail);
 /* Static description of a status code. */
 const char* fg_status_string(int status);
 
-/* Test hook for the time-out path: while enabled, the next GEMM launches have their
- * operand producer skip its first stage, so the MMA issuer's bounded wait runs out
- * after timeout_us microseconds, the kernel records FG_ERR_DEVICE_TIMEOUT and every
+/* Test hook for the time-out path: while enabled, the next launches of the GEMMs, of the decode
+ * step's MoE MLP and projection, and of the attention over many rows a request have their
+ * operand producer hold back its first stage (key tile), so the MMA issuer's bounded wait runs
+ * out after timeout_us microseconds, the kernel records FG_ERR_DEVICE_TIMEOUT and every
  * role exits cleanly.  enable = 0 restores normal operation and the default time-out. */
 void fg_debug_inject_stall(int enable, uint32_t timeout_us);
 

@@ -3,7 +3,8 @@
 // Mathematics.  For the R = group x new-token rows that share a kv head, with keys k_j = sum over blocks b of
 // s_jb * (codes), per 16 tokens:
 //   S^T = K Q^T      16 tokens x 8 rows per mma (m16n8k16, FP16 codes, FP16 q scaled to [2^8, 2^9) by a
-//                    power of two per row, exact); one FP32 accumulator per block of 32, then times s_jb
+//                    power of two per row: exact down to 2^-22 of the row's largest element, off by up to 2^-33 of it
+//                    below); one FP32 accumulator per block of 32, then times s_jb
 //   w_jb = 2^(S_j - M) * t_jb      t_jb: the value's block scale; M follows the maximum of S_j + max_b log2 t_jb,
 //                    so that w <= 2^15 in FP16 however far the scales of different tokens lie apart
 //   O^T += V^T W^T   32 elements of block b x 16 tokens x 8 rows, FP16 codes, FP32 accumulators
@@ -13,21 +14,21 @@
 // speaks for all blocks, so that is 2^-25 of a block's own largest w as long as the scales of a token lie within 2^8 of each
 // other.  From the first tile on in which they do not (the same vote), or in which a score passes 2^20 (whose rounding then
 // is more than FP16's range takes), a warp multiplies its piece's weights and values in FP32 on the CUDA cores, M the largest
-// score: called alone, 64 requests of up to 8192 tokens then take 229 us for 69, one of 131072 127 for 45.
-// The check costs 0.6 of 67.7 us; with the FP32 products in the same loop it was 4.3 (registers).
+// score: called alone, 64 requests of up to 8192 tokens then take 233 us for 69, one of 131072 129 for 44.
+// The looks cost 0.7 of 67.7 us (D = 64: 1.1 of 46.2); with the FP32 products in the same loop it was 4.3 (registers).
 //
 // Work.  An item (fg_attn.cuh: request, chunk of kRows rows, kv head) is walked in blocks of 128 tokens, of which each of
 // a CTA's eight warps takes 16 with accumulators of its own, joined at the end through shared memory.  Codes and scales
 // come through a ring of kStages tiles of 16 tokens that each warp has to itself (asynchronous 16-byte copies, no
 // barrier of the CTA); the cache's order puts what a lane needs of a row into one load, and sixteen tokens never
-// cross a page.  Three stages: 64 requests of up to 8192 tokens, 64 query heads on 8 of 128, take 67.8 us, with four 68.1,
-// with five 69.7; one of 131072 40.1, 40.6 and 41.7.
+// cross a page.  Three stages: with four 64 requests of up to 8192 tokens, 64 query heads on 8 of 128, took 0.3 us longer,
+// with five 1.9; one of 131072 0.5 and 1.6.
 //
 // Bound: the ALU pipe (conversions of codes, which take 52 % of it over a launch and more inside the loop) beside HBM
-// bytes: the loop streams at 6.3 TB/s, all of a launch at 4.3 (66.0 us); the rest is the cut
-// (2.2 us: every CTA scans the lengths), q and the first pages (3), joins (1 to 4) and the last CTAs' tail.  FP16 codes on
-// mma.sync: 1022 products a clock and SM suffice for few rows, and E4M3 operands, four times as fast, would leave a weight
-// four significant bits.
+// bytes: the loop streams at 6.3 TB/s, all of a launch at 4.2 (64 requests of up to 8192 tokens 67.7 us, one of 131072
+// 38.4); the rest is the cut (2.2 us: every CTA scans the lengths), q and the first pages (3), joins (1 to 4) and the last
+// CTAs' tail.  FP16 codes on mma.sync: its 1022 products a clock and SM suffice for few rows, and E4M3 operands would leave
+// a weight four significant bits.
 #include <cuda_runtime.h>
 
 #include <cstdio>

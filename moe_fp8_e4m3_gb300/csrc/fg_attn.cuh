@@ -79,7 +79,7 @@ struct AttnKeys {
 // Shared memory of a plan.
 template <int kThreads>
 struct AttnPlanSmem {
-    unsigned long long warp[kThreads / 32], strip[kThreads + 1];
+    unsigned long long warp[kThreads / 32], strip[kThreads];
     volatile unsigned long long line[4];       // shares, blocks of all items, this share's end, where the current item begins
     int last;
 };
@@ -216,7 +216,6 @@ struct AttnCursor {
             }
             const unsigned long long at = scan(sum, sm.warp, total_blocks);
             sm.strip[tid] = at;
-            if (tid == 0) sm.strip[kThreads] = total_blocks;
         }
         __syncthreads();
         return settle(p, sm, s_pre, total_blocks, false);

@@ -19,8 +19,8 @@
 // warps, which both reach on every tile, also after a wait that ran out; pieces of items follow one another with a CTA
 // barrier between.
 //
-// Bound: latency.  4 prompts of up to 512 tokens over 6000, 32 query heads on 4 of 128: 118 us (450 TFLOP/s; items of
-// one row tile 131), 2.9 us a key tile and pair of row tiles, with the tensor pipe at work in 27 % of it: decode, product,
+// Bound: latency.  4 prompts of up to 512 tokens over 6000, 32 query heads on 4 of 128: 117 us (449 TFLOP/s; with
+// other lengths of that range 87 to 148; items of one row tile 131), 2.9 us a key tile and pair of row tiles, with the tensor pipe at work in 27 % of it: decode, product,
 // exponentials, product are one chain over four hand-offs, and each role's warps issue once in 4 clocks.  Without
 // the decoders' arithmetic, the exponentials or half of the products a call is at most 8 % shorter, without all three 17 %.
 #include <cuda_runtime.h>

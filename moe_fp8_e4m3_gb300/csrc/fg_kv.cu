@@ -6,8 +6,8 @@
 // b + 1: lanes of neighbouring blocks trade one half word each, so every lane stores one whole word.
 // A thread has its part of one or two heads of a token in flight, keys and values both.
 // Bound: HBM bytes and, near them, instructions for many tokens (8192 tokens of 8 heads of 128 in and out
-// again, 85 MB: 15.2 us, 5.6 TB/s; an append runs some 200 instructions per 16 lanes' row), launch latency for few
-// (37 tokens: 3.5 us for both calls).
+// again, 85 MB: 17.3 us, 4.9 TB/s, 9.5 of them the append, which runs some 200 instructions per 16 lanes' row; 15.4 where
+// the same arrays are still in L2), launch latency for few (37 tokens: 3.5 us for both calls).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -195,7 +195,7 @@ int launch(F kernel, int rows, int per_block, const KvParams& p, int pdl, cudaSt
     return FG_OK;
 }
 // One head a thread where the device holds all their threads at once (37 tokens of 8 heads of 128 in and out again: 3.5
-// us, with two 4.1; 1024: 4.9 either way), two where it does not (2048: 6.3 us, with one 7.4; 8192: 15.2 and 18.6; with
+// us, with two 3.9; 1024: 4.8 either way), two where it does not (2048: 6.3 us, with one 7.4; 8192: 17.3 and 20.5; with
 // four 18.8).
 template <int L>
 int launch(bool append, const KvParams& p, const fg::HostState& st, cudaStream_t stream) {
