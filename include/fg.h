@@ -448,8 +448,8 @@ int fg_fp8_gemm_nt_lora(int M, int N, int K, int L, int R, const uint8_t* a, con
  * seq_lens may be context_lens, free_count_out may be free_count; other arrays do not overlap.  A call
  * repeated on the same inputs gives the same results.  Lengths below 0 (-1 in new_lens) or past max_pages
  * pages, more than T tokens or than the free pages, a free_count outside [0, free_len - pages given back]:
- * 0x107 is recorded and the step is empty (query_start 0, slots and positions -1, lengths and free pages as
- * they were).  A page id outside [0, num_pages): 0x107, and slot -1 for its tokens.
+ * 0x107 is recorded and the step is empty (query_start 0, slots and positions -1, free pages and lengths as
+ * they were, a length below 0 as 0).  A page id outside [0, num_pages): 0x107, and slot -1 for its tokens.
  * Supported: S <= 4000, T <= 2^18, max_pages <= 2^18.
  */
 int fg_build_block_tables(int S, int T, int page_size, int num_pages, int max_pages, int free_len,
